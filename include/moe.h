@@ -388,6 +388,79 @@ int moe_forward_ex(const moe_dims* d, const uint16_t* x, const float* logits,
                    const moe_debug_out* dbg, void* const* events, void* ws, size_t ws_bytes,
                    void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Operators around the expert FFN: what the transformer block that holds the layer
+ * needs next to it.  The pages have no counterpart (their layers run inside a serving
+ * engine that has them); the formulas are given with each call.  The same conventions:
+ * contiguous row-major device tensors, 16-byte aligned pointers (4-byte for the small
+ * fp32 / int32 vectors), asynchronous on `stream`, nothing allocated. */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
+
+/* Residual addition and RMS norm, with a bf16 output and / or FP8 codes:
+ *     a = x + residual;  h = a;  rstd = (mean(a^2) + eps)^(-1/2);
+ *     y = bf16(a * rstd * gain);  (q, s) = the activation rule above on the bf16 y.
+ *   x [rows][cols] bf16; residual [rows][cols] of res_dtype, or NULL (a = x); gain [cols]
+ *   of gain_dtype.  Outputs, each of which may be NULL (h, y or q must be given): h
+ *   [rows][cols] of res_dtype (the residual stream's new value), y [rows][cols] bf16, q
+ *   [rows][cols] E4M3 codes with s [rows][cols/128] scale bytes (both or neither;
+ *   cols % 128 == 0), rstd [rows] fp32 (what the gradient needs).
+ *   The sums run in fp32 on the unrounded a.  q, s equal moe_quant_act's of y, bit for
+ *   bit, whether y is written or not: they go straight to moe_grouped_gemm_w13.
+ *   h may be residual's buffer (a bf16 residual's also x's) and y may be x's; no other
+ *   two may overlap.  Any cols >= 1; whole 16-byte rows (cols % 8 == 0) are faster.
+ *   rows == 0 is a no-op. */
+int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* residual,
+                    int32_t res_dtype, const void* gain, int32_t gain_dtype, float eps, void* h,
+                    uint16_t* y, uint8_t* q, uint8_t* s, float* rstd, void* stream);
+
+/* Its gradient.  With n = h * rstd and u = dy * gain in each row:
+ *     dh = dh_in + rstd * (u - n * mean(u * n));   dgain = sum over rows of dy * n.
+ *   dy [rows][cols] bf16; h [rows][cols] of h_dtype and rstd [rows] as the forward wrote
+ *   them (h = x where there was no residual); dh_in [rows][cols] of h_dtype: the gradient
+ *   that reaches h by other ways (the residual stream), or NULL.  Outputs (at least one):
+ *   dh [rows][cols] of h_dtype, the gradient of the residual (and of x); dx the same
+ *   rounded to bf16 (x's type where the stream is fp32); dgain [cols] fp32, rows == 0: 0.
+ *   dh may be dh_in's or h's buffer, dx dy's.  fp32 sums in a fixed order, no atomics.
+ *   ws: moe_add_rmsnorm_backward_workspace_size bytes, 256-byte aligned (with dgain). */
+size_t moe_add_rmsnorm_backward_workspace_size(int32_t rows, int32_t cols);
+int moe_add_rmsnorm_backward(int32_t rows, int32_t cols, const uint16_t* dy, const void* h,
+                             int32_t h_dtype, const void* gain, int32_t gain_dtype,
+                             const float* rstd, const void* dh_in, void* dh, uint16_t* dx,
+                             float* dgain, void* ws, size_t ws_bytes, void* stream);
+
+/* Router balance loss per sequence, with the experts' counts.  p = softmax(logits[t]) over
+ * the E experts; for sequence s with n counted tokens:
+ *     counts[s][e] = how often e is in idx,   prob[s][e] = mean of p[t][e],
+ *     loss[s] = sum_e counts[s][e] * E / (k * n) * prob[s][e]   (1 when balanced),
+ *     z_loss[s] = mean of logsumexp(logits[t])^2.
+ *   logits [T][E] fp32 and idx [T][k] int32 as moe_route takes and gives them.
+ *   seq_offsets [S+1] int32, non-decreasing: sequence s is tokens [off[s], off[s+1]); NULL
+ *   with S == 1: all T.  token_mask [T] u8, or NULL: tokens with 0 (padding) and those of
+ *   no sequence count nowhere, whatever their logits and idx hold.  n = 0: all zero.
+ *   A token all of whose logits are -inf has p = 0 and adds nothing to z.
+ *   Outputs: counts [S][E] int32, n_tokens [S] int32 (n), prob [S][E], loss [S] fp32,
+ *   z_loss [S] fp32 or NULL.  Run-to-run identical (no floating-point atomics).
+ *   0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65535, T * k < 2^31.
+ *   ws: moe_balance_loss_workspace_size bytes, 256-byte aligned; moe_check_status(ws)
+ *   tells of an expert index outside [0, E) (not counted) or decreasing offsets. */
+size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t k, int32_t S);
+int moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits,
+                     const int32_t* idx, const int32_t* seq_offsets, const uint8_t* token_mask,
+                     int32_t* counts, int32_t* n_tokens, float* prob, float* loss, float* z_loss,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient (counts are constants), and that of moe_route's combine weights:
+ *     dlogits[t][e] = p_e * (A_e - sum_j A_j p_j) + p_e * 2 dz_loss[s] logsumexp / n
+ *                     + [e = idx[t][j]] w_j * (dw[t][j] - sum_i w_i dw[t][i]),
+ *   A_e = dloss[s] * counts[s][e] * E / (k n^2), w = softmax of the token's chosen logits.
+ *   counts and n_tokens as the forward wrote them; dloss [S], dz_loss [S], dw [T][k] fp32,
+ *   each NULL for none.  dlogits [T][E] fp32; rows that do not count (above) are zero. */
+int moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits,
+                              const int32_t* idx, const int32_t* seq_offsets,
+                              const uint8_t* token_mask, const int32_t* counts,
+                              const int32_t* n_tokens, const float* dloss, const float* dz_loss,
+                              const float* dw, float* dlogits, void* stream);
+
 /* Debug helper (synchronises `stream`): reads the device status word at the start of
  * a workspace used by the calls above.  Returns MOE_OK if no bit is set, else
  * MOE_ERR_DEVICE_CHECK and the bits in *bits_out (if not NULL).  The word is

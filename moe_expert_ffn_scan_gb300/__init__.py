@@ -126,6 +126,19 @@ def lib():
         for fn in ("moe_host_pipeline_create", "moe_host_pipeline_submit",
                    "moe_host_pipeline_sync", "moe_host_pipeline_destroy"):
             getattr(L, fn).restype = ctypes.c_int
+        _F = ctypes.c_float
+        L.moe_add_rmsnorm.argtypes = [_I, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, _P, _P, _P]
+        L.moe_add_rmsnorm_backward_workspace_size.argtypes = [_I, _I]
+        L.moe_add_rmsnorm_backward.argtypes = [_I, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P,
+                                               _P, _SZ, _P]
+        L.moe_balance_loss_workspace_size.argtypes = [_I] * 4
+        L.moe_balance_loss.argtypes = [_I] * 4 + [_P] * 10 + [_SZ, _P]
+        L.moe_balance_loss_backward.argtypes = [_I] * 4 + [_P] * 11
+        for fn in ("moe_add_rmsnorm_backward_workspace_size", "moe_balance_loss_workspace_size"):
+            getattr(L, fn).restype = _SZ
+        for fn in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_balance_loss",
+                   "moe_balance_loss_backward"):
+            getattr(L, fn).restype = ctypes.c_int
         for fn in ("moe_route", "moe_quant_act", "moe_grouped_gemm_w13", "moe_swiglu_quant",
                    "moe_grouped_gemm_w2", "moe_combine", "moe_forward", "moe_forward_timed",
                    "moe_check_status", "moe_forward_nvfp4", "moe_forward_nvfp4_timed",
@@ -141,7 +154,7 @@ def _p(t):
         return None
     if isinstance(t, int):
         return t
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensor must live on the GPU")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
@@ -151,6 +164,33 @@ def _p(t):
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _raw_stream(stream):
+    """_stream for calls short enough for its cost to show (tensors exist: CUDA is up)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _t(t, dtype, shape, name):
+    """_p of a tensor whose type and shape are checked first (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return _p(t)
+
+
+_DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}  # MOE_DTYPE_*
+
+
+def _dtype_code(t, name):
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return code
 
 
 def _check(fn, rc):
@@ -384,6 +424,100 @@ def moe_forward_timed(d, x, logits, w13, w13_s, w2, w2_s, out, ws, events, debug
         _d(d), _p(x), _p(logits), ctypes.byref(W), _p(out),
         ctypes.byref(dbg) if dbg is not None else None, ev, _p(ws), ws.numel(),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the expert FFN
+
+def add_rmsnorm_backward_workspace_size(rows, cols) -> int:
+    return lib().moe_add_rmsnorm_backward_workspace_size(rows, cols)
+
+
+def moe_add_rmsnorm(x, residual, gain, eps, h=None, y=None, q=None, s=None, rstd=None,
+                    stream=None):
+    """a = x + residual (or x), RMS norm of a times gain.  x [rows, cols] bf16, residual and h
+    bf16 or fp32 (the residual stream), gain bf16 or fp32 [cols].  Writes what is given of h
+    (a), y (bf16), q / s (uint8 E4M3 codes [rows, cols] and scale bytes [rows, cols / 128] of
+    y) and rstd [rows] fp32."""
+    rows, cols = shape = x.shape
+    st = residual if residual is not None else h
+    sd = st.dtype if st is not None else torch.bfloat16
+    sc = _dtype_code(st, "residual / h") if st is not None else 0
+    rc = lib().moe_add_rmsnorm(
+        rows, cols, _t(x, torch.bfloat16, shape, "x"), _t(residual, sd, shape, "residual"), sc,
+        _t(gain, gain.dtype, (cols,), "gain"), _dtype_code(gain, "gain"), eps,
+        _t(h, sd, shape, "h"), _t(y, torch.bfloat16, shape, "y"), _t(q, torch.uint8, shape, "q"),
+        _t(s, torch.uint8, (rows, cols // 128), "s"), _t(rstd, torch.float32, (rows,), "rstd"),
+        _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_add_rmsnorm", rc)
+
+
+def moe_add_rmsnorm_backward(dy, h, gain, rstd, ws, dh_in=None, dh=None, dx=None, dgain=None,
+                             stream=None):
+    """Gradient of moe_add_rmsnorm from dy [rows, cols] bf16, the forward's h and rstd, and
+    dh_in (the gradient that reaches h by other ways, or None).  Writes what is given of dh
+    (h's type), dx (dh in bf16) and dgain [cols] fp32.  ws:
+    add_rmsnorm_backward_workspace_size(rows, cols) bytes (None without dgain)."""
+    rows, cols = shape = dy.shape
+    hd = h.dtype
+    rc = lib().moe_add_rmsnorm_backward(
+        rows, cols, _t(dy, torch.bfloat16, shape, "dy"), _t(h, hd, shape, "h"),
+        _dtype_code(h, "h"), _t(gain, gain.dtype, (cols,), "gain"), _dtype_code(gain, "gain"),
+        _t(rstd, torch.float32, (rows,), "rstd"), _t(dh_in, hd, shape, "dh_in"),
+        _t(dh, hd, shape, "dh"), _t(dx, torch.bfloat16, shape, "dx"),
+        _t(dgain, torch.float32, (cols,), "dgain"), _p(ws), ws.numel() if ws is not None else 0,
+        _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_add_rmsnorm_backward", rc)
+
+
+def balance_loss_workspace_size(T, E, k, S=1) -> int:
+    return lib().moe_balance_loss_workspace_size(T, E, k, S)
+
+
+def _balance_args(logits, idx, seq_offsets, token_mask):
+    """(T, E, k, S) and the pointers of the four inputs, checked."""
+    T, E = logits.shape
+    k = idx.shape[1]
+    S = seq_offsets.shape[0] - 1 if seq_offsets is not None else 1
+    if token_mask is not None and token_mask.dtype is torch.bool:
+        token_mask = token_mask.view(torch.uint8)
+    return (T, E, k, S), (
+        _t(logits, torch.float32, (T, E), "logits"), _t(idx, torch.int32, (T, k), "idx"),
+        _t(seq_offsets, torch.int32, (S + 1,), "seq_offsets"),
+        _t(token_mask, torch.uint8, (T,), "token_mask"))
+
+
+def moe_balance_loss(logits, idx, counts, n_tokens, prob, loss, z_loss, ws, seq_offsets=None,
+                     token_mask=None, stream=None):
+    """Balance loss of logits [T, E] fp32 and the chosen experts idx [T, k] int32, for each of
+    the S sequences of seq_offsets [S + 1] int32 (None: one sequence of all tokens), without
+    the tokens whose token_mask [T] (uint8 or bool) is 0.  Writes counts [S, E] and n_tokens
+    [S] int32, prob [S, E], loss [S] and, if given, z_loss [S] fp32.  ws:
+    balance_loss_workspace_size(T, E, k, S) bytes; moe_check_status(ws) reads its checks."""
+    (T, E, k, S), inputs = _balance_args(logits, idx, seq_offsets, token_mask)
+    rc = lib().moe_balance_loss(
+        T, E, k, S, *inputs, _t(counts, torch.int32, (S, E), "counts"),
+        _t(n_tokens, torch.int32, (S,), "n_tokens"), _t(prob, torch.float32, (S, E), "prob"),
+        _t(loss, torch.float32, (S,), "loss"), _t(z_loss, torch.float32, (S,), "z_loss"),
+        _p(ws), ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_balance_loss", rc)
+
+
+def moe_balance_loss_backward(logits, idx, counts, n_tokens, dlogits, dloss=None, dz_loss=None,
+                              dw=None, seq_offsets=None, token_mask=None, stream=None):
+    """Gradient of the logits [T, E] from dloss [S], dz_loss [S] (moe_balance_loss's outputs)
+    and dw [T, k] (moe_route's combine weights), each None for none; counts and n_tokens as
+    the forward wrote them.  Writes dlogits [T, E] fp32."""
+    (T, E, k, S), inputs = _balance_args(logits, idx, seq_offsets, token_mask)
+    rc = lib().moe_balance_loss_backward(
+        T, E, k, S, *inputs, _t(counts, torch.int32, (S, E), "counts"),
+        _t(n_tokens, torch.int32, (S,), "n_tokens"), _t(dloss, torch.float32, (S,), "dloss"),
+        _t(dz_loss, torch.float32, (S,), "dz_loss"), _t(dw, torch.float32, (T, k), "dw"),
+        _t(dlogits, torch.float32, (T, E), "dlogits"), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_balance_loss_backward", rc)
 
 
 def moe_check_status(ws, stream=None) -> int:

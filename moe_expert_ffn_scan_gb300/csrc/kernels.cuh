@@ -126,6 +126,42 @@ cudaError_t launch_combine(const uint16_t* y2, const int32_t* inv, const float* 
                            int H, int has_shared, uint16_t* out, uint32_t* status,
                            cudaStream_t st);
 
+// Residual addition + RMS norm and its gradient (norm.cu).  part: the dgain partials,
+// [min(rows, kNormBwdCtas)][cols] fp32 (not read when dgain is null).
+constexpr int kNormBwdCtas = 608;  // 4 per SM
+cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* res, bool res_f32, const void* gain,
+                               bool gain_f32, float eps, int rows, int cols, void* h, uint16_t* y,
+                               uint8_t* q, uint8_t* s, float* rstd, cudaStream_t st);
+cudaError_t launch_add_rmsnorm_bwd(const uint16_t* dy, const void* h, bool h_f32, const void* gain,
+                                   bool gain_f32, const float* rstd, int rows, int cols,
+                                   const void* dh_in, void* dh, uint16_t* dx, float* dgain,
+                                   float* part, cudaStream_t st);
+
+// Router balance loss and its gradient (balance.cu).  The forward's first kernel runs
+// balance_ctas(T) <= kBalanceCtas CTAs and writes one partial slot per (CTA, sequence)
+// pair that has rows: balance_ctas(T) + S - 1 slots.
+constexpr int kBalanceCtas = 608;
+struct BalanceWs {
+  uint32_t* status;
+  uint32_t* flags;   // [balance_ctas(T)] status bits, by CTA
+  float* p;          // [slots][E] sums of p
+  int32_t* c;        // [slots][E] counts
+  float* z;          // [slots]
+  int32_t* n;        // [slots] counted tokens
+  int32_t* ticket;   // [S] arrivals
+  float* terms;      // [S][ceil(E / 32)] loss terms
+};
+int balance_ctas(int T);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
+                                const uint8_t* mask, int T, int E, int k, int S,
+                                const BalanceWs& w, int32_t* counts, int32_t* n_tokens,
+                                float* prob, float* loss, float* z_loss, cudaStream_t st);
+cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const int32_t* off,
+                               const uint8_t* mask, const int32_t* counts,
+                               const int32_t* n_tokens, const float* dloss, const float* dz,
+                               const float* dw, int T, int E, int k, int S, float* dlogits,
+                               cudaStream_t st);
+
 struct GemmLaunch {
   const uint8_t* w_codes;     // [G][N][K/2]
   const uint8_t* w_scales;    // [G][N][K/32]

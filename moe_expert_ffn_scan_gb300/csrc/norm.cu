@@ -1,0 +1,550 @@
+// Residual addition + RMS norm with bf16 and FP8 outputs, and its gradient.
+//
+//   a = x + r;  rstd = (mean(a^2) + eps)^(-1/2);  y = bf16(a * rstd * gain)
+//   q, s = the activation quantisation rule (moe.h) on the bf16 values of y
+//
+// a is kept in fp32 (the stored h is a rounded to the stream's type; the norm does not
+// see that rounding).  The codes are taken from the bf16 values of y, so that (q, s) is
+// what moe_quant_act gives for the stored y, bit for bit: the router reads y and W13 the
+// codes, and both then see one hidden state.
+//
+// Gradient, with n = h * rstd and u = dy * gain per row:
+//   dh = dh_in + rstd * (u - n * mean(u * n));   dgain = sum over rows of dy * n.
+//
+// Memory-bound for many rows (about one flop a byte), bound by one row's latency for few.
+// A row is read once and stays in registers between the sum and the outputs: kFwdNV (or
+// kBwdNV) 8-value vectors a thread, as many threads as the row needs, up to kMaxThreads; rows
+// too short to occupy more than one warp take a warp each.  Rows wider than the registers
+// of one CTA are read twice (the wide kernels).
+#include "kernels.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxThreads = 512;  // a row's threads: 128 registers each
+constexpr int kFwdNV = 4;         // 8-value vectors (or single values) a thread, forward
+constexpr int kBwdNV = 2;         // and backward, which holds three inputs and the dgain sums
+constexpr int kWarpRows = 8;      // rows (warps) per CTA when a row takes one warp
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<uint16_t> {
+  static __device__ __forceinline__ float get(const uint16_t* p) {
+    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+  }
+  static __device__ __forceinline__ void put(uint16_t* p, float v) {
+    *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  }
+};
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+};
+
+// Plain (not read-only-cache) loads: h may be the residual's buffer and y the input's.
+// The streams are used once, so they do not displace the gain from L1.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&b);
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_vec(const uint16_t* p, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 u = ld_stream(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    f[0] = Elem<uint16_t>::get(p);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_vec(const float* p, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 a = ld_stream(p), b = ld_stream(p + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  } else {
+    f[0] = *p;
+  }
+}
+// The gain: read by every row, through the read-only cache.
+template <int VEC>
+__device__ __forceinline__ void load_gain(const uint16_t* p, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    f[0] = __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_gain(const float* p, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    f[0] = __ldg(p);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(uint16_t* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                              pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  } else {
+    Elem<uint16_t>::put(p, f[0]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *p = f[0];
+  }
+}
+
+// Sum over a row's threads: a warp's, or the CTA's (in warp order: deterministic).
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  if constexpr (!kWarpRow) {
+    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[warp] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < nw; ++w) v += part[w];
+  }
+  return v;
+}
+
+struct NormOut {
+  void* h;
+  uint16_t* y;
+  uint8_t* q;
+  uint8_t* s;
+  float* rstd;
+};
+
+// Outputs of one vector: y, and for VEC = 8 the codes and the scale of its 128-column
+// block, which 16 consecutive lanes share (cols % 128 == 0: all of them are here).
+template <int VEC, typename GT>
+__device__ __forceinline__ void norm_store(const float (&a)[VEC], float rstd, const GT* gain,
+                                           size_t row, int cols, int c, const NormOut& o,
+                                           unsigned active) {
+  float g[VEC], y[VEC];
+  load_gain<VEC>(gain + c, g);
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    y[j] = __bfloat162float(__float2bfloat16_rn(a[j] * rstd * g[j]));
+  if (o.y) store_vec<VEC>(o.y + row * cols + c, y);
+  if constexpr (VEC == 8) {
+    if (o.q) {
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(active, amax, off));
+      const int e = fp8_scale_exponent(amax);
+      const float sc = pow2_neg(e);
+      const uint32_t lo = e4m3x2(y[0] * sc, y[1] * sc) |
+                          (static_cast<uint32_t>(e4m3x2(y[2] * sc, y[3] * sc)) << 16);
+      const uint32_t hi = e4m3x2(y[4] * sc, y[5] * sc) |
+                          (static_cast<uint32_t>(e4m3x2(y[6] * sc, y[7] * sc)) << 16);
+      *reinterpret_cast<uint2*>(o.q + row * cols + c) = make_uint2(lo, hi);
+      if ((c & 127) == 0)
+        o.s[row * (cols >> 7) + (c >> 7)] = static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+template <typename RT, typename GT, int VEC, bool kWarpRow>
+__global__ void __launch_bounds__(kMaxThreads)
+    k_add_rmsnorm(const uint16_t* x, const RT* res, const GT* gain, float eps, int rows, int cols,
+                  NormOut o) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float part[kMaxThreads / 32];
+  const size_t row = static_cast<size_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (row >= static_cast<size_t>(rows)) return;
+  const int stride = blockDim.x * VEC;
+  const int c0 = threadIdx.x * VEC;
+  float a[kFwdNV][VEC];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kFwdNV; ++i) {
+    const int c = c0 + i * stride;
+    if (c < cols) load_vec<VEC>(x + row * cols + c, a[i]);
+  }
+  if (res) {
+#pragma unroll
+    for (int i = 0; i < kFwdNV; ++i) {
+      const int c = c0 + i * stride;
+      float r[VEC];
+      if (c < cols) {
+        load_vec<VEC>(res + row * cols + c, r);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[i][j] += r[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFwdNV; ++i)
+    if (c0 + i * stride < cols) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum = fmaf(a[i][j], a[i][j], sum);
+    }
+  sum = row_sum<kWarpRow>(sum, part);
+  const float rstd = rsqrtf(sum / static_cast<float>(cols) + eps);
+  if (threadIdx.x == 0 && o.rstd) o.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < kFwdNV; ++i) {
+    const int c = c0 + i * stride;
+    const unsigned active = __ballot_sync(0xFFFFFFFFu, c < cols);
+    if (c < cols) {
+      if (o.h) store_vec<VEC>(static_cast<RT*>(o.h) + row * cols + c, a[i]);
+      norm_store<VEC, GT>(a[i], rstd, gain, row, cols, c, o, active);
+    }
+  }
+}
+
+// Rows of more than kMaxThreads * kFwdNV * VEC columns: read twice (the second time from
+// L2), one CTA a row.
+template <typename RT, typename GT, int VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    k_add_rmsnorm_wide(const uint16_t* x, const RT* res, const GT* gain, float eps, int cols,
+                       NormOut o) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float part[kMaxThreads / 32];
+  const size_t row = blockIdx.x;
+  const long long stride = static_cast<long long>(blockDim.x) * VEC;
+  const long long c0 = static_cast<long long>(threadIdx.x) * VEC;
+  auto load = [&](long long c, float (&a)[VEC]) {
+    load_vec<VEC>(x + row * cols + c, a);
+    if (res) {
+      float r[VEC];
+      load_vec<VEC>(res + row * cols + c, r);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) a[j] += r[j];
+    }
+  };
+  float sum = 0.f;
+  for (long long c = c0; c < cols; c += stride) {
+    float a[VEC];
+    load(c, a);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sum = fmaf(a[j], a[j], sum);
+  }
+  sum = row_sum<false>(sum, part);
+  const float rstd = rsqrtf(sum / static_cast<float>(cols) + eps);
+  if (threadIdx.x == 0 && o.rstd) o.rstd[row] = rstd;
+  for (long long b = 0; b < cols; b += stride) {
+    const long long c = b + c0;
+    const unsigned active = __ballot_sync(0xFFFFFFFFu, c < cols);
+    if (c < cols) {
+      float a[VEC];
+      load(c, a);
+      if (o.h) store_vec<VEC>(static_cast<RT*>(o.h) + row * cols + c, a);
+      norm_store<VEC, GT>(a, rstd, gain, row, cols, static_cast<int>(c), o, active);
+    }
+  }
+}
+
+struct NormBwd {
+  const uint16_t* dy;
+  const void* h;
+  const void* gain;
+  const float* rstd;
+  const void* dh_in;
+  void* dh;
+  uint16_t* dx;
+  float* part;  // [CTAs][cols] sums of dy * n, or null
+};
+
+// Each CTA walks rows blockIdx.x * blockDim.y + threadIdx.y, + grid, ...; a thread keeps
+// the dgain sums of its columns over all of them and the CTA writes one partial row, which
+// k_dgain_sum adds up in CTA order (no atomics: run-to-run identical).
+template <typename RT, typename GT, int VEC, bool kWarpRow>
+__global__ void __launch_bounds__(kMaxThreads)
+    k_add_rmsnorm_bwd(const NormBwd p, int rows, int cols) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ float dyn[];  // kWarpRow: [kWarpRows][cols] dgain sums
+  __shared__ float part[2][kMaxThreads / 32];
+  const int stride = blockDim.x * VEC;
+  const int c0 = threadIdx.x * VEC;
+  const RT* h = static_cast<const RT*>(p.h);
+  const RT* dhi = static_cast<const RT*>(p.dh_in);
+  const GT* gain = static_cast<const GT*>(p.gain);
+  float dg[kBwdNV][VEC], g[kBwdNV][VEC];
+#pragma unroll
+  for (int i = 0; i < kBwdNV; ++i) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) dg[i][j] = 0.f;
+    if (c0 + i * stride < cols) load_gain<VEC>(gain + c0 + i * stride, g[i]);
+  }
+  int flip = 0;
+  for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < rows;
+       row += static_cast<long long>(gridDim.x) * blockDim.y, flip ^= 1) {
+    float u[kBwdNV][VEC], n[kBwdNV][VEC], add[kBwdNV][VEC];
+    const size_t base = static_cast<size_t>(row) * cols;
+    const float rs = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < kBwdNV; ++i) {
+      const int c = c0 + i * stride;
+      if (c < cols) {
+        load_vec<VEC>(p.dy + base + c, u[i]);
+        load_vec<VEC>(h + base + c, n[i]);
+        if (dhi) load_vec<VEC>(dhi + base + c, add[i]);
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBwdNV; ++i)
+      if (c0 + i * stride < cols) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          n[i][j] *= rs;
+          dg[i][j] = fmaf(u[i][j], n[i][j], dg[i][j]);
+          u[i][j] *= g[i][j];
+          dot = fmaf(u[i][j], n[i][j], dot);
+        }
+      }
+    // two buffers: a row's partials are read while the next row's are written
+    dot = row_sum<kWarpRow>(dot, part[flip]) / static_cast<float>(cols);
+#pragma unroll
+    for (int i = 0; i < kBwdNV; ++i) {
+      const int c = c0 + i * stride;
+      if (c < cols) {
+        float d[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          // (fmaf spelled out: the same bits whichever outputs are asked for)
+          const float t = fmaf(-n[i][j], dot, u[i][j]);
+          d[j] = dhi ? fmaf(rs, t, add[i][j]) : rs * t;
+        }
+        if (p.dh) store_vec<VEC>(static_cast<RT*>(p.dh) + base + c, d);
+        if (p.dx) store_vec<VEC>(p.dx + base + c, d);
+      }
+    }
+  }
+  if (!p.part) return;
+  float* out = p.part + static_cast<size_t>(blockIdx.x) * cols;
+  if constexpr (kWarpRow) {
+#pragma unroll
+    for (int i = 0; i < kBwdNV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c0 + i * stride < cols) dyn[threadIdx.y * cols + c0 + i * stride + j] = dg[i][j];
+    __syncthreads();
+    for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += kWarpRows * 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarpRows; ++w) v += dyn[w * cols + c];
+      out[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBwdNV; ++i)
+      if (c0 + i * stride < cols) store_vec<VEC>(out + c0 + i * stride, dg[i]);
+  }
+}
+
+// Wide rows: dh with two reads of the row, one CTA a row ...
+template <typename RT, typename GT>
+__global__ void __launch_bounds__(kMaxThreads)
+    k_add_rmsnorm_bwd_wide(const NormBwd p, int cols) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float part[kMaxThreads / 32];
+  const size_t base = static_cast<size_t>(blockIdx.x) * cols;
+  const RT* h = static_cast<const RT*>(p.h);
+  const RT* dhi = static_cast<const RT*>(p.dh_in);
+  const GT* gain = static_cast<const GT*>(p.gain);
+  const float rs = p.rstd[blockIdx.x];
+  float dot = 0.f;
+  for (int c = threadIdx.x; c < cols; c += blockDim.x)
+    dot = fmaf(Elem<uint16_t>::get(p.dy + base + c) * Elem<GT>::get(gain + c),
+               Elem<RT>::get(h + base + c) * rs, dot);
+  dot = row_sum<false>(dot, part) / static_cast<float>(cols);
+  for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+    const float u = Elem<uint16_t>::get(p.dy + base + c) * Elem<GT>::get(gain + c);
+    const float n = Elem<RT>::get(h + base + c) * rs;
+    const float t = fmaf(-n, dot, u);
+    const float d = dhi ? fmaf(rs, t, Elem<RT>::get(dhi + base + c)) : rs * t;
+    if (p.dh) Elem<RT>::put(static_cast<RT*>(p.dh) + base + c, d);
+    if (p.dx) Elem<uint16_t>::put(p.dx + base + c, d);
+  }
+}
+
+// ... and the dgain partials of row block blockIdx.y, one column a thread.  Runs before the
+// kernel above, whose dh may overwrite h or dh_in.
+template <typename RT>
+__global__ void __launch_bounds__(256)
+    k_dgain_wide(const NormBwd p, int rows, int cols, int per) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
+  const RT* h = static_cast<const RT*>(p.h);
+  const long long r0 = static_cast<long long>(blockIdx.y) * per;
+  const long long r1 = r0 + per < rows ? r0 + per : rows;
+  float v = 0.f;
+#pragma unroll 4
+  for (long long r = r0; r < r1; ++r) {
+    const size_t at = static_cast<size_t>(r) * cols + c;
+    v = fmaf(Elem<uint16_t>::get(p.dy + at), Elem<RT>::get(h + at) * p.rstd[r], v);
+  }
+  p.part[static_cast<size_t>(blockIdx.y) * cols + c] = v;
+}
+
+// dgain[c] = sum of nparts partial rows: 32 columns a CTA, its 32 warps take every 32nd
+// partial each, then the warps' sums are added in warp order.
+__global__ void __launch_bounds__(1024)
+    k_dgain_sum(const float* part, int nparts, int cols, float* dgain) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < cols) {
+#pragma unroll 4
+    for (int r = warp; r < nparts; r += 32) v += part[static_cast<size_t>(r) * cols + c];
+  }
+  red[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) v += red[w][lane];
+    dgain[c] = v;
+  }
+}
+
+// Threads a row takes with nv vectors each: whole warps.
+int row_threads(int cols, int vec, int nv) {
+  const int vecs = cols / vec;
+  const int t = (vecs + nv - 1) / nv;
+  return (t + 31) / 32 * 32;
+}
+
+template <typename RT, typename GT>
+cudaError_t fwd_types(const uint16_t* x, const void* res, const void* gain, float eps, int rows,
+                      int cols, const NormOut& o, cudaStream_t st) {
+  const RT* r = static_cast<const RT*>(res);
+  const GT* g = static_cast<const GT*>(gain);
+  const bool vec = cols % 8 == 0;
+  const long long regs = static_cast<long long>(kMaxThreads) * kFwdNV * (vec ? 8 : 1);
+  if (cols > regs) {
+    return vec ? launch_k(k_add_rmsnorm_wide<RT, GT, 8>, rows, kMaxThreads, 0, st, x, r, g, eps,
+                          cols, o)
+               : launch_k(k_add_rmsnorm_wide<RT, GT, 1>, rows, kMaxThreads, 0, st, x, r, g, eps,
+                          cols, o);
+  }
+  const int t = row_threads(cols, vec ? 8 : 1, kFwdNV);
+  if (t == 32) {
+    const unsigned grid = (static_cast<unsigned>(rows) + kWarpRows - 1) / kWarpRows;
+    const dim3 block(32, kWarpRows);
+    return vec ? launch_k(k_add_rmsnorm<RT, GT, 8, true>, grid, block, 0, st, x, r, g, eps, rows,
+                          cols, o)
+               : launch_k(k_add_rmsnorm<RT, GT, 1, true>, grid, block, 0, st, x, r, g, eps, rows,
+                          cols, o);
+  }
+  return vec ? launch_k(k_add_rmsnorm<RT, GT, 8, false>, rows, t, 0, st, x, r, g, eps, rows, cols,
+                        o)
+             : launch_k(k_add_rmsnorm<RT, GT, 1, false>, rows, t, 0, st, x, r, g, eps, rows, cols,
+                        o);
+}
+
+template <typename RT, typename GT>
+cudaError_t bwd_types(const NormBwd& p, int rows, int cols, float* dgain, cudaStream_t st) {
+  const bool vec = cols % 8 == 0;
+  const long long regs = static_cast<long long>(kMaxThreads) * kBwdNV * (vec ? 8 : 1);
+  int parts = 0;
+  cudaError_t e = cudaSuccess;
+  if (rows == 0) {
+  } else if (cols > regs) {
+    const int per = (rows + kNormBwdCtas - 1) / kNormBwdCtas;
+    parts = (rows + per - 1) / per;
+    if (p.part) {
+      const dim3 grid((cols + 255) / 256, parts);
+      e = launch_k(k_dgain_wide<RT>, grid, 256, 0, st, p, rows, cols, per);
+      if (e != cudaSuccess) return e;
+    }
+    e = launch_k(k_add_rmsnorm_bwd_wide<RT, GT>, rows, kMaxThreads, 0, st, p, cols);
+  } else {
+    const int t = row_threads(cols, vec ? 8 : 1, kBwdNV);
+    const int per_cta = t == 32 ? kWarpRows : 1;
+    // about 1024 threads an SM (the registers' limit), within the partials' rows
+    const int want = kNormBwdCtas / 4 * (t == 32 ? 4 : t <= 256 ? 4 : 2);
+    const int need = (rows + per_cta - 1) / per_cta;
+    parts = need < want ? need : want;
+    const size_t smem = t == 32 ? sizeof(float) * kWarpRows * cols : 0;
+    const dim3 block(t, per_cta);
+    if (t == 32)
+      e = vec ? launch_k(k_add_rmsnorm_bwd<RT, GT, 8, true>, parts, block, smem, st, p, rows, cols)
+              : launch_k(k_add_rmsnorm_bwd<RT, GT, 1, true>, parts, block, smem, st, p, rows, cols);
+    else
+      e = vec ? launch_k(k_add_rmsnorm_bwd<RT, GT, 8, false>, parts, block, 0, st, p, rows, cols)
+              : launch_k(k_add_rmsnorm_bwd<RT, GT, 1, false>, parts, block, 0, st, p, rows, cols);
+  }
+  if (e != cudaSuccess || !dgain) return e;
+  return launch_k(k_dgain_sum, (cols + 31) / 32, 1024, 0, st, p.part, parts, cols, dgain);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* res, bool res_f32, const void* gain,
+                               bool gain_f32, float eps, int rows, int cols, void* h, uint16_t* y,
+                               uint8_t* q, uint8_t* s, float* rstd, cudaStream_t st) {
+  const NormOut o = {h, y, q, s, rstd};
+  if (res_f32)
+    return gain_f32 ? fwd_types<float, float>(x, res, gain, eps, rows, cols, o, st)
+                    : fwd_types<float, uint16_t>(x, res, gain, eps, rows, cols, o, st);
+  return gain_f32 ? fwd_types<uint16_t, float>(x, res, gain, eps, rows, cols, o, st)
+                  : fwd_types<uint16_t, uint16_t>(x, res, gain, eps, rows, cols, o, st);
+}
+
+cudaError_t launch_add_rmsnorm_bwd(const uint16_t* dy, const void* h, bool h_f32, const void* gain,
+                                   bool gain_f32, const float* rstd, int rows, int cols,
+                                   const void* dh_in, void* dh, uint16_t* dx, float* dgain,
+                                   float* part, cudaStream_t st) {
+  const NormBwd p = {dy, h, gain, rstd, dh_in, dh, dx, dgain ? part : nullptr};
+  if (h_f32)
+    return gain_f32 ? bwd_types<float, float>(p, rows, cols, dgain, st)
+                    : bwd_types<float, uint16_t>(p, rows, cols, dgain, st);
+  return gain_f32 ? bwd_types<uint16_t, float>(p, rows, cols, dgain, st)
+                  : bwd_types<uint16_t, uint16_t>(p, rows, cols, dgain, st);
+}
+
+}  // namespace moe

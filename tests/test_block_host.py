@@ -1,0 +1,114 @@
+"""Refusals of the operators around the expert FFN, before anything is launched (no GPU)."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import moe_expert_ffn_scan_gb300 as moe
+
+P = ctypes.c_void_p
+OK, ARG, SHAPE, SMALL = 0, 1, 2, 3
+A = P(0x10000)          # an aligned address that is never read
+BAD = P(0x10000 + 8)    # not 16-byte aligned
+ODD = P(0x10000 + 2)    # not 4-byte aligned
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        from moe_expert_ffn_scan_gb300 import build
+        build.build()
+    return moe.lib()
+
+
+def _with(args, i, v):
+    return [*args[:i], v, *args[i + 1:]]
+
+
+def test_add_rmsnorm_refusals(lib):
+    f = lib.moe_add_rmsnorm
+    #       rows cols x  res dt gain dt eps   h  y  q  s  rstd stream
+    good = [4, 256, A, A, 0, A, 0, 1e-6, A, A, A, A, A, None]
+    assert f(*_with(good, 0, 0)) == OK          # no rows: nothing to launch
+    assert f(*_with(good, 0, -1)) == SHAPE
+    assert f(*_with(good, 1, 0)) == SHAPE
+    assert f(*_with(good, 1, 200)) == SHAPE     # codes want whole 128-column blocks
+    for i in (2, 5):
+        assert f(*_with(good, i, None)) == ARG
+    for i in (2, 3, 5, 8, 9, 10):
+        assert f(*_with(good, i, BAD)) == ARG
+    assert f(*_with(good, 12, ODD)) == ARG
+    for i in (4, 6):
+        assert f(*_with(good, i, 2)) == ARG
+    assert f(*_with(good, 7, -1.0)) == ARG and f(*_with(good, 7, float("nan"))) == ARG
+    assert f(*_with(good, 11, None)) == ARG     # codes without scales
+    assert f(*_with(good, 10, None)) == ARG     # scales without codes
+    none = [4, 256, A, A, 0, A, 0, 1e-6, None, None, None, None, A, None]
+    assert f(*none) == ARG                      # no output
+
+
+def test_add_rmsnorm_backward_refusals(lib):
+    f, size = lib.moe_add_rmsnorm_backward, lib.moe_add_rmsnorm_backward_workspace_size
+    assert size(4, 256) == 4 * 256 * 4 and size(10 ** 6, 256) < 2 ** 20
+    assert size(-1, 256) == 0 and size(4, 0) == 0
+    #       rows cols dy h dt gain dt rstd dh_in dh dx dgain ws bytes stream
+    good = [4, 256, A, A, 0, A, 0, A, A, A, A, A, A, 1 << 20, None]
+    assert f(*_with(good, 0, -1)) == SHAPE and f(*_with(good, 1, 0)) == SHAPE
+    for i in (2, 3, 5, 7, 12):
+        assert f(*_with(good, i, None)) == ARG
+    for i in (2, 3, 5, 8, 9, 10, 12):
+        assert f(*_with(good, i, BAD)) == ARG
+    for i in (7, 11):
+        assert f(*_with(good, i, ODD)) == ARG
+    for i in (4, 6):
+        assert f(*_with(good, i, -1)) == ARG
+    assert f(*_with(good, 13, 16)) == SMALL
+    none = _with(_with(_with(good, 9, None), 10, None), 11, None)
+    assert f(*none) == ARG
+
+
+def test_balance_loss_refusals(lib):
+    f, size = lib.moe_balance_loss, lib.moe_balance_loss_workspace_size
+    assert size(64, 8, 2, 1) > 0 and size(0, 8, 2, 1) > 0
+    for bad in ((64, 0, 1, 1), (64, 1025, 2, 1), (64, 8, 9, 1), (64, 64, 17, 1), (64, 8, 0, 1),
+                (-1, 8, 2, 1), (64, 8, 2, 0), (64, 8, 2, 65536), (1 << 28, 16, 8, 1)):
+        assert size(*bad) == 0
+        assert f(*bad, *[A] * 10, 1 << 40, None) == SHAPE
+        assert lib.moe_balance_loss_backward(*bad, *[A] * 10, None) == SHAPE
+    #       T   E  k  S  lg idx off mask counts n prob loss z ws bytes stream
+    good = [64, 8, 2, 2, A, A, A, A, A, A, A, A, A, A, 1 << 40, None]
+    for i in (4, 5, 6, 8, 9, 10, 11, 13):
+        assert f(*_with(good, i, None)) == ARG
+    for i in (4, 13):
+        assert f(*_with(good, i, BAD)) == ARG
+    for i in (5, 6, 8, 9, 10, 11, 12):
+        assert f(*_with(good, i, ODD)) == ARG
+    assert f(*_with(good, 14, 64)) == SMALL
+
+
+def test_balance_loss_backward_refusals(lib):
+    f = lib.moe_balance_loss_backward
+    #       T   E  k  S  lg idx off mask counts n dloss dz dw dlogits stream
+    good = [64, 8, 2, 2, A, A, A, A, A, A, A, A, A, A, None]
+    assert f(*_with(good, 0, 0)) == OK
+    for i in (4, 5, 6, 8, 9, 13):
+        assert f(*_with(good, i, None)) == ARG
+    for i in (4, 13):
+        assert f(*_with(good, i, BAD)) == ARG
+    for i in (5, 6, 8, 9, 10, 11, 12):
+        assert f(*_with(good, i, ODD)) == ARG
+
+
+def test_binding_refuses_host_tensors_types_and_shapes():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    w = torch.ones(256)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.moe_add_rmsnorm(x, None, w, 1e-6, y=x)
+    with pytest.raises(ValueError, match="x: expected"):
+        moe.moe_add_rmsnorm(x.float(), None, w, 1e-6, y=x)
+    with pytest.raises(ValueError, match="expected bfloat16 or float32"):
+        moe.moe_add_rmsnorm(x, x.half(), w, 1e-6, y=x)
+    with pytest.raises(ValueError, match="logits: expected"):
+        moe.moe_balance_loss_backward(x, torch.zeros(4, 2, dtype=torch.int32), None, None, None)
