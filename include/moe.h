@@ -461,6 +461,43 @@ int moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t S, const 
                               const int32_t* n_tokens, const float* dloss, const float* dz_loss,
                               const float* dw, float* dlogits, void* stream);
 
+/* Dense projection with its epilogue, on the tensor cores:
+ *     z = x W^T + bias,   y = act(z) + residual.
+ *   x [M][K] and w [N][K] bf16; bias [N] of bias_dtype or NULL; residual [M][N] of y_dtype
+ *   or NULL; y [M][N] of y_dtype; z [M][N] bf16 or NULL (what the gradient of an activation
+ *   needs).  fp32 products and sums, one rounding to y's (and z's) type.  Row strides ld* in
+ *   elements, 0 = contiguous; y may be residual's buffer (the same stride).
+ *   act: MOE_ACT_*; silu(z) = z / (1 + e^-z), gelu(z) = z/2 (1 + erf(z / sqrt(2))).
+ *   Any M >= 0 (0: no-op), 1 <= N, K <= 2^22.  x and w whose row stride is not a multiple of
+ *   8 elements are first copied to padded rows in the workspace (the strides decide; a
+ *   weight kept with a padded stride saves that copy in every call).
+ *   ws: moe_linear_workspace_size bytes, 256-byte aligned.  Its first 4 bytes are a status
+ *   word that these two calls only set bits of: zero it once, before the first use;
+ *   moe_check_status reads it. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
+typedef struct moe_linear_desc {
+  int32_t M, N, K;
+  int32_t act;                       /* MOE_ACT_*                                       */
+  int32_t bias_dtype, y_dtype;       /* MOE_DTYPE_*                                     */
+  int64_t ldx, ldw, ldr, ldy, ldz;   /* row strides of x, w, residual, y (or dy), z     */
+} moe_linear_desc;
+size_t moe_linear_workspace_size(const moe_linear_desc* d);
+int moe_linear(const moe_linear_desc* d, const uint16_t* x, const uint16_t* w, const void* bias,
+               const void* residual, void* y, uint16_t* z, void* ws, size_t ws_bytes,
+               void* stream);
+
+/* Its gradient, from dy [M][N] bf16 (the residual's gradient is dy itself):
+ *     dz = dy * act'(z);   dx = dz W,   dw = dz^T x,   dbias = sum over rows of dz.
+ *   x, w, z as in the forward (z: with an activation; x only for dw, w only for dx).
+ *   Outputs, at least one: dx [M][K], dw [N][K] bf16 contiguous, dbias [N] fp32 (sums of
+ *   unrounded fp32 dz in a fixed order).  The products take dz rounded to bf16, as the
+ *   tensor cores do; their sums are fp32.  M = 0: dw and dbias are zero.  bias_dtype and
+ *   y_dtype are not used.  ws: moe_linear_backward_workspace_size bytes, as above. */
+size_t moe_linear_backward_workspace_size(const moe_linear_desc* d);
+int moe_linear_backward(const moe_linear_desc* d, const uint16_t* x, const uint16_t* w,
+                        const uint16_t* z, const uint16_t* dy, uint16_t* dx, uint16_t* dw,
+                        float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 /* Debug helper (synchronises `stream`): reads the device status word at the start of
  * a workspace used by the calls above.  Returns MOE_OK if no bit is set, else
  * MOE_ERR_DEVICE_CHECK and the bits in *bits_out (if not NULL).  The word is

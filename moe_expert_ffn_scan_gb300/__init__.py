@@ -49,6 +49,14 @@ class moe_weights_nvfp4(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w13", "w13_s", "w13_gs", "w2", "w2_s", "w2_gs")]
 
 
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("M", "N", "K", "act", "bias_dtype", "y_dtype")] +
+                [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldr", "ldy", "ldz")])
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # MOE_ACT_*
+
+
 DEBUG_FIELDS = ("idx", "w", "counts", "offsets", "perm_src", "inv", "xq", "xs", "y13", "hq",
                 "hs", "y2")
 
@@ -134,10 +142,16 @@ def lib():
         L.moe_balance_loss_workspace_size.argtypes = [_I] * 4
         L.moe_balance_loss.argtypes = [_I] * 4 + [_P] * 10 + [_SZ, _P]
         L.moe_balance_loss_backward.argtypes = [_I] * 4 + [_P] * 11
-        for fn in ("moe_add_rmsnorm_backward_workspace_size", "moe_balance_loss_workspace_size"):
+        _LD = ctypes.POINTER(moe_linear_desc)
+        L.moe_linear_workspace_size.argtypes = [_LD]
+        L.moe_linear.argtypes = [_LD] + [_P] * 7 + [_SZ, _P]
+        L.moe_linear_backward_workspace_size.argtypes = [_LD]
+        L.moe_linear_backward.argtypes = [_LD] + [_P] * 8 + [_SZ, _P]
+        for fn in ("moe_add_rmsnorm_backward_workspace_size", "moe_balance_loss_workspace_size",
+                   "moe_linear_workspace_size", "moe_linear_backward_workspace_size"):
             getattr(L, fn).restype = _SZ
         for fn in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_balance_loss",
-                   "moe_balance_loss_backward"):
+                   "moe_balance_loss_backward", "moe_linear", "moe_linear_backward"):
             getattr(L, fn).restype = ctypes.c_int
         for fn in ("moe_route", "moe_quant_act", "moe_grouped_gemm_w13", "moe_swiglu_quant",
                    "moe_grouped_gemm_w2", "moe_combine", "moe_forward", "moe_forward_timed",
@@ -237,8 +251,11 @@ def gemm_workspace_size(d) -> int:
 
 
 def alloc_workspace(nbytes, device="cuda"):
-    """A workspace tensor (torch allocations are 256-byte aligned or better)."""
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    """A workspace tensor (torch allocations are 256-byte aligned or better), its status
+    word zeroed."""
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def moe_route(d, logits, idx, w, counts, offsets, perm_src, inv, ws, stream=None):
@@ -518,6 +535,80 @@ def moe_balance_loss_backward(logits, idx, counts, n_tokens, dlogits, dloss=None
         _t(dlogits, torch.float32, (T, E), "dlogits"), _raw_stream(stream))
     if rc:
         raise MoeError("moe_balance_loss_backward", rc)
+
+
+def _linear_desc(M, N, K, act="none", ldx=0, ldw=0, ldr=0, ldy=0, ldz=0):
+    return moe_linear_desc(M, N, K, ACTS[act], 0, 0, ldx, ldw, ldr, ldy, ldz)
+
+
+def linear_workspace_size(M, N, K, ldx=0, ldw=0) -> int:
+    """ldx, ldw: row strides of x and w in elements (0: contiguous)."""
+    return lib().moe_linear_workspace_size(ctypes.byref(_linear_desc(M, N, K, ldx=ldx, ldw=ldw)))
+
+
+def linear_backward_workspace_size(M, N, K, ldx=0, ldw=0, lddy=0, act="silu") -> int:
+    """The default act gives the size that does for all of them."""
+    return lib().moe_linear_backward_workspace_size(
+        ctypes.byref(_linear_desc(M, N, K, act, ldx, ldw, ldy=lddy)))
+
+
+def _m(t, dtype, shape, name):
+    """Pointer and row stride of a matrix whose columns are contiguous (None: null)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    rows, cols = shape
+    ld, step = t.stride()
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return t.data_ptr(), ld if rows > 1 else 0
+
+
+def moe_linear(x, w, y, ws, bias=None, residual=None, z=None, act="none", stream=None):
+    """y [M, N] = act(x [M, K] . w [N, K]^T + bias [N]) + residual [M, N].  x, w bf16; y and
+    residual bf16 or fp32; bias bf16 or fp32; z [M, N] bf16 takes the value in front of the
+    activation.  Matrices may have any row stride.  act: one of ACTS.  ws:
+    linear_workspace_size(M, N, K[, ldx, ldw]) bytes."""
+    (M, K), N = x.shape, w.shape[0]
+    yd, out = y.dtype, (M, N)
+    xp, ldx = _m(x, torch.bfloat16, (M, K), "x")
+    wp, ldw = _m(w, torch.bfloat16, (N, K), "w")
+    rp, ldr = _m(residual, yd, out, "residual")
+    yp, ldy = _m(y, yd, out, "y")
+    zp, ldz = _m(z, torch.bfloat16, out, "z")
+    bp, bd = None, 0
+    if bias is not None:
+        bd = _dtype_code(bias, "bias")
+        bp = _t(bias, bias.dtype, (N,), "bias")
+    d = moe_linear_desc(M, N, K, ACTS[act], bd, _dtype_code(y, "y"), ldx, ldw, ldr, ldy, ldz)
+    rc = lib().moe_linear(ctypes.byref(d), xp, wp, bp, rp, yp, zp, _p(ws), ws.numel(),
+                          _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_linear", rc)
+
+
+def moe_linear_backward(x, w, dy, ws, z=None, act="none", dx=None, dw=None, dbias=None,
+                        stream=None):
+    """Gradient of moe_linear from dy [M, N] bf16 and, with an activation, its z.  Writes
+    what is given of dx [M, K], dw [N, K] bf16 and dbias [N] fp32 (contiguous).  ws:
+    linear_backward_workspace_size(M, N, K[, ldx, ldw, lddy]) bytes."""
+    (M, K), N = x.shape, w.shape[0]
+    out = (M, N)
+    xp, ldx = _m(x, torch.bfloat16, (M, K), "x")
+    wp, ldw = _m(w, torch.bfloat16, (N, K), "w")
+    gp, ldg = _m(dy, torch.bfloat16, out, "dy")
+    zp, ldz = _m(z, torch.bfloat16, out, "z")
+    d = moe_linear_desc(M, N, K, ACTS[act], 0, 0, ldx, ldw, 0, ldg, ldz)
+    rc = lib().moe_linear_backward(
+        ctypes.byref(d), xp, wp, zp, gp, _t(dx, torch.bfloat16, (M, K), "dx"),
+        _t(dw, torch.bfloat16, (N, K), "dw"), _t(dbias, torch.float32, (N,), "dbias"), _p(ws),
+        ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_linear_backward", rc)
 
 
 def moe_check_status(ws, stream=None) -> int:

@@ -53,9 +53,130 @@ BalanceWs carve_balance(Carver& c, int T, int E, int S) {
   return w;
 }
 
+// Row strides with their defaults (0: contiguous).  One row: any stride does.
+struct LinearLd {
+  long long x, w, r, y, z;
+};
+LinearLd linear_ld(const moe_linear_desc* d) {
+  LinearLd l = {d->ldx ? d->ldx : d->K, d->ldw ? d->ldw : d->K, d->ldr ? d->ldr : d->N,
+                d->ldy ? d->ldy : d->N, d->ldz ? d->ldz : d->N};
+  if (d->M == 1) {
+    l.x = linear_padded(d->K);
+    l.r = l.y = l.z = linear_padded(d->N);
+  }
+  if (d->N == 1) l.w = linear_padded(d->K);
+  return l;
+}
+
+bool linear_ok(const moe_linear_desc* d) {
+  if (!d || d->M < 0 || d->N < 1 || d->K < 1) return false;
+  const long long most = 1LL << 36;  // elements: TMA strides and tile counts stay in range
+  if (d->M > kMaxTokens || d->N > (1 << 22) || d->K > (1 << 22)) return false;
+  if (static_cast<long long>(d->M) * d->N > most || static_cast<long long>(d->M) * d->K > most)
+    return false;
+  const LinearLd l = linear_ld(d);
+  return l.x >= d->K && l.w >= d->K && l.r >= d->N && l.y >= d->N && l.z >= d->N &&
+         l.x < most && l.w < most && l.r < most && l.y < most && l.z < most;
+}
+
+struct LinearWs {
+  uint32_t* status;
+  uint16_t *x_pad, *w_pad, *dz;
+  float* part;
+};
+
+LinearWs carve_linear(Carver& c, const moe_linear_desc* d, bool backward) {
+  LinearWs w = {};
+  const LinearLd l = linear_ld(d);
+  w.status = c.take<uint32_t>(64);
+  if (l.x % 8) w.x_pad = c.take<uint16_t>(static_cast<size_t>(d->M) * linear_padded(d->K));
+  if (l.w % 8) w.w_pad = c.take<uint16_t>(static_cast<size_t>(d->N) * linear_padded(d->K));
+  if (backward) {
+    if (d->act != MOE_ACT_NONE || l.y % 8)
+      w.dz = c.take<uint16_t>(static_cast<size_t>(d->M) * linear_padded(d->N));
+    w.part = c.take<float>(static_cast<size_t>(kLinearDbParts) * d->N);
+  }
+  return w;
+}
+
+bool linear_args_ok(const moe_linear_desc* d) {
+  return d->act >= MOE_ACT_NONE && d->act <= MOE_ACT_GELU && dtype_ok(d->y_dtype) &&
+         dtype_ok(d->bias_dtype);
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t moe_linear_workspace_size(const moe_linear_desc* d) {
+  if (!linear_ok(d)) return 0;
+  Carver c(nullptr);
+  carve_linear(c, d, false);
+  return c.used;
+}
+
+int moe_linear(const moe_linear_desc* d, const uint16_t* x, const uint16_t* w, const void* bias,
+               const void* residual, void* y, uint16_t* z, void* ws, size_t ws_bytes,
+               void* stream) {
+  if (!linear_ok(d)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!linear_args_ok(d)) return MOE_ERR_INVALID_ARG;
+  if (d->M == 0) return MOE_OK;
+  if (!x || !w || !y || !ws || !aligned(x, 16) || !aligned(w, 16) || !null_or(bias, 4) ||
+      !null_or(residual, 16) || !aligned(y, 16) || !null_or(z, 16) || !aligned(ws, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  Carver c(ws);
+  const LinearWs s = carve_linear(c, d, false);
+  if (ws_bytes < c.used) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const LinearLd l = linear_ld(d);
+  LinearCall a = {};
+  a.M = d->M, a.N = d->N, a.K = d->K, a.act = d->act;
+  a.x = x, a.w = w, a.bias = bias, a.res = residual, a.y = y, a.z = z;
+  a.ldx = l.x, a.ldw = l.w, a.ldr = l.r, a.ldy = l.y, a.ldz = l.z;
+  a.bias_f32 = d->bias_dtype == MOE_DTYPE_F32;
+  a.y_f32 = d->y_dtype == MOE_DTYPE_F32;
+  a.x_pad = s.x_pad, a.w_pad = s.w_pad, a.status = s.status;
+  return cuda_rc(launch_linear(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_linear_backward_workspace_size(const moe_linear_desc* d) {
+  if (!linear_ok(d)) return 0;
+  Carver c(nullptr);
+  carve_linear(c, d, true);
+  return c.used;
+}
+
+int moe_linear_backward(const moe_linear_desc* d, const uint16_t* x, const uint16_t* w,
+                        const uint16_t* z, const uint16_t* dy, uint16_t* dx, uint16_t* dw,
+                        float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  if (!linear_ok(d)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!linear_args_ok(d) || (!dx && !dw && !dbias)) return MOE_ERR_INVALID_ARG;
+  if (d->M > 0 && (!dy || (dx && !w) || (dw && !x) || (d->act != MOE_ACT_NONE && !z)))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, kAlign) || !null_or(x, 16) || !null_or(w, 16) || !null_or(z, 16) ||
+      !null_or(dy, 16) || !null_or(dx, 16) || !null_or(dw, 16) || !null_or(dbias, 4))
+    return MOE_ERR_INVALID_ARG;
+  Carver c(ws);
+  const LinearWs s = carve_linear(c, d, true);
+  if (ws_bytes < c.used) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->M == 0) {  // sums over no rows
+    if (dw && cudaMemsetAsync(dw, 0, static_cast<size_t>(d->N) * d->K * 2, st) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(d->N) * 4, st) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const LinearLd l = linear_ld(d);
+  LinearBwdCall a = {};
+  a.M = d->M, a.N = d->N, a.K = d->K, a.act = d->act;
+  a.x = x, a.w = w, a.z = z, a.dy = dy, a.dx = dx, a.dw = dw, a.db = dbias;
+  a.ldx = l.x, a.ldw = l.w, a.ldz = l.z, a.lddy = l.y, a.lddx = d->K, a.lddw = d->K;
+  // without the products only the sums are wanted
+  a.dz = dx || dw ? s.dz : nullptr;
+  a.part = dbias ? s.part : nullptr;
+  a.x_pad = s.x_pad, a.w_pad = s.w_pad, a.status = s.status;
+  return cuda_rc(launch_linear_bwd(a, st));
+}
 
 int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* residual,
                     int32_t res_dtype, const void* gain, int32_t gain_dtype, float eps, void* h,

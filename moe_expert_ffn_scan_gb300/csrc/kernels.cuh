@@ -137,6 +137,40 @@ cudaError_t launch_add_rmsnorm_bwd(const uint16_t* dy, const void* h, bool h_f32
                                    const void* dh_in, void* dh, uint16_t* dx, float* dgain,
                                    float* part, cudaStream_t st);
 
+// out[c] = sum over `parts` rows of part[.][cols], in a fixed order (norm.cu).
+cudaError_t launch_column_sum(const float* part, int parts, int cols, float* out,
+                              cudaStream_t st);
+
+// Dense projection and its gradient (linear.cu).  Row strides in elements.  x_pad / w_pad
+// are non-null where that operand's rows are not whole 16-byte vectors: room for a copy
+// with rows of linear_padded(columns).
+inline long long linear_padded(int cols) { return (static_cast<long long>(cols) + 7) / 8 * 8; }
+struct LinearCall {
+  int M, N, K, act;
+  const uint16_t *x, *w;
+  const void *bias, *res;
+  void* y;
+  uint16_t* z;
+  long long ldx, ldw, ldr, ldy, ldz;
+  int bias_f32, y_f32;  // the residual has y's type
+  uint16_t *x_pad, *w_pad;
+  uint32_t* status;
+};
+cudaError_t launch_linear(const LinearCall& a, cudaStream_t st);
+constexpr int kLinearDbParts = 64;  // row blocks of the bias gradient's partial sums
+struct LinearBwdCall {
+  int M, N, K, act;
+  const uint16_t *x, *w, *z, *dy;
+  long long ldx, ldw, ldz, lddy, lddx, lddw;
+  uint16_t *dx, *dw;  // or null
+  float* db;          // or null
+  uint16_t* dz;       // [M][linear_padded(N)] where dy itself is not the products' operand
+  float* part;        // [kLinearDbParts][N] with db
+  uint16_t *x_pad, *w_pad;
+  uint32_t* status;
+};
+cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st);
+
 // Router balance loss and its gradient (balance.cu).  The forward's first kernel runs
 // balance_ctas(T) <= kBalanceCtas CTAs and writes one partial slot per (CTA, sequence)
 // pair that has rows: balance_ctas(T) + S - 1 slots.

@@ -1,0 +1,780 @@
+// Dense projection with its epilogue, y = act(x W^T + bias) + residual, and its gradient.
+//
+// Every product is out[t][f] = sum_c P[t][c] * Q[f][c] of bf16 operands with fp32 sums:
+//   forward   P = x  [M][K]        Q = W [N][K]         c = K
+//   dx        P = dz [M][N]        Q = W read as [K][N]  c = N
+//   dW        P = dz read as [N][M] Q = x read as [K][M]  c = M
+// An operand "read as" its transpose stays where it is: its tiles are loaded with the other
+// index contiguous and the MMA takes them as MN-major.  Operands whose rows are not whole
+// 16-byte vectors cannot be loaded by TMA and are first copied to padded rows.
+//
+// Two kernels:
+//   * k_linear_pair: 256 x 256 outputs per SM pair (cta_group::2 MMAs of M = 256, N = 256),
+//     64 columns of c a stage, persistent, two accumulators in TMEM so that a tile's
+//     epilogue runs under the next tile's MMAs.  Bound by the tensor cores.
+//   * k_linear_split: for outputs with too few such tiles.  128 features (the MMA's M side:
+//     the weights fill its rows even for one token) x NT tokens a tile, c split among the
+//     CTAs of a cluster, whose partial sums meet in distributed shared memory and are added
+//     in rank order (no atomics, no workspace).  Bound by reading W for few tokens.
+// Every wait is bounded; one that expires sets the workspace's status word.
+#include "kernels.cuh"
+
+#include <math.h>
+
+namespace moe {
+
+namespace {
+
+constexpr int kBK = 64;            // contraction columns per stage: one 128-byte swizzle row
+constexpr int kRowBytes = kBK * 2;
+
+// One operand: its matrix in memory and which index is contiguous.
+struct Operand {
+  const uint16_t* p;
+  long long ld;  // elements; ld % 8 == 0
+  int rows;      // t or f extent
+  int mn;        // 1: [c][rows] (rows contiguous), 0: [rows][c]
+};
+
+struct Epi {
+  const void* bias;  // [F] or null
+  const void* res;   // [R][ldr] or null
+  void* out;         // [R][ldo]
+  uint16_t* z;       // [R][ldz] or null: the value in front of the activation
+  long long ldr, ldo, ldz;
+  int bias_f32, out_f32, act;  // residual has the output's type
+  int vec;           // rows of out, res and z are whole 16-byte vectors
+};
+
+struct LinearParams {
+  int R, F, C;  // out rows, out columns, contraction
+  int p_mn, q_mn;
+  Epi e;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ float bf16_up(uint16_t v) {
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+__device__ __forceinline__ uint16_t bf16_down(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&b);
+}
+
+// Activations and their slopes, in fp32 (expf and erff within a few units of 2^-24).
+__device__ __forceinline__ float act_value(float z, int act) {
+  if (act == MOE_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  if (act == MOE_ACT_SILU) return z / (1.f + expf(-z));
+  if (act == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+  return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == MOE_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  if (act == MOE_ACT_SILU) {
+    const float s = 1.f / (1.f + expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  if (act == MOE_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+  return 1.f;
+}
+
+__device__ __forceinline__ float bias_at(const Epi& e, int f) {
+  return e.bias_f32 ? __ldg(static_cast<const float*>(e.bias) + f)
+                    : bf16_up(__ldg(static_cast<const uint16_t*>(e.bias) + f));
+}
+
+// One output value.
+__device__ __forceinline__ void emit_one(const Epi& e, int t, int f, float v) {
+  if (e.bias) v += bias_at(e, f);
+  if (e.z) e.z[static_cast<size_t>(t) * e.ldz + f] = bf16_down(v);
+  v = act_value(v, e.act);
+  const size_t ro = static_cast<size_t>(t) * e.ldr + f, oo = static_cast<size_t>(t) * e.ldo + f;
+  if (e.out_f32) {
+    if (e.res) v += static_cast<const float*>(e.res)[ro];
+    static_cast<float*>(e.out)[oo] = v;
+  } else {
+    if (e.res) v += bf16_up(static_cast<const uint16_t*>(e.res)[ro]);
+    static_cast<uint16_t*>(e.out)[oo] = bf16_down(v);
+  }
+}
+
+// 32 consecutive columns f0.. of row t, as whole vectors (f0 + 32 <= F).
+__device__ __forceinline__ void emit_row32(const Epi& e, int t, int f0, float (&v)[32]) {
+  if (e.bias) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += bias_at(e, f0 + i);
+  }
+  if (e.z) {
+    uint4* zp = reinterpret_cast<uint4*>(e.z + static_cast<size_t>(t) * e.ldz + f0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      zp[i] = make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
+                         bf16_pair(v[8 * i + 4], v[8 * i + 5]),
+                         bf16_pair(v[8 * i + 6], v[8 * i + 7]));
+  }
+  if (e.act == MOE_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
+  } else if (e.act == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_SILU);
+  } else if (e.act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
+  }
+  const size_t ro = static_cast<size_t>(t) * e.ldr + f0, oo = static_cast<size_t>(t) * e.ldo + f0;
+  if (e.out_f32) {
+    if (e.res) {
+      const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(e.res) + ro);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = r[i];
+        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+      }
+    }
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(e.out) + oo);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    if (e.res) {
+      const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + ro);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = r[i];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+      }
+    }
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + oo);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
+                        bf16_pair(v[8 * i + 4], v[8 * i + 5]),
+                        bf16_pair(v[8 * i + 6], v[8 * i + 7]));
+  }
+}
+
+// Instruction descriptor, kind::f16: D fp32, A and B bf16, M x n, transposed operands.
+__device__ __forceinline__ uint32_t idesc_bf16(int m, int n, int a_mn, int b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// A stage's tile of `rows` (a multiple of 64, or 16 / 32 when K-major) x 64 c:
+//   K-major:  [rows][64 c], 128-byte swizzled rows; 16 c further is 32 bytes further.
+//   MN-major: [rows / 64][64 c][64 rows], 128-byte swizzled rows; 8 c are 1024 bytes (the
+//             stride offset), 64 rows 8192 (the leading offset), 16 c 2048 further.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t base, int mn, int kk) {
+  return mn ? smem_desc(base + kk * 16 * kRowBytes, kBK * kRowBytes, 1024, kLayoutSw128)
+            : smem_desc(base + kk * 32, 0, 1024, kLayoutSw128);
+}
+
+// ---------------------------------------------------------------- SM pairs ----------
+
+constexpr int kPTile = 256;                      // output rows and columns per pair
+constexpr int kPStages = 6;
+constexpr int kPOpBytes = 128 * kRowBytes;       // one operand's stage in one CTA
+constexpr int kPStageBytes = 2 * kPOpBytes;
+constexpr int kPOffBar = kPStages * kPStageBytes;
+// full[S], empty[S], acc_full[2], acc_empty[2], drain
+constexpr int kPOffMisc = kPOffBar + (2 * kPStages + 5) * 8;
+constexpr int kPSmem = kPOffMisc + 16;
+// Tiles are walked in bands of this many output rows' tiles, column by column, so that the
+// tiles in flight share both operands' blocks in L2.
+constexpr int kPBand = 8;
+
+struct PairTile {
+  int t0, f0;
+};
+__device__ __forceinline__ PairTile pair_tile(int L, int tiles_t, int tiles_f) {
+  const int per = kPBand * tiles_f;
+  const int band = L / per, in = L - band * per;
+  const int first = band * kPBand;
+  const int h = tiles_t - first < kPBand ? tiles_t - first : kPBand;
+  PairTile r;
+  r.t0 = (first + in % h) * kPTile;
+  r.f0 = (in / h) * kPTile;
+  return r;
+}
+
+// CTA r of a pair: output rows 128 r.. of the tile (its P rows and accumulator lanes) and Q
+// rows 128 r.. (half of the MMA's N side).
+__global__ void __launch_bounds__(256, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                  const LinearParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPOffBar);
+  uint64_t* empty = full + kPStages;
+  uint64_t* acc_full = empty + kPStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kPOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 8);
+    }
+    mbar_init(drain, 1);
+    // swizzled tiles need a 1024-byte aligned base: a misaligned one makes every role a
+    // no-op (the CTA still takes part in the pair's set-up and teardown)
+    const bool bad = (smem_u32(smem) & 1023u) != 0;
+    *abort_flag = bad ? 1 : 0;
+    if (bad) set_status(p.status, STATUS_BAD_PLAN);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles_t = (p.R + kPTile - 1) / kPTile, tiles_f = (p.F + kPTile - 1) / kPTile;
+  const int total = tiles_t * tiles_f;
+  const int nk = (p.C + kBK - 1) / kBK;
+  const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  auto leader_addr = [&](const uint64_t* b) -> uint32_t { return mapa_shared(smem_u32(b), 0); };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int L = cl; L < total && ok && !*abort_flag; L += ncl) {
+        const PairTile tl = pair_tile(L, tiles_t, tiles_f);
+        const int t0 = tl.t0 + static_cast<int>(rank) * 128;
+        const int f0 = tl.f0 + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kPStages;
+          if (it >= kPStages &&
+              !mbar_wait(&empty[s], ((it / kPStages) & 1u) ^ 1u, p.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * kPStageBytes);
+          const uint32_t fb = leader_addr(&full[s]);
+          uint8_t* a = smem + s * kPStageBytes;
+          uint8_t* b = a + kPOpBytes;
+          if (p.p_mn) {
+            tma_load_2d_pair(a, &tmP, fb, t0, kb * kBK);
+            tma_load_2d_pair(a + kPOpBytes / 2, &tmP, fb, t0 + 64, kb * kBK);
+          } else {
+            tma_load_2d_pair(a, &tmP, fb, kb * kBK, t0);
+          }
+          if (p.q_mn) {
+            tma_load_2d_pair(b, &tmQ, fb, f0, kb * kBK);
+            tma_load_2d_pair(b + kPOpBytes / 2, &tmQ, fb, f0 + 64, kb * kBK);
+          } else {
+            tma_load_2d_pair(b, &tmQ, fb, kb * kBK, f0);
+          }
+        }
+      }
+      // after an abort: the pair's loads still in flight (all counted on these barriers)
+      if (leader && *abort_flag) {
+        const uint32_t from = it > kPStages ? it - kPStages : 0;
+        for (uint32_t i = from; i < it; ++i)
+          mbar_wait_drain(&full[i % kPStages], (i / kPStages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    if (leader && lane == 0) {
+      uint32_t it = 0, tc = 0;
+      const uint32_t idesc = idesc_bf16(256, 256, p.p_mn, p.q_mn);
+      bool ok = true;
+      for (int L = cl; L < total && ok && !*abort_flag; L += ncl, ++tc) {
+        const uint32_t b = tc & 1u, use = tc >> 1;
+        if (tc >= 2 && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + b * kPTile;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kPStages;
+          if (!mbar_wait(&full[s], (it / kPStages) & 1u, p.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * kPStageBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ss_pair(d, tile_desc(a0, p.p_mn, kk), tile_desc(a0 + kPOpBytes, p.q_mn, kk),
+                             idesc, kb > 0 || kk > 0);
+          tc_commit_pair_mc(&empty[s], 3);
+        }
+        if (ok) tc_commit_pair_mc(&acc_full[b], 3);
+      }
+      // after an abort: the MMAs already issued
+      if (*abort_flag) {
+        tc_commit_pair_mc(drain, 1);
+        mbar_wait_drain(drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp - 4;
+    uint32_t tc = 0;
+    for (int L = cl; L < total; L += ncl, ++tc) {  // (an abort makes the wait fail)
+      const PairTile tl = pair_tile(L, tiles_t, tiles_f);
+      const uint32_t b = tc & 1u, use = tc >> 1;
+      int w_ok = 1;
+      if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
+      if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
+      tc_fence_after();
+      const int t = tl.t0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kPTile;
+      for (int c = 0; c < kPTile && tl.f0 + c < p.F; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + c, r);
+        tmem_ld_wait();
+        if (t < p.R) {
+          const int f = tl.f0 + c;
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (p.e.vec && f + 32 <= p.F) {
+            emit_row32(p.e, t, f, v);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 32 && f + i < p.F; ++i) {
+              float x = v[0];
+#pragma unroll
+              for (int j = 1; j < 32; ++j) x = i == j ? v[j] : x;
+              emit_one(p.e, t, f + i, x);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(&acc_empty[b]);
+        else mbar_arrive_cluster(leader_addr(&acc_empty[b]));
+      }
+    }
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA releases TMEM or shared memory the pair still uses
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- split contraction --
+
+constexpr int kSFeat = 128;  // features per tile
+
+template <int NT>
+struct SplitCfg {
+  static constexpr int kQBytes = kSFeat * kRowBytes;
+  static constexpr int kPBytes = NT * kRowBytes;
+  static constexpr int kStageBytes = kQBytes + kPBytes;
+  static constexpr int kStages = 100 * 1024 / kStageBytes;  // two CTAs per SM
+  static constexpr int kOffBar = kStages * kStageBytes;
+  static constexpr int kOffMisc = kOffBar + (2 * kStages + 2) * 8;
+  static constexpr int kSmem = kOffMisc + 16;
+  static constexpr int kTmemCols = NT < 32 ? 32 : NT;
+  static_assert(NT * kSFeat * 4 <= kOffBar, "the partial sums reuse the ring");
+};
+
+// grid (splits, feature tiles, token tiles), cluster (splits, 1, 1).  CTA r sums its share
+// of the contraction blocks; then token j of the tile is finished by CTA j % splits.
+template <int NT>
+__global__ void __launch_bounds__(256, 2)
+    k_linear_split(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                   const LinearParams p) {
+  using C = SplitCfg<NT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    const bool bad = (smem_u32(smem) & 1023u) != 0;
+    *abort_flag = bad ? 1 : 0;
+    if (bad) set_status(p.status, STATUS_BAD_PLAN);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem = *tmem_slot;
+  const int splits = gridDim.x, part = blockIdx.x;
+  const int f0 = blockIdx.y * kSFeat, t0 = blockIdx.z * NT;
+  const int nk = (p.C + kBK - 1) / kBK;
+  const int kb0 = static_cast<int>(static_cast<long long>(nk) * part / splits);
+  const int kb1 = static_cast<int>(static_cast<long long>(nk) * (part + 1) / splits);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % C::kStages;
+        if (*abort_flag ||
+            (it >= C::kStages &&
+             !mbar_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u, p.status, abort_flag)))
+          break;
+        uint8_t* a = smem + s * C::kStageBytes;
+        uint8_t* b = a + C::kQBytes;
+        mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+        if (p.q_mn) {
+          tma_load_2d(a, &tmQ, &full[s], f0, kb * kBK);
+          tma_load_2d(a + C::kQBytes / 2, &tmQ, &full[s], f0 + 64, kb * kBK);
+        } else {
+          tma_load_2d(a, &tmQ, &full[s], kb * kBK, f0);
+        }
+        if (NT >= 64 && p.p_mn) {
+          tma_load_2d(b, &tmP, &full[s], t0, kb * kBK);
+          if (NT == 128) tma_load_2d(b + C::kPBytes / 2, &tmP, &full[s], t0 + 64, kb * kBK);
+        } else {
+          tma_load_2d(b, &tmP, &full[s], kb * kBK, t0);
+        }
+      }
+      if (*abort_flag) {
+        const uint32_t from = it > C::kStages ? it - C::kStages : 0;
+        for (uint32_t i = from; i < it; ++i)
+          mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(kSFeat, NT, p.q_mn, NT >= 64 ? p.p_mn : 0);
+      uint32_t it = 0;
+      bool ok = !*abort_flag;
+      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+        const int s = it % C::kStages;
+        if (!mbar_wait(&full[s], (it / C::kStages) & 1u, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(smem + s * C::kStageBytes);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ss(tmem, tile_desc(a0, p.q_mn, kk),
+                      tile_desc(a0 + C::kQBytes, NT >= 64 ? p.p_mn : 0, kk), idesc,
+                      kb > kb0 || kk > 0);
+        tc_commit(&empty[s]);
+      }
+      if (ok) {
+        tc_commit(acc_full);
+      } else {
+        tc_commit(drain);
+        mbar_wait_drain(drain, 0);
+      }
+    }
+  }
+  __syncwarp();
+  // The epilogue's threads: warps 4-7, one feature each.
+  const int q = warp - 4;
+  const int fl = q * 32 + lane, f = f0 + fl;
+  const int nt = p.R - t0 < NT ? p.R - t0 : NT;
+  const bool any = kb1 > kb0;  // (splits <= nk: always)
+  int w_ok = 0;
+  if (warp >= 4) {
+    w_ok = 1;
+    if (lane == 0) w_ok = any && mbar_wait(acc_full, 0, p.status, abort_flag);
+    w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
+    tc_fence_after();
+  }
+  float* sums = reinterpret_cast<float*>(smem);  // [NT][128], in the drained ring
+  if (warp >= 4 && w_ok) {
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    for (int c = 0; c < nt; c += 16) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(acc + c, r);
+      tmem_ld_wait();
+      if (splits == 1) {
+        if (f < p.F) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < nt) emit_one(p.e, t0 + c + i, f, __uint_as_float(r[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[(c + i) * kSFeat + fl] = __uint_as_float(r[i]);
+      }
+    }
+  }
+  if (splits > 1) {
+    cluster_sync();  // every CTA's partial sums are in place
+    if (warp >= 4 && f < p.F) {
+      const uint32_t mine = smem_u32(sums + fl);
+      for (int j = part; j < nt; j += splits) {
+        float v = 0.f;
+        for (int r = 0; r < splits; ++r)
+          v += ld_shared_cluster(mapa_shared(mine, r) + j * kSFeat * 4);
+        emit_one(p.e, t0 + j, f, v);
+      }
+    }
+    cluster_sync();  // no CTA leaves while its sums are read
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- elementwise --------
+
+// Rows copied to a row length that TMA can load (the columns past `cols` are never read).
+__global__ void __launch_bounds__(256)
+    k_repack(const uint16_t* __restrict__ src, long long lds, int rows, int cols,
+             uint16_t* __restrict__ dst, long long ldd) {
+  pdl_wait();
+  pdl_trigger();
+  for (int r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256)
+      dst[static_cast<size_t>(r) * ldd + c] = src[static_cast<size_t>(r) * lds + c];
+}
+
+// dz = bf16(dy * act'(z)) (the products take bf16 operands; the rounding is 2^-9 of each
+// element), and with part the column sums of the unrounded values over rows [blockIdx.y *
+// per, + per): a thread owns 2 columns.  dz null: only the sums.
+__global__ void __launch_bounds__(256)
+    k_linear_dz(const uint16_t* __restrict__ dy, long long ldy, const uint16_t* __restrict__ z,
+                long long ldz, int act, int M, int N, int per, uint16_t* __restrict__ dz,
+                long long ldd, float* __restrict__ part) {
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = (blockIdx.x * 256 + threadIdx.x) * 2;
+  if (c0 >= N) return;
+  const bool two = c0 + 1 < N;
+  const int r0 = blockIdx.y * per, r1 = M - r0 < per ? M : r0 + per;
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    const uint16_t* yp = dy + static_cast<size_t>(r) * ldy + c0;
+    float a = bf16_up(yp[0]), b = two ? bf16_up(yp[1]) : 0.f;
+    if (z) {
+      const uint16_t* zp = z + static_cast<size_t>(r) * ldz + c0;
+      a *= act_slope(bf16_up(zp[0]), act);
+      if (two) b *= act_slope(bf16_up(zp[1]), act);
+    }
+    s0 += a;
+    s1 += b;
+    if (dz) {
+      uint16_t* o = dz + static_cast<size_t>(r) * ldd + c0;
+      *reinterpret_cast<uint32_t*>(o) = bf16_pair(a, b);  // ldd is even and > c0
+    }
+  }
+  if (part) {
+    part[static_cast<size_t>(blockIdx.y) * N + c0] = s0;
+    if (two) part[static_cast<size_t>(blockIdx.y) * N + c0 + 1] = s1;
+  }
+}
+
+// ---------------------------------------------------------------- host side ----------
+
+bool encode(CUtensorMap* m, const Operand& o, int C, int box_rows) {
+  EncodeTiledFn enc = get_encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t inner = o.mn ? o.rows : C, outer = o.mn ? C : o.rows;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(o.ld) * 2};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(o.mn ? kBK : box_rows)};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(o.p), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Per-device facts of a kernel, set up once per context.
+struct KernelState {
+  unsigned long long ctx[64] = {};
+  int clusters[64] = {};
+};
+
+cudaError_t launch_cluster(const void* kern, KernelState& ks, int smem, int cluster, dim3 grid,
+                           bool persistent, cudaStream_t st, void** args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  const unsigned long long ctx = current_context_id();
+  if (ctx == 0 || ks.ctx[dev] != ctx) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (persistent) {
+      int sms = 0, n = 0;
+      e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3(sms / cluster * cluster);
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      ks.clusters[dev] = n;
+    }
+    ks.ctx[dev] = current_context_id();
+  }
+  if (persistent && grid.x > static_cast<unsigned>(ks.clusters[dev]) * cluster)
+    grid.x = ks.clusters[dev] * cluster;
+  cfg.gridDim = grid;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+template <int NT>
+cudaError_t launch_split(const Operand& P, const Operand& Q, const LinearParams& p, int splits,
+                         cudaStream_t st) {
+  static KernelState ks;
+  CUtensorMap tmP, tmQ;
+  if (!encode(&tmP, P, p.C, NT) || !encode(&tmQ, Q, p.C, kSFeat)) return cudaErrorInvalidValue;
+  const dim3 grid(splits, (p.F + kSFeat - 1) / kSFeat, (p.R + NT - 1) / NT);
+  if (grid.y > 65535 || grid.z > 65535) return cudaErrorInvalidValue;
+  void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
+  return launch_cluster(reinterpret_cast<const void*>(k_linear_split<NT>), ks, SplitCfg<NT>::kSmem,
+                        splits, grid, false, st, args);
+}
+
+cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearParams& p,
+                              cudaStream_t st) {
+  static KernelState ks;
+  CUtensorMap tmP, tmQ;
+  if (!encode(&tmP, P, p.C, 128) || !encode(&tmQ, Q, p.C, 128)) return cudaErrorInvalidValue;
+  const long long tiles = static_cast<long long>((p.R + kPTile - 1) / kPTile) *
+                          ((p.F + kPTile - 1) / kPTile);
+  if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
+  void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
+  return launch_cluster(reinterpret_cast<const void*>(k_linear_pair), ks, kPSmem, 2,
+                        dim3(static_cast<unsigned>(2 * tiles)), true, st, args);
+}
+
+// One product.  Time of a 256 x 256 pair tile = 1: a wave of pairs takes 1 for up to 76
+// tiles; a 128 x 128 tile takes one SM half as long, and with the contraction split the
+// waves come in finer steps.
+cudaError_t product(const Operand& P, const Operand& Q, const LinearParams& p, cudaStream_t st) {
+  const long long tiles = static_cast<long long>((p.R + kPTile - 1) / kPTile) *
+                          ((p.F + kPTile - 1) / kPTile);
+  const int nk = (p.C + kBK - 1) / kBK;
+  if (tiles >= 76) return launch_pair_tiles(P, Q, p, st);
+  const int nt = p.p_mn ? (p.R <= 64 ? 64 : 128)
+                        : p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
+  const long long items = static_cast<long long>((p.F + kSFeat - 1) / kSFeat) *
+                          ((p.R + nt - 1) / nt);
+  int splits = 1;
+  while (splits < 8 && items * splits * 2 <= 304 && nk >= 4 * splits) splits *= 2;
+  switch (nt) {
+    case 16: return launch_split<16>(P, Q, p, splits, st);
+    case 32: return launch_split<32>(P, Q, p, splits, st);
+    case 64: return launch_split<64>(P, Q, p, splits, st);
+    default: return launch_split<128>(P, Q, p, splits, st);
+  }
+}
+
+cudaError_t repack(Operand& o, int C, uint16_t* to, cudaStream_t st) {
+  if (!to) return cudaSuccess;
+  const int rows = o.mn ? C : o.rows, cols = o.mn ? o.rows : C;
+  const long long ld = linear_padded(cols);
+  const int grid = rows < 4096 ? rows : 4096;
+  const cudaError_t e = launch_k(k_repack, grid, 256, 0, st, o.p, o.ld, rows, cols, to, ld);
+  o.p = to;
+  o.ld = ld;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearCall& a, cudaStream_t st) {
+  Operand P = {a.x, a.ldx, a.M, 0}, Q = {a.w, a.ldw, a.N, 0};
+  cudaError_t e = repack(P, a.K, a.x_pad, st);
+  if (e == cudaSuccess) e = repack(Q, a.K, a.w_pad, st);
+  if (e != cudaSuccess) return e;
+  const int ow = a.y_f32 ? 4 : 8;  // elements in 16 bytes
+  LinearParams p = {a.M, a.N, a.K, 0, 0, {}, a.status};
+  p.e = {a.bias, a.res, a.y, a.z, a.ldr, a.ldy, a.ldz, a.bias_f32, a.y_f32, a.act, 0};
+  p.e.vec = a.ldy % ow == 0 && (!a.res || a.ldr % ow == 0) && (!a.z || a.ldz % 8 == 0);
+  return product(P, Q, p, st);
+}
+
+cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  Operand x = {a.x, a.ldx, a.K, 1};   // dW's Q: [c = M][K]
+  Operand w = {a.w, a.ldw, a.K, 1};   // dx's Q: [c = N][K]
+  const uint16_t* dz = a.dy;
+  long long ldz = a.lddy;
+  if (a.dz || a.part) {
+    const int per = (a.M + kLinearDbParts - 1) / kLinearDbParts;
+    const int parts = (a.M + per - 1) / per;
+    const dim3 grid((a.N + 511) / 512, parts);
+    e = launch_k(k_linear_dz, grid, 256, 0, st, a.dy, a.lddy, a.act == MOE_ACT_NONE ? nullptr : a.z,
+                 a.ldz, a.act, a.M, a.N, per, a.dz, linear_padded(a.N), a.part);
+    if (e != cudaSuccess) return e;
+    if (a.part) {
+      e = launch_column_sum(a.part, parts, a.N, a.db, st);
+      if (e != cudaSuccess) return e;
+    }
+    if (a.dz) dz = a.dz, ldz = linear_padded(a.N);
+  }
+  if (a.dx) {
+    e = repack(w, a.N, a.w_pad, st);
+    if (e != cudaSuccess) return e;
+    LinearParams p = {a.M, a.K, a.N, 0, 1, {}, a.status};
+    p.e = {nullptr, nullptr, a.dx, nullptr, 0, a.lddx, 0, 0, 0, MOE_ACT_NONE, a.lddx % 8 == 0};
+    e = product({dz, ldz, a.M, 0}, w, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dw) {
+    e = repack(x, a.M, a.x_pad, st);
+    if (e != cudaSuccess) return e;
+    LinearParams p = {a.N, a.K, a.M, 1, 1, {}, a.status};
+    p.e = {nullptr, nullptr, a.dw, nullptr, 0, a.lddw, 0, 0, 0, MOE_ACT_NONE, a.lddw % 8 == 0};
+    e = product({dz, ldz, a.N, 1}, x, p, st);
+  }
+  return e;
+}
+
+}  // namespace moe

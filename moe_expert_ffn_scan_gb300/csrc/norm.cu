@@ -292,7 +292,7 @@ struct NormBwd {
 
 // Each CTA walks rows blockIdx.x * blockDim.y + threadIdx.y, + grid, ...; a thread keeps
 // the dgain sums of its columns over all of them and the CTA writes one partial row, which
-// k_dgain_sum adds up in CTA order (no atomics: run-to-run identical).
+// k_column_sum adds up in CTA order (no atomics: run-to-run identical).
 template <typename RT, typename GT, int VEC, bool kWarpRow>
 __global__ void __launch_bounds__(kMaxThreads)
     k_add_rmsnorm_bwd(const NormBwd p, int rows, int cols) {
@@ -427,10 +427,10 @@ __global__ void __launch_bounds__(256)
   p.part[static_cast<size_t>(blockIdx.y) * cols + c] = v;
 }
 
-// dgain[c] = sum of nparts partial rows: 32 columns a CTA, its 32 warps take every 32nd
+// out[c] = sum of nparts partial rows: 32 columns a CTA, its 32 warps take every 32nd
 // partial each, then the warps' sums are added in warp order.
 __global__ void __launch_bounds__(1024)
-    k_dgain_sum(const float* part, int nparts, int cols, float* dgain) {
+    k_column_sum(const float* part, int nparts, int cols, float* out) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[32][33];
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(1024)
     v = 0.f;
 #pragma unroll
     for (int w = 0; w < 32; ++w) v += red[w][lane];
-    dgain[c] = v;
+    out[c] = v;
   }
 }
 
@@ -519,10 +519,15 @@ cudaError_t bwd_types(const NormBwd& p, int rows, int cols, float* dgain, cudaSt
               : launch_k(k_add_rmsnorm_bwd<RT, GT, 1, false>, parts, block, 0, st, p, rows, cols);
   }
   if (e != cudaSuccess || !dgain) return e;
-  return launch_k(k_dgain_sum, (cols + 31) / 32, 1024, 0, st, p.part, parts, cols, dgain);
+  return launch_column_sum(p.part, parts, cols, dgain, st);
 }
 
 }  // namespace
+
+cudaError_t launch_column_sum(const float* part, int parts, int cols, float* out,
+                              cudaStream_t st) {
+  return launch_k(k_column_sum, (cols + 31) / 32, 1024, 0, st, part, parts, cols, out);
+}
 
 cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* res, bool res_f32, const void* gain,
                                bool gain_f32, float eps, int rows, int cols, void* h, uint16_t* y,

@@ -112,3 +112,56 @@ def test_binding_refuses_host_tensors_types_and_shapes():
         moe.moe_add_rmsnorm(x, x.half(), w, 1e-6, y=x)
     with pytest.raises(ValueError, match="logits: expected"):
         moe.moe_balance_loss_backward(x, torch.zeros(4, 2, dtype=torch.int32), None, None, None)
+
+
+def _desc(**kw):
+    d = dict(M=4, N=64, K=32, act=0, bias_dtype=0, y_dtype=0)
+    d.update(kw)
+    return ctypes.byref(moe.moe_linear_desc(**d))
+
+
+def test_linear_refusals(lib):
+    f, size = lib.moe_linear, lib.moe_linear_workspace_size
+    big = 1 << 30
+    assert size(_desc()) == 256                                    # the status word alone
+    assert size(_desc(K=33)) > 256 and size(_desc(ldw=33)) > 256   # room for padded rows
+    assert size(_desc(K=33, ldx=40, ldw=40)) == 256
+    good = [A, A, A, A, A, A, A, big, None]  # x w bias residual y z ws bytes stream
+    for bad in (dict(M=-1), dict(N=0), dict(K=0), dict(ldx=31), dict(ldw=16), dict(ldy=63),
+                dict(ldr=1), dict(ldz=-64), dict(N=(1 << 22) + 1), dict(M=1 << 29, N=1 << 20)):
+        assert size(_desc(**bad)) == 0 and f(_desc(**bad), *good) == SHAPE
+        assert lib.moe_linear_backward(_desc(**bad), *[A] * 8, big, None) == SHAPE
+    assert f(None, *good) == SHAPE
+    for bad in (dict(act=4), dict(act=-1), dict(y_dtype=2), dict(bias_dtype=7)):
+        assert f(_desc(**bad), *good) == ARG
+    assert f(_desc(M=0), *good) == OK
+    for i in (0, 1, 4, 6):
+        assert f(_desc(), *_with(good, i, None)) == ARG
+    for i in (0, 1, 3, 4, 5, 6):
+        assert f(_desc(), *_with(good, i, BAD)) == ARG
+    assert f(_desc(), *_with(good, 2, ODD)) == ARG
+    assert f(_desc(), *_with(good, 7, 255)) == SMALL
+
+
+def test_linear_backward_refusals(lib):
+    f, size = lib.moe_linear_backward, lib.moe_linear_backward_workspace_size
+    good = [A, A, A, A, A, A, A, A, 1 << 30, None]  # x w z dy dx dw dbias ws bytes stream
+    assert size(_desc(act=2)) > size(_desc()) > 0
+    for i in (0, 1, 2, 3, 7):
+        assert f(_desc(act=1), *_with(good, i, None)) == ARG
+    for i in (0, 1, 2, 3, 4, 5, 7):
+        assert f(_desc(act=1), *_with(good, i, BAD)) == ARG
+    assert f(_desc(), *_with(good, 6, ODD)) == ARG
+    assert f(_desc(), *good[:4], None, None, None, *good[7:]) == ARG
+    assert f(_desc(), *_with(good, 8, 256)) == SMALL
+
+
+def test_linear_binding_refuses_shapes_types_and_strides():
+    x, w = torch.zeros(4, 32, dtype=torch.bfloat16), torch.zeros(64, 32, dtype=torch.bfloat16)
+    y, ws = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x: expected"):
+        moe.moe_linear(x.float(), w, y, ws)
+    with pytest.raises(ValueError, match="GPU"):
+        moe.moe_linear(x, w, y, ws)
+    with pytest.raises(KeyError):
+        moe.linear_backward_workspace_size(4, 64, 32, act="tanh")
