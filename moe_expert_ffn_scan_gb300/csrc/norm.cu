@@ -12,8 +12,8 @@
 //   dh = dh_in + rstd * (u - n * mean(u * n));   dgain = sum over rows of dy * n.
 //
 // Memory-bound for many rows (about one flop a byte), bound by one row's latency for few.
-// A row is read once and stays in registers between the sum and the outputs: kFwdNV (or
-// kBwdNV) 8-value vectors a thread, as many threads as the row needs, up to kMaxThreads; rows
+// A row is read once and stays in registers between the sum and the outputs: kOddNV (or
+// kOddBwdNV) 8-value vectors a thread, as many threads as the row needs, up to kMaxThreads; rows
 // too short to occupy more than one warp take a warp each.  Rows wider than the registers
 // of one CTA are read twice (the wide kernels).
 #include "kernels.cuh"
@@ -22,9 +22,12 @@ namespace moe {
 
 namespace {
 
+constexpr int kSms = 152;
+constexpr int kSmemMax = 227 * 1024 - 1024;  // dynamic shared memory of one CTA
 constexpr int kMaxThreads = 512;  // a row's threads: 128 registers each
-constexpr int kFwdNV = 4;         // 8-value vectors (or single values) a thread, forward
-constexpr int kBwdNV = 2;         // and backward, which holds three inputs and the dgain sums
+constexpr int kOddNV = 4;         // values a thread, odd widths, forward
+constexpr int kOddBwdNV = 2;      // and backward
+constexpr int kStages = 2;
 constexpr int kWarpRows = 8;      // rows (warps) per CTA when a row takes one warp
 
 template <typename T>
@@ -53,6 +56,19 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                : "l"(p)
                : "memory");
   return v;
+}
+
+// 16 bytes into shared memory, asynchronously and past L1.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -123,24 +139,34 @@ __device__ __forceinline__ void store_vec(uint16_t* p, const float (&f)[VEC]) {
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&f)[VEC]) {
   if constexpr (VEC == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {  // 32 bytes at once: a whole sector
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                   "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]),
+                   "f"(f[7])
+                   : "memory");
+    } else {  // a buffer aligned to 16 bytes only
+      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   } else {
     *p = f[0];
   }
 }
 
-// Sum over a row's threads: a warp's, or the CTA's (in warp order: deterministic).
-template <bool kWarpRow>
-__device__ __forceinline__ float row_sum(float v, float* part) {
+// Sum over a row's threads: a warp's, or the CTA's (at most 32 warps; a fixed order).
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
+}
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+  v = warp_sum(v);
   if constexpr (!kWarpRow) {
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) part[warp] = v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) part[warp] = v;
     __syncthreads();
-    v = 0.f;
-    for (int w = 0; w < nw; ++w) v += part[w];
+    v = warp_sum(lane < nw ? part[lane] : 0.f);
   }
   return v;
 }
@@ -186,27 +212,147 @@ __device__ __forceinline__ void norm_store(const float (&a)[VEC], float rstd, co
   }
 }
 
-template <typename RT, typename GT, int VEC, bool kWarpRow>
+// Vectors of 8 values in flight: a warp copies its own vectors of its row kStages rows ahead
+// into shared memory and reads back only what it copied, so the copies need no CTA barrier,
+// and a row's sum and stores run under the next rows' loads.  An array of T takes
+// kChunks<T> 16-byte chunks a vector, a warp's chunks of one vector index in column order:
+// the lanes copy consecutive chunks (whole sectors in each request: with each lane copying
+// its own 32 bytes of an fp32 row in two requests, L2 serves every sector twice, and the
+// gradient of 8192 x 7168 took 0.20 ms instead of 0.16), and then read their own.
+template <typename T>
+constexpr int kChunks = sizeof(T) / 2;
+
+// p: the warp's first value of this vector index, n: how many of the row's values start
+// there (the warp takes up to 256).  slots: the warp's chunks.
+template <typename T>
+__device__ __forceinline__ void stage_vec(uint4* slots, const T* p, int n, int lane) {
+#pragma unroll
+  for (int k = 0; k < kChunks<T>; ++k) {
+    const int q = k * 32 + lane;
+    if (q * static_cast<int>(16 / sizeof(T)) < n)
+      cp_async16(slots + q, reinterpret_cast<const uint4*>(p) + q);
+  }
+}
+__device__ __forceinline__ void unstage_vec(const uint4* slots, int lane, const uint16_t*,
+                                            float (&f)[8]) {
+  const uint4 u = slots[lane];
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unstage_vec(const uint4* slots, int lane, const float*,
+                                            float (&f)[8]) {
+  const uint4 a = slots[2 * lane], b = slots[2 * lane + 1];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+}
+
+// One row at a time per blockIdx.x / threadIdx.y; whole 16-byte vectors.
+template <typename RT, typename GT, int NV, bool kWarpRow>
+__global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 1 : 2)
+    k_add_rmsnorm_vec(const uint16_t* x, const RT* res, const GT* gain, float eps, int rows,
+                      int cols, NormOut o) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float part[2][kMaxThreads / 32];
+  const int threads = blockDim.x * blockDim.y;
+  const int stride = blockDim.x * 8, c0 = threadIdx.x * 8;
+  const int nv = (cols + stride - 1) / stride;
+  const float inv = 1.f / static_cast<float>(cols);
+  const int row_slots = nv * (1 + (res ? kChunks<RT> : 0)) * threads;
+  const int lane = threadIdx.x & 31, w0 = c0 - lane * 8;  // the warp's first column
+  // the warp's chunks of vector i: x at i * threads, the residual behind all of x's
+  const int wid = threadIdx.y * blockDim.x + threadIdx.x - lane;
+  uint4* ring_x = ring + wid;
+  uint4* ring_r = ring + nv * threads + wid * kChunks<RT>;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  const long long first = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  auto fetch = [&](long long row, int st) {
+    if (row < rows) {
+      const int sl = st * row_slots;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = w0 + i * stride;
+        if (c < cols) {
+          stage_vec(ring_x + sl + i * threads, x + row * cols + c, cols - c, lane);
+          if (res)
+            stage_vec(ring_r + sl + i * kChunks<RT> * threads, res + row * cols + c, cols - c,
+                      lane);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) fetch(first + st * step, st);
+  int st = 0, flip = 0;
+  for (long long row = first; row < rows; row += step) {
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int sl = st * row_slots;
+    float a[NV][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (c0 + i * stride < cols) {
+        unstage_vec(ring_x + sl + i * threads, lane, x, a[i]);
+        if (res) {
+          float r[8];
+          unstage_vec(ring_r + sl + i * kChunks<RT> * threads, lane, res, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[i][j] += r[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(a[i][j], a[i][j], sum);
+      }
+    __syncwarp();  // the slot has been read
+    fetch(row + kStages * step, st);
+    // two buffers: a row's partials are read while the next row's are written
+    sum = row_sum<kWarpRow>(sum, part[flip]);
+    const float rstd = rsqrtf(sum * inv + eps);
+    if (threadIdx.x == 0 && o.rstd) o.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * stride;
+      const unsigned active = __ballot_sync(0xFFFFFFFFu, c < cols);
+      if (c < cols) {
+        if (o.h) store_vec<8>(static_cast<RT*>(o.h) + row * cols + c, a[i]);
+        norm_store<8, GT>(a[i], rstd, gain, row, cols, c, o, active);
+      }
+    }
+    st = st + 1 == kStages ? 0 : st + 1;
+    flip ^= 1;
+  }
+}
+
+// Any width, one value at a time: rows are not whole vectors.
+template <typename RT, typename GT, bool kWarpRow>
 __global__ void __launch_bounds__(kMaxThreads)
-    k_add_rmsnorm(const uint16_t* x, const RT* res, const GT* gain, float eps, int rows, int cols,
+    k_add_rmsnorm_odd(const uint16_t* x, const RT* res, const GT* gain, float eps, int rows, int cols,
                   NormOut o) {
   pdl_wait();
   pdl_trigger();
   __shared__ float part[kMaxThreads / 32];
+  constexpr int VEC = 1;
   const size_t row = static_cast<size_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= static_cast<size_t>(rows)) return;
   const int stride = blockDim.x * VEC;
   const int c0 = threadIdx.x * VEC;
-  float a[kFwdNV][VEC];
+  float a[kOddNV][VEC];
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kFwdNV; ++i) {
+  for (int i = 0; i < kOddNV; ++i) {
     const int c = c0 + i * stride;
     if (c < cols) load_vec<VEC>(x + row * cols + c, a[i]);
   }
   if (res) {
 #pragma unroll
-    for (int i = 0; i < kFwdNV; ++i) {
+    for (int i = 0; i < kOddNV; ++i) {
       const int c = c0 + i * stride;
       float r[VEC];
       if (c < cols) {
@@ -217,7 +363,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
   }
 #pragma unroll
-  for (int i = 0; i < kFwdNV; ++i)
+  for (int i = 0; i < kOddNV; ++i)
     if (c0 + i * stride < cols) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) sum = fmaf(a[i][j], a[i][j], sum);
@@ -226,7 +372,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   const float rstd = rsqrtf(sum / static_cast<float>(cols) + eps);
   if (threadIdx.x == 0 && o.rstd) o.rstd[row] = rstd;
 #pragma unroll
-  for (int i = 0; i < kFwdNV; ++i) {
+  for (int i = 0; i < kOddNV; ++i) {
     const int c = c0 + i * stride;
     const unsigned active = __ballot_sync(0xFFFFFFFFu, c < cols);
     if (c < cols) {
@@ -236,7 +382,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   }
 }
 
-// Rows of more than kMaxThreads * kFwdNV * VEC columns: read twice (the second time from
+// Rows of more than kMaxThreads * kOddNV * VEC columns: read twice (the second time from
 // L2), one CTA a row.
 template <typename RT, typename GT, int VEC>
 __global__ void __launch_bounds__(kMaxThreads)
@@ -290,12 +436,133 @@ struct NormBwd {
   float* part;  // [CTAs][cols] sums of dy * n, or null
 };
 
-// Each CTA walks rows blockIdx.x * blockDim.y + threadIdx.y, + grid, ...; a thread keeps
-// the dgain sums of its columns over all of them and the CTA writes one partial row, which
-// k_column_sum adds up in CTA order (no atomics: run-to-run identical).
-template <typename RT, typename GT, int VEC, bool kWarpRow>
+// Whole 16-byte vectors.  Each CTA walks rows blockIdx.x * blockDim.y + threadIdx.y, + grid,
+// ... with the forward's copies in flight; a thread keeps the dgain sums of its columns over
+// all its rows and the CTA writes one partial row, which k_column_sum adds up in CTA order
+// (no atomics: run-to-run identical).
+template <typename RT, typename GT, int NV, bool kWarpRow>
 __global__ void __launch_bounds__(kMaxThreads)
-    k_add_rmsnorm_bwd(const NormBwd p, int rows, int cols) {
+    k_add_rmsnorm_bwd_vec(const NormBwd p, int rows, int cols) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ float part[2][32];
+  constexpr int CH = kChunks<RT>;
+  const int threads = blockDim.x * blockDim.y;
+  const int stride = blockDim.x * 8, c0 = threadIdx.x * 8;
+  const int lane = threadIdx.x & 31, w0 = c0 - lane * 8;  // the warp's first column
+  const RT* h = static_cast<const RT*>(p.h);
+  const RT* dhi = static_cast<const RT*>(p.dh_in);
+  const GT* gain = static_cast<const GT*>(p.gain);
+  const int row_slots = NV * (1 + (dhi ? 2 : 1) * CH) * threads;
+  const int wid = threadIdx.y * blockDim.x + threadIdx.x - lane;
+  uint4* ring_y = ring + wid;  // the warp's chunks of dy, h and dh_in
+  uint4* ring_h = ring + NV * threads + wid * CH;
+  uint4* ring_i = ring_h + NV * CH * threads;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  const long long first = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const float inv = 1.f / static_cast<float>(cols);
+  auto fetch = [&](long long row, int st) {
+    if (row < rows) {
+      const int sl = st * row_slots;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = w0 + i * stride;
+        if (c < cols) {
+          const size_t at = static_cast<size_t>(row) * cols + c;
+          stage_vec(ring_y + sl + i * threads, p.dy + at, cols - c, lane);
+          stage_vec(ring_h + sl + i * CH * threads, h + at, cols - c, lane);
+          if (dhi) stage_vec(ring_i + sl + i * CH * threads, dhi + at, cols - c, lane);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) fetch(first + st * step, st);
+  float dg[NV][8], g[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
+    if (c0 + i * stride < cols) load_gain<8>(gain + c0 + i * stride, g[i]);
+  }
+  int flip = 0, st = 0;
+  float rs = first < rows ? p.rstd[first] : 0.f;
+  for (long long row = first; row < rows; row += step) {
+    const float rs_next = row + step < rows ? p.rstd[row + step] : 0.f;
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int sl = st * row_slots;
+    float u[NV][8], n[NV][8], add[NV][8];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (c0 + i * stride < cols) {
+        unstage_vec(ring_y + sl + i * threads, lane, p.dy, u[i]);
+        unstage_vec(ring_h + sl + i * CH * threads, lane, h, n[i]);
+        if (dhi) unstage_vec(ring_i + sl + i * CH * threads, lane, dhi, add[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n[i][j] *= rs;
+          dg[i][j] = fmaf(u[i][j], n[i][j], dg[i][j]);
+          u[i][j] *= g[i][j];
+          dot = fmaf(u[i][j], n[i][j], dot);
+        }
+      }
+    __syncwarp();  // the slot has been read
+    fetch(row + kStages * step, st);
+    // two buffers: a row's partials are read while the next row's are written
+    dot = row_sum<kWarpRow>(dot, part[flip]) * inv;
+    const size_t base = static_cast<size_t>(row) * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * stride;
+      if (c < cols) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // (fmaf spelled out: the same bits whichever outputs are asked for)
+          const float t = fmaf(-n[i][j], dot, u[i][j]);
+          u[i][j] = dhi ? fmaf(rs, t, add[i][j]) : rs * t;
+        }
+        if (p.dh) store_vec<8>(static_cast<RT*>(p.dh) + base + c, u[i]);
+        if (p.dx) store_vec<8>(p.dx + base + c, u[i]);
+      }
+    }
+    rs = rs_next;
+    st = st + 1 == kStages ? 0 : st + 1;
+    flip ^= 1;
+  }
+  if (!p.part) return;
+  float* out = p.part + static_cast<size_t>(blockIdx.x) * cols;
+  if constexpr (kWarpRow) {
+    cp_async_wait<0>();
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring);  // [kWarpRows][cols]
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + i * stride < cols) sums[threadIdx.y * cols + c0 + i * stride + j] = dg[i][j];
+    __syncthreads();
+    for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += kWarpRows * 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarpRows; ++w) v += sums[w * cols + c];
+      out[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (c0 + i * stride < cols) store_vec<8>(out + c0 + i * stride, dg[i]);
+  }
+}
+
+// The same for any width, one value at a time.
+template <typename RT, typename GT, bool kWarpRow>
+__global__ void __launch_bounds__(kMaxThreads)
+    k_add_rmsnorm_bwd_odd(const NormBwd p, int rows, int cols) {
+  constexpr int VEC = 1;
   pdl_wait();
   pdl_trigger();
   extern __shared__ float dyn[];  // kWarpRow: [kWarpRows][cols] dgain sums
@@ -305,9 +572,9 @@ __global__ void __launch_bounds__(kMaxThreads)
   const RT* h = static_cast<const RT*>(p.h);
   const RT* dhi = static_cast<const RT*>(p.dh_in);
   const GT* gain = static_cast<const GT*>(p.gain);
-  float dg[kBwdNV][VEC], g[kBwdNV][VEC];
+  float dg[kOddBwdNV][VEC], g[kOddBwdNV][VEC];
 #pragma unroll
-  for (int i = 0; i < kBwdNV; ++i) {
+  for (int i = 0; i < kOddBwdNV; ++i) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dg[i][j] = 0.f;
     if (c0 + i * stride < cols) load_gain<VEC>(gain + c0 + i * stride, g[i]);
@@ -315,11 +582,11 @@ __global__ void __launch_bounds__(kMaxThreads)
   int flip = 0;
   for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < rows;
        row += static_cast<long long>(gridDim.x) * blockDim.y, flip ^= 1) {
-    float u[kBwdNV][VEC], n[kBwdNV][VEC], add[kBwdNV][VEC];
+    float u[kOddBwdNV][VEC], n[kOddBwdNV][VEC], add[kOddBwdNV][VEC];
     const size_t base = static_cast<size_t>(row) * cols;
     const float rs = p.rstd[row];
 #pragma unroll
-    for (int i = 0; i < kBwdNV; ++i) {
+    for (int i = 0; i < kOddBwdNV; ++i) {
       const int c = c0 + i * stride;
       if (c < cols) {
         load_vec<VEC>(p.dy + base + c, u[i]);
@@ -329,7 +596,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < kBwdNV; ++i)
+    for (int i = 0; i < kOddBwdNV; ++i)
       if (c0 + i * stride < cols) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
@@ -342,7 +609,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     // two buffers: a row's partials are read while the next row's are written
     dot = row_sum<kWarpRow>(dot, part[flip]) / static_cast<float>(cols);
 #pragma unroll
-    for (int i = 0; i < kBwdNV; ++i) {
+    for (int i = 0; i < kOddBwdNV; ++i) {
       const int c = c0 + i * stride;
       if (c < cols) {
         float d[VEC];
@@ -361,7 +628,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   float* out = p.part + static_cast<size_t>(blockIdx.x) * cols;
   if constexpr (kWarpRow) {
 #pragma unroll
-    for (int i = 0; i < kBwdNV; ++i)
+    for (int i = 0; i < kOddBwdNV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
         if (c0 + i * stride < cols) dyn[threadIdx.y * cols + c0 + i * stride + j] = dg[i][j];
@@ -374,7 +641,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kBwdNV; ++i)
+    for (int i = 0; i < kOddBwdNV; ++i)
       if (c0 + i * stride < cols) store_vec<VEC>(out + c0 + i * stride, dg[i]);
   }
 }
@@ -458,42 +725,73 @@ int row_threads(int cols, int vec, int nv) {
   return (t + 31) / 32 * 32;
 }
 
+// At most as many CTAs as fit on the GPU at once (which the shared memory and the 1024
+// threads of 64 registers a CTA decide), no more than `need`.
+template <auto kern, typename... Args>
+cudaError_t launch_resident(int need, dim3 block, int smem, cudaStream_t st, int* grid_out,
+                            Args... args) {
+  static unsigned long long attr_ctx[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const unsigned long long ctx = current_context_id();
+  if (ctx == 0 || attr_ctx[dev] != ctx) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    attr_ctx[dev] = current_context_id();
+  }
+  int per_sm = 0;
+  if (need > kSms) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, block.x * block.y, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  }
+  const int grid = need <= kSms ? need : min(need, kSms * per_sm);
+  if (grid_out) *grid_out = grid;
+  return launch_k(kern, grid, block, smem, st, args...);
+}
+
 template <typename RT, typename GT>
 cudaError_t fwd_types(const uint16_t* x, const void* res, const void* gain, float eps, int rows,
                       int cols, const NormOut& o, cudaStream_t st) {
   const RT* r = static_cast<const RT*>(res);
   const GT* g = static_cast<const GT*>(gain);
-  const bool vec = cols % 8 == 0;
-  const long long regs = static_cast<long long>(kMaxThreads) * kFwdNV * (vec ? 8 : 1);
-  if (cols > regs) {
-    return vec ? launch_k(k_add_rmsnorm_wide<RT, GT, 8>, rows, kMaxThreads, 0, st, x, r, g, eps,
-                          cols, o)
-               : launch_k(k_add_rmsnorm_wide<RT, GT, 1>, rows, kMaxThreads, 0, st, x, r, g, eps,
-                          cols, o);
+  if (cols % 8 == 0) {
+    if (cols > kMaxThreads * 4 * 8)
+      return launch_k(k_add_rmsnorm_wide<RT, GT, 8>, rows, kMaxThreads, 0, st, x, r, g, eps, cols,
+                      o);
+    const int nv = cols <= kMaxThreads * 2 * 8 ? 2 : 4;
+    const int t = row_threads(cols, 8, nv);
+    const int per_cta = t == 32 ? kWarpRows : 1;
+    const dim3 block(t, per_cta);
+    const int need = static_cast<int>((static_cast<long long>(rows) + per_cta - 1) / per_cta);
+    const int used = (cols + t * 8 - 1) / (t * 8);  // vectors a thread has
+    const int smem = kStages * used * (1 + (r ? kChunks<RT> : 0)) * t * per_cta * 16;
+    if (t == 32)
+      return launch_resident<k_add_rmsnorm_vec<RT, GT, 2, true>>(need, block, smem, st, nullptr, x, r, g,
+                                                                 eps, rows, cols, o);
+    return nv == 2 ? launch_resident<k_add_rmsnorm_vec<RT, GT, 2, false>>(
+                         need, block, smem, st, nullptr, x, r, g, eps, rows, cols, o)
+                   : launch_resident<k_add_rmsnorm_vec<RT, GT, 4, false>>(
+                         need, block, smem, st, nullptr, x, r, g, eps, rows, cols, o);
   }
-  const int t = row_threads(cols, vec ? 8 : 1, kFwdNV);
-  if (t == 32) {
-    const unsigned grid = (static_cast<unsigned>(rows) + kWarpRows - 1) / kWarpRows;
-    const dim3 block(32, kWarpRows);
-    return vec ? launch_k(k_add_rmsnorm<RT, GT, 8, true>, grid, block, 0, st, x, r, g, eps, rows,
-                          cols, o)
-               : launch_k(k_add_rmsnorm<RT, GT, 1, true>, grid, block, 0, st, x, r, g, eps, rows,
-                          cols, o);
-  }
-  return vec ? launch_k(k_add_rmsnorm<RT, GT, 8, false>, rows, t, 0, st, x, r, g, eps, rows, cols,
-                        o)
-             : launch_k(k_add_rmsnorm<RT, GT, 1, false>, rows, t, 0, st, x, r, g, eps, rows, cols,
-                        o);
+  if (cols > kMaxThreads * kOddNV)
+    return launch_k(k_add_rmsnorm_wide<RT, GT, 1>, rows, kMaxThreads, 0, st, x, r, g, eps, cols, o);
+  const int t = row_threads(cols, 1, kOddNV);
+  if (t == 32)
+    return launch_k(k_add_rmsnorm_odd<RT, GT, true>, (rows - 1) / kWarpRows + 1,
+                    dim3(32, kWarpRows), 0, st, x, r, g, eps, rows, cols, o);
+  return launch_k(k_add_rmsnorm_odd<RT, GT, false>, rows, t, 0, st, x, r, g, eps, rows, cols, o);
 }
 
 template <typename RT, typename GT>
 cudaError_t bwd_types(const NormBwd& p, int rows, int cols, float* dgain, cudaStream_t st) {
   const bool vec = cols % 8 == 0;
-  const long long regs = static_cast<long long>(kMaxThreads) * kBwdNV * (vec ? 8 : 1);
   int parts = 0;
   cudaError_t e = cudaSuccess;
   if (rows == 0) {
-  } else if (cols > regs) {
+  } else if (cols > (vec ? 8192 : kMaxThreads * kOddBwdNV)) {
     const int per = (rows + kNormBwdCtas - 1) / kNormBwdCtas;
     parts = (rows + per - 1) / per;
     if (p.part) {
@@ -502,21 +800,31 @@ cudaError_t bwd_types(const NormBwd& p, int rows, int cols, float* dgain, cudaSt
       if (e != cudaSuccess) return e;
     }
     e = launch_k(k_add_rmsnorm_bwd_wide<RT, GT>, rows, kMaxThreads, 0, st, p, cols);
-  } else {
-    const int t = row_threads(cols, vec ? 8 : 1, kBwdNV);
+  } else if (vec) {
+    constexpr int nv = 2;
+    const int t = row_threads(cols, 8, nv);
     const int per_cta = t == 32 ? kWarpRows : 1;
-    // about 1024 threads an SM (the registers' limit), within the partials' rows
-    const int want = kNormBwdCtas / 4 * (t == 32 ? 4 : t <= 256 ? 4 : 2);
-    const int need = (rows + per_cta - 1) / per_cta;
-    parts = need < want ? need : want;
-    const size_t smem = t == 32 ? sizeof(float) * kWarpRows * cols : 0;
     const dim3 block(t, per_cta);
+    int need = (rows - 1) / per_cta + 1;
+    if (need > kNormBwdCtas) need = kNormBwdCtas;
+    int smem = kStages * nv * (1 + (p.dh_in ? 2 : 1) * kChunks<RT>) * t * per_cta * 16;
+    if (t == 32) smem = max(smem, kWarpRows * cols * 4);
     if (t == 32)
-      e = vec ? launch_k(k_add_rmsnorm_bwd<RT, GT, 8, true>, parts, block, smem, st, p, rows, cols)
-              : launch_k(k_add_rmsnorm_bwd<RT, GT, 1, true>, parts, block, smem, st, p, rows, cols);
+      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, true>>(need, block, smem, st, &parts, p,
+                                                                  rows, cols);
     else
-      e = vec ? launch_k(k_add_rmsnorm_bwd<RT, GT, 8, false>, parts, block, 0, st, p, rows, cols)
-              : launch_k(k_add_rmsnorm_bwd<RT, GT, 1, false>, parts, block, 0, st, p, rows, cols);
+      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, false>>(need, block, smem, st, &parts,
+                                                                   p, rows, cols);
+  } else {
+    const int t = row_threads(cols, 1, kOddBwdNV);
+    const int per_cta = t == 32 ? kWarpRows : 1;
+    const int need = (rows - 1) / per_cta + 1;
+    parts = need < kNormBwdCtas ? need : kNormBwdCtas;
+    if (t == 32)
+      e = launch_k(k_add_rmsnorm_bwd_odd<RT, GT, true>, parts, dim3(32, kWarpRows),
+                   sizeof(float) * kWarpRows * cols, st, p, rows, cols);
+    else
+      e = launch_k(k_add_rmsnorm_bwd_odd<RT, GT, false>, parts, t, 0, st, p, rows, cols);
   }
   if (e != cudaSuccess || !dgain) return e;
   return launch_column_sum(p.part, parts, cols, dgain, st);

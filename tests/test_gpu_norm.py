@@ -168,6 +168,31 @@ def test_backward_against_differences():
         assert abs((f(h64, w64 + d) - f(h64, w64 - d)) / (2 * step) - dg[j].item()) < 1e-4
 
 
+@pytest.mark.parametrize("cols", [512, 1000, 7168, 1023])
+def test_buffers_aligned_to_16_bytes_only(cols):
+    """fp32 rows that start at an odd multiple of 16 bytes."""
+    def off(t):
+        flat = torch.empty(t.numel() + 4, dtype=t.dtype, device=DEV)[4:] if t.dtype is F32 else (
+            torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[8:])
+        flat = flat.view(t.shape)
+        flat.copy_(t)
+        return flat
+    x, r, w = _data(5, cols, "fp32", "fp32", seed=8)
+    outs = lambda: (torch.empty_like(r), torch.empty_like(x))  # noqa: E731
+    h, y = outs()
+    moe.moe_add_rmsnorm(x, r, w, EPS, h=h, y=y)
+    h2, y2 = (off(t) for t in outs())
+    moe.moe_add_rmsnorm(off(x), off(r), off(w), EPS, h=h2, y=y2)
+    assert torch.equal(h, h2) and torch.equal(y, y2)
+    rstd = torch.rsqrt(h.square().mean(1) + EPS)
+    ws = moe.alloc_workspace(moe.add_rmsnorm_backward_workspace_size(5, cols))
+    dh, dg = torch.empty_like(h), torch.empty(cols, dtype=F32, device=DEV)
+    moe.moe_add_rmsnorm_backward(y, h, w, rstd, ws, dh_in=r, dh=dh, dgain=dg)
+    dh2, dg2 = off(dh), torch.empty_like(dg)
+    moe.moe_add_rmsnorm_backward(off(y), off(h), off(w), rstd, ws, dh_in=off(r), dh=dh2, dgain=dg2)
+    assert torch.equal(dh, dh2) and torch.equal(dg, dg2)
+
+
 def test_no_rows():
     x = torch.empty(0, 256, dtype=BF16, device=DEV)
     w = torch.ones(256, dtype=BF16, device=DEV)
