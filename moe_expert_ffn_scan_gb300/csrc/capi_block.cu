@@ -197,7 +197,7 @@ int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* r
 
 size_t moe_add_rmsnorm_backward_workspace_size(int32_t rows, int32_t cols) {
   if (rows < 0 || cols < 1) return 0;
-  const size_t parts = rows < kNormBwdCtas ? (rows > 0 ? rows : 1) : kNormBwdCtas;
+  const size_t parts = norm_bwd_parts(rows, cols);
   return align_up(parts * static_cast<size_t>(cols) * sizeof(float));
 }
 

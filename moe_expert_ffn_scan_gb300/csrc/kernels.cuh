@@ -127,8 +127,8 @@ cudaError_t launch_combine(const uint16_t* y2, const int32_t* inv, const float* 
                            cudaStream_t st);
 
 // Residual addition + RMS norm and its gradient (norm.cu).  part: the dgain partials,
-// [min(rows, kNormBwdCtas)][cols] fp32 (not read when dgain is null).
-constexpr int kNormBwdCtas = 608;  // 4 per SM
+// [norm_bwd_parts(rows, cols)][cols] fp32 (not read when dgain is null).
+int norm_bwd_parts(int rows, int cols);
 cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* res, bool res_f32, const void* gain,
                                bool gain_f32, float eps, int rows, int cols, void* h, uint16_t* y,
                                uint8_t* q, uint8_t* s, float* rstd, cudaStream_t st);

@@ -25,9 +25,9 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kSmemMax = 227 * 1024 - 1024;  // dynamic shared memory of one CTA
 constexpr int kMaxThreads = 512;  // a row's threads: 128 registers each
-constexpr int kOddNV = 4;         // values a thread, odd widths, forward
-constexpr int kOddBwdNV = 2;      // and backward
-constexpr int kStages = 2;
+constexpr int kRaggedFew = 4;     // columns a thread in rows that are no whole vectors: up to
+constexpr int kRaggedMany = 8;    // 1024 columns, and up to 8192
+constexpr int kStages = 2;         // rows in flight (3: fewer CTAs fit, prefill 333 -> 371 us)
 constexpr int kWarpRows = 8;      // rows (warps) per CTA when a row takes one warp
 
 template <typename T>
@@ -330,59 +330,114 @@ __global__ void __launch_bounds__(kMaxThreads, NV == 4 ? 1 : 2)
   }
 }
 
-// Any width, one value at a time: rows are not whole vectors.
-template <typename RT, typename GT, bool kWarpRow>
-__global__ void __launch_bounds__(kMaxThreads)
-    k_add_rmsnorm_odd(const uint16_t* x, const RT* res, const GT* gain, float eps, int rows, int cols,
-                  NormOut o) {
+// Any width: rows start anywhere inside a 16-byte chunk.  The CTA copies the aligned chunks
+// that hold its row, kStages rows ahead, and a thread then reads columns threadIdx.x,
+// + blockDim.x, ... from shared memory: the gain of its columns stays in registers, and
+// every shared and global access of a warp is to consecutive values.
+//
+// A row of T in the ring: its chunks, the first of which starts up to 15 bytes before it.
+template <typename T>
+struct RaggedRow {
+  const uint8_t* from;  // the first chunk
+  int lead;             // bytes in front of the row
+  int chunks, last;     // how many, and the bytes of the last one that lie in the tensor
+  __device__ __forceinline__ RaggedRow(const T* base, long long row, int rows, int cols) {
+    const size_t begin = static_cast<size_t>(row) * cols * sizeof(T);
+    const size_t end = begin + cols * sizeof(T);
+    const size_t all = static_cast<size_t>(rows) * cols * sizeof(T);
+    const size_t at = begin & ~static_cast<size_t>(15);
+    lead = static_cast<int>(begin - at);
+    chunks = static_cast<int>((end - at + 15) >> 4);
+    const size_t stop = at + (static_cast<size_t>(chunks) << 4);
+    last = 16 - static_cast<int>(stop > all ? stop - all : 0);
+    from = reinterpret_cast<const uint8_t*>(base) + at;
+  }
+  __device__ __forceinline__ void fetch(uint8_t* slot) const {
+    for (int q = threadIdx.x; q < chunks; q += blockDim.x) {
+      const int n = q == chunks - 1 ? last : 16;  // the rest of the chunk is zero-filled
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot + q * 16)),
+                   "l"(from + static_cast<size_t>(q) * 16), "r"(n)
+                   : "memory");
+    }
+  }
+};
+// Bytes of a row's slot.
+template <typename T>
+__host__ __device__ constexpr int ragged_slot(int cols) {
+  return (cols * static_cast<int>(sizeof(T)) + 15) / 16 * 16 + 16;
+}
+// Bytes in front of row `row` in its slot.
+template <typename T>
+__device__ __forceinline__ int ragged_lead(long long row, int cols) {
+  return static_cast<int>((static_cast<size_t>(row) * cols * sizeof(T)) & 15);
+}
+
+template <typename RT, typename GT, int NE>
+__global__ void __launch_bounds__(NE == kRaggedFew ? 256 : 1024)
+    k_add_rmsnorm_any(const uint16_t* x, const RT* res, const GT* gain, float eps, int rows,
+                      int cols, NormOut o) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float part[kMaxThreads / 32];
-  constexpr int VEC = 1;
-  const size_t row = static_cast<size_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (row >= static_cast<size_t>(rows)) return;
-  const int stride = blockDim.x * VEC;
-  const int c0 = threadIdx.x * VEC;
-  float a[kOddNV][VEC];
-  float sum = 0.f;
+  extern __shared__ __align__(16) uint8_t ring8[];
+  __shared__ float part[2][32];
+  const int slot_x = ragged_slot<uint16_t>(cols);
+  const int slot = slot_x + (res ? ragged_slot<RT>(cols) : 0);
+  const float inv = 1.f / static_cast<float>(cols);
+  auto fetch = [&](long long row, int st) {
+    if (row < rows) {
+      RaggedRow<uint16_t>(x, row, rows, cols).fetch(ring8 + st * slot);
+      if (res) RaggedRow<RT>(res, row, rows, cols).fetch(ring8 + st * slot + slot_x);
+    }
+    cp_async_commit();
+  };
 #pragma unroll
-  for (int i = 0; i < kOddNV; ++i) {
-    const int c = c0 + i * stride;
-    if (c < cols) load_vec<VEC>(x + row * cols + c, a[i]);
+  for (int st = 0; st < kStages; ++st)
+    fetch(blockIdx.x + static_cast<long long>(st) * gridDim.x, st);
+  float g[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    g[i] = c < cols ? Elem<GT>::get(gain + c) : 0.f;
   }
-  if (res) {
+  int st = 0;
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    cp_async_wait<kStages - 1>();
+    __syncthreads();
+    const uint16_t* xs =
+        reinterpret_cast<const uint16_t*>(ring8 + st * slot + ragged_lead<uint16_t>(row, cols));
+    const RT* rs =
+        reinterpret_cast<const RT*>(ring8 + st * slot + slot_x + ragged_lead<RT>(row, cols));
+    float a[NE];
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kOddNV; ++i) {
-      const int c = c0 + i * stride;
-      float r[VEC];
+    for (int i = 0; i < NE; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      a[i] = 0.f;
       if (c < cols) {
-        load_vec<VEC>(res + row * cols + c, r);
+        a[i] = Elem<uint16_t>::get(xs + c);
+        if (res) a[i] += Elem<RT>::get(rs + c);
+      }
+      sum = fmaf(a[i], a[i], sum);
+    }
+    // (the barrier in here: every thread has read the slot)
+    sum = row_sum<false>(sum, part[st & 1]);
+    fetch(row + static_cast<long long>(kStages) * gridDim.x, st);
+    const float rstd = rsqrtf(sum * inv + eps);
+    if (threadIdx.x == 0 && o.rstd) o.rstd[row] = rstd;
+    const size_t base = static_cast<size_t>(row) * cols;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a[i][j] += r[j];
+    for (int i = 0; i < NE; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < cols) {
+        if (o.h) Elem<RT>::put(static_cast<RT*>(o.h) + base + c, a[i]);
+        if (o.y) Elem<uint16_t>::put(o.y + base + c, a[i] * rstd * g[i]);
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < kOddNV; ++i)
-    if (c0 + i * stride < cols) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) sum = fmaf(a[i][j], a[i][j], sum);
-    }
-  sum = row_sum<kWarpRow>(sum, part);
-  const float rstd = rsqrtf(sum / static_cast<float>(cols) + eps);
-  if (threadIdx.x == 0 && o.rstd) o.rstd[row] = rstd;
-#pragma unroll
-  for (int i = 0; i < kOddNV; ++i) {
-    const int c = c0 + i * stride;
-    const unsigned active = __ballot_sync(0xFFFFFFFFu, c < cols);
-    if (c < cols) {
-      if (o.h) store_vec<VEC>(static_cast<RT*>(o.h) + row * cols + c, a[i]);
-      norm_store<VEC, GT>(a[i], rstd, gain, row, cols, c, o, active);
-    }
+    st = st + 1 == kStages ? 0 : st + 1;
   }
 }
 
-// Rows of more than kMaxThreads * kOddNV * VEC columns: read twice (the second time from
+// Rows too wide for the registers of one CTA: read twice (the second time from
 // L2), one CTA a row.
 template <typename RT, typename GT, int VEC>
 __global__ void __launch_bounds__(kMaxThreads)
@@ -440,6 +495,9 @@ struct NormBwd {
 // ... with the forward's copies in flight; a thread keeps the dgain sums of its columns over
 // all its rows and the CTA writes one partial row, which k_column_sum adds up in CTA order
 // (no atomics: run-to-run identical).
+// Rows in flight: 16384 fp32 columns fill the shared memory once.
+__host__ __device__ constexpr int bwd_stages(int nv) { return nv == 4 ? 1 : kStages; }
+
 template <typename RT, typename GT, int NV, bool kWarpRow>
 __global__ void __launch_bounds__(kMaxThreads)
     k_add_rmsnorm_bwd_vec(const NormBwd p, int rows, int cols) {
@@ -448,6 +506,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float part[2][32];
   constexpr int CH = kChunks<RT>;
+  constexpr int ST = bwd_stages(NV);
   const int threads = blockDim.x * blockDim.y;
   const int stride = blockDim.x * 8, c0 = threadIdx.x * 8;
   const int lane = threadIdx.x & 31, w0 = c0 - lane * 8;  // the warp's first column
@@ -479,7 +538,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     cp_async_commit();
   };
 #pragma unroll
-  for (int st = 0; st < kStages; ++st) fetch(first + st * step, st);
+  for (int st = 0; st < ST; ++st) fetch(first + st * step, st);
   float dg[NV][8], g[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -491,7 +550,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   float rs = first < rows ? p.rstd[first] : 0.f;
   for (long long row = first; row < rows; row += step) {
     const float rs_next = row + step < rows ? p.rstd[row + step] : 0.f;
-    cp_async_wait<kStages - 1>();
+    cp_async_wait<ST - 1>();
     __syncwarp();
     const int sl = st * row_slots;
     float u[NV][8], n[NV][8], add[NV][8];
@@ -511,7 +570,7 @@ __global__ void __launch_bounds__(kMaxThreads)
         }
       }
     __syncwarp();  // the slot has been read
-    fetch(row + kStages * step, st);
+    fetch(row + ST * step, st);
     // two buffers: a row's partials are read while the next row's are written
     dot = row_sum<kWarpRow>(dot, part[flip]) * inv;
     const size_t base = static_cast<size_t>(row) * cols;
@@ -530,7 +589,7 @@ __global__ void __launch_bounds__(kMaxThreads)
       }
     }
     rs = rs_next;
-    st = st + 1 == kStages ? 0 : st + 1;
+    st = st + 1 == ST ? 0 : st + 1;
     flip ^= 1;
   }
   if (!p.part) return;
@@ -558,91 +617,87 @@ __global__ void __launch_bounds__(kMaxThreads)
   }
 }
 
-// The same for any width, one value at a time.
-template <typename RT, typename GT, bool kWarpRow>
-__global__ void __launch_bounds__(kMaxThreads)
-    k_add_rmsnorm_bwd_odd(const NormBwd p, int rows, int cols) {
-  constexpr int VEC = 1;
+// Any width (see k_add_rmsnorm_any).
+template <typename RT, typename GT, int NE>
+__global__ void __launch_bounds__(NE == kRaggedFew ? 256 : 1024)
+    k_add_rmsnorm_bwd_any(const NormBwd p, int rows, int cols) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float dyn[];  // kWarpRow: [kWarpRows][cols] dgain sums
-  __shared__ float part[2][kMaxThreads / 32];
-  const int stride = blockDim.x * VEC;
-  const int c0 = threadIdx.x * VEC;
+  extern __shared__ __align__(16) uint8_t ring8[];
+  __shared__ float part[2][32];
   const RT* h = static_cast<const RT*>(p.h);
   const RT* dhi = static_cast<const RT*>(p.dh_in);
   const GT* gain = static_cast<const GT*>(p.gain);
-  float dg[kOddBwdNV][VEC], g[kOddBwdNV][VEC];
-#pragma unroll
-  for (int i = 0; i < kOddBwdNV; ++i) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) dg[i][j] = 0.f;
-    if (c0 + i * stride < cols) load_gain<VEC>(gain + c0 + i * stride, g[i]);
-  }
-  int flip = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < rows;
-       row += static_cast<long long>(gridDim.x) * blockDim.y, flip ^= 1) {
-    float u[kOddBwdNV][VEC], n[kOddBwdNV][VEC], add[kOddBwdNV][VEC];
-    const size_t base = static_cast<size_t>(row) * cols;
-    const float rs = p.rstd[row];
-#pragma unroll
-    for (int i = 0; i < kOddBwdNV; ++i) {
-      const int c = c0 + i * stride;
-      if (c < cols) {
-        load_vec<VEC>(p.dy + base + c, u[i]);
-        load_vec<VEC>(h + base + c, n[i]);
-        if (dhi) load_vec<VEC>(dhi + base + c, add[i]);
-      }
+  const int off_h = ragged_slot<uint16_t>(cols), off_i = off_h + ragged_slot<RT>(cols);
+  const int slot = off_i + (dhi ? ragged_slot<RT>(cols) : 0);
+  const float inv = 1.f / static_cast<float>(cols);
+  auto fetch = [&](long long row, int st) {
+    if (row < rows) {
+      uint8_t* to = ring8 + st * slot;
+      RaggedRow<uint16_t>(p.dy, row, rows, cols).fetch(to);
+      const RaggedRow<RT> rr(h, row, rows, cols);
+      rr.fetch(to + off_h);
+      if (dhi) RaggedRow<RT>(dhi, row, rows, cols).fetch(to + off_i);
     }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < kStages; ++st)
+    fetch(blockIdx.x + static_cast<long long>(st) * gridDim.x, st);
+  float g[NE], dg[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    g[i] = c < cols ? Elem<GT>::get(gain + c) : 0.f;
+    dg[i] = 0.f;
+  }
+  int st = 0;
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    const float rs = p.rstd[row];
+    cp_async_wait<kStages - 1>();
+    __syncthreads();
+    const uint8_t* sl = ring8 + st * slot;
+    const int lead = ragged_lead<RT>(row, cols);
+    const uint16_t* ys =
+        reinterpret_cast<const uint16_t*>(sl + ragged_lead<uint16_t>(row, cols));
+    const RT* hs = reinterpret_cast<const RT*>(sl + off_h + lead);
+    const RT* is = reinterpret_cast<const RT*>(sl + off_i + lead);
+    float u[NE], n[NE], add[NE];
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < kOddBwdNV; ++i)
-      if (c0 + i * stride < cols) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          n[i][j] *= rs;
-          dg[i][j] = fmaf(u[i][j], n[i][j], dg[i][j]);
-          u[i][j] *= g[i][j];
-          dot = fmaf(u[i][j], n[i][j], dot);
-        }
-      }
-    // two buffers: a row's partials are read while the next row's are written
-    dot = row_sum<kWarpRow>(dot, part[flip]) / static_cast<float>(cols);
-#pragma unroll
-    for (int i = 0; i < kOddBwdNV; ++i) {
-      const int c = c0 + i * stride;
+    for (int i = 0; i < NE; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      u[i] = n[i] = add[i] = 0.f;
       if (c < cols) {
-        float d[VEC];
+        u[i] = Elem<uint16_t>::get(ys + c);
+        n[i] = Elem<RT>::get(hs + c) * rs;
+        if (dhi) add[i] = Elem<RT>::get(is + c);
+      }
+      dg[i] = fmaf(u[i], n[i], dg[i]);
+      u[i] *= g[i];
+      dot = fmaf(u[i], n[i], dot);
+    }
+    // (the barrier in here: every thread has read the slot)
+    dot = row_sum<false>(dot, part[st & 1]) * inv;
+    fetch(row + static_cast<long long>(kStages) * gridDim.x, st);
+    const size_t base = static_cast<size_t>(row) * cols;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          // (fmaf spelled out: the same bits whichever outputs are asked for)
-          const float t = fmaf(-n[i][j], dot, u[i][j]);
-          d[j] = dhi ? fmaf(rs, t, add[i][j]) : rs * t;
-        }
-        if (p.dh) store_vec<VEC>(static_cast<RT*>(p.dh) + base + c, d);
-        if (p.dx) store_vec<VEC>(p.dx + base + c, d);
+    for (int i = 0; i < NE; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (c < cols) {
+        const float t = fmaf(-n[i], dot, u[i]);
+        const float d = dhi ? fmaf(rs, t, add[i]) : rs * t;
+        if (p.dh) Elem<RT>::put(static_cast<RT*>(p.dh) + base + c, d);
+        if (p.dx) Elem<uint16_t>::put(p.dx + base + c, d);
       }
     }
+    st = st + 1 == kStages ? 0 : st + 1;
   }
   if (!p.part) return;
-  float* out = p.part + static_cast<size_t>(blockIdx.x) * cols;
-  if constexpr (kWarpRow) {
 #pragma unroll
-    for (int i = 0; i < kOddBwdNV; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        if (c0 + i * stride < cols) dyn[threadIdx.y * cols + c0 + i * stride + j] = dg[i][j];
-    __syncthreads();
-    for (int c = threadIdx.y * 32 + threadIdx.x; c < cols; c += kWarpRows * 32) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarpRows; ++w) v += dyn[w * cols + c];
-      out[c] = v;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kOddBwdNV; ++i)
-      if (c0 + i * stride < cols) store_vec<VEC>(out + c0 + i * stride, dg[i]);
+  for (int i = 0; i < NE; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (c < cols) p.part[static_cast<size_t>(blockIdx.x) * cols + c] = dg[i];
   }
 }
 
@@ -718,6 +773,8 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+constexpr int kBwdMaxCols = 16384;  // (vectors; 8192 otherwise) wider rows are read twice
+
 // Threads a row takes with nv vectors each: whole warps.
 int row_threads(int cols, int vec, int nv) {
   const int vecs = cols / vec;
@@ -776,61 +833,90 @@ cudaError_t fwd_types(const uint16_t* x, const void* res, const void* gain, floa
                    : launch_resident<k_add_rmsnorm_vec<RT, GT, 4, false>>(
                          need, block, smem, st, nullptr, x, r, g, eps, rows, cols, o);
   }
-  if (cols > kMaxThreads * kOddNV)
+  if (cols > kRaggedMany * 1024)
     return launch_k(k_add_rmsnorm_wide<RT, GT, 1>, rows, kMaxThreads, 0, st, x, r, g, eps, cols, o);
-  const int t = row_threads(cols, 1, kOddNV);
-  if (t == 32)
-    return launch_k(k_add_rmsnorm_odd<RT, GT, true>, (rows - 1) / kWarpRows + 1,
-                    dim3(32, kWarpRows), 0, st, x, r, g, eps, rows, cols, o);
-  return launch_k(k_add_rmsnorm_odd<RT, GT, false>, rows, t, 0, st, x, r, g, eps, rows, cols, o);
+  const bool few = cols <= kRaggedFew * 256;
+  const int t = row_threads(cols, 1, few ? kRaggedFew : kRaggedMany);
+  const int smem = kStages * (ragged_slot<uint16_t>(cols) + (r ? ragged_slot<RT>(cols) : 0));
+  return few ? launch_resident<k_add_rmsnorm_any<RT, GT, kRaggedFew>>(
+                   rows, t, smem, st, nullptr, x, r, g, eps, rows, cols, o)
+             : launch_resident<k_add_rmsnorm_any<RT, GT, kRaggedMany>>(
+                   rows, t, smem, st, nullptr, x, r, g, eps, rows, cols, o);
+}
+
+// The gradient's launch: threads a row, rows a CTA, vectors (or columns) a thread.
+struct BwdShape {
+  bool vec, wide;
+  int t, per_cta, nv;
+};
+BwdShape bwd_shape(int cols) {
+  BwdShape b = {};
+  b.vec = cols % 8 == 0;
+  b.wide = cols > (b.vec ? kBwdMaxCols : kRaggedMany * 1024);
+  b.per_cta = 1;
+  if (b.vec) {
+    b.nv = cols <= 8192 ? 2 : 4;
+    b.t = row_threads(cols, 8, b.nv);
+    if (b.t == 32) b.per_cta = kWarpRows;
+  } else {
+    b.nv = cols <= kRaggedFew * 256 ? kRaggedFew : kRaggedMany;
+    b.t = row_threads(cols, 1, b.nv);
+  }
+  return b;
 }
 
 template <typename RT, typename GT>
 cudaError_t bwd_types(const NormBwd& p, int rows, int cols, float* dgain, cudaStream_t st) {
-  const bool vec = cols % 8 == 0;
+  const BwdShape b = bwd_shape(cols);
   int parts = 0;
   cudaError_t e = cudaSuccess;
+  const int most = norm_bwd_parts(rows, cols);
   if (rows == 0) {
-  } else if (cols > (vec ? 8192 : kMaxThreads * kOddBwdNV)) {
-    const int per = (rows + kNormBwdCtas - 1) / kNormBwdCtas;
-    parts = (rows + per - 1) / per;
+  } else if (b.wide) {
+    const int per = static_cast<int>((static_cast<long long>(rows) + most - 1) / most);
+    parts = (rows - 1) / per + 1;
     if (p.part) {
       const dim3 grid((cols + 255) / 256, parts);
       e = launch_k(k_dgain_wide<RT>, grid, 256, 0, st, p, rows, cols, per);
       if (e != cudaSuccess) return e;
     }
     e = launch_k(k_add_rmsnorm_bwd_wide<RT, GT>, rows, kMaxThreads, 0, st, p, cols);
-  } else if (vec) {
-    constexpr int nv = 2;
-    const int t = row_threads(cols, 8, nv);
-    const int per_cta = t == 32 ? kWarpRows : 1;
-    const dim3 block(t, per_cta);
-    int need = (rows - 1) / per_cta + 1;
-    if (need > kNormBwdCtas) need = kNormBwdCtas;
-    int smem = kStages * nv * (1 + (p.dh_in ? 2 : 1) * kChunks<RT>) * t * per_cta * 16;
-    if (t == 32) smem = max(smem, kWarpRows * cols * 4);
-    if (t == 32)
-      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, true>>(need, block, smem, st, &parts, p,
+  } else if (b.vec) {
+    const dim3 block(b.t, b.per_cta);
+    int smem = bwd_stages(b.nv) * b.nv * (1 + (p.dh_in ? 2 : 1) * kChunks<RT>) * b.t * b.per_cta * 16;
+    if (b.t == 32) smem = max(smem, kWarpRows * cols * 4);
+    if (b.t == 32)
+      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, true>>(most, block, smem, st, &parts, p,
                                                                   rows, cols);
+    else if (b.nv == 2)
+      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, false>>(most, block, smem, st, &parts,
+                                                                   p, rows, cols);
     else
-      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, false>>(need, block, smem, st, &parts,
+      e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 4, false>>(most, block, smem, st, &parts,
                                                                    p, rows, cols);
   } else {
-    const int t = row_threads(cols, 1, kOddBwdNV);
-    const int per_cta = t == 32 ? kWarpRows : 1;
-    const int need = (rows - 1) / per_cta + 1;
-    parts = need < kNormBwdCtas ? need : kNormBwdCtas;
-    if (t == 32)
-      e = launch_k(k_add_rmsnorm_bwd_odd<RT, GT, true>, parts, dim3(32, kWarpRows),
-                   sizeof(float) * kWarpRows * cols, st, p, rows, cols);
-    else
-      e = launch_k(k_add_rmsnorm_bwd_odd<RT, GT, false>, parts, t, 0, st, p, rows, cols);
+    const int smem = kStages * (ragged_slot<uint16_t>(cols) +
+                                (p.dh_in ? 2 : 1) * ragged_slot<RT>(cols));
+    e = b.nv == kRaggedFew
+            ? launch_resident<k_add_rmsnorm_bwd_any<RT, GT, kRaggedFew>>(most, b.t, smem, st,
+                                                                         &parts, p, rows, cols)
+            : launch_resident<k_add_rmsnorm_bwd_any<RT, GT, kRaggedMany>>(most, b.t, smem, st,
+                                                                          &parts, p, rows, cols);
   }
   if (e != cudaSuccess || !dgain) return e;
   return launch_column_sum(p.part, parts, cols, dgain, st);
 }
 
 }  // namespace
+
+// At most 8 CTAs of the gradient per SM (4: rows of 1024 bf16 values take 61 us instead of
+// 46 at 32768 rows; 12: the same), fewer where their threads do not fit.
+int norm_bwd_parts(int rows, int cols) {
+  const BwdShape b = bwd_shape(cols);
+  const int need = rows > 0 ? (rows - 1) / b.per_cta + 1 : 1;
+  const int fit = b.wide ? 4 : 2048 / (b.t * b.per_cta);
+  return min(need, kSms * (fit < 1 ? 1 : fit > 8 ? 8 : fit));
+}
 
 cudaError_t launch_column_sum(const float* part, int parts, int cols, float* out,
                               cudaStream_t st) {
