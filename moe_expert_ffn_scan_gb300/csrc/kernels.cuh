@@ -157,7 +157,7 @@ struct LinearCall {
   uint32_t* status;
 };
 cudaError_t launch_linear(const LinearCall& a, cudaStream_t st);
-constexpr int kLinearDbParts = 64;  // row blocks of the bias gradient's partial sums
+constexpr int kLinearDbParts = 256;  // row blocks of the bias gradient's partial sums
 struct LinearBwdCall {
   int M, N, K, act;
   const uint16_t *x, *w, *z, *dy;

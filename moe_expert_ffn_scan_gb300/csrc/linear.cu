@@ -64,21 +64,24 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&b);
 }
 
-// Activations and their slopes, in fp32 (expf and erff within a few units of 2^-24).
+// Activations and their slopes, in fp32.  The sigmoid from ex2.approx and rcp.approx (each
+// within 2 units of 2^-23; the argument's rounding adds |z| * 2^-24): expf and the IEEE
+// quotient would double the gradient pass's instructions, which bound it.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 __device__ __forceinline__ float act_value(float z, int act) {
   if (act == MOE_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == MOE_ACT_SILU) return z / (1.f + expf(-z));
+  if (act == MOE_ACT_SILU) return z * sigmoid(z);
   if (act == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
   return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == MOE_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
   if (act == MOE_ACT_SILU) {
-    const float s = 1.f / (1.f + expf(-z));
-    return s * (1.f + z * (1.f - s));
+    const float s = sigmoid(z);
+    return s * fmaf(z, 1.f - s, 1.f);
   }
   if (act == MOE_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+    return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
   return 1.f;
 }
 
@@ -99,6 +102,38 @@ __device__ __forceinline__ void emit_one(const Epi& e, int t, int f, float v) {
   } else {
     if (e.res) v += bf16_up(static_cast<const uint16_t*>(e.res)[ro]);
     static_cast<uint16_t*>(e.out)[oo] = bf16_down(v);
+  }
+}
+
+// Column f of N rows t0, t0 + step, ... (those with on[i]); b: the column's bias.  All
+// residuals are loaded before the first store, which might alias them.
+template <int N>
+__device__ __forceinline__ void emit_column(const Epi& e, int t0, int step, int f, float b,
+                                            const bool (&on)[N], float (&v)[N]) {
+  float r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    r[i] = 0.f;
+    if (e.res && on[i]) {
+      const size_t at = static_cast<size_t>(t0 + i * step) * e.ldr + f;
+      r[i] = e.out_f32 ? static_cast<const float*>(e.res)[at]
+                       : bf16_up(static_cast<const uint16_t*>(e.res)[at]);
+    }
+    v[i] += b;
+  }
+  if (e.z) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) e.z[static_cast<size_t>(t0 + i * step) * e.ldz + f] = bf16_down(v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float y = act_value(v[i], e.act) + r[i];
+    if (on[i]) {
+      const size_t at = static_cast<size_t>(t0 + i * step) * e.ldo + f;
+      if (e.out_f32) static_cast<float*>(e.out)[at] = y;
+      else static_cast<uint16_t*>(e.out)[at] = bf16_down(y);
+    }
   }
 }
 
@@ -385,6 +420,7 @@ __global__ void __launch_bounds__(256, 1)
 
 // ---------------------------------------------------------------- split contraction --
 
+#define SLOTS 304
 constexpr int kSFeat = 128;  // features per tile
 
 template <int NT>
@@ -434,6 +470,7 @@ __global__ void __launch_bounds__(256, 2)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  pdl_trigger();  // (after the TMEM allocation: a successor's cannot come in between)
   const uint32_t tmem = *tmem_slot;
   const int splits = gridDim.x, part = blockIdx.x;
   const int f0 = blockIdx.y * kSFeat, t0 = blockIdx.z * NT;
@@ -501,31 +538,31 @@ __global__ void __launch_bounds__(256, 2)
     }
   }
   __syncwarp();
-  // The epilogue's threads: warps 4-7, one feature each.
-  const int q = warp - 4;
+  // Epilogue: a thread has one feature; warps 4-7 read the accumulator.
+  const int q = warp & 3;
   const int fl = q * 32 + lane, f = f0 + fl;
   const int nt = p.R - t0 < NT ? p.R - t0 : NT;
-  const bool any = kb1 > kb0;  // (splits <= nk: always)
-  int w_ok = 0;
+  const float bias = p.e.bias && f < p.F ? bias_at(p.e, f) : 0.f;
+  float* sums = reinterpret_cast<float*>(smem);  // [NT][128], in the drained ring
   if (warp >= 4) {
-    w_ok = 1;
-    if (lane == 0) w_ok = any && mbar_wait(acc_full, 0, p.status, abort_flag);
+    int w_ok = 1;
+    if (lane == 0) w_ok = mbar_wait(acc_full, 0, p.status, abort_flag);
     w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
     tc_fence_after();
-  }
-  float* sums = reinterpret_cast<float*>(smem);  // [NT][128], in the drained ring
-  if (warp >= 4 && w_ok) {
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    for (int c = 0; c < nt; c += 16) {
+    for (int c = 0; c < nt && w_ok; c += 16) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(acc + c, r);
       tmem_ld_wait();
       if (splits == 1) {
-        if (f < p.F) {
+        float v[16];
+        bool on[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < nt) emit_one(p.e, t0 + c + i, f, __uint_as_float(r[i]));
+        for (int i = 0; i < 16; ++i) {
+          v[i] = __uint_as_float(r[i]);
+          on[i] = f < p.F && c + i < nt;
         }
+        emit_column<16>(p.e, t0 + c, 1, f, bias, on, v);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) sums[(c + i) * kSFeat + fl] = __uint_as_float(r[i]);
@@ -534,18 +571,28 @@ __global__ void __launch_bounds__(256, 2)
   }
   if (splits > 1) {
     cluster_sync();  // every CTA's partial sums are in place
-    if (warp >= 4 && f < p.F) {
-      const uint32_t mine = smem_u32(sums + fl);
-      for (int j = part; j < nt; j += splits) {
-        float v = 0.f;
-        for (int r = 0; r < splits; ++r)
-          v += ld_shared_cluster(mapa_shared(mine, r) + j * kSFeat * 4);
-        emit_one(p.e, t0 + j, f, v);
+    // this CTA's tokens part, part + splits, ...: half of them for each four warps, kTok at
+    // a time, all of whose loads are in flight together
+    constexpr int kTok = 8;
+    const uint32_t mine = smem_u32(sums + fl);
+    for (int j0 = part + (warp >> 2) * splits; j0 < nt && f < p.F; j0 += 2 * kTok * splits) {
+      float v[kTok];
+      bool on[kTok];
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        v[i] = 0.f;
+        on[i] = j0 + i * 2 * splits < nt;
       }
+      for (int r = 0; r < splits; ++r) {
+        const uint32_t at = mapa_shared(mine, r) + j0 * kSFeat * 4;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+          if (on[i]) v[i] += ld_shared_cluster(at + i * 2 * splits * kSFeat * 4);
+      }
+      emit_column<kTok>(p.e, t0 + j0, 2 * splits, f, bias, on, v);
     }
     cluster_sync();  // no CTA leaves while its sums are read
   }
-  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -557,50 +604,84 @@ __global__ void __launch_bounds__(256, 2)
 
 // ---------------------------------------------------------------- elementwise --------
 
-// Rows copied to a row length that TMA can load (the columns past `cols` are never read).
-__global__ void __launch_bounds__(256)
-    k_repack(const uint16_t* __restrict__ src, long long lds, int rows, int cols,
-             uint16_t* __restrict__ dst, long long ldd) {
+// Rows copied to a row length that TMA can load (the columns past `cols` are never read);
+// blockIdx.y: which of up to two matrices.
+struct Repack {
+  const uint16_t* src;
+  uint16_t* dst;
+  long long lds, ldd;
+  int rows, cols;
+};
+__global__ void __launch_bounds__(256) k_repack(const Repack a, const Repack b) {
   pdl_wait();
   pdl_trigger();
-  for (int r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < cols; c += 256)
-      dst[static_cast<size_t>(r) * ldd + c] = src[static_cast<size_t>(r) * lds + c];
+  const Repack m = blockIdx.y ? b : a;
+  for (int r = blockIdx.x; r < m.rows; r += gridDim.x) {
+    const uint16_t* src = m.src + static_cast<size_t>(r) * m.lds;
+    uint16_t* dst = m.dst + static_cast<size_t>(r) * m.ldd;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < m.cols; c += 256) dst[c] = src[c];
+  }
 }
 
 // dz = bf16(dy * act'(z)) (the products take bf16 operands; the rounding is 2^-9 of each
 // element), and with part the column sums of the unrounded values over rows [blockIdx.y *
-// per, + per): a thread owns 2 columns.  dz null: only the sums.
-__global__ void __launch_bounds__(256)
+// per, + per): a thread owns VEC columns.  dz null: only the sums.  Memory-bound: VEC = 8
+// where all rows are whole 16-byte vectors (4096 x 6144: DZ_NOW us; two columns a thread 63).
+template <int VEC>
+__global__ void __launch_bounds__(128)
     k_linear_dz(const uint16_t* __restrict__ dy, long long ldy, const uint16_t* __restrict__ z,
                 long long ldz, int act, int M, int N, int per, uint16_t* __restrict__ dz,
                 long long ldd, float* __restrict__ part) {
   pdl_wait();
   pdl_trigger();
-  const int c0 = (blockIdx.x * 256 + threadIdx.x) * 2;
+  const int c0 = (blockIdx.x * 128 + threadIdx.x) * VEC;
   if (c0 >= N) return;
-  const bool two = c0 + 1 < N;
   const int r0 = blockIdx.y * per, r1 = M - r0 < per ? M : r0 + per;
-  float s0 = 0.f, s1 = 0.f;
+  float sum[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sum[i] = 0.f;
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) {
-    const uint16_t* yp = dy + static_cast<size_t>(r) * ldy + c0;
-    float a = bf16_up(yp[0]), b = two ? bf16_up(yp[1]) : 0.f;
-    if (z) {
-      const uint16_t* zp = z + static_cast<size_t>(r) * ldz + c0;
-      a *= act_slope(bf16_up(zp[0]), act);
-      if (two) b *= act_slope(bf16_up(zp[1]), act);
+    float a[VEC], s[VEC];
+    if constexpr (VEC == 8) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(dy + r * ldy + c0));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[2 * i] = __uint_as_float(w[i] << 16);
+        a[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+      if (z) {
+        const uint4 t = __ldg(reinterpret_cast<const uint4*>(z + r * ldz + c0));
+        const uint32_t y[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[2 * i] = __uint_as_float(y[i] << 16);
+          s[2 * i + 1] = __uint_as_float(y[i] & 0xFFFF0000u);
+        }
+      }
+    } else {
+      a[0] = bf16_up(__ldg(dy + r * ldy + c0));
+      if (z) s[0] = bf16_up(__ldg(z + r * ldz + c0));
     }
-    s0 += a;
-    s1 += b;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      if (z) a[i] *= act_slope(s[i], act);
+      sum[i] += a[i];
+    }
     if (dz) {
-      uint16_t* o = dz + static_cast<size_t>(r) * ldd + c0;
-      *reinterpret_cast<uint32_t*>(o) = bf16_pair(a, b);  // ldd is even and > c0
+      if constexpr (VEC == 8)
+        *reinterpret_cast<uint4*>(dz + r * ldd + c0) =
+            make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]),
+                       bf16_pair(a[6], a[7]));
+      else
+        dz[r * ldd + c0] = bf16_down(a[0]);
     }
   }
   if (part) {
-    part[static_cast<size_t>(blockIdx.y) * N + c0] = s0;
-    if (two) part[static_cast<size_t>(blockIdx.y) * N + c0 + 1] = s1;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) part[static_cast<size_t>(blockIdx.y) * N + c0 + i] = sum[i];
   }
 }
 
@@ -705,8 +786,9 @@ cudaError_t product(const Operand& P, const Operand& Q, const LinearParams& p, c
                         : p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
   const long long items = static_cast<long long>((p.F + kSFeat - 1) / kSFeat) *
                           ((p.R + nt - 1) / nt);
-  int splits = 1;
-  while (splits < 8 && items * splits * 2 <= 304 && nk >= 4 * splits) splits *= 2;
+  int splits = static_cast<int>(SLOTS / items);
+  splits = splits > nk / 4 ? nk / 4 : splits;
+  splits = splits > 8 ? 8 : splits < 1 ? 1 : splits;
   switch (nt) {
     case 16: return launch_split<16>(P, Q, p, splits, st);
     case 32: return launch_split<32>(P, Q, p, splits, st);
@@ -715,23 +797,30 @@ cudaError_t product(const Operand& P, const Operand& Q, const LinearParams& p, c
   }
 }
 
-cudaError_t repack(Operand& o, int C, uint16_t* to, cudaStream_t st) {
-  if (!to) return cudaSuccess;
-  const int rows = o.mn ? C : o.rows, cols = o.mn ? o.rows : C;
-  const long long ld = linear_padded(cols);
-  const int grid = rows < 4096 ? rows : 4096;
-  const cudaError_t e = launch_k(k_repack, grid, 256, 0, st, o.p, o.ld, rows, cols, to, ld);
-  o.p = to;
-  o.ld = ld;
-  return e;
+// Points o at its copy in `to` (null: it stays where it is); returns the copy to make.
+Repack repack(Operand& o, int C, uint16_t* to) {
+  Repack r = {};
+  if (!to) return r;
+  r.src = o.p, r.lds = o.ld;
+  r.rows = o.mn ? C : o.rows, r.cols = o.mn ? o.rows : C;
+  r.dst = to, r.ldd = linear_padded(r.cols);
+  o.p = to, o.ld = r.ldd;
+  return r;
+}
+cudaError_t run_repack(Repack a, Repack b, cudaStream_t st) {
+  if (!a.rows) a = b, b = Repack{};
+  if (!a.rows) return cudaSuccess;
+  const int rows = a.rows > b.rows ? a.rows : b.rows;
+  const dim3 grid(rows < 4096 ? rows : 4096, b.rows ? 2 : 1);
+  return launch_k(k_repack, grid, 256, 0, st, a, b);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearCall& a, cudaStream_t st) {
   Operand P = {a.x, a.ldx, a.M, 0}, Q = {a.w, a.ldw, a.N, 0};
-  cudaError_t e = repack(P, a.K, a.x_pad, st);
-  if (e == cudaSuccess) e = repack(Q, a.K, a.w_pad, st);
+  const Repack rp = repack(P, a.K, a.x_pad), rq = repack(Q, a.K, a.w_pad);
+  const cudaError_t e = run_repack(rp, rq, st);
   if (e != cudaSuccess) return e;
   const int ow = a.y_f32 ? 4 : 8;  // elements in 16 bytes
   LinearParams p = {a.M, a.N, a.K, 0, 0, {}, a.status};
@@ -747,11 +836,19 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st) {
   const uint16_t* dz = a.dy;
   long long ldz = a.lddy;
   if (a.dz || a.part) {
-    const int per = (a.M + kLinearDbParts - 1) / kLinearDbParts;
-    const int parts = (a.M + per - 1) / per;
-    const dim3 grid((a.N + 511) / 512, parts);
-    e = launch_k(k_linear_dz, grid, 256, 0, st, a.dy, a.lddy, a.act == MOE_ACT_NONE ? nullptr : a.z,
-                 a.ldz, a.act, a.M, a.N, per, a.dz, linear_padded(a.N), a.part);
+    const uint16_t* z = a.act == MOE_ACT_NONE ? nullptr : a.z;
+    const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && (!z || a.ldz % 8 == 0);
+    const int blocks = (a.N + (vec ? 1023 : 127)) / (vec ? 1024 : 128);
+    // row blocks: about four CTAs of 128 threads per SM
+    int parts = (608 + blocks - 1) / blocks;
+    parts = parts > kLinearDbParts ? kLinearDbParts : parts;
+    const int per = (a.M + parts - 1) / parts;
+    parts = (a.M + per - 1) / per;
+    const dim3 grid(blocks, parts);
+    e = vec ? launch_k(k_linear_dz<8>, grid, 128, 0, st, a.dy, a.lddy, z, a.ldz, a.act, a.M, a.N,
+                       per, a.dz, linear_padded(a.N), a.part)
+            : launch_k(k_linear_dz<1>, grid, 128, 0, st, a.dy, a.lddy, z, a.ldz, a.act, a.M, a.N,
+                       per, a.dz, linear_padded(a.N), a.part);
     if (e != cudaSuccess) return e;
     if (a.part) {
       e = launch_column_sum(a.part, parts, a.N, a.db, st);
@@ -759,17 +856,17 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st) {
     }
     if (a.dz) dz = a.dz, ldz = linear_padded(a.N);
   }
+  const Repack rw = repack(w, a.N, a.dx ? a.w_pad : nullptr);
+  const Repack rx = repack(x, a.M, a.dw ? a.x_pad : nullptr);
+  e = run_repack(rw, rx, st);
+  if (e != cudaSuccess) return e;
   if (a.dx) {
-    e = repack(w, a.N, a.w_pad, st);
-    if (e != cudaSuccess) return e;
     LinearParams p = {a.M, a.K, a.N, 0, 1, {}, a.status};
     p.e = {nullptr, nullptr, a.dx, nullptr, 0, a.lddx, 0, 0, 0, MOE_ACT_NONE, a.lddx % 8 == 0};
     e = product({dz, ldz, a.M, 0}, w, p, st);
     if (e != cudaSuccess) return e;
   }
   if (a.dw) {
-    e = repack(x, a.M, a.x_pad, st);
-    if (e != cudaSuccess) return e;
     LinearParams p = {a.N, a.K, a.M, 1, 1, {}, a.status};
     p.e = {nullptr, nullptr, a.dw, nullptr, 0, a.lddw, 0, 0, 0, MOE_ACT_NONE, a.lddw % 8 == 0};
     e = product({dz, ldz, a.N, 1}, x, p, st);
