@@ -43,7 +43,7 @@ struct Epi {
   uint16_t* z;       // [R][ldz] or null: the value in front of the activation
   long long ldr, ldo, ldz;
   int bias_f32, out_f32, act;  // residual has the output's type
-  int vec;           // rows of out, res and z are whole 16-byte vectors
+  int whole;         // rows of out, res and z are whole 32-byte sectors
 };
 
 struct LinearParams {
@@ -90,27 +90,12 @@ __device__ __forceinline__ float bias_at(const Epi& e, int f) {
                     : bf16_up(__ldg(static_cast<const uint16_t*>(e.bias) + f));
 }
 
-// One output value.
-__device__ __forceinline__ void emit_one(const Epi& e, int t, int f, float v) {
-  if (e.bias) v += bias_at(e, f);
-  if (e.z) e.z[static_cast<size_t>(t) * e.ldz + f] = bf16_down(v);
-  v = act_value(v, e.act);
-  const size_t ro = static_cast<size_t>(t) * e.ldr + f, oo = static_cast<size_t>(t) * e.ldo + f;
-  if (e.out_f32) {
-    if (e.res) v += static_cast<const float*>(e.res)[ro];
-    static_cast<float*>(e.out)[oo] = v;
-  } else {
-    if (e.res) v += bf16_up(static_cast<const uint16_t*>(e.res)[ro]);
-    static_cast<uint16_t*>(e.out)[oo] = bf16_down(v);
-  }
-}
-
-// Column f of N rows t0, t0 + step, ... (those with on[i]); b: the column's bias.  All
-// residuals are loaded before the first store, which might alias them.
+// Column f of N rows t0, t0 + step, ... (those with on[i]) in two steps, so that the
+// residuals (which the output might alias) can be loaded long before they are needed and all
+// before the first store.  b: the column's bias.
 template <int N>
-__device__ __forceinline__ void emit_column(const Epi& e, int t0, int step, int f, float b,
-                                            const bool (&on)[N], float (&v)[N]) {
-  float r[N];
+__device__ __forceinline__ void load_column(const Epi& e, int t0, int step, int f,
+                                            const bool (&on)[N], float (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     r[i] = 0.f;
@@ -119,8 +104,14 @@ __device__ __forceinline__ void emit_column(const Epi& e, int t0, int step, int 
       r[i] = e.out_f32 ? static_cast<const float*>(e.res)[at]
                        : bf16_up(static_cast<const uint16_t*>(e.res)[at]);
     }
-    v[i] += b;
   }
+}
+template <int N>
+__device__ __forceinline__ void emit_column(const Epi& e, int t0, int step, int f, float b,
+                                            const bool (&on)[N], const float (&r)[N],
+                                            float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] += b;
   if (e.z) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -137,20 +128,50 @@ __device__ __forceinline__ void emit_column(const Epi& e, int t0, int step, int 
   }
 }
 
-// 32 consecutive columns f0.. of row t, as whole vectors (f0 + 32 <= F).
-__device__ __forceinline__ void emit_row32(const Epi& e, int t, int f0, float (&v)[32]) {
+// 32 bytes at once: a whole sector of a row (p 32-byte aligned).
+__device__ __forceinline__ void ld_sector(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// 32 columns from f0 of a row of F: n = how many of them there are, whole sectors.
+__device__ __forceinline__ void st_bf16x32(uint16_t* p, const float (&v)[32], int n) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bf16_pair(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
+    if (16 * h < n) st_sector(p + 16 * h, w);
+  }
+}
+
+// The next 32 columns' residual, loaded ahead where it is bf16 (two sectors) ...
+struct RowRes {
+  uint32_t w[2][8];
+};
+__device__ __forceinline__ void load_row32(const Epi& e, int t, int f0, int n, RowRes& r) {
+  if (!e.res || e.out_f32) return;
+  const uint16_t* p = static_cast<const uint16_t*>(e.res) + static_cast<size_t>(t) * e.ldr + f0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (16 * h < n) ld_sector(p + 16 * h, r.w[h]);
+}
+// ... and the outputs.
+__device__ __forceinline__ void emit_row32(const Epi& e, int t, int f0, int n, const RowRes& r,
+                                           float (&v)[32]) {
   if (e.bias) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += bias_at(e, f0 + i);
+    for (int i = 0; i < 32; ++i)
+      if (i < n) v[i] += bias_at(e, f0 + i);
   }
-  if (e.z) {
-    uint4* zp = reinterpret_cast<uint4*>(e.z + static_cast<size_t>(t) * e.ldz + f0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      zp[i] = make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
-                         bf16_pair(v[8 * i + 4], v[8 * i + 5]),
-                         bf16_pair(v[8 * i + 6], v[8 * i + 7]));
-  }
+  if (e.z) st_bf16x32(e.z + static_cast<size_t>(t) * e.ldz + f0, v, n);
   if (e.act == MOE_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
@@ -161,40 +182,31 @@ __device__ __forceinline__ void emit_row32(const Epi& e, int t, int f0, float (&
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
   }
-  const size_t ro = static_cast<size_t>(t) * e.ldr + f0, oo = static_cast<size_t>(t) * e.ldo + f0;
+  const size_t at = static_cast<size_t>(t) * e.ldo + f0;
   if (e.out_f32) {
-    if (e.res) {
-      const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(e.res) + ro);
+    const float* rp = static_cast<const float*>(e.res) + static_cast<size_t>(t) * e.ldr + f0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 x = r[i];
-        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[8];
+      if (8 * i < n) {
+        if (e.res) ld_sector(rp + 8 * i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j] = __float_as_uint(v[8 * i + j] + (e.res ? __uint_as_float(w[j]) : 0.f));
+        st_sector(static_cast<float*>(e.out) + at + 8 * i, w);
       }
     }
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(e.out) + oo);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   } else {
     if (e.res) {
-      const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.res) + ro);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = r[i];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int j = 0; j < 8; ++j) {
+          v[16 * i + 2 * j] += __uint_as_float(r.w[i][j] << 16);
+          v[16 * i + 2 * j + 1] += __uint_as_float(r.w[i][j] & 0xFFFF0000u);
         }
-      }
     }
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + oo);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
-                        bf16_pair(v[8 * i + 4], v[8 * i + 5]),
-                        bf16_pair(v[8 * i + 6], v[8 * i + 7]));
+    st_bf16x32(static_cast<uint16_t*>(e.out) + at, v, n);
   }
 }
 
@@ -223,7 +235,9 @@ constexpr int kPStageBytes = 2 * kPOpBytes;
 constexpr int kPOffBar = kPStages * kPStageBytes;
 // full[S], empty[S], acc_full[2], acc_empty[2], drain
 constexpr int kPOffMisc = kPOffBar + (2 * kPStages + 5) * 8;
-constexpr int kPSmem = kPOffMisc + 16;
+constexpr int kPOffTurn = kPOffMisc + 16;  // eight epilogue warps' 32 x 33 blocks (not kWhole)
+constexpr int kPSmem = kPOffTurn + 8 * 32 * 33 * 4;
+static_assert(kPSmem <= 232448, "dynamic shared memory of one CTA");
 // Tiles are walked in bands of this many output rows' tiles, column by column, so that the
 // tiles in flight share both operands' blocks in L2.
 constexpr int kPBand = 8;
@@ -244,7 +258,11 @@ __device__ __forceinline__ PairTile pair_tile(int L, int tiles_t, int tiles_f) {
 
 // CTA r of a pair: output rows 128 r.. of the tile (its P rows and accumulator lanes) and Q
 // rows 128 r.. (half of the MMA's N side).
-__global__ void __launch_bounds__(256, 1)
+constexpr int kPThreads = 384;  // TMA warp, MMA warp, two idle, eight epilogue warps
+
+// kWhole: the output's rows (and the residual's and z's) are whole 32-byte sectors.
+template <bool kWhole>
+__global__ void __launch_bounds__(kPThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                   const LinearParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -265,7 +283,7 @@ __global__ void __launch_bounds__(256, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);
+      mbar_init(&acc_empty[b], 16);  // two CTAs' eight epilogue warps
     }
     mbar_init(drain, 1);
     // swizzled tiles need a 1024-byte aligned base: a misaligned one makes every role a
@@ -366,37 +384,71 @@ __global__ void __launch_bounds__(256, 1)
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp - 4;
+    // eight warps: four for the accumulator's lanes, twice for halves of its columns
+    const int q = warp & 3, half = (warp - 4) >> 2;
     uint32_t tc = 0;
     for (int L = cl; L < total; L += ncl, ++tc) {  // (an abort makes the wait fail)
       const PairTile tl = pair_tile(L, tiles_t, tiles_f);
       const uint32_t b = tc & 1u, use = tc >> 1;
+      const int t = tl.t0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int f0 = tl.f0 + half * (kPTile / 2);
+      const int cols = p.F - f0 < kPTile / 2 ? p.F - f0 : kPTile / 2;
+      // the next 32 columns' residual is in flight under these columns' stores, the first
+      // ones' under the tile's last MMAs
+      RowRes res;
+      if (kWhole && t < p.R) load_row32(p.e, t, f0, cols, res);
       int w_ok = 1;
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
       tc_fence_after();
-      const int t = tl.t0 + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kPTile;
-      for (int c = 0; c < kPTile && tl.f0 + c < p.F; c += 32) {
+      const uint32_t acc =
+          tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kPTile + half * (kPTile / 2);
+      for (int c = 0; c < cols; c += 32) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(acc + c, r);
         tmem_ld_wait();
-        if (t < p.R) {
-          const int f = tl.f0 + c;
-          float v[32];
+        if constexpr (kWhole) {
+          const RowRes now = res;
+          if (t < p.R) {
+            if (c + 32 < cols) load_row32(p.e, t, f0 + c + 32, cols - c - 32, res);
+            float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (p.e.vec && f + 32 <= p.F) {
-            emit_row32(p.e, t, f, v);
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < 32 && f + i < p.F; ++i) {
-              float x = v[0];
-#pragma unroll
-              for (int j = 1; j < 32; ++j) x = i == j ? v[j] : x;
-              emit_one(p.e, t, f + i, x);
-            }
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            emit_row32(p.e, t, f0 + c, cols - c, now, v);
           }
+        } else {
+          // the 32 x 32 block turned in shared memory, so that a warp stores 32 consecutive
+          // values of a row
+          float* turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * 32 * 33;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = __uint_as_float(r[i]);
+          __syncwarp();
+          const int tw = t - lane, fc = f0 + c + lane;
+          const bool live = fc < p.F;
+          const float bias = p.e.bias && live ? bias_at(p.e, fc) : 0.f;
+          constexpr int kRows = 16;
+          float next[kRows];
+          bool on[kRows];
+          auto fetch = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) on[j] = live && tw + i + j < p.R;
+            load_column<kRows>(p.e, tw + i, 1, fc, on, next);
+          };
+          fetch(0);
+#pragma unroll 1
+          for (int i = 0; i < 32 && tw + i < p.R; i += kRows) {
+            float v[kRows], rr[kRows];
+            bool here[kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+              v[j] = turn[(i + j) * 33 + lane];
+              rr[j] = next[j];
+              here[j] = on[j];
+            }
+            if (i + kRows < 32) fetch(i + kRows);
+            emit_column<kRows>(p.e, tw + i, 1, fc, bias, here, rr, v);
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -420,7 +472,7 @@ __global__ void __launch_bounds__(256, 1)
 
 // ---------------------------------------------------------------- split contraction --
 
-#define SLOTS 304
+#define FORCE 0
 constexpr int kSFeat = 128;  // features per tile
 
 template <int NT>
@@ -538,61 +590,68 @@ __global__ void __launch_bounds__(256, 2)
     }
   }
   __syncwarp();
-  // Epilogue: a thread has one feature; warps 4-7 read the accumulator.
-  const int q = warp & 3;
+  // Epilogue: a thread has one feature, four warps the tile's 128, eight warps two sets of
+  // tokens.  What the contraction does not decide (bias, the first residuals) is loaded
+  // before the wait for it.
+  const int q = warp & 3, set = warp >> 2;
   const int fl = q * 32 + lane, f = f0 + fl;
+  const bool live = f < p.F;
   const int nt = p.R - t0 < NT ? p.R - t0 : NT;
-  const float bias = p.e.bias && f < p.F ? bias_at(p.e, f) : 0.f;
+  const float bias = p.e.bias && live ? bias_at(p.e, f) : 0.f;
+  const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+  // one CTA: tokens in blocks of kTok, alternating between the sets
+  // a cluster: tokens part + splits * (set + 2 i), kTok of them at a time
+  // (kTok = 16 makes the code so long that fetching it costs a single token 2 us)
+  constexpr int kTok = 8;
+  const bool alone = splits == 1;
+  const int step = alone ? 1 : 2 * splits, first = alone ? set * kTok : part + set * splits;
+  const int block = alone ? 2 * kTok : kTok * step;
+  float res[kTok];
+  bool on[kTok];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) on[i] = live && j0 + i * step < nt;
+    load_column<kTok>(p.e, t0 + j0, step, f, on, res);
+  };
+  fetch(first);
+  int w_ok = 1;
+  if (lane == 0) w_ok = mbar_wait(acc_full, 0, p.status, abort_flag);
+  w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
+  tc_fence_after();
   float* sums = reinterpret_cast<float*>(smem);  // [NT][128], in the drained ring
-  if (warp >= 4) {
-    int w_ok = 1;
-    if (lane == 0) w_ok = mbar_wait(acc_full, 0, p.status, abort_flag);
-    w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
-    tc_fence_after();
-    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    for (int c = 0; c < nt && w_ok; c += 16) {
-      uint32_t r[16];
-      tmem_ld_32x32b_x16(acc + c, r);
+  if (!alone) {
+    for (int c = set * 8; c < nt && w_ok; c += 16) {
+      uint32_t r[8];
+      tmem_ld_32x32b_x8(acc + c, r);
       tmem_ld_wait();
-      if (splits == 1) {
-        float v[16];
-        bool on[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[i] = __uint_as_float(r[i]);
-          on[i] = f < p.F && c + i < nt;
-        }
-        emit_column<16>(p.e, t0 + c, 1, f, bias, on, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sums[(c + i) * kSFeat + fl] = __uint_as_float(r[i]);
-      }
+      for (int i = 0; i < 8; ++i) sums[(c + i) * kSFeat + fl] = __uint_as_float(r[i]);
     }
-  }
-  if (splits > 1) {
     cluster_sync();  // every CTA's partial sums are in place
-    // this CTA's tokens part, part + splits, ...: half of them for each four warps, kTok at
-    // a time, all of whose loads are in flight together
-    constexpr int kTok = 8;
-    const uint32_t mine = smem_u32(sums + fl);
-    for (int j0 = part + (warp >> 2) * splits; j0 < nt && f < p.F; j0 += 2 * kTok * splits) {
-      float v[kTok];
-      bool on[kTok];
+  }
+  for (int j0 = first; j0 < nt && w_ok; j0 += block) {
+    float v[kTok];
+    if (alone) {
+      uint32_t r[8];
+      tmem_ld_32x32b_x8(acc + j0, r);
+      tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        v[i] = 0.f;
-        on[i] = j0 + i * 2 * splits < nt;
-      }
+      for (int i = 0; i < kTok; ++i) v[i] = __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) v[i] = 0.f;
+      const uint32_t mine = smem_u32(sums + j0 * kSFeat + fl);
       for (int r = 0; r < splits; ++r) {
-        const uint32_t at = mapa_shared(mine, r) + j0 * kSFeat * 4;
+        const uint32_t at = mapa_shared(mine, r);
 #pragma unroll
         for (int i = 0; i < kTok; ++i)
-          if (on[i]) v[i] += ld_shared_cluster(at + i * 2 * splits * kSFeat * 4);
+          if (j0 + i * step < nt) v[i] += ld_shared_cluster(at + i * step * kSFeat * 4);
       }
-      emit_column<kTok>(p.e, t0 + j0, 2 * splits, f, bias, on, v);
     }
-    cluster_sync();  // no CTA leaves while its sums are read
+    emit_column<kTok>(p.e, t0 + j0, step, f, bias, on, res, v);
+    if (j0 + block < nt) fetch(j0 + block);
   }
+  if (!alone) cluster_sync();  // no CTA leaves while its sums are read
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -687,6 +746,8 @@ __global__ void __launch_bounds__(128)
 
 // ---------------------------------------------------------------- host side ----------
 
+bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 bool encode(CUtensorMap* m, const Operand& o, int C, int box_rows) {
   EncodeTiledFn enc = get_encode_tiled_fn();
   if (!enc) return false;
@@ -707,7 +768,7 @@ struct KernelState {
 };
 
 cudaError_t launch_cluster(const void* kern, KernelState& ks, int smem, int cluster, dim3 grid,
-                           bool persistent, cudaStream_t st, void** args) {
+                           int threads, bool persistent, cudaStream_t st, void** args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -720,7 +781,7 @@ cudaError_t launch_cluster(const void* kern, KernelState& ks, int smem, int clus
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -758,9 +819,10 @@ cudaError_t launch_split(const Operand& P, const Operand& Q, const LinearParams&
   if (grid.y > 65535 || grid.z > 65535) return cudaErrorInvalidValue;
   void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
   return launch_cluster(reinterpret_cast<const void*>(k_linear_split<NT>), ks, SplitCfg<NT>::kSmem,
-                        splits, grid, false, st, args);
+                        splits, grid, 256, false, st, args);
 }
 
+template <bool kWhole>
 cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearParams& p,
                               cudaStream_t st) {
   static KernelState ks;
@@ -770,30 +832,60 @@ cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearPa
                           ((p.F + kPTile - 1) / kPTile);
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
   void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
-  return launch_cluster(reinterpret_cast<const void*>(k_linear_pair), ks, kPSmem, 2,
-                        dim3(static_cast<unsigned>(2 * tiles)), true, st, args);
+  return launch_cluster(reinterpret_cast<const void*>(k_linear_pair<kWhole>), ks,
+                        kWhole ? kPOffTurn : kPSmem, 2,
+                        dim3(static_cast<unsigned>(2 * tiles)), kPThreads, true, st, args);
 }
 
-// One product.  Time of a 256 x 256 pair tile = 1: a wave of pairs takes 1 for up to 76
-// tiles; a 128 x 128 tile takes one SM half as long, and with the contraction split the
-// waves come in finer steps.
+// One product, on the kernel and tile that should take the least time, by costs measured on
+// GB300 (us).  A pair tile: 0.29 per 64 columns of c, 76 tiles at a time, a tile's epilogue
+// (6 with whole rows, 15 without) under the next tile's MMAs.  Split tiles: the loads of all
+// at 12.5 TB/s from L2, W's at 6.9 from HBM, one CTA's stages 0.35 each, 304 CTAs at a time;
+// then 1.3 per 8 tokens of a thread's epilogue, 0.8 for the cluster, 3.5 for the launch.
+// Both sides: 7168 x 7168 weights, 128 rows: pairs 38, split 28; 192: 39, 41; 512: 40, 67;
+// 1024 x 1024 x 8192: 42, 25; 300 x 1024 x 256: 7.6, 7.4; 8192 x 256 x 1024: 11.5, 17.8.
+struct Choice {
+  double us;
+  int nt, splits;  // nt = 0: pairs
+};
+Choice choose(int R, int F, int C, bool p_mn, bool whole) {
+  const int nk = (C + kBK - 1) / kBK;
+  const long long tiles =
+      static_cast<long long>((R + kPTile - 1) / kPTile) * ((F + kPTile - 1) / kPTile);
+  const double waves = static_cast<double>((tiles + 75) / 76);
+  const double mma = 0.29 * nk, epi = whole ? 6.0 : 15.0;
+  Choice best = {(waves - 1) * (mma > epi ? mma : epi) + mma + epi, 0, 1};
+  if (FORCE == 2) best.us = 1e30;
+  if (FORCE == 1) return best;
+  const long long ft = (F + kSFeat - 1) / kSFeat;
+  for (int nt = p_mn ? 64 : 16; nt <= 128; nt *= 2) {
+    const long long tt = (R + nt - 1) / nt;
+    if (tt > 65535 || ft > 65535) continue;
+    const int rows = R < nt ? R : nt;
+    const double l2 = ft * tt * static_cast<double>(nk) * (kSFeat + nt) * kRowBytes / 12.5e6;
+    const double hbm = static_cast<double>(F) * C * 2 / 6.9e6;
+    for (int splits = 1; splits <= 8 && splits <= nk; ++splits) {
+      const double w = static_cast<double>((ft * tt * splits + 303) / 304);
+      const double chain = w * 0.35 * ((nk + splits - 1) / splits);
+      double us = l2 > hbm ? l2 : hbm;
+      us = (us > chain ? us : chain) + 0.1 * chain + 3.5 + (splits > 1 ? 0.8 : 0.0) +
+           w * 1.3 * ((rows + 16 * splits - 1) / (16 * splits));
+      if (us < best.us) best = {us, nt, splits};
+    }
+  }
+  return best;
+}
+
 cudaError_t product(const Operand& P, const Operand& Q, const LinearParams& p, cudaStream_t st) {
-  const long long tiles = static_cast<long long>((p.R + kPTile - 1) / kPTile) *
-                          ((p.F + kPTile - 1) / kPTile);
-  const int nk = (p.C + kBK - 1) / kBK;
-  if (tiles >= 76) return launch_pair_tiles(P, Q, p, st);
-  const int nt = p.p_mn ? (p.R <= 64 ? 64 : 128)
-                        : p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
-  const long long items = static_cast<long long>((p.F + kSFeat - 1) / kSFeat) *
-                          ((p.R + nt - 1) / nt);
-  int splits = static_cast<int>(SLOTS / items);
-  splits = splits > nk / 4 ? nk / 4 : splits;
-  splits = splits > 8 ? 8 : splits < 1 ? 1 : splits;
-  switch (nt) {
-    case 16: return launch_split<16>(P, Q, p, splits, st);
-    case 32: return launch_split<32>(P, Q, p, splits, st);
-    case 64: return launch_split<64>(P, Q, p, splits, st);
-    default: return launch_split<128>(P, Q, p, splits, st);
+  const Choice c = choose(p.R, p.F, p.C, p.p_mn, p.e.whole);
+  switch (c.nt) {
+    case 0:
+      return p.e.whole ? launch_pair_tiles<true>(P, Q, p, st)
+                       : launch_pair_tiles<false>(P, Q, p, st);
+    case 16: return launch_split<16>(P, Q, p, c.splits, st);
+    case 32: return launch_split<32>(P, Q, p, c.splits, st);
+    case 64: return launch_split<64>(P, Q, p, c.splits, st);
+    default: return launch_split<128>(P, Q, p, c.splits, st);
   }
 }
 
@@ -822,10 +914,12 @@ cudaError_t launch_linear(const LinearCall& a, cudaStream_t st) {
   const Repack rp = repack(P, a.K, a.x_pad), rq = repack(Q, a.K, a.w_pad);
   const cudaError_t e = run_repack(rp, rq, st);
   if (e != cudaSuccess) return e;
-  const int ow = a.y_f32 ? 4 : 8;  // elements in 16 bytes
   LinearParams p = {a.M, a.N, a.K, 0, 0, {}, a.status};
   p.e = {a.bias, a.res, a.y, a.z, a.ldr, a.ldy, a.ldz, a.bias_f32, a.y_f32, a.act, 0};
-  p.e.vec = a.ldy % ow == 0 && (!a.res || a.ldr % ow == 0) && (!a.z || a.ldz % 8 == 0);
+  const int ow = a.y_f32 && !a.z ? 8 : 16;  // columns in whole sectors of every matrix
+  p.e.whole = a.N % ow == 0 && a.ldy % ow == 0 && on32(a.y) &&
+              (!a.res || (a.ldr % ow == 0 && on32(a.res))) &&
+              (!a.z || (a.ldz % ow == 0 && on32(a.z)));
   return product(P, Q, p, st);
 }
 
@@ -862,13 +956,15 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (a.dx) {
     LinearParams p = {a.M, a.K, a.N, 0, 1, {}, a.status};
-    p.e = {nullptr, nullptr, a.dx, nullptr, 0, a.lddx, 0, 0, 0, MOE_ACT_NONE, a.lddx % 8 == 0};
+    p.e = {nullptr, nullptr, a.dx, nullptr, 0, a.lddx, 0, 0, 0, MOE_ACT_NONE,
+           a.K % 16 == 0 && on32(a.dx)};
     e = product({dz, ldz, a.M, 0}, w, p, st);
     if (e != cudaSuccess) return e;
   }
   if (a.dw) {
     LinearParams p = {a.N, a.K, a.M, 1, 1, {}, a.status};
-    p.e = {nullptr, nullptr, a.dw, nullptr, 0, a.lddw, 0, 0, 0, MOE_ACT_NONE, a.lddw % 8 == 0};
+    p.e = {nullptr, nullptr, a.dw, nullptr, 0, a.lddw, 0, 0, 0, MOE_ACT_NONE,
+           a.K % 16 == 0 && on32(a.dw)};
     e = product({dz, ldz, a.N, 1}, x, p, st);
   }
   return e;
