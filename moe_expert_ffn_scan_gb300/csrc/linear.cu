@@ -97,13 +97,19 @@ template <int N>
 __device__ __forceinline__ void load_column(const Epi& e, int t0, int step, int f,
                                             const bool (&on)[N], float (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    r[i] = 0.f;
-    if (e.res && on[i]) {
-      const size_t at = static_cast<size_t>(t0 + i * step) * e.ldr + f;
-      r[i] = e.out_f32 ? static_cast<const float*>(e.res)[at]
-                       : bf16_up(static_cast<const uint16_t*>(e.res)[at]);
-    }
+  for (int i = 0; i < N; ++i) r[i] = 0.f;
+  if (!e.res) return;
+  const long long at = t0 * e.ldr + f, inc = step * e.ldr;
+  if (e.out_f32) {
+    const float* p = static_cast<const float*>(e.res) + at;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) r[i] = p[i * inc];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(e.res) + at;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) r[i] = bf16_up(p[i * inc]);
   }
 }
 template <int N>
@@ -113,18 +119,27 @@ __device__ __forceinline__ void emit_column(const Epi& e, int t0, int step, int 
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] += b;
   if (e.z) {
+    uint16_t* p = e.z + t0 * e.ldz + f;
+    const long long inc = step * e.ldz;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (on[i]) e.z[static_cast<size_t>(t0 + i * step) * e.ldz + f] = bf16_down(v[i]);
+      if (on[i]) p[i * inc] = bf16_down(v[i]);
   }
+  if (e.act != MOE_ACT_NONE) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float y = act_value(v[i], e.act) + r[i];
-    if (on[i]) {
-      const size_t at = static_cast<size_t>(t0 + i * step) * e.ldo + f;
-      if (e.out_f32) static_cast<float*>(e.out)[at] = y;
-      else static_cast<uint16_t*>(e.out)[at] = bf16_down(y);
-    }
+    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], e.act);
+  }
+  const long long at = t0 * e.ldo + f, inc = step * e.ldo;
+  if (e.out_f32) {
+    float* p = static_cast<float*>(e.out) + at;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) p[i * inc] = v[i] + r[i];
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(e.out) + at;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (on[i]) p[i * inc] = bf16_down(v[i] + r[i]);
   }
 }
 
@@ -424,29 +439,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = __uint_as_float(r[i]);
           __syncwarp();
           const int tw = t - lane, fc = f0 + c + lane;
-          const bool live = fc < p.F;
-          const float bias = p.e.bias && live ? bias_at(p.e, fc) : 0.f;
-          constexpr int kRows = 16;
-          float next[kRows];
-          bool on[kRows];
-          auto fetch = [&](int i) {
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) on[j] = live && tw + i + j < p.R;
-            load_column<kRows>(p.e, tw + i, 1, fc, on, next);
-          };
-          fetch(0);
+          const int rows = fc < p.F ? p.R - tw : 0;  // this lane's, from tw
+          const float bias = p.e.bias && rows > 0 ? bias_at(p.e, fc) : 0.f;
+          constexpr int kRows = 16;  // (8: a sixth slower; 32: out of registers)
 #pragma unroll 1
-          for (int i = 0; i < 32 && tw + i < p.R; i += kRows) {
+          for (int i = 0; i < 32; i += kRows) {
             float v[kRows], rr[kRows];
-            bool here[kRows];
+            bool on[kRows];
 #pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-              v[j] = turn[(i + j) * 33 + lane];
-              rr[j] = next[j];
-              here[j] = on[j];
-            }
-            if (i + kRows < 32) fetch(i + kRows);
-            emit_column<kRows>(p.e, tw + i, 1, fc, bias, here, rr, v);
+            for (int j = 0; j < kRows; ++j) on[j] = i + j < rows;
+            load_column<kRows>(p.e, tw + i, 1, fc, on, rr);
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) v[j] = turn[(i + j) * 33 + lane];
+            emit_column<kRows>(p.e, tw + i, 1, fc, bias, on, rr, v);
           }
           __syncwarp();
         }
@@ -472,7 +477,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
 // ---------------------------------------------------------------- split contraction --
 
-#define FORCE 0
 constexpr int kSFeat = 128;  // features per tile
 
 template <int NT>
@@ -641,11 +645,22 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
       for (int i = 0; i < kTok; ++i) v[i] = 0.f;
       const uint32_t mine = smem_u32(sums + j0 * kSFeat + fl);
-      for (int r = 0; r < splits; ++r) {
-        const uint32_t at = mapa_shared(mine, r);
+      for (int r0 = 0; r0 < splits; r0 += 4) {  // four CTAs' sums in flight
+        float u[4][kTok];
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-          if (j0 + i * step < nt) v[i] += ld_shared_cluster(at + i * step * kSFeat * 4);
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t at = mapa_shared(mine, r0 + r < splits ? r0 + r : 0);
+#pragma unroll
+          for (int i = 0; i < kTok; ++i) {
+            u[r][i] = 0.f;
+            if (r0 + r < splits && j0 + i * step < nt)
+              u[r][i] = ld_shared_cluster(at + i * step * kSFeat * 4);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < kTok; ++i) v[i] += u[r][i];
       }
     }
     emit_column<kTok>(p.e, t0 + j0, step, f, bias, on, res, v);
@@ -675,18 +690,31 @@ __global__ void __launch_bounds__(256) k_repack(const Repack a, const Repack b) 
   pdl_wait();
   pdl_trigger();
   const Repack m = blockIdx.y ? b : a;
+  // two values a thread: a destination word from one source word, or where the row starts on
+  // an odd value from the halves of two (5001 x 5001: 30 us; value by value 50)
+  const int full = (m.cols - 1) / 2;  // words with a value of the row behind them
   for (int r = blockIdx.x; r < m.rows; r += gridDim.x) {
     const uint16_t* src = m.src + static_cast<size_t>(r) * m.lds;
-    uint16_t* dst = m.dst + static_cast<size_t>(r) * m.ldd;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(m.dst + static_cast<size_t>(r) * m.ldd);
+    const bool odd = (reinterpret_cast<uintptr_t>(src) & 2) != 0;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(src - (odd ? 1 : 0));
+    if (odd) {
 #pragma unroll 4
-    for (int c = threadIdx.x; c < m.cols; c += 256) dst[c] = src[c];
+      for (int w = threadIdx.x; w < full; w += 256)
+        dst[w] = __funnelshift_r(words[w], words[w + 1], 16);
+    } else {
+#pragma unroll 4
+      for (int w = threadIdx.x; w < full; w += 256) dst[w] = words[w];
+    }
+    if (threadIdx.x == 0)  // the last one or two values, and nothing past the row
+      for (int c = full * 2; c < m.cols; ++c) reinterpret_cast<uint16_t*>(dst)[c] = src[c];
   }
 }
 
 // dz = bf16(dy * act'(z)) (the products take bf16 operands; the rounding is 2^-9 of each
 // element), and with part the column sums of the unrounded values over rows [blockIdx.y *
 // per, + per): a thread owns VEC columns.  dz null: only the sums.  Memory-bound: VEC = 8
-// where all rows are whole 16-byte vectors (4096 x 6144: DZ_NOW us; two columns a thread 63).
+// where all rows are whole 16-byte vectors (4096 x 6144: 30 us; two columns a thread 63).
 template <int VEC>
 __global__ void __launch_bounds__(128)
     k_linear_dz(const uint16_t* __restrict__ dy, long long ldy, const uint16_t* __restrict__ z,
@@ -839,11 +867,13 @@ cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearPa
 
 // One product, on the kernel and tile that should take the least time, by costs measured on
 // GB300 (us).  A pair tile: 0.29 per 64 columns of c, 76 tiles at a time, a tile's epilogue
-// (6 with whole rows, 15 without) under the next tile's MMAs.  Split tiles: the loads of all
-// at 12.5 TB/s from L2, W's at 6.9 from HBM, one CTA's stages 0.35 each, 304 CTAs at a time;
-// then 1.3 per 8 tokens of a thread's epilogue, 0.8 for the cluster, 3.5 for the launch.
-// Both sides: 7168 x 7168 weights, 128 rows: pairs 38, split 28; 192: 39, 41; 512: 40, 67;
-// 1024 x 1024 x 8192: 42, 25; 300 x 1024 x 256: 7.6, 7.4; 8192 x 256 x 1024: 11.5, 17.8.
+// (6.3 with whole rows, 18 without) under the next tile's MMAs.  Split tiles: their loads
+// together at 12.5 TB/s from L2, W's at 6.9 from HBM, a CTA's stages 0.27 to 0.41 each; per
+// wave of 304 CTAs 3 for launch and first load, 0.87 per 16 tokens of a CTA's epilogue and
+// 0.02 per token that a cluster exchanges.  Clusters of 3, 5 and 6 fit the GPU's partitions
+// badly (7 x 7168 x 7168 in 4 parts 20.2, in 5 20.9, in 6 27.4) and are not used.
+// Both sides: 7168 x 7168 weights, 128 rows: pairs 38, split 26.5; 192: 39, 41; 512: 40, 67;
+// 1024 x 1024 x 8192: 42, 25; 300 x 1024 x 256: 7.6, 4.4; 8192 x 256 x 1024: 11.5, 17.8.
 struct Choice {
   double us;
   int nt, splits;  // nt = 0: pairs
@@ -853,10 +883,8 @@ Choice choose(int R, int F, int C, bool p_mn, bool whole) {
   const long long tiles =
       static_cast<long long>((R + kPTile - 1) / kPTile) * ((F + kPTile - 1) / kPTile);
   const double waves = static_cast<double>((tiles + 75) / 76);
-  const double mma = 0.29 * nk, epi = whole ? 6.0 : 15.0;
+  const double mma = 0.29 * nk, epi = whole ? 6.3 : 18.0;
   Choice best = {(waves - 1) * (mma > epi ? mma : epi) + mma + epi, 0, 1};
-  if (FORCE == 2) best.us = 1e30;
-  if (FORCE == 1) return best;
   const long long ft = (F + kSFeat - 1) / kSFeat;
   for (int nt = p_mn ? 64 : 16; nt <= 128; nt *= 2) {
     const long long tt = (R + nt - 1) / nt;
@@ -864,12 +892,14 @@ Choice choose(int R, int F, int C, bool p_mn, bool whole) {
     const int rows = R < nt ? R : nt;
     const double l2 = ft * tt * static_cast<double>(nk) * (kSFeat + nt) * kRowBytes / 12.5e6;
     const double hbm = static_cast<double>(F) * C * 2 / 6.9e6;
-    for (int splits = 1; splits <= 8 && splits <= nk; ++splits) {
+    const double stage = nt == 128 ? 0.41 : nt == 64 ? 0.31 : 0.27;
+    for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
       const double w = static_cast<double>((ft * tt * splits + 303) / 304);
-      const double chain = w * 0.35 * ((nk + splits - 1) / splits);
+      const double chain = w * stage * ((nk + splits - 1) / splits);
       double us = l2 > hbm ? l2 : hbm;
-      us = (us > chain ? us : chain) + 0.1 * chain + 3.5 + (splits > 1 ? 0.8 : 0.0) +
-           w * 1.3 * ((rows + 16 * splits - 1) / (16 * splits));
+      us = (us > chain ? us : chain) + 0.1 * chain + (splits == 8 ? 2.0 : 0.0) +
+           w * (3.0 + 0.87 * ((rows + 16 * splits - 1) / (16 * splits)) +
+                (splits > 1 ? 0.2 + 0.02 * rows : 0.0));
       if (us < best.us) best = {us, nt, splits};
     }
   }
@@ -933,8 +963,8 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st) {
     const uint16_t* z = a.act == MOE_ACT_NONE ? nullptr : a.z;
     const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && (!z || a.ldz % 8 == 0);
     const int blocks = (a.N + (vec ? 1023 : 127)) / (vec ? 1024 : 128);
-    // row blocks: about four CTAs of 128 threads per SM
-    int parts = (608 + blocks - 1) / blocks;
+    // row blocks: about 8 CTAs of 128 threads per SM (4: 53 us)
+    int parts = (152 * 8 + blocks - 1) / blocks;
     parts = parts > kLinearDbParts ? kLinearDbParts : parts;
     const int per = (a.M + parts - 1) / parts;
     parts = (a.M + per - 1) / per;
