@@ -184,17 +184,24 @@ def _raw_stream(stream):
     """_stream for calls short enough for its cost to show (tensors exist: CUDA is up)."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _current_raw_stream(_current_device())
+
+
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
 def _t(t, dtype, shape, name):
     """_p of a tensor whose type and shape are checked first (None stays None)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    return _p(t)
+    return _p(t)  # raises
 
 
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}  # MOE_DTYPE_*

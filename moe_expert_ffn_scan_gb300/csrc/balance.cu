@@ -32,23 +32,30 @@ __device__ __forceinline__ float exp_diff(float v, float m) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((v - m) * 1.44269504f));
   return r;
 }
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float warp_sum(float v) {
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (LPR == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
-// A lane's experts: VEC consecutive ones from lane * VEC + i * 32 * VEC.  Missing experts
-// read as -inf (probability 0).
-template <int NV, int VEC>
+// A lane's experts in a row over LPR lanes: VEC consecutive ones from (lane + i * LPR) *
+// VEC.  Missing experts read as -inf (probability 0).
+template <int NV, int VEC, int LPR>
 struct Row {
   float v[NV][VEC];
-  __device__ __forceinline__ static int at(int lane, int i) { return (i * 32 + lane) * VEC; }
+  __device__ __forceinline__ static int at(int lane, int i) { return (i * LPR + lane) * VEC; }
   __device__ __forceinline__ void load(const float* p, int E, int lane) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -62,6 +69,28 @@ struct Row {
       }
     }
   }
+  // The lane's own part of a row into shared memory, asynchronously, and out of it.
+  __device__ __forceinline__ static void fetch(float* slot, const float* p, int E, int lane) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at(lane, i) < E) {
+        if constexpr (VEC == 4) cp_async16(slot + at(lane, i), p + at(lane, i));
+        else cp_async4(slot + at(lane, i), p + at(lane, i));
+      }
+  }
+  __device__ __forceinline__ void take(const float* slot, int E, int lane) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = at(lane, i);
+      if constexpr (VEC == 4) {
+        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e < E) f = *reinterpret_cast<const float4*>(slot + e);
+        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+      } else {
+        v[i][0] = e < E ? slot[e] : -INFINITY;
+      }
+    }
+  }
   // v becomes exp(v - max) (a NaN or infinity leaves a NaN in the sum); returns the maximum.
   // A row of -inf alone has no probabilities: zeros.
   __device__ __forceinline__ float exps() {
@@ -70,7 +99,7 @@ struct Row {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) m = fmaxf(m, v[i][j]);
-    m = warp_max(m);
+    m = row_max<LPR>(m);
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -154,8 +183,9 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) acc[i][j] = 0.f;
     // one row ahead: its logits, mask and choices are in flight under this row's softmax
-    // (masked rows too: their values are loaded and dropped)
-    Row<NV, VEC> nx;
+    // (masked rows too: their values are loaded and dropped).  (16 lanes a token and a ring in
+    // shared memory, as in the gradient: the same 17 us for 32768 x 384, slower elsewhere.)
+    Row<NV, VEC, 32> nx;
     bool nx_on = false;
     int nx_e = -1;
     auto fetch = [&](int r) {
@@ -167,7 +197,7 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
     };
     fetch(r0 + warp);
     for (int r = r0 + warp; r < r1; r += W) {
-      Row<NV, VEC> x = nx;
+      Row<NV, VEC, 32> x = nx;
       const bool on = nx_on;
       const int e = nx_e;
       fetch(r + W);
@@ -178,7 +208,7 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
       }
       const float m = x.exps();
       float r1s;
-      const float lse = lse_of(m, warp_sum(x.total()), r1s);
+      const float lse = lse_of(m, row_sum<32>(x.total()), r1s);
       z = fmaf(lse, lse, z);
       ++n;
 #pragma unroll
@@ -190,7 +220,7 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const int e = Row<NV, VEC>::at(lane, i) + j;
+        const int e = Row<NV, VEC, 32>::at(lane, i) + j;
         if (e < E) dyn[warp * E + e] = acc[i][j];
       }
     if (lane == 0) zs[warp] = z, ns[warp] = n;
@@ -321,13 +351,14 @@ __global__ void __launch_bounds__(WARPS * 32)
   if (lane == 0) loss[s] = sum * (static_cast<float>(E) / static_cast<float>(k));
 }
 
-// CTAs per SM by the registers a lane's values take.
+// CTAs per SM: by the registers a lane's values take, and no more (32768 x 384 with three 26
+// us, with four 30: each row's lanes load their counts first, and few rows follow).
 __host__ __device__ constexpr int bwd_ctas_per_sm(int E) {
-  return E <= 384 ? 4 : E <= 512 ? 2 : 1;
+  return E <= 512 ? 2 : 1;
 }
 
-template <int NV, int VEC>
-__global__ void __launch_bounds__(kWarps * 32, bwd_ctas_per_sm(NV * VEC * 32))
+template <int NV, int VEC, int LPR>
+__global__ void __launch_bounds__(kWarps * 32, bwd_ctas_per_sm(NV * VEC * LPR))
     k_balance_bwd(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                   const int32_t* __restrict__ off, const uint8_t* __restrict__ mask,
                   const int32_t* __restrict__ counts, const int32_t* __restrict__ n_tokens,
@@ -336,45 +367,68 @@ __global__ void __launch_bounds__(kWarps * 32, bwd_ctas_per_sm(NV * VEC * 32))
                   float* __restrict__ dlogits) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ __align__(16) float dyn[];  // with dw: [kWarps][E], terms of the warp's row
+  using R = Row<NV, VEC, LPR>;
+  constexpr int RPW = 32 / LPR;  // rows a warp takes at once
+  extern __shared__ __align__(16) float dyn[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* mine = dyn + warp * E;
+  const int sub = lane / LPR, ll = lane % LPR;
+  // this row's lanes': [E] the chosen experts' terms (zero between rows; with dw)
+  float* mine = dyn + (warp * RPW + sub) * E;
+  // and the row that is on its way
+  float* next = dyn + (kWarps * RPW + warp * RPW + sub) * E;
   if (dw) {
-    for (int e = lane; e < E; e += 32) mine[e] = 0.f;
+    for (int e = ll; e < E; e += LPR) mine[e] = 0.f;
     __syncwarp();
   }
-  // a warp takes `per` consecutive rows, so that its sequence seldom changes
-  const long long first = (static_cast<long long>(blockIdx.x) * kWarps + warp) * per;
-  const int r0 = first < T ? static_cast<int>(first) : T;
-  const int r1 = T - r0 < per ? T : r0 + per;
-  if (r0 >= r1) return;
-  int s = seq_of(off, S, T, r0), have = -1;
+  // a CTA takes `per` * (its rows at once) consecutive rows, its rows at once side by side:
+  // few streams for HBM (each row's lanes on a stretch of their own: 26 us instead of 22),
+  // and the sequence seldom changes
+  constexpr int STEP = kWarps * RPW;
+  const long long begin = static_cast<long long>(blockIdx.x) * STEP * per;
+  const long long end = begin + static_cast<long long>(STEP) * per;
+  const int r0 = static_cast<int>(begin) + warp * RPW + sub;
+  const int r1 = end < T ? static_cast<int>(end) : T;
+  int s = r0 < r1 ? seq_of(off, S, T, r0) : 0, have = -1;
   int sb = seq_off(off, s, S, T), se = seq_off(off, s + 1, S, T);
-  float a[NV][VEC];
+  float a[NV][VEC] = {};
   float zc = 0.f;
-  for (int r = r0; r < r1; ++r) {
-    // (the other warps hide these loads; a row ahead in registers costs more of them: 26 us
-    // instead of 24 for 32768 x 384)
-    Row<NV, VEC> x;
-    x.load(logits + static_cast<size_t>(r) * E, E, lane);
-    const bool on = !mask || __ldg(mask + r) != 0;
-    int chosen = -1;
-    float g = 0.f;
-    if (dw && lane < k) {
-      chosen = __ldg(idx + static_cast<size_t>(r) * k + lane);
-      g = __ldg(dw + static_cast<size_t>(r) * k + lane);
+  auto fetch = [&](int r) {
+    if (r < r1) R::fetch(next, logits + static_cast<size_t>(r) * E, E, ll);
+    cp_async_commit();
+  };
+  int nx_e = -1;
+  float nx_g = 0.f;
+  auto fetch_choice = [&](int r) {
+    if (dw && r < r1 && ll < k) {
+      nx_e = __ldg(idx + static_cast<size_t>(r) * k + ll);
+      nx_g = __ldg(dw + static_cast<size_t>(r) * k + ll);
     }
-    while (r >= se && s + 1 < S) {
+  };
+  fetch(r0);
+  fetch_choice(r0);
+  // the lanes of a warp stay together: every row of the block, there or not
+  for (int i = 0; i < per; ++i) {
+    const int r = r0 + i * STEP;
+    const bool in = r < r1;
+    if (!__any_sync(0xFFFFFFFFu, in)) break;
+    while (in && r >= se && s + 1 < S) {
       ++s;
       sb = seq_off(off, s, S, T), se = seq_off(off, s + 1, S, T);
     }
-    float* out = dlogits + static_cast<size_t>(r) * E;
-    if (!on || r < sb || r >= se) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x.v[i][j] = 0.f;
-    } else {
+    const bool on = in && r >= sb && r < se && (!mask || __ldg(mask + r) != 0);
+    R x;
+    const int chosen = on ? nx_e : -1;
+    const float g = nx_g;
+    const bool use = static_cast<unsigned>(chosen) < static_cast<unsigned>(E);
+    float l = -INFINITY;  // lane j < k: the j-th chosen expert's logit
+    fetch_choice(r + STEP);
+    cp_async_wait<0>();
+    __syncwarp();
+    x.take(next, E, ll);
+    if (dw && use) l = next[chosen];
+    __syncwarp();
+    fetch(r + STEP);
+    if (on) {
       if (have != s) {
         have = s;
         const int n = __ldg(n_tokens + s);
@@ -384,115 +438,119 @@ __global__ void __launch_bounds__(kWarps * 32, bwd_ctas_per_sm(NV * VEC * 32))
                               : 0.f;
         zc = dz ? 2.f * __ldg(dz + s) * inv : 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int q = 0; q < NV; ++q)
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int e = Row<NV, VEC>::at(lane, i) + j;
-            a[i][j] = e < E ? f * static_cast<float>(__ldg(counts + static_cast<size_t>(s) * E + e))
+            const int e = R::at(ll, q) + j;
+            a[q][j] = e < E ? f * static_cast<float>(__ldg(counts + static_cast<size_t>(s) * E + e))
                             : 0.f;
           }
       }
-      const bool use = dw && lane < k && static_cast<unsigned>(chosen) < static_cast<unsigned>(E);
-      float delta = 0.f;
-      if (dw) {
-        // lane j < k: the j-th chosen expert's logit, weight and term
-        const float l = use ? __ldg(logits + static_cast<size_t>(r) * E + chosen) : -INFINITY;
-        const float m = warp_max(l);
-        const float w = use && m != -INFINITY ? exp_diff(l, m) : 0.f;
-        float ws = w, wg = use ? w * g : 0.f;
+    } else {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          ws += __shfl_xor_sync(0xFFFFFFFFu, ws, o);
-          wg += __shfl_xor_sync(0xFFFFFFFFu, wg, o);
-        }
-        const float q = ws != 0.f ? 1.f / ws : 0.f;
-        delta = use ? w * q * (g - wg * q) : 0.f;
-        // into the row's layout through shared memory (zero between rows); an expert listed
-        // twice gets both terms, in order
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, use ? chosen : -1 - lane);
-        if (__any_sync(0xFFFFFFFFu, same & (same - 1))) {
-          for (int j = 0; j < k; ++j) {
-            if (lane == j && use) mine[chosen] += delta;
-            __syncwarp();
-          }
-        } else {
-          if (use) mine[chosen] = delta;
+      for (int q = 0; q < NV; ++q)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x.v[q][j] = -INFINITY;
+    }
+    if (dw) {
+      // its weight and term
+      const float m = row_max<16>(l);
+      const float w = use && m != -INFINITY ? exp_diff(l, m) : 0.f;
+      const float ws = row_sum<16>(w), wg = row_sum<16>(use ? w * g : 0.f);
+      const float q = ws != 0.f ? __fdividef(1.f, ws) : 0.f;
+      const float delta = use ? w * q * (g - wg * q) : 0.f;
+      // into the row's layout through shared memory; an expert listed twice gets both terms,
+      // in order
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, use ? sub * 1024 + chosen : -1 - lane);
+      if (__any_sync(0xFFFFFFFFu, same & (same - 1))) {
+        for (int j = 0; j < k; ++j) {
+          if (ll == j && use) mine[chosen] += delta;
           __syncwarp();
         }
-      }
-      const float m = x.exps();
-      float dot = 0.f, sum = x.total();
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dot = fmaf(a[i][j], x.v[i][j], dot);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-      }
-      float inv;
-      const float lse = lse_of(m, sum, inv);
-      const float shift = zc * lse - dot * inv;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x.v[i][j] *= (a[i][j] + shift) * inv;
-      if (dw) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = Row<NV, VEC>::at(lane, i);
-          if (e < E) {
-            float term[VEC];
-            if constexpr (VEC == 4) {
-              const float4 f = *reinterpret_cast<const float4*>(mine + e);
-              term[0] = f.x, term[1] = f.y, term[2] = f.z, term[3] = f.w;
-            } else {
-              term[0] = mine[e];
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) x.v[i][j] += term[j];
-          }
-        }
-        __syncwarp();
-        if (use) mine[chosen] = 0.f;
+      } else {
+        if (use) mine[chosen] = delta;
         __syncwarp();
       }
     }
+    const float m = x.exps();
+    float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = Row<NV, VEC>::at(lane, i);
-      if (e < E) {
-        if constexpr (VEC == 4)
-          *reinterpret_cast<float4*>(out + e) =
-              make_float4(x.v[i][0], x.v[i][1], x.v[i][2], x.v[i][3]);
-        else
-          out[e] = x.v[i][0];
+    for (int q = 0; q < NV; ++q)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) dot = fmaf(a[q][j], x.v[q][j], dot);
+    const float sum = row_sum<LPR>(x.total());
+    dot = row_sum<LPR>(dot);
+    if (in) {
+      float inv;
+      const float lse = lse_of(m, sum, inv);
+      const float shift = zc * lse - dot * inv;
+      float* out = dlogits + static_cast<size_t>(r) * E;
+#pragma unroll
+      for (int q = 0; q < NV; ++q) {
+        const int e = R::at(ll, q);
+        if (e < E) {
+          float d[VEC];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            d[j] = on ? x.v[q][j] * ((a[q][j] + shift) * inv) : 0.f;
+          if constexpr (VEC == 4) {
+            if (dw) {
+              const float4 t = *reinterpret_cast<const float4*>(mine + e);
+              d[0] += t.x, d[1] += t.y, d[2] += t.z, d[3] += t.w;
+            }
+            *reinterpret_cast<float4*>(out + e) = make_float4(d[0], d[1], d[2], d[3]);
+          } else {
+            out[e] = d[0] + (dw ? mine[e] : 0.f);
+          }
+        }
       }
+    }
+    if (dw) {
+      __syncwarp();
+      if (use) mine[chosen] = 0.f;
+      __syncwarp();
     }
   }
 }
 
-// Calls f with the (NV, VEC) of E: vectors of 4 when rows are whole 16-byte vectors.
-template <int N>
-struct Num {
-  static constexpr int value = N;
+// Calls f with the (NV, VEC, LPR) of E: vectors of 4 when rows are whole 16-byte vectors.  In
+// the gradient a token takes 16 lanes while their registers allow (the row's sums, logarithm,
+// quotients and the chosen experts' terms then cost one instruction for two tokens).
+template <int NV_, int VEC_, int LPR_>
+struct Shape {
+  static constexpr int NV = NV_, VEC = VEC_, LPR = LPR_;
 };
 template <typename F>
-cudaError_t with_row(int E, F f) {
+cudaError_t with_warp_row(int E, F f) {
   if (E % 4 == 0) {
-    if (E <= 128) return f(Num<1>(), Num<4>());
-    if (E <= 256) return f(Num<2>(), Num<4>());
-    if (E <= 384) return f(Num<3>(), Num<4>());
-    if (E <= 512) return f(Num<4>(), Num<4>());
-    return f(Num<8>(), Num<4>());
+    if (E <= 128) return f(Shape<1, 4, 32>());
+    if (E <= 256) return f(Shape<2, 4, 32>());
+    if (E <= 384) return f(Shape<3, 4, 32>());
+    if (E <= 512) return f(Shape<4, 4, 32>());
+    return f(Shape<8, 4, 32>());
   }
-  if (E <= 32) return f(Num<1>(), Num<1>());
-  if (E <= 64) return f(Num<2>(), Num<1>());
-  if (E <= 128) return f(Num<4>(), Num<1>());
-  if (E <= 256) return f(Num<8>(), Num<1>());
-  if (E <= 512) return f(Num<16>(), Num<1>());
-  return f(Num<32>(), Num<1>());
+  if (E <= 32) return f(Shape<1, 1, 32>());
+  if (E <= 64) return f(Shape<2, 1, 32>());
+  if (E <= 128) return f(Shape<4, 1, 32>());
+  if (E <= 256) return f(Shape<8, 1, 32>());
+  if (E <= 512) return f(Shape<16, 1, 32>());
+  return f(Shape<32, 1, 32>());
+}
+template <typename F>
+cudaError_t with_half_row(int E, F f) {
+  if (E % 4 == 0) {
+    if (E <= 64) return f(Shape<1, 4, 16>());
+    if (E <= 128) return f(Shape<2, 4, 16>());
+    if (E <= 256) return f(Shape<4, 4, 16>());
+    if (E <= 384) return f(Shape<6, 4, 16>());
+  } else {
+    if (E <= 32) return f(Shape<2, 1, 16>());
+    if (E <= 64) return f(Shape<4, 1, 16>());
+    if (E <= 128) return f(Shape<8, 1, 16>());
+    if (E <= 256) return f(Shape<16, 1, 16>());
+    if (E <= 512) return f(Shape<32, 1, 16>());
+  }
+  return with_warp_row(E, f);
 }
 
 }  // namespace
@@ -516,10 +574,10 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
   const int per = balance_rows_per_cta(T, E);
   const int ctas = balance_ctas(T, E);
   const size_t smem = sizeof(float) * (fwd_warps(E) + 1) * E;
-  cudaError_t e = with_row(E, [&](auto nv, auto vec) {
-    return launch_k(k_balance_partial<decltype(nv)::value, decltype(vec)::value>, ctas,
-                    fwd_warps(decltype(nv)::value * decltype(vec)::value * 32) * 32, smem, st, logits, idx, off, mask, T, E, k, S, per, w.p, w.c,
-                    w.z, w.n, w.ticket, w.flags);
+  cudaError_t e = with_warp_row(E, [&](auto sh) {
+    using H = decltype(sh);
+    return launch_k(k_balance_partial<H::NV, H::VEC>, ctas, fwd_warps(E) * 32, smem, st, logits,
+                    idx, off, mask, T, E, k, S, per, w.p, w.c, w.z, w.n, w.ticket, w.flags);
   });
   if (e != cudaSuccess) return e;
   const dim3 grid((E + 31) / 32, S);
@@ -540,15 +598,18 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const in
                                const float* dw, int T, int E, int k, int S, float* dlogits,
                                cudaStream_t st) {
   if (T == 0) return cudaSuccess;
-  const long long warps = 152 * bwd_ctas_per_sm(E) * kWarps;  // all resident
-  const int per = static_cast<int>((T + warps - 1) / warps);
-  const int ctas = static_cast<int>((T + static_cast<long long>(per) * kWarps - 1) /
-                                    (static_cast<long long>(per) * kWarps));
-  const size_t smem = dw ? sizeof(float) * kWarps * E : 0;
-  return with_row(E, [&](auto nv, auto vec) {
-    return launch_k(k_balance_bwd<decltype(nv)::value, decltype(vec)::value>, ctas, kWarps * 32,
-                    smem, st, logits, idx, off, mask, counts, n_tokens, dloss, dz, dw, T, E, k, S,
-                    per, dlogits);
+  return with_half_row(E, [&](auto sh) {
+    using H = decltype(sh);
+    constexpr int rows = kWarps * (32 / H::LPR);  // a CTA's at once
+    const long long all = 152LL * bwd_ctas_per_sm(H::NV * H::VEC * H::LPR) * rows;  // resident
+    const int per = static_cast<int>((T + all - 1) / all);
+    const int ctas = static_cast<int>((T + static_cast<long long>(per) * rows - 1) /
+                                      (static_cast<long long>(per) * rows));
+    constexpr auto kern = k_balance_bwd<H::NV, H::VEC, H::LPR>;
+    const size_t smem = sizeof(float) * rows * E * 2;
+    const cudaError_t a = allow_smem<kern>();
+    if (a != cudaSuccess) return a;
+    return launch_k(kern, ctas, kWarps * 32, smem, st, logits, idx, off, mask, counts, n_tokens, dloss, dz, dw, T, E, k, S, per, dlogits);
   });
 }
 

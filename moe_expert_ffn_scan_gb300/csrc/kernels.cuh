@@ -278,6 +278,23 @@ cudaError_t launch_expand_rows(const uint8_t* xq, const uint8_t* xs, const int32
 // a context created after cudaDeviceReset has a new id, so the state is set up again.
 unsigned long long current_context_id();
 
+// Lets `kern` take all of a CTA's shared memory that its static arrays leave (at most 1 KB),
+// once per context.
+constexpr int kSmemMax = 226 * 1024;
+template <auto kern>
+cudaError_t allow_smem() {
+  static unsigned long long attr_ctx[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const unsigned long long ctx = current_context_id();
+  if (ctx != 0 && attr_ctx[dev] == ctx) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (e == cudaSuccess) attr_ctx[dev] = current_context_id();
+  return e;
+}
+
 // Transaction bytes one 128 x 128 weight-tile TMA load reports to its mbarrier: the
 // packed global size (128 rows x 64 bytes), not the 16-byte-aligned shared-memory
 // footprint (which is twice that).

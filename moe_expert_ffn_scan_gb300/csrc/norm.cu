@@ -18,12 +18,13 @@
 // of one CTA are read twice (the wide kernels).
 #include "kernels.cuh"
 
+#include <atomic>
+
 namespace moe {
 
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kSmemMax = 227 * 1024 - 1024;  // dynamic shared memory of one CTA
 constexpr int kMaxThreads = 512;  // a row's threads: 128 registers each
 constexpr int kRaggedFew = 4;     // columns a thread in rows that are no whole vectors: up to
 constexpr int kRaggedMany = 8;    // 1024 columns, and up to 8192
@@ -56,19 +57,6 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                : "l"(p)
                : "memory");
   return v;
-}
-
-// 16 bytes into shared memory, asynchronously and past L1.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -782,29 +770,30 @@ int row_threads(int cols, int vec, int nv) {
   return (t + 31) / 32 * 32;
 }
 
-// At most as many CTAs as fit on the GPU at once (which the shared memory and the 1024
-// threads of 64 registers a CTA decide), no more than `need`.
+// At most as many CTAs as fit on the GPU at once (which the shared memory and the registers
+// decide), no more than `need`.
 template <auto kern, typename... Args>
 cudaError_t launch_resident(int need, dim3 block, int smem, cudaStream_t st, int* grid_out,
                             Args... args) {
-  static unsigned long long attr_ctx[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const unsigned long long ctx = current_context_id();
-  if (ctx == 0 || attr_ctx[dev] != ctx) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-    if (e != cudaSuccess) return e;
-    attr_ctx[dev] = current_context_id();
-  }
-  int per_sm = 0;
+  int grid = need;
   if (need > kSms) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, block.x * block.y, smem);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    // the last answer, with the question (threads and bytes; the kernel is this function's)
+    static std::atomic<uint64_t> last{0};
+    const int threads = block.x * block.y;
+    const uint64_t key = static_cast<uint64_t>(threads) << 48 | static_cast<uint64_t>(smem) << 16;
+    uint64_t known = last.load(std::memory_order_relaxed);
+    if (known >> 16 != key >> 16) {
+      int per_sm = 0;
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+      if (e != cudaSuccess) return e;
+      if (per_sm < 1) return cudaErrorInvalidConfiguration;
+      known = key | static_cast<uint64_t>(per_sm);
+      last.store(known, std::memory_order_relaxed);
+    }
+    grid = min(need, kSms * static_cast<int>(known & 0xFFFF));
   }
-  const int grid = need <= kSms ? need : min(need, kSms * per_sm);
   if (grid_out) *grid_out = grid;
   return launch_k(kern, grid, block, smem, st, args...);
 }
