@@ -51,7 +51,7 @@ def test_add_rmsnorm_refusals(lib):
 
 def test_add_rmsnorm_backward_refusals(lib):
     f, size = lib.moe_add_rmsnorm_backward, lib.moe_add_rmsnorm_backward_workspace_size
-    assert size(4, 256) == 4 * 256 * 4 and size(10 ** 6, 256) < 2 ** 21
+    assert size(4, 256) >= 256 * 4 and size(10 ** 6, 256) < 2 ** 21
     assert size(-1, 256) == 0 and size(4, 0) == 0
     #       rows cols dy h dt gain dt rstd dh_in dh dx dgain ws bytes stream
     good = [4, 256, A, A, 0, A, 0, A, A, A, A, A, A, 1 << 20, None]
