@@ -276,13 +276,17 @@ __device__ __forceinline__ PairTile pair_tile(int L, int tiles_t, int tiles_f) {
 constexpr int kPThreads = 384;  // TMA warp, MMA warp, two idle, eight epilogue warps
 
 // kWhole: the output's rows (and the residual's and z's) are whole 32-byte sectors.
-template <bool kWhole>
+// S > 1 (few tiles): one tile per cluster of S pairs, each of which sums an S-th of c; the
+// partial sums meet in distributed shared memory (the drained rings), where pair i finishes
+// the i-th part of the tile's columns, adding in pair order.
+template <bool kWhole, int S>
 __global__ void __launch_bounds__(kPThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                   const LinearParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1, pair = crank >> 1;
   const bool leader = rank == 0;
+  const uint16_t both = static_cast<uint16_t>(3u << (crank & ~1u));  // this pair's CTAs
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPOffBar);
   uint64_t* empty = full + kPStages;
   uint64_t* acc_full = empty + kPStages;
@@ -320,8 +324,36 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int tiles_t = (p.R + kPTile - 1) / kPTile, tiles_f = (p.F + kPTile - 1) / kPTile;
   const int total = tiles_t * tiles_f;
   const int nk = (p.C + kBK - 1) / kBK;
-  const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
-  auto leader_addr = [&](const uint64_t* b) -> uint32_t { return mapa_shared(smem_u32(b), 0); };
+  const int kb0 = static_cast<int>(static_cast<long long>(nk) * pair / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(nk) * (pair + 1) / S);
+  const int cl = blockIdx.x / (2 * S), ncl = gridDim.x / (2 * S);
+  auto leader_addr = [&](const uint64_t* b) -> uint32_t {
+    return mapa_shared(smem_u32(b), crank & ~1u);
+  };
+  // 32 columns f.. of the warp's 32 rows t - lane.., not whole sectors: turned in shared
+  // memory, so that a warp stores 32 consecutive values of a row
+  auto ragged = [&](const float (&v32)[32], int t, int f) {
+    float* turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * 32 * 33;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v32[i];
+    __syncwarp();
+    const int tw = t - lane, fc = f + lane;
+    const int rows = fc < p.F ? p.R - tw : 0;  // this lane's, from tw
+    const float bias = p.e.bias && rows > 0 ? bias_at(p.e, fc) : 0.f;
+    constexpr int kRows = 16;  // (8: a sixth slower; 32: out of registers)
+#pragma unroll 1
+    for (int i = 0; i < 32; i += kRows) {
+      float v[kRows], rr[kRows];
+      bool on[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) on[j] = i + j < rows;
+      load_column<kRows>(p.e, tw + i, 1, fc, on, rr);
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) v[j] = turn[(i + j) * 33 + lane];
+      emit_column<kRows>(p.e, tw + i, 1, fc, bias, on, rr, v);
+    }
+    __syncwarp();
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
@@ -332,7 +364,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const PairTile tl = pair_tile(L, tiles_t, tiles_f);
         const int t0 = tl.t0 + static_cast<int>(rank) * 128;
         const int f0 = tl.f0 + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % kPStages;
           if (it >= kPStages &&
               !mbar_wait(&empty[s], ((it / kPStages) & 1u) ^ 1u, p.status, abort_flag)) {
@@ -375,7 +407,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (tc >= 2 && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + b * kPTile;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % kPStages;
           if (!mbar_wait(&full[s], (it / kPStages) & 1u, p.status, abort_flag)) {
             ok = false;
@@ -386,18 +418,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_bf16_ss_pair(d, tile_desc(a0, p.p_mn, kk), tile_desc(a0 + kPOpBytes, p.q_mn, kk),
-                             idesc, kb > 0 || kk > 0);
-          tc_commit_pair_mc(&empty[s], 3);
+                             idesc, kb > kb0 || kk > 0);
+          tc_commit_pair_mc(&empty[s], both);
         }
-        if (ok) tc_commit_pair_mc(&acc_full[b], 3);
+        if (ok) tc_commit_pair_mc(&acc_full[b], both);
       }
       // after an abort: the MMAs already issued
       if (*abort_flag) {
-        tc_commit_pair_mc(drain, 1);
+        tc_commit_pair_mc(drain, static_cast<uint16_t>(1u << crank));
         mbar_wait_drain(drain, 0);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && S == 1) {
     // ---------------------------------------------------------------- epilogue
     // eight warps: four for the accumulator's lanes, twice for halves of its columns
     const int q = warp & 3, half = (warp - 4) >> 2;
@@ -432,28 +464,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             emit_row32(p.e, t, f0 + c, cols - c, now, v);
           }
         } else {
-          // the 32 x 32 block turned in shared memory, so that a warp stores 32 consecutive
-          // values of a row
-          float* turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * 32 * 33;
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = __uint_as_float(r[i]);
-          __syncwarp();
-          const int tw = t - lane, fc = f0 + c + lane;
-          const int rows = fc < p.F ? p.R - tw : 0;  // this lane's, from tw
-          const float bias = p.e.bias && rows > 0 ? bias_at(p.e, fc) : 0.f;
-          constexpr int kRows = 16;  // (8: a sixth slower; 32: out of registers)
-#pragma unroll 1
-          for (int i = 0; i < 32; i += kRows) {
-            float v[kRows], rr[kRows];
-            bool on[kRows];
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) on[j] = i + j < rows;
-            load_column<kRows>(p.e, tw + i, 1, fc, on, rr);
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) v[j] = turn[(i + j) * 33 + lane];
-            emit_column<kRows>(p.e, tw + i, 1, fc, bias, on, rr, v);
-          }
-          __syncwarp();
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          ragged(v, t, f0 + c);
         }
       }
       tc_fence_before();
@@ -463,6 +477,63 @@ __global__ void __launch_bounds__(kPThreads, 1)
         else mbar_arrive_cluster(leader_addr(&acc_empty[b]));
       }
     }
+  }
+  if constexpr (S > 1) {
+    // ---------------------------------------------------------------- joined epilogue
+    constexpr int CW = kPTile / S;  // columns a pair finishes
+    const PairTile tl = pair_tile(cl, tiles_t, tiles_f);
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int row = q * 32 + lane, t = tl.t0 + static_cast<int>(rank) * 128 + row;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float* sums = reinterpret_cast<float*>(smem);  // [column of the tile][128 rows]
+    int w_ok = 0;
+    if (warp >= 4) {
+      if (lane == 0) w_ok = mbar_wait(&acc_full[0], 0, p.status, abort_flag);
+      w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
+      tc_fence_after();
+      for (int c = half * 32; c < kPTile && w_ok; c += 64) {
+        if (c / CW == static_cast<int>(pair) || tl.f0 + c >= p.F) continue;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sums[(c + i) * 128 + row] = __uint_as_float(r[i]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // every pair's sums are in place
+    if (warp >= 4) {
+      for (int c = static_cast<int>(pair) * CW + half * 32; c < (static_cast<int>(pair) + 1) * CW;
+           c += 64) {
+        const int f = tl.f0 + c;
+        if (!w_ok || f >= p.F) break;
+        RowRes res;
+        if (kWhole && t < p.R) load_row32(p.e, t, f, p.F - f, res);
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + c, r);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        tmem_ld_wait();
+#pragma unroll
+        for (int o = 0; o < S; ++o) {
+          const uint32_t at = mapa_shared(smem_u32(sums + c * 128 + row), 2 * o + rank);
+          float u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            u[i] = o == static_cast<int>(pair) ? __uint_as_float(r[i])
+                                               : ld_shared_cluster(at + i * 512);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += u[i];
+        }
+        if constexpr (kWhole) {
+          if (t < p.R) emit_row32(p.e, t, f, p.F - f, res, v);
+        } else {
+          ragged(v, t, f);
+        }
+      }
+    }
+    __syncwarp();
   }
   pdl_trigger();
   tc_fence_before();
@@ -850,7 +921,7 @@ cudaError_t launch_split(const Operand& P, const Operand& Q, const LinearParams&
                         splits, grid, 256, false, st, args);
 }
 
-template <bool kWhole>
+template <bool kWhole, int S>
 cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearParams& p,
                               cudaStream_t st) {
   static KernelState ks;
@@ -858,11 +929,17 @@ cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearPa
   if (!encode(&tmP, P, p.C, 128) || !encode(&tmQ, Q, p.C, 128)) return cudaErrorInvalidValue;
   const long long tiles = static_cast<long long>((p.R + kPTile - 1) / kPTile) *
                           ((p.F + kPTile - 1) / kPTile);
-  if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
+  if (tiles > (1LL << 28)) return cudaErrorInvalidValue;
   void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
-  return launch_cluster(reinterpret_cast<const void*>(k_linear_pair<kWhole>), ks,
-                        kWhole ? kPOffTurn : kPSmem, 2,
-                        dim3(static_cast<unsigned>(2 * tiles)), kPThreads, true, st, args);
+  return launch_cluster(reinterpret_cast<const void*>(k_linear_pair<kWhole, S>), ks,
+                        kWhole ? kPOffTurn : kPSmem, 2 * S,
+                        dim3(static_cast<unsigned>(2 * S * tiles)), kPThreads, S == 1, st, args);
+}
+template <bool kWhole>
+cudaError_t launch_pairs(const Operand& P, const Operand& Q, const LinearParams& p, int splits,
+                         cudaStream_t st) {
+  if (splits == 2) return launch_pair_tiles<kWhole, 2>(P, Q, p, st);
+  return launch_pair_tiles<kWhole, 1>(P, Q, p, st);
 }
 
 // One product, on the kernel and tile that should take the least time, by costs measured on
@@ -872,11 +949,12 @@ cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearPa
 // wave of 304 CTAs 3 for launch and first load, 0.87 per 16 tokens of a CTA's epilogue and
 // 0.02 per token that a cluster exchanges.  Clusters of 3, 5 and 6 fit the GPU's partitions
 // badly (7 x 7168 x 7168 in 4 parts 20.2, in 5 20.9, in 6 27.4) and are not used.
-// Both sides: 7168 x 7168 weights, 128 rows: pairs 38, split 26.5; 192: 39, 41; 512: 40, 67;
-// 1024 x 1024 x 8192: 42, 25; 300 x 1024 x 256: 7.6, 4.4; 8192 x 256 x 1024: 11.5, 17.8.
+// Both sides (pairs, two pairs a tile, split): 7168 x 7168 weights, 128 rows: 38, 28, 26.5;
+// 256: 39, 28, 41; 512: 40, -, 67; 1024 x 1024 x 8192: 42, 26, 24; 1024 x 2048 x 2048: 15.5,
+// 13.2, 18.7; 300 x 1024 x 256: 7.6, -, 4.4; 8192 x 256 x 1024: 11.5, -, 17.8.
 struct Choice {
   double us;
-  int nt, splits;  // nt = 0: pairs
+  int nt, splits;  // nt = 0: SM pairs
 };
 Choice choose(int R, int F, int C, bool p_mn, bool whole) {
   const int nk = (C + kBK - 1) / kBK;
@@ -885,6 +963,10 @@ Choice choose(int R, int F, int C, bool p_mn, bool whole) {
   const double waves = static_cast<double>((tiles + 75) / 76);
   const double mma = 0.29 * nk, epi = whole ? 6.3 : 18.0;
   Choice best = {(waves - 1) * (mma > epi ? mma : epi) + mma + epi, 0, 1};
+  // two pairs a tile, while all their clusters fit (four: clusters of eight CTAs with an SM
+  // each fit badly, 7168 x 7168 weights and 256 rows 40 us)
+  const double two_us = 0.16 * nk + (whole ? 8.5 : 11.5);
+  if (tiles <= 36 && nk >= 2 && two_us < best.us) best = {two_us, 0, 2};
   const long long ft = (F + kSFeat - 1) / kSFeat;
   for (int nt = p_mn ? 64 : 16; nt <= 128; nt *= 2) {
     const long long tt = (R + nt - 1) / nt;
@@ -910,8 +992,8 @@ cudaError_t product(const Operand& P, const Operand& Q, const LinearParams& p, c
   const Choice c = choose(p.R, p.F, p.C, p.p_mn, p.e.whole);
   switch (c.nt) {
     case 0:
-      return p.e.whole ? launch_pair_tiles<true>(P, Q, p, st)
-                       : launch_pair_tiles<false>(P, Q, p, st);
+      return p.e.whole ? launch_pairs<true>(P, Q, p, c.splits, st)
+                       : launch_pairs<false>(P, Q, p, c.splits, st);
     case 16: return launch_split<16>(P, Q, p, c.splits, st);
     case 32: return launch_split<32>(P, Q, p, c.splits, st);
     case 64: return launch_split<64>(P, Q, p, c.splits, st);

@@ -21,7 +21,8 @@ U16, U32 = ref.U16, ref.U32
 
 SHAPES = [(1, 1, 1), (1, 128, 64), (7, 7168, 512), (16, 130, 72), (17, 129, 65), (33, 257, 129),
           (64, 64, 64), (65, 300, 200), (130, 384, 320), (333, 1111, 777), (300, 20000, 64),
-          (2600, 2100, 136), (5000, 1024, 1), (256, 7168, 1024)]
+          (2600, 2100, 136), (5000, 1024, 1), (256, 7168, 1024), (700, 1984, 2100),
+          (600, 1031, 3001)]
 
 
 def _ints(g, *shape, hi=3):
