@@ -68,10 +68,28 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 // within 2 units of 2^-23; the argument's rounding adds |z| * 2^-24): expf and the IEEE
 // quotient would double the gradient pass's instructions, which bound it.
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// The normal distribution's tail beyond |z|, 0.5 * erfc(|z| / sqrt(2)), by Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error 1.5e-7 of erfc), and
+// e = exp(-z^2 / 2), which its density shares: half of erff's instructions, in an epilogue
+// that they bound (8192 x 4096 x 1024 with GELU: GELU_NOW us; with erff 114).
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+  const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
+  e = __expf(-0.5f * z * z);
+  float s = 1.061405429f;
+  s = fmaf(s, t, -1.453152027f);
+  s = fmaf(s, t, 1.421413741f);
+  s = fmaf(s, t, -0.284496736f);
+  s = fmaf(s, t, 0.254829592f);
+  return 0.5f * s * t * e;
+}
 __device__ __forceinline__ float act_value(float z, int act) {
   if (act == MOE_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
   if (act == MOE_ACT_SILU) return z * sigmoid(z);
-  if (act == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+  if (act == MOE_ACT_GELU) {
+    float e;
+    const float h = normal_tail(z, e);
+    return z * (z > 0.f ? 1.f - h : h);
+  }
   return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
@@ -80,8 +98,11 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     const float s = sigmoid(z);
     return s * fmaf(z, 1.f - s, 1.f);
   }
-  if (act == MOE_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+  if (act == MOE_ACT_GELU) {
+    float e;
+    const float h = normal_tail(z, e);
+    return fmaf(z * 0.39894228f, e, z > 0.f ? 1.f - h : h);
+  }
   return 1.f;
 }
 
@@ -180,11 +201,13 @@ __device__ __forceinline__ void load_row32(const Epi& e, int t, int f0, int n, R
 }
 // ... and the outputs.
 __device__ __forceinline__ void emit_row32(const Epi& e, int t, int f0, int n, const RowRes& r,
-                                           float (&v)[32]) {
-  if (e.bias) {
+                                           const float* bias, float (&v)[32]) {
+  if (e.bias) {  // bias: the 32 columns', in shared memory (16-byte aligned)
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) v[i] += bias_at(e, f0 + i);
+    for (int i = 0; i < 8; ++i) {
+      const float4 b = reinterpret_cast<const float4*>(bias)[i];
+      v[4 * i] += b.x, v[4 * i + 1] += b.y, v[4 * i + 2] += b.z, v[4 * i + 3] += b.w;
+    }
   }
   if (e.z) st_bf16x32(e.z + static_cast<size_t>(t) * e.ldz + f0, v, n);
   if (e.act == MOE_ACT_RELU) {
@@ -250,7 +273,9 @@ constexpr int kPStageBytes = 2 * kPOpBytes;
 constexpr int kPOffBar = kPStages * kPStageBytes;
 // full[S], empty[S], acc_full[2], acc_empty[2], drain
 constexpr int kPOffMisc = kPOffBar + (2 * kPStages + 5) * 8;
-constexpr int kPOffTurn = kPOffMisc + 16;  // eight epilogue warps' 32 x 33 blocks (not kWhole)
+constexpr int kPOffTurn = (kPOffMisc + 16 + 15) / 16 * 16;
+// eight epilogue warps' bias of their half of the columns (kWhole), or 32 x 33 blocks
+constexpr int kPSmemWhole = kPOffTurn + 8 * (kPTile / 2) * 4;
 constexpr int kPSmem = kPOffTurn + 8 * 32 * 33 * 4;
 static_assert(kPSmem <= 232448, "dynamic shared memory of one CTA");
 // Tiles are walked in bands of this many output rows' tiles, column by column, so that the
@@ -443,7 +468,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // the next 32 columns' residual is in flight under these columns' stores, the first
       // ones' under the tile's last MMAs
       RowRes res;
-      if (kWhole && t < p.R) load_row32(p.e, t, f0, cols, res);
+      float* bias = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * (kPTile / 2);
+      if constexpr (kWhole) {
+        if (t < p.R) load_row32(p.e, t, f0, cols, res);
+        if (p.e.bias) {
+          __syncwarp();  // (the last tile's has been read)
+          for (int c = lane; c < cols; c += 32) bias[c] = bias_at(p.e, f0 + c);
+          __syncwarp();
+        }
+      }
       int w_ok = 1;
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
@@ -461,7 +494,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-            emit_row32(p.e, t, f0 + c, cols - c, now, v);
+            emit_row32(p.e, t, f0 + c, cols - c, now, bias + c, v);
           }
         } else {
           float v[32];
@@ -508,7 +541,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int f = tl.f0 + c;
         if (!w_ok || f >= p.F) break;
         RowRes res;
-        if (kWhole && t < p.R) load_row32(p.e, t, f, p.F - f, res);
+        float* bias = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * (kPTile / 2);
+        if constexpr (kWhole) {
+          if (t < p.R) load_row32(p.e, t, f, p.F - f, res);
+          if (p.e.bias) {
+            __syncwarp();
+            if (f + lane < p.F) bias[lane] = bias_at(p.e, f + lane);
+            __syncwarp();
+          }
+        }
         uint32_t r[32];
         tmem_ld_32x32b_x32(acc + c, r);
         float v[32];
@@ -527,7 +568,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           for (int i = 0; i < 32; ++i) v[i] += u[i];
         }
         if constexpr (kWhole) {
-          if (t < p.R) emit_row32(p.e, t, f, p.F - f, res, v);
+          if (t < p.R) emit_row32(p.e, t, f, p.F - f, res, bias, v);
         } else {
           ragged(v, t, f);
         }
@@ -932,7 +973,7 @@ cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearPa
   if (tiles > (1LL << 28)) return cudaErrorInvalidValue;
   void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
   return launch_cluster(reinterpret_cast<const void*>(k_linear_pair<kWhole, S>), ks,
-                        kWhole ? kPOffTurn : kPSmem, 2 * S,
+                        kWhole ? kPSmemWhole : kPSmem, 2 * S,
                         dim3(static_cast<unsigned>(2 * S * tiles)), kPThreads, S == 1, st, args);
 }
 template <bool kWhole>
