@@ -68,28 +68,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 // within 2 units of 2^-23; the argument's rounding adds |z| * 2^-24): expf and the IEEE
 // quotient would double the gradient pass's instructions, which bound it.
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-// The normal distribution's tail beyond |z|, 0.5 * erfc(|z| / sqrt(2)), by Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error 1.5e-7 of erfc), and
-// e = exp(-z^2 / 2), which its density shares: half of erff's instructions, in an epilogue
-// that they bound (8192 x 4096 x 1024 with GELU: GELU_NOW us; with erff 114).
-__device__ __forceinline__ float normal_tail(float z, float& e) {
-  const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
-  e = __expf(-0.5f * z * z);
-  float s = 1.061405429f;
-  s = fmaf(s, t, -1.453152027f);
-  s = fmaf(s, t, 1.421413741f);
-  s = fmaf(s, t, -0.284496736f);
-  s = fmaf(s, t, 0.254829592f);
-  return 0.5f * s * t * e;
-}
 __device__ __forceinline__ float act_value(float z, int act) {
   if (act == MOE_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
   if (act == MOE_ACT_SILU) return z * sigmoid(z);
-  if (act == MOE_ACT_GELU) {
-    float e;
-    const float h = normal_tail(z, e);
-    return z * (z > 0.f ? 1.f - h : h);
-  }
+  if (act == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
   return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
@@ -98,11 +80,8 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     const float s = sigmoid(z);
     return s * fmaf(z, 1.f - s, 1.f);
   }
-  if (act == MOE_ACT_GELU) {
-    float e;
-    const float h = normal_tail(z, e);
-    return fmaf(z * 0.39894228f, e, z > 0.f ? 1.f - h : h);
-  }
+  if (act == MOE_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
   return 1.f;
 }
 
