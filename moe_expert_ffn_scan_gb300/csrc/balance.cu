@@ -11,7 +11,7 @@
 // One pass over the logits: a warp holds a token's E logits in registers (E <= 1024), so
 // the maximum, the sum, the probabilities and their products are register work; both
 // directions are bound by reading (and in the gradient writing) T x E fp32 values.
-// No floating-point atomics: partial sums are added in a fixed order.
+// No floating-point atomics: partial sums are added in a fixed order, or in fixed point.
 #include "kernels.cuh"
 
 namespace moe {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
                       const int32_t* __restrict__ off, const uint8_t* __restrict__ mask, int T,
                       int E, int k, int S, int per, float* __restrict__ part_p,
                       int32_t* __restrict__ part_c, float* __restrict__ part_z,
-                      int32_t* __restrict__ part_n, int32_t* __restrict__ ticket,
+                      int32_t* __restrict__ part_n, unsigned long long* __restrict__ acc,
                       uint32_t* __restrict__ flags) {
   pdl_wait();
   pdl_trigger();
@@ -161,9 +161,9 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
   __shared__ int ns[W];
   int32_t* hist = reinterpret_cast<int32_t*>(dyn + W * E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the arrival counters of the kernel after this one
+  // the loss sums of the kernel after this one
   for (int s = blockIdx.x * blockDim.x + threadIdx.x; s < S; s += gridDim.x * blockDim.x)
-    ticket[s] = 0;
+    acc[s] = 0;
   const int begin = blockIdx.x * per, end = T - begin < per ? T : begin + per;
   int row = begin;
   uint32_t bad = 0;  // data-dependent checks of this thread (STATUS_*)
@@ -251,13 +251,13 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
 
 // Adds up the partials of sequence blockIdx.y for 32 experts; warp w takes the slots
 // first + w, + WARPS, ... and the warps' sums are added in order.  The CTA that finishes its
-// sequence last adds the CTAs' loss terms, in CTA order.
+// sequence last has the sum of the CTAs' loss terms.
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS * 32)
     k_balance_final(const int32_t* __restrict__ off, int T, int E, int k, int S, int per,
                     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
                     const float* __restrict__ part_z, const int32_t* __restrict__ part_n,
-                    int32_t* ticket, float* terms, int32_t* __restrict__ counts,
+                    unsigned long long* acc, int32_t* __restrict__ counts,
                     int32_t* __restrict__ n_tokens, float* __restrict__ prob,
                     float* __restrict__ loss, float* __restrict__ z_loss,
                     const uint32_t* __restrict__ flags, int nflags, uint32_t* status) {
@@ -331,24 +331,23 @@ __global__ void __launch_bounds__(WARPS * 32)
   float term = static_cast<float>(c) * inv * p;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, o);
-  if (blockIdx.x == 0 && lane == 0) {
+  if (lane != 0) return;
+  if (blockIdx.x == 0) {
     n_tokens[s] = n;
     if (z_loss) z_loss[s] = z * inv;
   }
-  int done = 0;
-  if (lane == 0) {
-    terms[static_cast<size_t>(s) * gridDim.x + blockIdx.x] = term;
-    __threadfence();
-    done = atomicAdd(ticket + s, 1) == static_cast<int>(gridDim.x) - 1;
-    __threadfence();
-  }
-  if (!__shfl_sync(0xFFFFFFFFu, done, 0)) return;
-  float sum = 0.f;  // (gridDim.x <= 32)
-  if (lane < static_cast<int>(gridDim.x))
-    sum = __ldcg(terms + static_cast<size_t>(s) * gridDim.x + lane);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) loss[s] = sum * (static_cast<float>(E) / static_cast<float>(k));
+  // One atomic does the loss's sum and the arrival: [51:0] the terms in fixed point (each at
+  // most k <= 16, to 2^-47: whatever the order, the same sum), [57:52] how many were NaN,
+  // [63:58] arrivals.  The last CTA has it all.
+  const bool bad = !(term <= 32.f);
+  const unsigned long long add =
+      (1ull << 58) | (bad ? 1ull << 52 : static_cast<unsigned long long>(
+                                             static_cast<double>(term) * 140737488355328.0));
+  const unsigned long long all = atomicAdd(acc + s, add) + add;
+  if (all >> 58 != gridDim.x) return;
+  const double sum = (all >> 52 & 63) ? nan("") : static_cast<double>(all & ((1ull << 52) - 1)) /
+                                                       140737488355328.0;
+  loss[s] = static_cast<float>(sum * E / k);
 }
 
 // CTAs per SM: by the registers a lane's values take, and no more (32768 x 384 with three 26
@@ -564,7 +563,7 @@ static int balance_rows_per_cta(int T, int E) {
 int balance_ctas(int T, int E) {
   const int per = balance_rows_per_cta(T, E);
   const int n = static_cast<int>((static_cast<long long>(T) + per - 1) / per);
-  return n < 1 ? 1 : n;  // (T = 0: one CTA, which clears the tickets)
+  return n < 1 ? 1 : n;  // (T = 0: one CTA, which clears the sums)
 }
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
@@ -577,7 +576,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
   cudaError_t e = with_warp_row(E, [&](auto sh) {
     using H = decltype(sh);
     return launch_k(k_balance_partial<H::NV, H::VEC>, ctas, fwd_warps(E) * 32, smem, st, logits,
-                    idx, off, mask, T, E, k, S, per, w.p, w.c, w.z, w.n, w.ticket, w.flags);
+                    idx, off, mask, T, E, k, S, per, w.p, w.c, w.z, w.n, w.acc, w.flags);
   });
   if (e != cudaSuccess) return e;
   const dim3 grid((E + 31) / 32, S);
@@ -585,10 +584,10 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
   // 32768 tokens with 1024 threads each: 28 us instead of 18)
   if (S > 8)
     return launch_k(k_balance_final<8>, grid, 256, 0, st, off, T, E, k, S, per, w.p, w.c, w.z, w.n,
-                    w.ticket, w.terms, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
+                    w.acc, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
                     w.status);
   return launch_k(k_balance_final<32>, grid, 1024, 0, st, off, T, E, k, S, per, w.p, w.c, w.z, w.n,
-                  w.ticket, w.terms, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
+                  w.acc, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
                   w.status);
 }
 

@@ -48,8 +48,7 @@ BalanceWs carve_balance(Carver& c, int T, int E, int S) {
   w.c = c.take<int32_t>(slots * E);
   w.z = c.take<float>(slots);
   w.n = c.take<int32_t>(slots);
-  w.ticket = c.take<int32_t>(S);
-  w.terms = c.take<float>(static_cast<size_t>(S) * ((E + 31) / 32));
+  w.acc = c.take<unsigned long long>(S);
   return w;
 }
 

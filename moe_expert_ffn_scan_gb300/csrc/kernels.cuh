@@ -182,8 +182,7 @@ struct BalanceWs {
   int32_t* c;        // [slots][E] counts
   float* z;          // [slots]
   int32_t* n;        // [slots] counted tokens
-  int32_t* ticket;   // [S] arrivals
-  float* terms;      // [S][ceil(E / 32)] loss terms
+  unsigned long long* acc;  // [S] loss sums and arrivals
 };
 int balance_ctas(int T, int E);
 cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,

@@ -157,6 +157,18 @@ def test_rows_of_minus_infinity():
     assert torch.count_nonzero(out[5]).item() == 0
 
 
+def test_nan_shows():
+    """A NaN in a token that counts is seen in its sequence's sums, and only there."""
+    lg, idx, _, _ = _make(40, 100, 4, 1, False, seed=9)
+    off = torch.tensor([0, 15, 40], dtype=I32)
+    clean, _ = _forward(*_dev(lg, idx, off), None, 2, 100)
+    lg[20, 77] = float("nan")
+    o, _ = _forward(*_dev(lg, idx, off), None, 2, 100)
+    assert torch.equal(o["counts"], clean["counts"])
+    for n in ("loss", "z_loss", "prob"):
+        assert torch.equal(o[n][0], clean[n][0]) and bool(torch.isnan(o[n][1]).all())
+
+
 def test_device_checks():
     """Experts out of range are reported and not counted; so are decreasing offsets."""
     lg, idx, _, _ = _make(50, 16, 2, 1, False, seed=6)
