@@ -48,8 +48,8 @@ class MoEBlock:
             moe.balance_loss_workspace_size(T, self.E, self.k, n_seq), dev)
         self.ws_grad = moe.alloc_workspace(max(
             moe.linear_backward_workspace_size(T, N, K),
-            moe.linear_backward_workspace_size(T, self.E, self.H),
-            moe.add_rmsnorm_backward_workspace_size(T, self.H)), dev)
+            moe.linear_backward_workspace_size(T, self.E, self.H)), dev)
+        self.ws_norm = moe.alloc_workspace(moe.add_rmsnorm_backward_workspace_size(T, self.H), dev)
 
     def forward(self, attn, stream):
         """attn [T, K] bf16 (the attention's output), stream [T, H] bf16.  Returns the experts'
@@ -99,7 +99,7 @@ class MoEBlock:
         moe.moe_linear_backward(f["y"], self.wg.to(bf), g["dlogits"].to(bf), self.ws_grad,
                                 dx=g["dy"], dw=g["dwg"])
         g["dh"], g["dgain"] = new(T, H, dt=bf), new(H)
-        moe.moe_add_rmsnorm_backward(g["dy"], f["h"], self.gain, f["rstd"], self.ws_grad,
+        moe.moe_add_rmsnorm_backward(g["dy"], f["h"], self.gain, f["rstd"], self.ws_norm,
                                      dh=g["dh"], dgain=g["dgain"])
         # h = attn W_o^T + stream: dh goes to the stream as it is
         g["dattn"], g["dw_o"] = torch.empty_like(f["attn"]), torch.empty_like(self.w_o)
@@ -109,7 +109,8 @@ class MoEBlock:
 
     def check(self):
         """The device-side checks of the calls since the workspaces were made."""
-        return [moe.moe_check_status(w) for w in (self.ws, self.ws_linear, self.ws_balance)]
+        return [moe.moe_check_status(w) for w in (self.ws, self.ws_linear, self.ws_balance,
+                                                 self.ws_grad)]
 
 
 def make_block(T, size="tiny", seed=0, n_seq=1, device="cuda"):

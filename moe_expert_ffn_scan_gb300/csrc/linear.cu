@@ -8,14 +8,18 @@
 // index contiguous and the MMA takes them as MN-major.  Operands whose rows are not whole
 // 16-byte vectors cannot be loaded by TMA and are first copied to padded rows.
 //
-// Two kernels:
+// Two kernels, chosen per product by their measured costs (choose below):
 //   * k_linear_pair: 256 x 256 outputs per SM pair (cta_group::2 MMAs of M = 256, N = 256),
-//     64 columns of c a stage, persistent, two accumulators in TMEM so that a tile's
-//     epilogue runs under the next tile's MMAs.  Bound by the tensor cores.
+//     64 columns of c a stage in a ring of six, persistent, two accumulators in TMEM so that a
+//     tile's epilogue runs under the next tile's MMAs; with few tiles two pairs share one,
+//     each summing half of c.  Bound by the tensor cores (16384 x 7168 x 7168 with residual:
+//     1.00 ms, 1.68 PFLOP/s) or, for short c, by the epilogue's elementwise work (8192 x 4096
+//     x 1024: 44 us plain, 45 with bias, 52 with SiLU, 65 with GELU).
 //   * k_linear_split: for outputs with too few such tiles.  128 features (the MMA's M side:
 //     the weights fill its rows even for one token) x NT tokens a tile, c split among the
 //     CTAs of a cluster, whose partial sums meet in distributed shared memory and are added
-//     in rank order (no atomics, no workspace).  Bound by reading W for few tokens.
+//     in rank order (no atomics, no workspace).  Bound by reading W for few tokens (7 x 7168
+//     x 7168: 20 us, 15.4 of them the weights' at the copy bandwidth).
 // Every wait is bounded; one that expires sets the workspace's status word.
 #include "kernels.cuh"
 

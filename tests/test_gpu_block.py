@@ -22,7 +22,7 @@ def _np(t):
 def test_forward_is_the_layers_own(T):
     block, attn, stream = make_block(T)
     f = block.forward(attn, stream)
-    assert block.check() == [0, 0, 0]
+    assert block.check() == [0, 0, 0, 0]
     h = _np(attn) @ _np(block.w_o).T + _np(stream)
     assert_float_close(_np(f["h"]), h, "h")
     y = ref.norm(_np(f["h"]), None, _np(block.gain), block.eps)[2]
@@ -43,7 +43,7 @@ def test_router_step():
     mask[40:60] = False
     f = block.forward(attn, stream)
     o, g = block.router_step(f, seq_offsets=off, token_mask=mask, balance=1.0, z=0.1)
-    assert block.check() == [0, 0, 0]
+    assert block.check() == [0, 0, 0, 0]
     args = (_np(f["logits"]), f["idx"].cpu().numpy(), off.cpu().numpy(), mask.cpu().numpy(), S)
     counts, n, prob, loss, z = ref.balance(*args)
     assert np.array_equal(o["counts"].cpu().numpy(), counts)
