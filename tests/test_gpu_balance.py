@@ -215,3 +215,26 @@ def test_counts_agree_with_the_route():
                   moe.alloc_workspace(moe.route_workspace_size(d)))
     o, _ = _forward(lg, idx, None, None, 1, 64)
     assert torch.equal(o["counts"][0], counts)
+
+
+@pytest.mark.parametrize("E", [1024, 1023])
+def test_offsets_past_32_bits(E):
+    """More than 2^31 logits: the last sequence comes out as in a call of its own."""
+    T, k, n = (1 << 31) // E + 500, 4, 300
+    g = torch.Generator(device=DEV).manual_seed(2)
+    lg = torch.empty(T, E, device=DEV).normal_(generator=g)
+    idx = torch.randint(0, E, (T, k), generator=g, device=DEV, dtype=I32)
+    off = torch.tensor([0, T - n, T], dtype=I32, device=DEV)
+    o, ws = _forward(lg, idx, off, None, 2, E)
+    assert moe.moe_check_status(ws) == 0 and o["n_tokens"].tolist() == [T - n, n]
+    assert o["counts"].sum(1).tolist() == [(T - n) * k, n * k]
+    last, li = lg[-n:].clone(), idx[-n:].clone()
+    own, _ = _forward(last, li, None, None, 1, E)
+    assert torch.equal(o["counts"][1], own["counts"][0])
+    assert bool(((o["prob"][1] - own["prob"][0]).abs() <= TOL * own["prob"][0]).all())
+    out, one = torch.empty_like(lg), torch.ones(2, device=DEV)
+    moe.moe_balance_loss_backward(lg, idx, o["counts"], o["n_tokens"], out, one, one,
+                                  seq_offsets=off)
+    o1 = torch.empty_like(last)
+    moe.moe_balance_loss_backward(last, li, own["counts"], own["n_tokens"], o1, one[:1], one[:1])
+    assert torch.equal(out[-n:], o1)

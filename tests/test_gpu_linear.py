@@ -213,3 +213,23 @@ def test_on_another_stream():
     moe.moe_linear(x, w, y, ws, stream=st)
     torch.cuda.current_stream().wait_stream(st)
     assert torch.equal(y, (x.to(F64) @ w.to(F64).t()).float())
+
+
+@pytest.mark.parametrize("N", [8192, 8191])
+def test_offsets_past_32_bits(N):
+    """More than 2^31 outputs: first, middle and last rows exactly."""
+    M, K = (1 << 31) // N + 300, 40
+    g = _gen(N)
+    x, w = _ints(g, M, K), _ints(g, N, K)
+    y, ws = torch.empty(M, N, dtype=BF16, device=DEV), _ws(M, N, K)
+    moe.moe_linear(x, w, y, ws)
+    for r in (slice(0, 7), slice(M // 2, M // 2 + 7), slice(M - 7, M)):
+        assert torch.equal(y[r], (x[r].to(F64) @ w.to(F64).t()).float().to(BF16))
+    dx, db = torch.empty_like(x), torch.empty(N, dtype=F32, device=DEV)
+    wb = moe.alloc_workspace(moe.linear_backward_workspace_size(M, N, K, act="none"))
+    moe.moe_linear_backward(x, w, y, wb, dx=dx, dbias=db)
+    r = slice(M - 7, M)
+    want = y[r].to(F64) @ w.to(F64)
+    e = N * 2 * U32 * (y[r].to(F64).abs() @ w.to(F64).abs())
+    assert bool(((dx[r].to(F64) - want).abs() <= e + U16 * (want.abs() + e)).all())
+    assert moe.moe_check_status(ws) == 0 and moe.moe_check_status(wb) == 0

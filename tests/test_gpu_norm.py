@@ -217,3 +217,21 @@ def test_on_another_stream():
         moe.moe_add_rmsnorm(x, r, w, EPS, y=y2)
     torch.cuda.current_stream().wait_stream(st)
     assert torch.equal(y0, y2)
+
+
+@pytest.mark.parametrize("cols", [8192, 8191])
+def test_offsets_past_32_bits(cols):
+    """More than 2^31 values: the last rows come out as in a call of their own."""
+    rows = (1 << 31) // cols + 300
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(rows, cols, dtype=BF16, device=DEV).normal_(generator=g)
+    w = torch.ones(cols, dtype=BF16, device=DEV)
+    y, rstd = torch.empty_like(x), torch.empty(rows, dtype=F32, device=DEV)
+    moe.moe_add_rmsnorm(x, None, w, EPS, y=y, rstd=rstd)
+    last, y1, r1 = x[-5:].clone(), torch.empty(5, cols, dtype=BF16, device=DEV), rstd[-5:].clone()
+    moe.moe_add_rmsnorm(last, None, w, EPS, y=y1)
+    assert torch.equal(y[-5:], y1)
+    dh, dh1 = torch.empty_like(x), torch.empty_like(last)
+    moe.moe_add_rmsnorm_backward(y, x, w, rstd, None, dh=dh)
+    moe.moe_add_rmsnorm_backward(y1, last, w, r1, None, dh=dh1)
+    assert torch.equal(dh[-5:], dh1)
