@@ -250,17 +250,24 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t base, int mn, int kk) {
 // ---------------------------------------------------------------- SM pairs ----------
 
 constexpr int kPTile = 256;                      // output rows and columns per pair
-constexpr int kPStages = 6;
 constexpr int kPOpBytes = 128 * kRowBytes;       // one operand's stage in one CTA
 constexpr int kPStageBytes = 2 * kPOpBytes;
-constexpr int kPOffBar = kPStages * kPStageBytes;
-// full[S], empty[S], acc_full[2], acc_empty[2], drain
-constexpr int kPOffMisc = kPOffBar + (2 * kPStages + 5) * 8;
-constexpr int kPOffTurn = (kPOffMisc + 16 + 15) / 16 * 16;
-// eight epilogue warps' bias of their half of the columns (kWhole), or 32 x 33 blocks
-constexpr int kPSmemWhole = kPOffTurn + 8 * (kPTile / 2) * 4;
-constexpr int kPSmem = kPOffTurn + 8 * 32 * 33 * 4;
-static_assert(kPSmem <= 232448, "dynamic shared memory of one CTA");
+template <bool kWhole>
+struct PairCfg {
+  // Rows that are no whole sectors cost the epilogue more: twice the warps, a stage less (2000
+  // x 3001 x 1504 33 us, with eight warps 47).
+  static constexpr int kStages = kWhole ? 6 : 5;
+  static constexpr int kWarps = kWhole ? 8 : 16;              // epilogue warps
+  static constexpr int kCols = kPTile / (kWarps / 4);         // a warp's columns of the tile
+  static constexpr int kThreads = 128 + 32 * kWarps;          // TMA, MMA, two idle warps
+  static constexpr int kOffBar = kStages * kPStageBytes;
+  // full[S], empty[S], acc_full[2], acc_empty[2], drain
+  static constexpr int kOffMisc = kOffBar + (2 * kStages + 5) * 8;
+  // per epilogue warp: its columns' bias (kWhole), or a 32 x 33 block
+  static constexpr int kOffTurn = (kOffMisc + 16 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffTurn + kWarps * (kWhole ? kCols * 4 : 32 * 33 * 4);
+  static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
+};
 // Tiles are walked in bands of this many output rows' tiles, column by column, so that the
 // tiles in flight share both operands' blocks in L2.
 constexpr int kPBand = 8;
@@ -281,36 +288,35 @@ __device__ __forceinline__ PairTile pair_tile(int L, int tiles_t, int tiles_f) {
 
 // CTA r of a pair: output rows 128 r.. of the tile (its P rows and accumulator lanes) and Q
 // rows 128 r.. (half of the MMA's N side).
-constexpr int kPThreads = 384;  // TMA warp, MMA warp, two idle, eight epilogue warps
-
 // kWhole: the output's rows (and the residual's and z's) are whole 32-byte sectors.
 // S > 1 (few tiles): one tile per cluster of S pairs, each of which sums an S-th of c; the
 // partial sums meet in distributed shared memory (the drained rings), where pair i finishes
 // the i-th part of the tile's columns, adding in pair order.
 template <bool kWhole, int S>
-__global__ void __launch_bounds__(kPThreads, 1)
+__global__ void __launch_bounds__(PairCfg<kWhole>::kThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                   const LinearParams p) {
+  using C = PairCfg<kWhole>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t crank = cluster_ctarank(), rank = crank & 1, pair = crank >> 1;
   const bool leader = rank == 0;
   const uint16_t both = static_cast<uint16_t>(3u << (crank & ~1u));  // this pair's CTAs
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPOffBar);
-  uint64_t* empty = full + kPStages;
-  uint64_t* acc_full = empty + kPStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kPOffMisc + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 16);  // two CTAs' eight epilogue warps
+      mbar_init(&acc_empty[b], 2 * C::kWarps);  // two CTAs' epilogue warps
     }
     mbar_init(drain, 1);
     // swizzled tiles need a 1024-byte aligned base: a misaligned one makes every role a
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   // 32 columns f.. of the warp's 32 rows t - lane.., not whole sectors: turned in shared
   // memory, so that a warp stores 32 consecutive values of a row
   auto ragged = [&](const float (&v32)[32], int t, int f) {
-    float* turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * 32 * 33;
+    float* turn = reinterpret_cast<float*>(smem + C::kOffTurn) + (warp - 4) * 32 * 33;
 #pragma unroll
     for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v32[i];
     __syncwarp();
@@ -373,9 +379,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int t0 = tl.t0 + static_cast<int>(rank) * 128;
         const int f0 = tl.f0 + static_cast<int>(rank) * 128;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kPStages;
-          if (it >= kPStages &&
-              !mbar_wait(&empty[s], ((it / kPStages) & 1u) ^ 1u, p.status, abort_flag)) {
+          const int s = it % C::kStages;
+          if (it >= C::kStages &&
+              !mbar_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u, p.status, abort_flag)) {
             ok = false;
             break;
           }
@@ -399,9 +405,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       // after an abort: the pair's loads still in flight (all counted on these barriers)
       if (leader && *abort_flag) {
-        const uint32_t from = it > kPStages ? it - kPStages : 0;
+        const uint32_t from = it > C::kStages ? it - C::kStages : 0;
         for (uint32_t i = from; i < it; ++i)
-          mbar_wait_drain(&full[i % kPStages], (i / kPStages) & 1u);
+          mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1u);
       }
     }
   } else if (warp == 1) {
@@ -416,8 +422,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + b * kPTile;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kPStages;
-          if (!mbar_wait(&full[s], (it / kPStages) & 1u, p.status, abort_flag)) {
+          const int s = it % C::kStages;
+          if (!mbar_wait(&full[s], (it / C::kStages) & 1u, p.status, abort_flag)) {
             ok = false;
             break;
           }
@@ -439,19 +445,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else if (warp >= 4 && S == 1) {
     // ---------------------------------------------------------------- epilogue
-    // eight warps: four for the accumulator's lanes, twice for halves of its columns
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    // four warps for the accumulator's lanes, and so for each share of its columns
+    const int q = warp & 3, share = (warp - 4) >> 2;
     uint32_t tc = 0;
     for (int L = cl; L < total; L += ncl, ++tc) {  // (an abort makes the wait fail)
       const PairTile tl = pair_tile(L, tiles_t, tiles_f);
       const uint32_t b = tc & 1u, use = tc >> 1;
       const int t = tl.t0 + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const int f0 = tl.f0 + half * (kPTile / 2);
-      const int cols = p.F - f0 < kPTile / 2 ? p.F - f0 : kPTile / 2;
+      const int f0 = tl.f0 + share * C::kCols;
+      const int cols = p.F - f0 < C::kCols ? p.F - f0 : C::kCols;
       // the next 32 columns' residual is in flight under these columns' stores, the first
       // ones' under the tile's last MMAs
       RowRes res;
-      float* bias = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * (kPTile / 2);
+      float* bias = reinterpret_cast<float*>(smem + C::kOffTurn) + (warp - 4) * C::kCols;
       if constexpr (kWhole) {
         if (t < p.R) load_row32(p.e, t, f0, cols, res);
         if (p.e.bias) {
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
       tc_fence_after();
       const uint32_t acc =
-          tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kPTile + half * (kPTile / 2);
+          tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kPTile + share * C::kCols;
       for (int c = 0; c < cols; c += 32) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(acc + c, r);
@@ -498,7 +504,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // ---------------------------------------------------------------- joined epilogue
     constexpr int CW = kPTile / S;  // columns a pair finishes
     const PairTile tl = pair_tile(cl, tiles_t, tiles_f);
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int q = warp & 3, share = (warp - 4) >> 2;
+    constexpr int kStep = 32 * (C::kWarps / 4);  // columns from a warp's block to its next
     const int row = q * 32 + lane, t = tl.t0 + static_cast<int>(rank) * 128 + row;
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
     float* sums = reinterpret_cast<float*>(smem);  // [column of the tile][128 rows]
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) w_ok = mbar_wait(&acc_full[0], 0, p.status, abort_flag);
       w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
       tc_fence_after();
-      for (int c = half * 32; c < kPTile && w_ok; c += 64) {
+      for (int c = share * 32; c < kPTile && w_ok; c += kStep) {
         if (c / CW == static_cast<int>(pair) || tl.f0 + c >= p.F) continue;
         uint32_t r[32];
         tmem_ld_32x32b_x32(acc + c, r);
@@ -519,12 +526,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __syncwarp();
     cluster_sync();  // every pair's sums are in place
     if (warp >= 4) {
-      for (int c = static_cast<int>(pair) * CW + half * 32; c < (static_cast<int>(pair) + 1) * CW;
-           c += 64) {
+      for (int c = static_cast<int>(pair) * CW + share * 32;
+           c < (static_cast<int>(pair) + 1) * CW; c += kStep) {
         const int f = tl.f0 + c;
         if (!w_ok || f >= p.F) break;
         RowRes res;
-        float* bias = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 4) * (kPTile / 2);
+        float* bias = reinterpret_cast<float*>(smem + C::kOffTurn) + (warp - 4) * C::kCols;
         if constexpr (kWhole) {
           if (t < p.R) load_row32(p.e, t, f, p.F - f, res);
           if (p.e.bias) {
@@ -956,8 +963,9 @@ cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearPa
   if (tiles > (1LL << 28)) return cudaErrorInvalidValue;
   void* args[] = {&tmP, &tmQ, const_cast<LinearParams*>(&p)};
   return launch_cluster(reinterpret_cast<const void*>(k_linear_pair<kWhole, S>), ks,
-                        kWhole ? kPSmemWhole : kPSmem, 2 * S,
-                        dim3(static_cast<unsigned>(2 * S * tiles)), kPThreads, S == 1, st, args);
+                        PairCfg<kWhole>::kSmem, 2 * S,
+                        dim3(static_cast<unsigned>(2 * S * tiles)), PairCfg<kWhole>::kThreads,
+                        S == 1, st, args);
 }
 template <bool kWhole>
 cudaError_t launch_pairs(const Operand& P, const Operand& Q, const LinearParams& p, int splits,
@@ -968,7 +976,7 @@ cudaError_t launch_pairs(const Operand& P, const Operand& Q, const LinearParams&
 
 // One product, on the kernel and tile that should take the least time, by costs measured on
 // GB300 (us).  A pair tile: 0.29 per 64 columns of c, 76 tiles at a time, a tile's epilogue
-// (6.3 with whole rows, 18 without) under the next tile's MMAs.  Split tiles: their loads
+// (6.3 with whole rows, 9 without) under the next tile's MMAs.  Split tiles: their loads
 // together at 12.5 TB/s from L2, W's at 6.9 from HBM, a CTA's stages 0.27 to 0.41 each; per
 // wave of 304 CTAs 3 for launch and first load, 0.87 per 16 tokens of a CTA's epilogue and
 // 0.02 per token that a cluster exchanges.  Clusters of 3, 5 and 6 fit the GPU's partitions
@@ -985,11 +993,11 @@ Choice choose(int R, int F, int C, bool p_mn, bool whole) {
   const long long tiles =
       static_cast<long long>((R + kPTile - 1) / kPTile) * ((F + kPTile - 1) / kPTile);
   const double waves = static_cast<double>((tiles + 75) / 76);
-  const double mma = 0.29 * nk, epi = whole ? 6.3 : 18.0;
+  const double mma = 0.29 * nk, epi = whole ? 6.3 : 9.0;
   Choice best = {(waves - 1) * (mma > epi ? mma : epi) + mma + epi, 0, 1};
   // two pairs a tile, while all their clusters fit (four: clusters of eight CTAs with an SM
   // each fit badly, 7168 x 7168 weights and 256 rows 40 us)
-  const double two_us = 0.16 * nk + (whole ? 8.5 : 11.5);
+  const double two_us = 0.16 * nk + (whole ? 8.5 : 10.0);
   if (tiles <= 36 && nk >= 2 && two_us < best.us) best = {two_us, 0, 2};
   const long long ft = (F + kSFeat - 1) / kSFeat;
   for (int nt = p_mn ? 64 : 16; nt <= 128; nt *= 2) {
