@@ -36,6 +36,7 @@ constexpr int kMaxThreads = 512;  // a row's threads: 128 registers each
 constexpr int kRaggedFew = 4;     // columns a thread in rows that are no whole vectors: up to
 constexpr int kRaggedMany = 8;    // 1024 columns, and up to 8192
 constexpr int kStages = 2;        // rows in flight (3: fewer CTAs fit, prefill 333 -> 371 us)
+static_assert(kStages == 2, "the rows' partial sums alternate with the stages");
 constexpr int kWarpRows = 8;      // rows (warps) per CTA when a row takes one warp
 
 template <typename T>
