@@ -15,7 +15,7 @@
 // the pass over 50 MB, the rest the second kernel's chain of dependent loads) and 21.9 us
 // backward (100 MB; 0.70 of the copy bandwidth).
 // No floating-point atomics: partial sums are added in a fixed order, or in fixed point.
-#include "kernels.cuh"
+#include "block.cuh"
 
 namespace moe {
 

@@ -1,6 +1,6 @@
 // C interface (include/moe.h) of the operators around the expert FFN: argument checks,
 // workspace carving and launches.  No allocation, no host synchronisation.
-#include "kernels.cuh"
+#include "block.cuh"
 
 using namespace moe;
 

@@ -126,75 +126,6 @@ cudaError_t launch_combine(const uint16_t* y2, const int32_t* inv, const float* 
                            int H, int has_shared, uint16_t* out, uint32_t* status,
                            cudaStream_t st);
 
-// Residual addition + RMS norm and its gradient (norm.cu).  part: the dgain partials,
-// [norm_bwd_parts(rows, cols)][cols] fp32 (not read when dgain is null).
-int norm_bwd_parts(int rows, int cols);
-cudaError_t launch_add_rmsnorm(const uint16_t* x, const void* res, bool res_f32, const void* gain,
-                               bool gain_f32, float eps, int rows, int cols, void* h, uint16_t* y,
-                               uint8_t* q, uint8_t* s, float* rstd, cudaStream_t st);
-cudaError_t launch_add_rmsnorm_bwd(const uint16_t* dy, const void* h, bool h_f32, const void* gain,
-                                   bool gain_f32, const float* rstd, int rows, int cols,
-                                   const void* dh_in, void* dh, uint16_t* dx, float* dgain,
-                                   float* part, cudaStream_t st);
-
-// out[c] = sum over `parts` rows of part[.][cols], in a fixed order (norm.cu).
-cudaError_t launch_column_sum(const float* part, int parts, int cols, float* out,
-                              cudaStream_t st);
-
-// Dense projection and its gradient (linear.cu).  Row strides in elements.  x_pad / w_pad
-// are non-null where that operand's rows are not whole 16-byte vectors: room for a copy
-// with rows of linear_padded(columns).
-inline long long linear_padded(int cols) { return (static_cast<long long>(cols) + 7) / 8 * 8; }
-struct LinearCall {
-  int M, N, K, act;
-  const uint16_t *x, *w;
-  const void *bias, *res;
-  void* y;
-  uint16_t* z;
-  long long ldx, ldw, ldr, ldy, ldz;
-  int bias_f32, y_f32;  // the residual has y's type
-  uint16_t *x_pad, *w_pad;
-  uint32_t* status;
-};
-cudaError_t launch_linear(const LinearCall& a, cudaStream_t st);
-constexpr int kLinearDbParts = 256;  // row blocks of the bias gradient's partial sums
-struct LinearBwdCall {
-  int M, N, K, act;
-  const uint16_t *x, *w, *z, *dy;
-  long long ldx, ldw, ldz, lddy, lddx, lddw;
-  uint16_t *dx, *dw;  // or null
-  float* db;          // or null
-  uint16_t* dz;       // [M][linear_padded(N)] where dy itself is not the products' operand
-  float* part;        // [kLinearDbParts][N] with db
-  uint16_t *x_pad, *w_pad;
-  uint32_t* status;
-};
-cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st);
-
-// Router balance loss and its gradient (balance.cu).  The forward's first kernel runs
-// balance_ctas(T, E) <= kBalanceCtas CTAs and writes one partial slot per (CTA, sequence)
-// pair that has rows: balance_ctas(T, E) + S - 1 slots.
-constexpr int kBalanceCtas = 304;
-struct BalanceWs {
-  uint32_t* status;
-  uint32_t* flags;   // [balance_ctas(T, E)] status bits, by CTA
-  float* p;          // [slots][E] sums of p
-  int32_t* c;        // [slots][E] counts
-  float* z;          // [slots]
-  int32_t* n;        // [slots] counted tokens
-  unsigned long long* acc;  // [S] loss sums and arrivals
-};
-int balance_ctas(int T, int E);
-cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
-                                const uint8_t* mask, int T, int E, int k, int S,
-                                const BalanceWs& w, int32_t* counts, int32_t* n_tokens,
-                                float* prob, float* loss, float* z_loss, cudaStream_t st);
-cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const int32_t* off,
-                               const uint8_t* mask, const int32_t* counts,
-                               const int32_t* n_tokens, const float* dloss, const float* dz,
-                               const float* dw, int T, int E, int k, int S, float* dlogits,
-                               cudaStream_t st);
-
 struct GemmLaunch {
   const uint8_t* w_codes;     // [G][N][K/2]
   const uint8_t* w_scales;    // [G][N][K/32]
@@ -276,23 +207,6 @@ cudaError_t launch_expand_rows(const uint8_t* xq, const uint8_t* xs, const int32
 // per-context state (a function attribute, a symbol's device address) are keyed on it:
 // a context created after cudaDeviceReset has a new id, so the state is set up again.
 unsigned long long current_context_id();
-
-// Lets `kern` take all of a CTA's shared memory that its static arrays leave (at most 1 KB),
-// once per context.
-constexpr int kSmemMax = 226 * 1024;
-template <auto kern>
-cudaError_t allow_smem() {
-  static unsigned long long attr_ctx[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const unsigned long long ctx = current_context_id();
-  if (ctx != 0 && attr_ctx[dev] == ctx) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-  if (e == cudaSuccess) attr_ctx[dev] = current_context_id();
-  return e;
-}
 
 // Transaction bytes one 128 x 128 weight-tile TMA load reports to its mbarrier: the
 // packed global size (128 rows x 64 bytes), not the 16-byte-aligned shared-memory

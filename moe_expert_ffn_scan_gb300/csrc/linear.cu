@@ -21,7 +21,7 @@
 //     in rank order (no atomics, no workspace).  Bound by reading W for few tokens (7 x 7168
 //     x 7168: 20 us, 15.4 of them the weights' at the copy bandwidth).
 // Every wait is bounded; one that expires sets the workspace's status word.
-#include "kernels.cuh"
+#include "block.cuh"
 
 #include <math.h>
 

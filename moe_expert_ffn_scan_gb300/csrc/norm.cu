@@ -23,7 +23,7 @@
 //   * any width up to 8192: the CTA copies the aligned chunks that hold its row, a thread
 //     reads single columns (20000 x 1023: 40 us, 53 with direct loads);
 //   * wider rows are read twice, the second time from L2.
-#include "kernels.cuh"
+#include "block.cuh"
 
 #include <atomic>
 
