@@ -197,7 +197,7 @@ int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* r
 size_t moe_add_rmsnorm_backward_workspace_size(int32_t rows, int32_t cols) {
   if (rows < 0 || cols < 1) return 0;
   const size_t parts = norm_bwd_parts(rows, cols);
-  return align_up(parts * static_cast<size_t>(cols) * sizeof(float));
+  return kAlign + align_up(parts * static_cast<size_t>(cols) * sizeof(float));
 }
 
 int moe_add_rmsnorm_backward(int32_t rows, int32_t cols, const uint16_t* dy, const void* h,
@@ -211,15 +211,18 @@ int moe_add_rmsnorm_backward(int32_t rows, int32_t cols, const uint16_t* dy, con
   if (!null_or(dy, 16) || !null_or(h, 16) || !null_or(gain, 16) || !null_or(rstd, 4) ||
       !null_or(dh_in, 16) || !null_or(dh, 16) || !null_or(dx, 16) || !null_or(dgain, 4))
     return MOE_ERR_INVALID_ARG;
+  float* part = nullptr;
   if (dgain) {
     if (!ws || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe_add_rmsnorm_backward_workspace_size(rows, cols))
       return MOE_ERR_WORKSPACE_TOO_SMALL;
+    // behind the first 256 bytes, a status word's place in every other workspace (which the
+    // binding's allocation clears on the stream that is current there)
+    part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAlign);
   }
   return cuda_rc(launch_add_rmsnorm_bwd(dy, h, h_dtype == MOE_DTYPE_F32, gain,
                                         gain_dtype == MOE_DTYPE_F32, rstd, rows, cols, dh_in, dh,
-                                        dx, dgain, static_cast<float*>(ws),
-                                        static_cast<cudaStream_t>(stream)));
+                                        dx, dgain, part, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t k, int32_t S) {
