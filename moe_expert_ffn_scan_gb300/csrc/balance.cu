@@ -611,7 +611,8 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const in
     const size_t smem = sizeof(float) * rows * E * 2;
     const cudaError_t a = allow_smem<kern>();
     if (a != cudaSuccess) return a;
-    return launch_k(kern, ctas, kWarps * 32, smem, st, logits, idx, off, mask, counts, n_tokens, dloss, dz, dw, T, E, k, S, per, dlogits);
+    return launch_k(kern, ctas, kWarps * 32, smem, st, logits, idx, off, mask, counts, n_tokens,
+                    dloss, dz, dw, T, E, k, S, per, dlogits);
   });
 }
 

@@ -823,8 +823,8 @@ cudaError_t fwd_types(const uint16_t* x, const void* res, const void* gain, floa
     const int used = (cols + t * 8 - 1) / (t * 8);  // vectors a thread has
     const int smem = kStages * used * (1 + (r ? kChunks<RT> : 0)) * t * per_cta * 16;
     if (t == 32)
-      return launch_resident<k_add_rmsnorm_vec<RT, GT, 2, true>>(need, block, smem, st, nullptr, x, r, g,
-                                                                 eps, rows, cols, o);
+      return launch_resident<k_add_rmsnorm_vec<RT, GT, 2, true>>(
+          need, block, smem, st, nullptr, x, r, g, eps, rows, cols, o);
     return nv == 2 ? launch_resident<k_add_rmsnorm_vec<RT, GT, 2, false>>(
                          need, block, smem, st, nullptr, x, r, g, eps, rows, cols, o)
                    : launch_resident<k_add_rmsnorm_vec<RT, GT, 4, false>>(
@@ -880,7 +880,8 @@ cudaError_t bwd_types(const NormBwd& p, int rows, int cols, float* dgain, cudaSt
     e = launch_k(k_add_rmsnorm_bwd_wide<RT, GT>, rows, kMaxThreads, 0, st, p, cols);
   } else if (b.vec) {
     const dim3 block(b.t, b.per_cta);
-    int smem = bwd_stages(b.nv) * b.nv * (1 + (p.dh_in ? 2 : 1) * kChunks<RT>) * b.t * b.per_cta * 16;
+    int smem =
+        bwd_stages(b.nv) * b.nv * (1 + (p.dh_in ? 2 : 1) * kChunks<RT>) * b.t * b.per_cta * 16;
     if (b.t == 32) smem = max(smem, kWarpRows * cols * 4);
     if (b.t == 32)
       e = launch_resident<k_add_rmsnorm_bwd_vec<RT, GT, 2, true>>(most, block, smem, st, &parts, p,
