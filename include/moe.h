@@ -488,6 +488,7 @@ int moe_linear(const moe_linear_desc* d, const uint16_t* x, const uint16_t* w, c
 
 /* Its gradient, from dy [M][N] bf16 (the residual's gradient is dy itself):
  *     dz = dy * act'(z);   dx = dz W,   dw = dz^T x,   dbias = sum over rows of dz.
+ *   (relu: dz = 0 where z <= 0, whatever dy holds there.)
  *   x, w, z as in the forward (z: with an activation; x only for dw, w only for dx).
  *   Outputs, at least one: dx [M][K], dw [N][K] bf16 contiguous, dbias [N] fp32 (sums of
  *   unrounded fp32 dz in a fixed order).  The products take dz rounded to bf16, as the

@@ -88,6 +88,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
   return 1.f;
 }
+// dy * act'(z); a ReLU that is off passes nothing on, an infinity or NaN neither
+__device__ __forceinline__ float act_grad(float dy, float z, int act) {
+  return act == MOE_ACT_RELU && z <= 0.f ? 0.f : dy * act_slope(z, act);
+}
 
 __device__ __forceinline__ float bias_at(const Epi& e, int f) {
   return e.bias_f32 ? __ldg(static_cast<const float*>(e.bias) + f)
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(128)
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      if (z) a[i] *= act_slope(s[i], act);
+      if (z) a[i] = act_grad(a[i], s[i], act);
       sum[i] += a[i];
     }
     if (dz) {

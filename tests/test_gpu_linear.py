@@ -194,6 +194,29 @@ def test_rows_do_not_meet():
         assert torch.equal(y0[keep], y1[keep]) and bool(torch.isnan(y1[3]).all())
 
 
+@pytest.mark.parametrize("N", [64, 61])
+def test_relu_passes_nothing_where_it_is_off(N):
+    """dy of NaN and infinities under z <= 0 reaches no gradient; a NaN in z does."""
+    M, K = 70, 96
+    g = _gen(M, N, K)
+    x, w, dy = _ints(g, M, K), _ints(g, N, K), _ints(g, M, N)
+    z = (torch.arange(M * N, device=DEV).view(M, N) % 3 - 1).to(BF16)
+    off = z <= 0
+    junk = torch.tensor([float("nan"), float("inf"), -float("inf")], device=DEV, dtype=BF16)
+    bad = torch.where(off, junk[torch.arange(M * N, device=DEV).view(M, N) % 3], dy)
+    dz = torch.where(off, torch.zeros_like(dy), dy).to(F64)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device=DEV)
+    ws = moe.alloc_workspace(moe.linear_backward_workspace_size(M, N, K))
+    moe.moe_linear_backward(x, w, bad, ws, z=z, act="relu", dx=dx, dw=dw, dbias=db)
+    assert torch.equal(dx, (dz @ w.to(F64)).float().to(BF16))
+    assert torch.equal(dw, (dz.t() @ x.to(F64)).float().to(BF16))
+    assert torch.equal(db, dz.sum(0).float())
+    z[3, 5] = float("nan")
+    moe.moe_linear_backward(x, w, dy, ws, z=z, act="relu", dx=dx, dw=dw, dbias=db)
+    assert bool(torch.isnan(dx[3]).all()) and bool(torch.isnan(dw[5]).all())
+    assert torch.nonzero(torch.isnan(db)).flatten().tolist() == [5]
+
+
 def test_no_rows():
     w = torch.ones(64, 32, dtype=BF16, device=DEV)
     x, y = torch.empty(0, 32, dtype=BF16, device=DEV), torch.empty(0, 64, dtype=BF16, device=DEV)
