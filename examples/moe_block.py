@@ -93,7 +93,7 @@ class MoEBlock:
             f["logits"], f["idx"], o["counts"], o["n_tokens"], g["dlogits"],
             dloss=torch.full((S,), balance, device=dev), dz_loss=torch.full((S,), z, device=dev),
             **seqs)
-        # the gate projection is one more product: bf16 operands, scaled into bf16's middle
+        # the gate projection is one more product, its operands in bf16
         bf = torch.bfloat16
         g["dy"], g["dwg"] = new(T, H, dt=bf), new(E, H, dt=bf)
         moe.moe_linear_backward(f["y"], self.wg.to(bf), g["dlogits"].to(bf), self.ws_grad,

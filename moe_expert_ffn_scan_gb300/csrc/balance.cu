@@ -569,6 +569,11 @@ int balance_ctas(int T, int E) {
   return n < 1 ? 1 : n;  // (T = 0: one CTA, which clears the sums)
 }
 
+int balance_ctas_most(int T, int E) {
+  const int n = static_cast<int>((static_cast<long long>(T) + fwd_warps(E) - 1) / fwd_warps(E));
+  return n < 1 ? 1 : n < kBalanceCtas ? n : kBalanceCtas;
+}
+
 cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
                                 const uint8_t* mask, int T, int E, int k, int S,
                                 const BalanceWs& w, int32_t* counts, int32_t* n_tokens,

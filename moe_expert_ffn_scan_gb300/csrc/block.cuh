@@ -132,11 +132,13 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st);
 
 // Router balance loss and its gradient (balance.cu).  The forward's first kernel runs
 // balance_ctas(T, E) <= kBalanceCtas CTAs and writes one partial slot per (CTA, sequence)
-// pair that has rows: balance_ctas(T, E) + S - 1 slots.
+// pair that has rows: balance_ctas(T, E) + S - 1 slots.  That count falls by some CTAs
+// wherever the rows of a CTA become one more; workspaces have balance_ctas_most(T, E), which
+// never falls: one made for the longest step does for every shorter one.
 constexpr int kBalanceCtas = 304;
 struct BalanceWs {
   uint32_t* status;
-  uint32_t* flags;   // [balance_ctas(T, E)] status bits, by CTA
+  uint32_t* flags;   // [balance_ctas_most(T, E)] status bits, by CTA
   float* p;          // [slots][E] sums of p
   int32_t* c;        // [slots][E] counts
   float* z;          // [slots]
@@ -144,6 +146,7 @@ struct BalanceWs {
   unsigned long long* acc;  // [S] loss sums and arrivals
 };
 int balance_ctas(int T, int E);
+int balance_ctas_most(int T, int E);
 cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const int32_t* off,
                                 const uint8_t* mask, int T, int E, int k, int S,
                                 const BalanceWs& w, int32_t* counts, int32_t* n_tokens,

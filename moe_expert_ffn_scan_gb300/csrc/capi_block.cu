@@ -41,9 +41,9 @@ bool balance_ok(int T, int E, int k, int S) {
 
 BalanceWs carve_balance(Carver& c, int T, int E, int S) {
   BalanceWs w;
-  const size_t slots = static_cast<size_t>(balance_ctas(T, E)) + S - 1;
+  const size_t ctas = balance_ctas_most(T, E), slots = ctas + S - 1;
   w.status = c.take<uint32_t>(64);
-  w.flags = c.take<uint32_t>(balance_ctas(T, E));
+  w.flags = c.take<uint32_t>(ctas);
   w.p = c.take<float>(slots * E);
   w.c = c.take<int32_t>(slots * E);
   w.z = c.take<float>(slots);

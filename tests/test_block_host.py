@@ -165,3 +165,16 @@ def test_linear_binding_refuses_shapes_types_and_strides():
         moe.moe_linear(x, w, y, ws)
     with pytest.raises(KeyError):
         moe.linear_backward_workspace_size(4, 64, 32, act="tanh")
+
+
+@pytest.mark.parametrize("size", [
+    *[lambda n, E=E, S=S: moe.balance_loss_workspace_size(n, E, 2, S)
+      for E, S in ((8, 1), (384, 3), (61, 37), (1000, 1))],
+    *[lambda n, cols=cols: moe.add_rmsnorm_backward_workspace_size(n, cols)
+      for cols in (1, 512, 1023, 7168, 20008)],
+    *[lambda n, N=N, K=K: moe.linear_workspace_size(n, N, K) for N, K in ((64, 64), (61, 77))],
+    *[lambda n, N=N, K=K: moe.linear_backward_workspace_size(n, N, K)
+      for N, K in ((64, 64), (61, 77), (8, 4096))]])
+def test_a_workspace_for_the_longest_step_does_for_every_shorter_one(lib, size):
+    sizes = [size(n) for n in range(6000)]
+    assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
