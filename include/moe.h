@@ -442,7 +442,8 @@ int moe_add_rmsnorm_backward(int32_t rows, int32_t cols, const uint16_t* dy, con
  *   z_loss [S] fp32 or NULL.  Run-to-run identical (no floating-point atomics).
  *   0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65535, T * k < 2^31.
  *   ws: moe_balance_loss_workspace_size bytes, 256-byte aligned; moe_check_status(ws)
- *   tells of an expert index outside [0, E) (not counted) or decreasing offsets. */
+ *   tells of an expert index outside [0, E) (not counted), of offsets outside [0, T] (read
+ *   as 0 or T) and of decreasing ones (all counts and n_tokens are then 0, the sums NaN). */
 size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t k, int32_t S);
 int moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t S, const float* logits,
                      const int32_t* idx, const int32_t* seq_offsets, const uint8_t* token_mask,

@@ -134,6 +134,10 @@ __device__ __forceinline__ int seq_off(const int32_t* off, int s, int S, int T) 
   return v < 0 ? 0 : v > T ? T : v;
 }
 
+// Beside the STATUS_* bits in a CTA's flags: the offsets decrease somewhere (as seq_off reads
+// them).  The slots that the first kernel fills are then not those that the second would add.
+constexpr uint32_t kDecreasing = 1u << 31;
+
 // The last sequence s with off[s] <= t (0 if there is none).
 __device__ __forceinline__ int seq_of(const int32_t* off, int S, int T, int t) {
   int lo = 0, hi = S - 1;
@@ -147,7 +151,9 @@ __device__ __forceinline__ int seq_of(const int32_t* off, int S, int T, int t) {
 
 // One CTA sums rows [blockIdx.x * per, + per), for each sequence s that has some of them
 // into partial slot blockIdx.x + s.  (Walking the (CTA, sequence) pairs in order, each step
-// raises one of the two, so the slots differ; there are CTAs + S - 1 of them.)
+// raises one of the two, so the slots differ; there are CTAs + S - 1 of them.)  The offsets
+// are checked apart from that walk, which need not come past every pair of them: thread i of
+// the grid has pairs i, i + threads, ...
 template <int NV, int VEC>
 __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
     k_balance_partial(const float* __restrict__ logits, const int32_t* __restrict__ idx,
@@ -164,15 +170,19 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
   __shared__ int ns[W];
   int32_t* hist = reinterpret_cast<int32_t*>(dyn + W * E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the loss sums of the kernel after this one
-  for (int s = blockIdx.x * blockDim.x + threadIdx.x; s < S; s += gridDim.x * blockDim.x)
-    acc[s] = 0;
+  uint32_t bad = 0;  // data-dependent checks of this thread (STATUS_*, kDecreasing)
+  for (int s = blockIdx.x * blockDim.x + threadIdx.x; s < S; s += gridDim.x * blockDim.x) {
+    acc[s] = 0;  // the loss sums of the kernel after this one
+    if (off) {
+      const int lo = __ldg(off + s), hi = __ldg(off + s + 1);
+      if (lo < 0 || hi > T || hi < lo) bad |= STATUS_BAD_PLAN;
+      if (seq_off(off, s + 1, S, T) < seq_off(off, s, S, T)) bad |= kDecreasing;
+    }
+  }
   const int begin = blockIdx.x * per, end = T - begin < per ? T : begin + per;
   int row = begin;
-  uint32_t bad = 0;  // data-dependent checks of this thread (STATUS_*)
   for (int s = seq_of(off, S, T, begin); s < S && row < end; ++s) {
     const int sb = seq_off(off, s, S, T), se = seq_off(off, s + 1, S, T);
-    if (se < sb) bad |= STATUS_BAD_PLAN;
     const int r0 = sb > row ? sb : row, r1 = se < end ? se : end;
     if (r0 >= r1) continue;  // (the same for the whole CTA)
     row = r1;
@@ -248,13 +258,16 @@ __global__ void __launch_bounds__(fwd_warps(NV * VEC * 32) * 32, 2)
   }
   const int plan = __syncthreads_or(bad & STATUS_BAD_PLAN);
   const int index = __syncthreads_or(bad & STATUS_BAD_INDEX);
+  const int decreasing = plan ? __syncthreads_or(bad & kDecreasing) : 0;
   if (threadIdx.x == 0)
-    flags[blockIdx.x] = (plan ? STATUS_BAD_PLAN : 0u) | (index ? STATUS_BAD_INDEX : 0u);
+    flags[blockIdx.x] = (plan ? STATUS_BAD_PLAN : 0u) | (index ? STATUS_BAD_INDEX : 0u) |
+                        (decreasing ? kDecreasing : 0u);
 }
 
 // Adds up the partials of sequence blockIdx.y for 32 experts; warp w takes the slots
 // first + w, + WARPS, ... and the warps' sums are added in order.  The CTA that finishes its
-// sequence last has the sum of the CTAs' loss terms.
+// sequence last has the sum of the CTAs' loss terms.  Decreasing offsets (the first `nchecks`
+// CTAs of the kernel before have looked for them): no slot is added, the sums are NaN.
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS * 32)
     k_balance_final(const int32_t* __restrict__ off, int T, int E, int k, int S, int per,
@@ -263,7 +276,8 @@ __global__ void __launch_bounds__(WARPS * 32)
                     unsigned long long* acc, int32_t* __restrict__ counts,
                     int32_t* __restrict__ n_tokens, float* __restrict__ prob,
                     float* __restrict__ loss, float* __restrict__ z_loss,
-                    const uint32_t* __restrict__ flags, int nflags, uint32_t* status) {
+                    const uint32_t* __restrict__ flags, int nflags, int nchecks,
+                    uint32_t* status) {
   pdl_wait();
   pdl_trigger();
   __shared__ float rp[WARPS][33];
@@ -325,7 +339,10 @@ __global__ void __launch_bounds__(WARPS * 32)
     z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
     n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
   }
-  const float inv = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
+  uint32_t checks = 0;
+  for (int i = lane; i < nchecks; i += 32) checks |= flags[i];
+  float inv = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
+  if (__any_sync(0xFFFFFFFFu, checks & kDecreasing)) c = 0, n = 0, inv = NAN, p = 0.f, z = 0.f;
   p *= inv;
   if (e < E) {
     prob[static_cast<size_t>(s) * E + e] = p;
@@ -588,15 +605,17 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
   });
   if (e != cudaSuccess) return e;
   const dim3 grid((E + 31) / 32, S);
+  const int threads = fwd_warps(E) * 32, checking = (S + threads - 1) / threads;
+  const int checks = !off ? 0 : checking < ctas ? checking : ctas;
   // one sequence has up to kBalanceCtas slots, one of many a share of them (64 sequences of
   // 32768 tokens with 1024 threads each: 28 us instead of 18)
   if (S > 8)
     return launch_k(k_balance_final<8>, grid, 256, 0, st, off, T, E, k, S, per, w.p, w.c, w.z, w.n,
                     w.acc, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
-                    w.status);
+                    checks, w.status);
   return launch_k(k_balance_final<32>, grid, 1024, 0, st, off, T, E, k, S, per, w.p, w.c, w.z, w.n,
                   w.acc, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
-                  w.status);
+                  checks, w.status);
 }
 
 cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const int32_t* off,

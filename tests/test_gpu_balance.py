@@ -238,3 +238,35 @@ def test_offsets_past_32_bits(E):
     o1 = torch.empty_like(last)
     moe.moe_balance_loss_backward(last, li, own["counts"], own["n_tokens"], o1, one[:1], one[:1])
     assert torch.equal(out[-n:], o1)
+
+
+@pytest.mark.parametrize("off", [[0, 30, 20, 50], [0, 32, 20, 50], [0, 50, 5, 50],
+                                 [0] * 1500 + [17, 16, 50], [50, 0], [0, 48, 50, 49]])
+def test_decreasing_offsets_are_reported_wherever_they_lie(off):
+    """Also where no block of rows that is summed at once has the pair inside it.  Nothing is
+    summed then: no counts, and the sums are NaN."""
+    lg, idx, _, _ = _make(50, 16, 2, 1, False, seed=6)
+    S, off = len(off) - 1, torch.tensor(off, dtype=I32)
+    o, ws = _forward(*_dev(lg, idx, off), None, S, 16)
+    assert moe.moe_check_status(ws) == moe.STATUS_BAD_PLAN
+    assert torch.count_nonzero(o["counts"]).item() == 0
+    assert torch.count_nonzero(o["n_tokens"]).item() == 0
+    assert all(bool(torch.isnan(o[n]).all()) for n in ("prob", "loss", "z_loss"))
+    # the gradient from these counts is zero
+    out = torch.full((50, 16), 7.0, device=DEV)
+    one = torch.ones(S, device=DEV)
+    moe.moe_balance_loss_backward(*_dev(lg, idx), o["counts"], o["n_tokens"], out, one, one,
+                                  seq_offsets=off.to(DEV))
+    assert torch.count_nonzero(out).item() == 0
+
+
+@pytest.mark.parametrize("off,inside", [([0, 20, 60], [0, 20, 50]), ([-3, 20, 50], [0, 20, 50]),
+                                        ([-9, -1, 70], [0, 0, 50])])
+def test_offsets_outside_the_tokens_are_reported(off, inside):
+    """They are read as the nearest token there is."""
+    lg, idx, _, _ = _make(50, 16, 2, 1, False, seed=6)
+    o, ws = _forward(*_dev(lg, idx, torch.tensor(off, dtype=I32)), None, 2, 16)
+    assert moe.moe_check_status(ws) == moe.STATUS_BAD_PLAN
+    want, ws = _forward(*_dev(lg, idx, torch.tensor(inside, dtype=I32)), None, 2, 16)
+    assert moe.moe_check_status(ws) == 0
+    assert all(torch.equal(o[n], want[n]) for n in o)
