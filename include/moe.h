@@ -473,8 +473,8 @@ int moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t S, const 
  *   8 elements are first copied to padded rows in the workspace (the strides decide; a
  *   weight kept with a padded stride saves that copy in every call).
  *   ws: moe_linear_workspace_size bytes, 256-byte aligned.  Its first 4 bytes are a status
- *   word that these two calls only set bits of: zero it once, before the first use, and keep
- *   the workspace to them; moe_check_status reads it. */
+ *   word that these two calls only set bits of: zero it once, before the first use and in an
+ *   order with it, and keep the workspace to them; moe_check_status reads it. */
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
 typedef struct moe_linear_desc {
   int32_t M, N, K;

@@ -257,11 +257,13 @@ def gemm_workspace_size(d) -> int:
     return lib().moe_gemm_workspace_size(_d(d))
 
 
-def alloc_workspace(nbytes, device="cuda"):
+def alloc_workspace(nbytes, device="cuda", stream=None):
     """A workspace tensor (torch allocations are 256-byte aligned or better), its status
-    word zeroed."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+    word zeroed.  It belongs to `stream` (None: the current one), which does the zeroing:
+    calls that use it on another stream have to be ordered behind that."""
+    with torch.cuda.stream(stream):
+        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+        ws[:256].zero_()
     return ws
 
 
@@ -687,6 +689,9 @@ class HostPipeline:
         if size == 0:
             raise ValueError(f"unsupported dims or depth {depth} (1..8)")
         self.ws = alloc_workspace(size, layer.w13.device)
+        # the pipeline's own streams wait for no other: what is queued for this memory (its
+        # zeroing, its last owner's kernels) and for the weights ends first
+        torch.cuda.current_stream(layer.w13.device).synchronize()
         self._weights = (layer.w13, layer.w13_s, layer.w2, layer.w2_s)  # kept alive
         W = moe_weights(*[_p(t) for t in self._weights])
         h = _P()
@@ -748,12 +753,12 @@ class MoELayer:
     def dims(self, T):
         return dims(T, self.H, self.I, self.E, self.k, self.has_shared)
 
-    def workspace(self, T):
+    def workspace(self, T, stream=None):
         if self._ws is None or self._T < T:
             size = (workspace_size if self.fmt == "mxfp4" else workspace_size_nvfp4)(self.dims(T))
             if size == 0:
                 raise ValueError(f"unsupported dims for {self.fmt} weights")
-            self._ws = alloc_workspace(size, self.w13.device)
+            self._ws = alloc_workspace(size, self.w13.device, stream)
             self._T = T
         return self._ws
 
@@ -761,10 +766,11 @@ class MoELayer:
         if self.fmt != "mxfp4":
             raise NotImplementedError(f"{what} takes MXFP4 weights")
 
-    def host_workspace(self, T):
+    def host_workspace(self, T, stream=None):
         self._mxfp4_only("the host-buffer forward")
         if getattr(self, "_hws", None) is None or self._hT < T:
-            self._hws = alloc_workspace(host_workspace_size(self.dims(T)), self.w13.device)
+            self._hws = alloc_workspace(host_workspace_size(self.dims(T)), self.w13.device,
+                                        stream)
             self._hT = T
         return self._hws
 
@@ -778,7 +784,7 @@ class MoELayer:
         (pinned) in, out_host [T, H] bf16 (pinned) written when the stream reaches it."""
         T = x_host.shape[0]
         moe_forward_host(self.dims(T), x_host, logits_host, self.w13, self.w13_s, self.w2,
-                         self.w2_s, out_host, self.host_workspace(T), stream=stream)
+                         self.w2_s, out_host, self.host_workspace(T, stream), stream=stream)
         return out_host
 
     def host_graph(self, T):
@@ -792,12 +798,12 @@ class MoELayer:
             out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
         if self.fmt == "mxfp4":
             moe_forward_ex(self.dims(T), x, logits, self.w13, self.w13_s, self.w2, self.w2_s, out,
-                           self.workspace(T), fuse_combine=self.fuse_combine,
+                           self.workspace(T, stream), fuse_combine=self.fuse_combine,
                            fuse_swiglu=self.fuse_swiglu, pair_tiles=self.pair_tiles,
                            large_chunk_rows=self.large_chunk_rows, debug=debug, stream=stream)
         else:
             moe_forward_nvfp4(self.dims(T), x, logits, self.w13, self.w13_s, self.w13_gs,
-                              self.w2, self.w2_s, self.w2_gs, out, self.workspace(T),
+                              self.w2, self.w2_s, self.w2_gs, out, self.workspace(T, stream),
                               debug=debug, stream=stream)
         return out
 
@@ -839,12 +845,12 @@ class MoELayer:
         T = x.shape[0]
         if self.fmt == "mxfp4":
             moe_forward_ex(self.dims(T), x, logits, self.w13, self.w13_s, self.w2, self.w2_s, out,
-                           self.workspace(T), fuse_combine=self.fuse_combine,
+                           self.workspace(T, stream), fuse_combine=self.fuse_combine,
                            fuse_swiglu=self.fuse_swiglu, pair_tiles=self.pair_tiles,
                            large_chunk_rows=self.large_chunk_rows, events=events,
                            stream=stream)
         else:
             moe_forward_nvfp4_timed(self.dims(T), x, logits, self.w13, self.w13_s, self.w13_gs,
-                                    self.w2, self.w2_s, self.w2_gs, out, self.workspace(T),
+                                    self.w2, self.w2_s, self.w2_gs, out, self.workspace(T, stream),
                                     events, stream=stream)
         return out
