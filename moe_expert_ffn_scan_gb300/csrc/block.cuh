@@ -2,6 +2,7 @@
 // interface, capi_block.cu): device helpers beyond common.cuh's and launch declarations.
 #pragma once
 
+#include "context_once.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -162,15 +163,14 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const in
 constexpr int kSmemMax = 226 * 1024;
 template <auto kern>
 cudaError_t allow_smem() {
-  static unsigned long long attr_ctx[64] = {};
+  static OncePerContext once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const unsigned long long ctx = current_context_id();
-  if (ctx != 0 && attr_ctx[dev] == ctx) return cudaSuccess;
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
+  if (once.ready(dev, current_context_id())) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-  if (e == cudaSuccess) attr_ctx[dev] = current_context_id();
+  if (e == cudaSuccess) once.set(dev, 0);
   return e;
 }
 

@@ -895,18 +895,13 @@ bool encode(CUtensorMap* m, const Operand& o, int C, int box_rows) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Per-device facts of a kernel, set up once per context.
-struct KernelState {
-  unsigned long long ctx[64] = {};
-  int clusters[64] = {};
-};
-
-cudaError_t launch_cluster(const void* kern, KernelState& ks, int smem, int cluster, dim3 grid,
+// ks: of a persistent kernel, how many of its clusters fit the GPU at once.
+cudaError_t launch_cluster(const void* kern, OncePerContext& ks, int smem, int cluster, dim3 grid,
                            int threads, bool persistent, cudaStream_t st, void** args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -919,25 +914,25 @@ cudaError_t launch_cluster(const void* kern, KernelState& ks, int smem, int clus
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  const unsigned long long ctx = current_context_id();
-  if (ctx == 0 || ks.ctx[dev] != ctx) {
+  int clusters = 0;
+  if (ks.ready(dev, current_context_id())) {
+    clusters = ks.value(dev);
+  } else {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (persistent) {
-      int sms = 0, n = 0;
+      int sms = 0;
       e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3(sms / cluster * cluster);
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
       if (e != cudaSuccess) return e;
-      if (n < 1) return cudaErrorInvalidConfiguration;
-      ks.clusters[dev] = n;
+      if (clusters < 1) return cudaErrorInvalidConfiguration;
     }
-    ks.ctx[dev] = current_context_id();
+    ks.set(dev, clusters);
   }
-  if (persistent && grid.x > static_cast<unsigned>(ks.clusters[dev]) * cluster)
-    grid.x = ks.clusters[dev] * cluster;
+  if (persistent && grid.x > static_cast<unsigned>(clusters) * cluster) grid.x = clusters * cluster;
   cfg.gridDim = grid;
   cfg.numAttrs = 2;
   return cudaLaunchKernelExC(&cfg, kern, args);
@@ -946,7 +941,7 @@ cudaError_t launch_cluster(const void* kern, KernelState& ks, int smem, int clus
 template <int NT>
 cudaError_t launch_split(const Operand& P, const Operand& Q, const LinearParams& p, int splits,
                          cudaStream_t st) {
-  static KernelState ks;
+  static OncePerContext ks;
   CUtensorMap tmP, tmQ;
   if (!encode(&tmP, P, p.C, NT) || !encode(&tmQ, Q, p.C, kSFeat)) return cudaErrorInvalidValue;
   const dim3 grid(splits, (p.F + kSFeat - 1) / kSFeat, (p.R + NT - 1) / NT);
@@ -959,7 +954,7 @@ cudaError_t launch_split(const Operand& P, const Operand& Q, const LinearParams&
 template <bool kWhole, int S>
 cudaError_t launch_pair_tiles(const Operand& P, const Operand& Q, const LinearParams& p,
                               cudaStream_t st) {
-  static KernelState ks;
+  static OncePerContext ks;
   CUtensorMap tmP, tmQ;
   if (!encode(&tmP, P, p.C, 128) || !encode(&tmQ, Q, p.C, 128)) return cudaErrorInvalidValue;
   const long long tiles = static_cast<long long>((p.R + kPTile - 1) / kPTile) *

@@ -1,0 +1,49 @@
+// Stand-ins of the CUDA runtime's functions that the launches call (_launch_threads.cu).  They
+// use relaxed atomics only: nothing in here orders one thread behind the other.
+#include <cuda_runtime_api.h>
+
+#include <atomic>
+#include <chrono>
+#include <thread>
+
+std::atomic<int> launches{0}, empty_grids{0};
+
+namespace {
+void setup_takes_a_while() { std::this_thread::sleep_for(std::chrono::milliseconds(2)); }
+}  // namespace
+
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { return *d = 0, cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { return *v = 152, cudaSuccess; }
+cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) {
+  setup_takes_a_while();
+  return cudaSuccess;
+}
+cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t* c) {
+  setup_takes_a_while();
+  return *n = 152 / static_cast<int>(c->attrs[0].val.clusterDim.x), cudaSuccess;
+}
+cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int* n, const void*, int, size_t,
+                                                                   unsigned) {
+  setup_takes_a_while();
+  return *n = 2, cudaSuccess;
+}
+cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void*, void**) {
+  launches.fetch_add(1, std::memory_order_relaxed);
+  if (c->gridDim.x == 0 || c->gridDim.y == 0 || c->gridDim.z == 0)
+    empty_grids.fetch_add(1, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+// what the compiler's registration code refers to
+void** __cudaRegisterFatBinary(void*) { return nullptr; }
+void __cudaRegisterFatBinaryEnd(void**) {}
+void __cudaUnregisterFatBinary(void**) {}
+char __cudaInitModule(void**) { return 1; }
+void __cudaRegisterFunction(void**, const char*, char*, const char*, int, uint3*, uint3*, dim3*,
+                            dim3*, int*) {}
+cudaError_t __cudaGetKernel(cudaKernel_t*, const void*) { return cudaSuccess; }
+cudaError_t __cudaLaunchKernel(cudaKernel_t, dim3, dim3, void**, size_t, cudaStream_t) {
+  return cudaSuccess;
+}
+cudaError_t __cudaPopCallConfiguration(dim3*, dim3*, size_t*, void*) { return cudaSuccess; }
+}
