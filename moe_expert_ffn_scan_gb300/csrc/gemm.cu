@@ -25,8 +25,10 @@
 //     warps 4-7 drain the double-buffered TMEM accumulator (fp32 -> bf16) while the
 //     next tile's MMAs run.
 //   * Every wait is bounded; an expired wait sets a status bit and the CTA unwinds.
+#include <atomic>
 #include <mutex>
 
+#include "context_once.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -1445,16 +1447,15 @@ EncodeTiledFn get_encode_tiled_fn() {
 
 namespace {
 
-struct DevInfo {
-  int sms = 0;
-};
-
-DevInfo& dev_info() {
-  static DevInfo info[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (info[dev].sms == 0) cudaDeviceGetAttribute(&info[dev].sms, cudaDevAttrMultiProcessorCount, dev);
-  return info[dev];
+// SMs of a device (a thread that finds no answer yet asks for it itself).
+int sm_count(int dev) {
+  static std::atomic<int> known[OncePerContext::kDevices] = {};
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
 }
 
 template <int BN_MAX, int STAGES, int KO, int OCC, bool F2>
@@ -1463,20 +1464,19 @@ cudaError_t launch_one_f(const CUtensorMap& tmW, const CUtensorMap& tmX, const G
   using C = GemmCfg<BN_MAX, STAGES, KO, OCC>;
   auto kern = k_gemm_mx<BN_MAX, STAGES, KO, OCC, F2>;
   // the shared-memory attribute is set once per context (again after a reset)
-  static unsigned long long attr_ctx[64] = {};
+  static OncePerContext once;
   int dev = 0;
   cudaGetDevice(&dev);
-  const unsigned long long ctx = current_context_id();
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (ctx == 0 || attr_ctx[dev] != ctx) {
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
+  if (!once.ready(dev, current_context_id())) {
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_ctx[dev] = current_context_id();
+    once.set(dev, 0);
   }
   const long long tiles = static_cast<long long>(max_items) * (p.N / 128);
   if (tiles == 0) return cudaSuccess;
-  const int slots = dev_info().sms * OCC;
+  const int slots = sm_count(dev) * OCC;
   const int grid = static_cast<int>(tiles < slots ? tiles : slots);
   GemmParams q = p;
   q.max_items = max_items;
@@ -1503,12 +1503,11 @@ cudaError_t launch_pair(const CUtensorMap& tmW, const CUtensorMap& tmX, const Ge
                         int max_items, cudaStream_t st) {
   using C = GemmCfg2<BN2, STAGES, SFS, F1>;
   auto kern = k_gemm_mx2<BN2, STAGES, SFS, F1>;
-  static unsigned long long attr_ctx[64] = {};
-  static int max_clusters[64] = {};
+  static OncePerContext once;  // how many clusters fit
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
   const long long pairs = static_cast<long long>(max_items) * (p.N / 256);
   if (pairs == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -1522,19 +1521,19 @@ cudaError_t launch_pair(const CUtensorMap& tmW, const CUtensorMap& tmX, const Ge
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const unsigned long long ctx = current_context_id();
-  if (ctx == 0 || attr_ctx[dev] != ctx) {
+  int fit = 0;
+  if (once.ready(dev, current_context_id())) {
+    fit = once.value(dev);
+  } else {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(2 * (dev_info().sms / 2));
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    cfg.gridDim = dim3(2 * (sm_count(dev) / 2));
+    e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
     if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    max_clusters[dev] = n;
-    attr_ctx[dev] = current_context_id();
+    if (fit < 1) return cudaErrorInvalidConfiguration;
+    once.set(dev, fit);
   }
-  const long long clusters = pairs < max_clusters[dev] ? pairs : max_clusters[dev];
+  const long long clusters = pairs < fit ? pairs : fit;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
   GemmParams q = p;
   q.max_items = max_items;

@@ -44,6 +44,7 @@
 // cut along K (SegWalk) so that no CTA decodes a whole tile alone while the others idle,
 // the part that completes a split tile adding the fp32 partials in part order.
 // Every wait is bounded; an expired wait sets a status bit and the CTA unwinds.
+#include "context_once.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -796,13 +797,12 @@ cudaError_t launch_nv_one(const NvGemmLaunch& a, int v, cudaStream_t st) {
   const int max_items = a.max_items[v];
   const long long tiles = static_cast<long long>(max_items) * (a.N / 128);
   if (tiles == 0) return cudaSuccess;
-  static unsigned long long attr_ctx[64] = {};
+  static OncePerContext once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const unsigned long long ctx = current_context_id();
-  if (ctx == 0 || attr_ctx[dev] != ctx) {
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
+  if (!once.ready(dev, current_context_id())) {
     if (LUT == 2) {  // the table-address immediate assumes this reserved size
       int reserved = -1;
       e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
@@ -811,7 +811,7 @@ cudaError_t launch_nv_one(const NvGemmLaunch& a, int v, cudaStream_t st) {
     }
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_ctx[dev] = current_context_id();
+    once.set(dev, 0);
   }
   int sms = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

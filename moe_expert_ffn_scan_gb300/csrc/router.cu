@@ -14,6 +14,7 @@
 //     thread, K staged 16 columns at a time in shared memory (x converted to fp32).
 // Both accumulate each logit's H products in one fixed order, so results are
 // reproducible run to run.
+#include "context_once.cuh"
 #include "kernels.cuh"
 
 namespace moe {
@@ -425,16 +426,15 @@ cudaError_t launch_router_logits_split(const uint16_t* x, const uint16_t* wg3, f
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  static unsigned long long attr_ctx[64] = {};
+  static OncePerContext once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  const unsigned long long ctx = current_context_id();
-  if (ctx == 0 || attr_ctx[dev] != ctx) {
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
+  if (!once.ready(dev, current_context_id())) {
     e = cudaFuncSetAttribute(k_router_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kRtSmem);
     if (e != cudaSuccess) return e;
-    attr_ctx[dev] = current_context_id();
+    once.set(dev, 0);
   }
   int sms = 0;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -1,4 +1,4 @@
-// Two host threads make their first calls of the operators' launches together, on stand-ins of
+// Two host threads make their first calls of the launches together, on stand-ins of
 // the CUDA runtime (_fake_cudart.cpp, no GPU), under ThreadSanitizer: what the launches keep
 // between calls has to be published in an order.  Each launch's grid is checked as well.
 #include <atomic>
@@ -11,16 +11,10 @@ extern std::atomic<int> launches, empty_grids;
 
 namespace {
 std::atomic<int> waiting{0};
-CUresult encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill) {
-  return CUDA_SUCCESS;
-}
 }  // namespace
 
 namespace moe {
 unsigned long long current_context_id() { return 1; }
-EncodeTiledFn get_encode_tiled_fn() { return encode; }
 }  // namespace moe
 
 namespace {
@@ -55,6 +49,23 @@ int calls() {
   for (int E : {8, 61, 384, 1024})
     failed += launch_balance_bwd(f, i, nullptr, nullptr, i, i, f, f, f, 5000, E, 2, 1, f,
                                  nullptr) != cudaSuccess;
+  // the layer's own: every list of the tile plan, one-SM and SM-pair kernels, both formats
+  uint8_t* c = reinterpret_cast<uint8_t*>(0x10000);
+  for (int form = 0; form < 4; ++form) {
+    GemmLaunch g = {};
+    g.w_codes = g.w_scales = g.act = g.act_scales = c, g.y = p;
+    g.G = 8, g.N = 512, g.K = 1024, g.rows_total = 4000;
+    NvGemmLaunch n = {};
+    n.w_codes = n.w_scales = c, n.act = p, n.y = p;
+    n.G = 8, n.N = 512, n.K = 1024, n.rows_total = 4000;
+    for (int v = 0; v < kNumVariants; ++v) g.max_items[v] = n.max_items[v] = 20;
+    g.max_group_rows = n.max_group_rows = 500;
+    g.pair_tiles = form == 1;
+    if (form == 2) g.hq = g.hs = c;
+    failed += (form < 3 ? launch_grouped_gemm(g, nullptr) : launch_grouped_gemm_nv(n, nullptr)) !=
+              cudaSuccess;
+  }
+  failed += launch_router_logits_split(p, p, f, 3000, 1024, 64, nullptr, nullptr) != cudaSuccess;
   return failed;
 }
 
@@ -71,5 +82,5 @@ int main() {
   a.join(), b.join();
   std::printf("%d launches, %d failed, %d empty grids\n", launches.load(), failed.load(),
               empty_grids.load());
-  return launches.load() > 40 && failed.load() == 0 && empty_grids.load() == 0 ? 0 : 1;
+  return launches.load() > 80 && failed.load() == 0 && empty_grids.load() == 0 ? 0 : 1;
 }

@@ -1,4 +1,4 @@
-"""The operators' host side from two threads at once, under ThreadSanitizer and without a GPU
+"""The launches' host side from two threads at once, under ThreadSanitizer and without a GPU
 (see _launch_threads.cu)."""
 
 import concurrent.futures as cf
@@ -31,7 +31,8 @@ def sanitizer(tmp_path_factory):
 def test_first_calls_of_two_threads(sanitizer):
     d = sanitizer
     flags = ["-gencode", "arch=compute_103a,code=compute_103a", *build.FLAGS, "-I" + build.CSRC]
-    sources = [*[os.path.join(build.CSRC, s) for s in ("linear.cu", "norm.cu", "balance.cu")],
+    sources = [*[os.path.join(build.CSRC, s) for s in
+                 ("linear.cu", "norm.cu", "balance.cu", "gemm.cu", "gemm_nv.cu", "router.cu")],
                os.path.join(HERE, "_launch_threads.cu")]
     objs = [str(d / os.path.basename(s)) + ".o" for s in sources]
     with cf.ThreadPoolExecutor(len(sources)) as ex:
