@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(WARPS * 32)
     k_balance_final(const int32_t* __restrict__ off, int T, int E, int k, int S, int per,
                     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
                     const float* __restrict__ part_z, const int32_t* __restrict__ part_n,
-                    unsigned long long* acc, int32_t* __restrict__ counts,
+                    unsigned long long* acc, float* terms, int32_t* __restrict__ counts,
                     int32_t* __restrict__ n_tokens, float* __restrict__ prob,
                     float* __restrict__ loss, float* __restrict__ z_loss,
                     const uint32_t* __restrict__ flags, int nflags, int nchecks,
@@ -358,15 +358,29 @@ __global__ void __launch_bounds__(WARPS * 32)
   }
   // One atomic does the loss's sum and the arrival: [51:0] the terms in fixed point (each at
   // most k <= 16, to 2^-47: whatever the order, the same sum), [57:52] how many were NaN,
-  // [63:58] arrivals.  The last CTA has it all.
+  // [63:58] arrivals.  The last CTA has it all.  Terms of less than 2^-18 (experts were chosen
+  // that have next to no probability) are left in fp32 as well: where the sum is that small,
+  // all of them are, and it is added up from these, in order.
+  constexpr float kSmall = 1.f / (1 << 18);
+  terms += static_cast<size_t>(s) * gridDim.x;
+  if (n > 0 && term < kSmall) {
+    terms[blockIdx.x] = term;
+    __threadfence();
+  }
   const bool bad = !(term <= 32.f);
   const unsigned long long add =
       (1ull << 58) | (bad ? 1ull << 52 : static_cast<unsigned long long>(
                                              static_cast<double>(term) * 140737488355328.0));
   const unsigned long long all = atomicAdd(acc + s, add) + add;
   if (all >> 58 != gridDim.x) return;
-  const double sum = (all >> 52 & 63) ? nan("") : static_cast<double>(all & ((1ull << 52) - 1)) /
-                                                       140737488355328.0;
+  double sum = static_cast<double>(all & ((1ull << 52) - 1)) / 140737488355328.0;
+  if (all >> 52 & 63) {
+    sum = nan("");
+  } else if (n > 0 && sum < kSmall) {
+    __threadfence();
+    sum = 0.0;
+    for (int i = 0; i < static_cast<int>(gridDim.x); ++i) sum += __ldcg(terms + i);
+  }
   loss[s] = static_cast<float>(sum * E / k);
 }
 
@@ -611,10 +625,10 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
   // 32768 tokens with 1024 threads each: 28 us instead of 18)
   if (S > 8)
     return launch_k(k_balance_final<8>, grid, 256, 0, st, off, T, E, k, S, per, w.p, w.c, w.z, w.n,
-                    w.acc, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
+                    w.acc, w.terms, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
                     checks, w.status);
   return launch_k(k_balance_final<32>, grid, 1024, 0, st, off, T, E, k, S, per, w.p, w.c, w.z, w.n,
-                  w.acc, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
+                  w.acc, w.terms, counts, n_tokens, prob, loss, z_loss, w.flags, ctas,
                   checks, w.status);
 }
 

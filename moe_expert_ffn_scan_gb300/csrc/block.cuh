@@ -145,6 +145,7 @@ struct BalanceWs {
   float* z;          // [slots]
   int32_t* n;        // [slots] counted tokens
   unsigned long long* acc;  // [S] loss sums and arrivals
+  float* terms;             // [S][E / 32, rounded up] the loss terms too small for acc
 };
 int balance_ctas(int T, int E);
 int balance_ctas_most(int T, int E);

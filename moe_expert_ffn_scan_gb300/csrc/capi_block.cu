@@ -49,6 +49,7 @@ BalanceWs carve_balance(Carver& c, int T, int E, int S) {
   w.z = c.take<float>(slots);
   w.n = c.take<int32_t>(slots);
   w.acc = c.take<unsigned long long>(S);
+  w.terms = c.take<float>(static_cast<size_t>(S) * ((E + 31) / 32));
   return w;
 }
 

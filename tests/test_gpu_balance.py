@@ -270,3 +270,23 @@ def test_offsets_outside_the_tokens_are_reported(off, inside):
     want, ws = _forward(*_dev(lg, idx, torch.tensor(inside, dtype=I32)), None, 2, 16)
     assert moe.moe_check_status(ws) == 0
     assert all(torch.equal(o[n], want[n]) for n in o)
+
+
+@pytest.mark.parametrize("E", [33, 64, 200, 1024])
+@pytest.mark.parametrize("gap", [12.0, 18.0, 40.0, 60.0])
+def test_small_losses(E, gap):
+    """Tokens that chose experts of small probability (e^-gap): the loss is small, and as near
+    to its value as any other."""
+    T, k, S = 70, 2, 3
+    g = torch.Generator().manual_seed(E)
+    lg = torch.randn(T, E, generator=g)
+    lg[:, E // 2:] -= gap
+    idx = (E // 2 + torch.randint(0, E // 4, (T, k), generator=g)).to(I32)
+    off = torch.tensor([0, 30, 30, 70], dtype=I32)
+    o, ws = _forward(*_dev(lg, idx, off), None, S, E)
+    assert moe.moe_check_status(ws) == 0
+    loss = ref.balance(lg.double().numpy(), idx.numpy(), off.numpy(), None, S)[3]
+    got = o["loss"].cpu().double().numpy()
+    assert np.all(np.abs(got - loss) <= 2 * TOL * loss) and got[1] == 0
+    again, _ = _forward(*_dev(lg, idx, off), None, S, E)
+    assert torch.equal(o["loss"], again["loss"])
