@@ -407,7 +407,7 @@ enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
  *   The sums run in fp32 on the unrounded a.  q, s equal moe_quant_act's of y, bit for
  *   bit, whether y is written or not: they go straight to moe_grouped_gemm_w13.
  *   h may be residual's buffer (a bf16 residual's also x's) and y may be x's; no other
- *   two may overlap.  Any cols >= 1; whole 16-byte rows (cols % 8 == 0) are faster.
+ *   two may overlap.  1 <= cols <= 2^30; whole 16-byte rows (cols % 8 == 0) are faster.
  *   rows == 0 is a no-op. */
 int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* residual,
                     int32_t res_dtype, const void* gain, int32_t gain_dtype, float eps, void* h,

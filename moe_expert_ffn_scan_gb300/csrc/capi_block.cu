@@ -33,6 +33,7 @@ struct Carver {
 };
 
 constexpr int kMaxTokens = 1 << 30;  // leaves room in 32-bit row arithmetic
+constexpr int kMaxCols = 1 << 30;    // and in the norm's column arithmetic
 
 bool balance_ok(int T, int E, int k, int S) {
   return T >= 0 && T <= kMaxTokens && E >= 1 && E <= 1024 && k >= 1 && k <= 16 && k <= E &&
@@ -181,7 +182,7 @@ int moe_linear_backward(const moe_linear_desc* d, const uint16_t* x, const uint1
 int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* residual,
                     int32_t res_dtype, const void* gain, int32_t gain_dtype, float eps, void* h,
                     uint16_t* y, uint8_t* q, uint8_t* s, float* rstd, void* stream) {
-  if (rows < 0 || cols < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows < 0 || cols < 1 || cols > kMaxCols) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (q && cols % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!dtype_ok(res_dtype) || !dtype_ok(gain_dtype) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
@@ -196,7 +197,7 @@ int moe_add_rmsnorm(int32_t rows, int32_t cols, const uint16_t* x, const void* r
 }
 
 size_t moe_add_rmsnorm_backward_workspace_size(int32_t rows, int32_t cols) {
-  if (rows < 0 || cols < 1) return 0;
+  if (rows < 0 || cols < 1 || cols > kMaxCols) return 0;
   const size_t parts = norm_bwd_parts(rows, cols);
   return kAlign + align_up(parts * static_cast<size_t>(cols) * sizeof(float));
 }
@@ -205,7 +206,7 @@ int moe_add_rmsnorm_backward(int32_t rows, int32_t cols, const uint16_t* dy, con
                              int32_t h_dtype, const void* gain, int32_t gain_dtype,
                              const float* rstd, const void* dh_in, void* dh, uint16_t* dx,
                              float* dgain, void* ws, size_t ws_bytes, void* stream) {
-  if (rows < 0 || cols < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows < 0 || cols < 1 || cols > kMaxCols) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!dtype_ok(h_dtype) || !dtype_ok(gain_dtype)) return MOE_ERR_INVALID_ARG;
   if (!dh && !dx && !dgain) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!dy || !h || !gain || !rstd)) return MOE_ERR_INVALID_ARG;

@@ -69,6 +69,16 @@ def test_add_rmsnorm_backward_refusals(lib):
     assert f(*none) == ARG
 
 
+@pytest.mark.parametrize("cols", [(1 << 30) + 128, (1 << 31) - 512, (1 << 31) - 1])
+def test_add_rmsnorm_refuses_rows_past_its_column_arithmetic(lib, cols):
+    """32-bit column indices step by up to 512 past the row's end."""
+    assert lib.moe_add_rmsnorm(1, cols, A, A, 0, A, 0, 1e-6, A, A, None, None, A, None) == SHAPE
+    assert lib.moe_add_rmsnorm_backward(1, cols, A, A, 0, A, 0, A, A, A, A, A, A, 1 << 50,
+                                        None) == SHAPE
+    assert lib.moe_add_rmsnorm_backward_workspace_size(1, cols) == 0
+    assert lib.moe_add_rmsnorm_backward_workspace_size(1, 1 << 30) > 4 << 30
+
+
 def test_balance_loss_refusals(lib):
     f, size = lib.moe_balance_loss, lib.moe_balance_loss_workspace_size
     assert size(64, 8, 2, 1) > 0 and size(0, 8, 2, 1) > 0
