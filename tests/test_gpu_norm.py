@@ -235,3 +235,27 @@ def test_offsets_past_32_bits(cols):
     moe.moe_add_rmsnorm_backward(y, x, w, rstd, None, dh=dh)
     moe.moe_add_rmsnorm_backward(y1, last, w, r1, None, dh=dh1)
     assert torch.equal(dh[-5:], dh1)
+
+
+# Several rows a CTA (a warp) in each form: rows of one warp, of a CTA's registers with two and
+# four vectors a thread, and odd widths with four and eight columns a thread.
+LONG = [(25000, 256), (4000, 2048), (2000, 7168), (700, 16384), (5000, 1023), (1500, 2049)]
+
+
+@pytest.mark.parametrize("rows,cols", LONG)
+@pytest.mark.parametrize("stream,gain,residual", [("bf16", "fp32", True), ("fp32", "bf16", True),
+                                                  ("bf16", "bf16", False)])
+def test_forward_of_many_rows(rows, cols, stream, gain, residual):
+    test_forward(rows, cols, stream, gain, residual)
+
+
+@pytest.mark.parametrize("rows,cols", [s for s in LONG if s[1] % 128 == 0])
+def test_codes_of_many_rows(rows, cols):
+    test_codes_are_those_of_the_bf16_output(rows, cols, "bf16", True)
+
+
+@pytest.mark.parametrize("rows,cols", LONG)
+@pytest.mark.parametrize("stream,dh_in", [("bf16", True), ("bf16", False), ("fp32", True),
+                                          ("fp32", False)])
+def test_backward_of_many_rows(rows, cols, stream, dh_in):
+    test_backward(rows, cols, stream, "bf16", dh_in)
