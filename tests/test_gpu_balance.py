@@ -290,3 +290,21 @@ def test_small_losses(E, gap):
     assert np.all(np.abs(got - loss) <= 2 * TOL * loss) and got[1] == 0
     again, _ = _forward(*_dev(lg, idx, off), None, S, E)
     assert torch.equal(o["loss"], again["loss"])
+
+
+# Expert counts of every shape that a row has in the lanes: scalar rows of up to 128 and 512
+# experts (100 and 500 above are whole vectors), and the ends of the vector rows.
+MORE = [(150, 101, 5, 3, True), (170, 385, 16, 2, True), (90, 511, 7, 4, False),
+        (60, 255, 4, 1, False), (80, 384, 8, 3, True), (77, 512, 8, 2, False),
+        (50, 260, 3, 2, True), (40, 516, 16, 1, False), (70, 513, 9, 2, True)]
+
+
+@pytest.mark.parametrize("T,E,k,S,mask", MORE)
+def test_forward_of_every_row_shape(T, E, k, S, mask):
+    test_forward(T, E, k, S, mask)
+
+
+@pytest.mark.parametrize("T,E,k,S,mask", MORE)
+@pytest.mark.parametrize("parts", ["all", "loss", "dw"])
+def test_backward_of_every_row_shape(T, E, k, S, mask, parts):
+    test_backward(T, E, k, S, mask, parts)
