@@ -469,6 +469,8 @@ int moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t S, const 
  *   needs).  fp32 products and sums, one rounding to y's (and z's) type.  Row strides ld* in
  *   elements, 0 = contiguous; y may be residual's buffer (the same stride).
  *   act: MOE_ACT_*; silu(z) = z / (1 + e^-z), gelu(z) = z/2 (1 + erf(z / sqrt(2))).
+ *   Finite for every finite z; an infinite z has what the formulas give (NaN for -inf, and in
+ *   the gradient for both).
  *   Any M >= 0 (0: no-op), 1 <= N, K <= 2^22.  x and w whose row stride is not a multiple of
  *   8 elements are first copied to padded rows in the workspace (the strides decide; a
  *   weight kept with a padded stride saves that copy in every call).

@@ -256,3 +256,84 @@ def test_offsets_past_32_bits(N):
     e = N * 2 * U32 * (y[r].to(F64).abs() @ w.to(F64).abs())
     assert bool(((dx[r].to(F64) - want).abs() <= e + U16 * (want.abs() + e)).all())
     assert moe.moe_check_status(ws) == 0 and moe.moe_check_status(wb) == 0
+
+
+# Every (tile, parts of the contraction) that the cost model chooses, of the split kernel
+# (16 to 128 tokens a tile) and of SM pairs (one or two pairs a tile), for whole and ragged rows.
+FORWARD = [(1, 8, 65), (1, 16, 74), (1, 8, 3426), (1, 16, 3360),                  # 16 tokens
+           (20, 2048, 7168), (31, 2048, 7168), (4966, 8, 10), (5062, 16, 11),     # 32
+           (624, 438, 359), (399, 656, 384), (610, 145, 423), (611, 176, 400),
+           (230, 152, 4028), (439, 16, 3856),
+           (5011, 132, 10), (980, 541, 742), (623, 944, 736), (392, 688, 688),    # 64
+           (319, 328, 5391), (471, 144, 5840),
+           (518, 6639, 16), (514, 6544, 32), (864, 816, 1184), (737, 518, 5091),  # 128
+           (579, 688, 5056),
+           (1288, 1327, 648), (300, 7001, 1100)]                                  # two pairs
+BACKWARD = [(5034, 16, 390), (4886, 16, 144), (808, 1152, 1360),                  # dx: pairs
+            (1, 66, 8), (1, 3454, 8), (4966, 8, 10), (5016, 8, 16),               # 16 and 32 tokens
+            (488, 353, 514), (847, 336, 288), (409, 421, 278), (422, 400, 272),
+            (209, 3929, 137), (255, 3856, 144),
+            (4925, 14, 135), (1003, 720, 528), (636, 656, 448), (300, 5389, 334),  # 64
+            (529, 11, 6648), (513, 16, 6672), (1131, 1232, 544), (639, 4695, 773),  # 128
+            (707, 5184, 528),
+            (849, 1570, 907), (1045, 917, 1184), (5000, 512, 520),                # dw: two pairs
+            (1, 8, 16), (202, 8, 16), (2823, 16, 16),                             # 64
+            (9, 6515, 513), (262, 68, 4947), (211, 80, 8288), (5393, 847, 385),   # 128
+            (4676, 608, 816)]
+
+
+@pytest.mark.parametrize("M,N,K", FORWARD)
+@pytest.mark.parametrize("y_dtype", [BF16, F32])
+def test_integers_exactly_on_every_tile(M, N, K, y_dtype):
+    for extras in (False, True):
+        test_integers_exactly(M, N, K, y_dtype, extras)
+
+
+@pytest.mark.parametrize("M,N,K", BACKWARD)
+def test_backward_integers_exactly_on_every_tile(M, N, K):
+    test_backward_integers_exactly(M, N, K)
+
+
+EXTREMES = [float("inf"), -float("inf"), float("nan"), 3.3e38, -3.3e38, 1.8e19, -1.8e19, 200.0,
+            -200.0, 100.0, -100.0, -89.0, -88.0, -87.0, -20.0, -6.0, 1e-38, -1e-38, 0.0, -0.0]
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (3, 37), (2600, 2048), (2600, 2050)])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_activations_of_extreme_values(M, N, act):
+    """Values as the formulas have them in fp32: finite for every finite z; -inf gives NaN in
+    silu and gelu (infinity times 0), +inf stays."""
+    z = torch.tensor((EXTREMES * (N // len(EXTREMES) + 1))[:N], device=DEV).to(BF16)
+    x, w = torch.zeros(M, 8, dtype=BF16, device=DEV), torch.zeros(N, 8, dtype=BF16, device=DEV)
+    x[:, 0], w[:, 0] = 1, z
+    y = torch.empty(M, N, dtype=F32, device=DEV)
+    moe.moe_linear(x, w, y, _ws(M, N, 8), act=act)
+    z64 = z.to(F64)
+    want = {"relu": z64.clamp(min=0), "silu": z64 / (1 + torch.exp(-z64)),
+            "gelu": 0.5 * z64 * (1 + torch.erf(z64 * 0.5 ** 0.5))}[act]
+    assert bool((y == y[:1]).logical_or(torch.isnan(y) & torch.isnan(y[:1])).all())
+    assert torch.equal(torch.isnan(y[0]), torch.isnan(want))
+    ok = torch.isfinite(want)
+    assert torch.equal(y[0][~ok & ~torch.isnan(want)].to(F64), want[~ok & ~torch.isnan(want)])
+    e = 32 * U32 * (1 + z64.abs())
+    assert bool(((y[0].to(F64) - want).abs() <= e)[ok].all())
+
+
+@pytest.mark.parametrize("N", [40, 37])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_slopes_of_extreme_values(N, act):
+    """One token with dy = 1: dbias is the slope; silu's and gelu's of an infinite z are NaN."""
+    z = torch.tensor((EXTREMES * 2)[:N], device=DEV).to(BF16).view(1, N)
+    dy, x, w = torch.ones_like(z), torch.zeros(1, 8, dtype=BF16, device=DEV), torch.zeros(
+        N, 8, dtype=BF16, device=DEV)
+    db = torch.empty(N, device=DEV)
+    ws = moe.alloc_workspace(moe.linear_backward_workspace_size(1, N, 8))
+    moe.moe_linear_backward(x, w, dy, ws, z=z, act=act, dbias=db)
+    z64 = z[0].to(F64)
+    want = torch.from_numpy(ref.act_slope(z64.cpu().numpy(), act)).to(DEV)
+    if act == "relu":
+        want[torch.isnan(z64)] = float("nan")
+    bad = torch.isnan(z64) if act == "relu" else ~torch.isfinite(z64)
+    assert torch.equal(torch.isnan(db), bad)
+    e = 32 * U32 * (1 + z64.abs())
+    assert bool(((db.to(F64) - want).abs() <= e)[~bad].all())
