@@ -12,9 +12,9 @@
 //   dh = dh_in + rstd * (u - n * mean(u * n));   dgain = sum over rows of dy * n.
 //
 // Memory-bound for many rows (about one flop a byte), bound by one row's latency and the
-// launch for few.  A row is read once and stays in registers between its sum and the outputs;
-// the next rows are on their way into shared memory meanwhile (cp.async), so that HBM does not
-// wait for the sums.  Measured: 32768 x 7168 bf16 with residual, y, codes and scales 333 us
+// launch for few.  A row is read once and stays in registers between its sum and the outputs
+// (in shared memory, in the gradient of more than 8192 columns); the next rows are on their way
+// into shared memory meanwhile (cp.async), so that HBM does not wait for the sums.  Measured: 32768 x 7168 bf16 with residual, y, codes and scales 333 us
 // (0.95 of the copy bandwidth; 421 with plain loads and a CTA a row), the gradient of 8192 x
 // 7168 fp32 with its incoming gradient 162 us (0.87; 224).  Three forms by the width:
 //   * whole 16-byte vectors (cols % 8 == 0, up to 16384): 2 vectors of 8 values a thread up to
@@ -493,6 +493,13 @@ struct NormBwd {
 // (no atomics: run-to-run identical).
 // Rows in flight: 16384 fp32 columns fill the shared memory once.
 __host__ __device__ constexpr int bwd_stages(int nv) { return nv == 4 ? 1 : kStages; }
+// With four vectors a thread only u and the dgain sums stay in registers over the row's sum:
+// h and dh_in are read from the row's slot again, the gain from L1 in every row, and the next
+// row's copies start behind the outputs.  8192 x 16384 fp32 361 us (0.78 of the copy
+// bandwidth), 12288 columns 302; bf16 247 and 220.  (All five arrays in registers spill a
+// kilobyte a thread: 1292, 969, 303 and 268 us; the form that reads rows twice 765 us for
+// 16512 fp32 columns.)
+__host__ __device__ constexpr bool bwd_rereads(int nv) { return nv == 4; }
 
 template <typename RT, typename GT, int NV, bool kWarpRow>
 __global__ void __launch_bounds__(kMaxThreads)
@@ -535,12 +542,14 @@ __global__ void __launch_bounds__(kMaxThreads)
   };
 #pragma unroll
   for (int st = 0; st < ST; ++st) fetch(first + st * step, st);
-  float dg[NV][8], g[NV][8];
+  constexpr bool kReread = bwd_rereads(NV);
+  constexpr int KV = kReread ? 1 : NV;  // vectors of g, n and dh_in that are kept
+  float dg[NV][8], g[KV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
-    if (c0 + i * stride < cols) load_gain<8>(gain + c0 + i * stride, g[i]);
+    if (!kReread && c0 + i * stride < cols) load_gain<8>(gain + c0 + i * stride, g[i % KV]);
   }
   int flip = 0, st = 0;
   float rs = first < rows ? p.rstd[first] : 0.f;
@@ -549,24 +558,28 @@ __global__ void __launch_bounds__(kMaxThreads)
     cp_async_wait<ST - 1>();
     __syncwarp();
     const int sl = st * row_slots;
-    float u[NV][8], n[NV][8], add[NV][8];
+    float u[NV][8], n[KV][8], add[KV][8];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (c0 + i * stride < cols) {
+        const int k = i % KV;
         unstage_vec(ring_y + sl + i * threads, lane, p.dy, u[i]);
-        unstage_vec(ring_h + sl + i * CH * threads, lane, h, n[i]);
-        if (dhi) unstage_vec(ring_i + sl + i * CH * threads, lane, dhi, add[i]);
+        unstage_vec(ring_h + sl + i * CH * threads, lane, h, n[k]);
+        if (!kReread && dhi) unstage_vec(ring_i + sl + i * CH * threads, lane, dhi, add[k]);
+        if (kReread) load_gain<8>(gain + c0 + i * stride, g[k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          n[i][j] *= rs;
-          dg[i][j] = fmaf(u[i][j], n[i][j], dg[i][j]);
-          u[i][j] *= g[i][j];
-          dot = fmaf(u[i][j], n[i][j], dot);
+          n[k][j] *= rs;
+          dg[i][j] = fmaf(u[i][j], n[k][j], dg[i][j]);
+          u[i][j] *= g[k][j];
+          dot = fmaf(u[i][j], n[k][j], dot);
         }
       }
-    __syncwarp();  // the slot has been read
-    fetch(row + ST * step, st);
+    if (!kReread) {
+      __syncwarp();  // the slot has been read
+      fetch(row + ST * step, st);
+    }
     // two buffers: a row's partials are read while the next row's are written
     dot = row_sum<kWarpRow>(dot, part[flip]) * inv;
     const size_t base = static_cast<size_t>(row) * cols;
@@ -574,15 +587,26 @@ __global__ void __launch_bounds__(kMaxThreads)
     for (int i = 0; i < NV; ++i) {
       const int c = c0 + i * stride;
       if (c < cols) {
+        const int k = i % KV;
+        if constexpr (kReread) {
+          unstage_vec(ring_h + sl + i * CH * threads, lane, h, n[k]);
+          if (dhi) unstage_vec(ring_i + sl + i * CH * threads, lane, dhi, add[k]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) n[k][j] *= rs;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           // (fmaf spelled out: the same bits whichever outputs are asked for)
-          const float t = fmaf(-n[i][j], dot, u[i][j]);
-          u[i][j] = dhi ? fmaf(rs, t, add[i][j]) : rs * t;
+          const float t = fmaf(-n[k][j], dot, u[i][j]);
+          u[i][j] = dhi ? fmaf(rs, t, add[k][j]) : rs * t;
         }
         if (p.dh) store_vec<8>(static_cast<RT*>(p.dh) + base + c, u[i]);
         if (p.dx) store_vec<8>(p.dx + base + c, u[i]);
       }
+    }
+    if (kReread) {
+      __syncwarp();
+      fetch(row + ST * step, st);
     }
     rs = rs_next;
     st = st + 1 == ST ? 0 : st + 1;
