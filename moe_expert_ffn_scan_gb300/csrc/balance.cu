@@ -546,15 +546,14 @@ __global__ void __launch_bounds__(kWarps * 32, bwd_ctas_per_sm(NV * VEC * LPR))
   }
 }
 
-// Calls f with the (NV, VEC, LPR) of E: vectors of 4 when rows are whole 16-byte vectors.  In
-// the gradient a token takes 16 lanes while their registers allow (the row's sums, logarithm,
-// quotients and the chosen experts' terms then cost one instruction for two tokens).
+// Calls f with the (NV, VEC, LPR) of E: vectors of 4 when rows are whole 16-byte vectors.
 template <int NV_, int VEC_, int LPR_>
 struct Shape {
   static constexpr int NV = NV_, VEC = VEC_, LPR = LPR_;
 };
+// The forward's: a token takes a warp.
 template <typename F>
-cudaError_t with_warp_row(int E, F f) {
+cudaError_t with_fwd_row(int E, F f) {
   if (E % 4 == 0) {
     if (E <= 128) return f(Shape<1, 4, 32>());
     if (E <= 256) return f(Shape<2, 4, 32>());
@@ -569,21 +568,27 @@ cudaError_t with_warp_row(int E, F f) {
   if (E <= 512) return f(Shape<16, 1, 32>());
   return f(Shape<32, 1, 32>());
 }
+// The gradient's: a token takes 16 lanes (the row's sums, logarithm, quotients and the chosen
+// experts' terms then cost one instruction for two tokens) up to 512 experts in vectors, a warp
+// above.  24000 tokens, 16 lanes and 32: 388 experts 17.5 and 19.3 us, 448 18.6 and 20.4, 512
+// 20.8 and 21.5.  Scalar rows, whose accesses are a fourth as wide, go over at 256: 129 experts
+// 14.0 and 16.8, 255 18.0 and 18.3, 385 26.9 and 25.8, 511 33.0 and 28.6.
 template <typename F>
-cudaError_t with_half_row(int E, F f) {
+cudaError_t with_bwd_row(int E, F f) {
   if (E % 4 == 0) {
     if (E <= 64) return f(Shape<1, 4, 16>());
     if (E <= 128) return f(Shape<2, 4, 16>());
     if (E <= 256) return f(Shape<4, 4, 16>());
     if (E <= 384) return f(Shape<6, 4, 16>());
-  } else {
-    if (E <= 32) return f(Shape<2, 1, 16>());
-    if (E <= 64) return f(Shape<4, 1, 16>());
-    if (E <= 128) return f(Shape<8, 1, 16>());
-    if (E <= 256) return f(Shape<16, 1, 16>());
-    if (E <= 512) return f(Shape<32, 1, 16>());
+    if (E <= 512) return f(Shape<8, 4, 16>());
+    return f(Shape<8, 4, 32>());
   }
-  return with_warp_row(E, f);
+  if (E <= 32) return f(Shape<2, 1, 16>());
+  if (E <= 64) return f(Shape<4, 1, 16>());
+  if (E <= 128) return f(Shape<8, 1, 16>());
+  if (E <= 256) return f(Shape<16, 1, 16>());
+  if (E <= 512) return f(Shape<16, 1, 32>());
+  return f(Shape<32, 1, 32>());
 }
 
 }  // namespace
@@ -612,7 +617,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* idx, const i
   const int per = balance_rows_per_cta(T, E);
   const int ctas = balance_ctas(T, E);
   const size_t smem = sizeof(float) * (fwd_warps(E) + 1) * E;
-  cudaError_t e = with_warp_row(E, [&](auto sh) {
+  cudaError_t e = with_fwd_row(E, [&](auto sh) {
     using H = decltype(sh);
     return launch_k(k_balance_partial<H::NV, H::VEC>, ctas, fwd_warps(E) * 32, smem, st, logits,
                     idx, off, mask, T, E, k, S, per, w.p, w.c, w.z, w.n, w.acc, w.flags);
@@ -638,7 +643,7 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const in
                                const float* dw, int T, int E, int k, int S, float* dlogits,
                                cudaStream_t st) {
   if (T == 0) return cudaSuccess;
-  return with_half_row(E, [&](auto sh) {
+  return with_bwd_row(E, [&](auto sh) {
     using H = decltype(sh);
     constexpr int rows = kWarps * (32 / H::LPR);  // a CTA's at once
     const long long all = 152LL * bwd_ctas_per_sm(H::NV * H::VEC * H::LPR) * rows;  // resident

@@ -14,9 +14,10 @@
 // Memory-bound for many rows (about one flop a byte), bound by one row's latency and the
 // launch for few.  A row is read once and stays in registers between its sum and the outputs
 // (in shared memory, in the gradient of more than 8192 columns); the next rows are on their way
-// into shared memory meanwhile (cp.async), so that HBM does not wait for the sums.  Measured: 32768 x 7168 bf16 with residual, y, codes and scales 333 us
-// (0.95 of the copy bandwidth; 421 with plain loads and a CTA a row), the gradient of 8192 x
-// 7168 fp32 with its incoming gradient 162 us (0.87; 224).  Three forms by the width:
+// into shared memory meanwhile (cp.async), so that HBM does not wait for the sums.  Measured:
+// 32768 x 7168 bf16 with residual, y, codes and scales 333 us (0.95 of the copy bandwidth; 421
+// with plain loads and a CTA a row), the gradient of 8192 x 7168 fp32 with its incoming gradient
+// 162 us (0.87; 224).  Three forms by the width:
 //   * whole 16-byte vectors (cols % 8 == 0, up to 16384): 2 vectors of 8 values a thread up to
 //     8192 columns, 4 above (fewer threads a row, but more registers: 344 and 355 us for the
 //     prefill above); rows of up to 512 columns take a warp each, eight to a CTA;
