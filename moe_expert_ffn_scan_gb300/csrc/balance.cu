@@ -646,7 +646,7 @@ cudaError_t launch_balance_bwd(const float* logits, const int32_t* idx, const in
   return with_bwd_row(E, [&](auto sh) {
     using H = decltype(sh);
     constexpr int rows = kWarps * (32 / H::LPR);  // a CTA's at once
-    const long long all = 152LL * bwd_ctas_per_sm(H::NV * H::VEC * H::LPR) * rows;  // resident
+    const long long all = 1LL * kSms * bwd_ctas_per_sm(H::NV * H::VEC * H::LPR) * rows;  // resident
     const int per = static_cast<int>((T + all - 1) / all);
     const int ctas = static_cast<int>((T + static_cast<long long>(per) * rows - 1) /
                                       (static_cast<long long>(per) * rows));

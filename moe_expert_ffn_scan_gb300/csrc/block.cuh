@@ -7,6 +7,9 @@
 
 namespace moe {
 
+// SMs of a GB300.  Grids and cost models go by it (results do not).
+constexpr int kSms = 152;
+
 // ------------------------------------------------------------------ cp.async ------
 
 // 16 bytes into shared memory, asynchronously and past L1.
@@ -136,7 +139,7 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st);
 // pair that has rows: balance_ctas(T, E) + S - 1 slots.  That count falls by some CTAs
 // wherever the rows of a CTA become one more; workspaces have balance_ctas_most(T, E), which
 // never falls: one made for the longest step does for every shorter one.
-constexpr int kBalanceCtas = 304;
+constexpr int kBalanceCtas = 2 * kSms;
 struct BalanceWs {
   uint32_t* status;
   uint32_t* flags;   // [balance_ctas_most(T, E)] status bits, by CTA

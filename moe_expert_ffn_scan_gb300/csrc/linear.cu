@@ -988,10 +988,11 @@ struct Choice {
   int nt, splits;  // nt = 0: SM pairs
 };
 Choice choose(int R, int F, int C, bool p_mn, bool whole) {
+  constexpr int kPairs = kSms / 2;  // pair tiles at a time; split CTAs: two per SM
   const int nk = (C + kBK - 1) / kBK;
   const long long tiles =
       static_cast<long long>((R + kPTile - 1) / kPTile) * ((F + kPTile - 1) / kPTile);
-  const double waves = static_cast<double>((tiles + 75) / 76);
+  const double waves = static_cast<double>((tiles + kPairs - 1) / kPairs);
   const double mma = 0.29 * nk, epi = whole ? 6.3 : 9.0;
   Choice best = {(waves - 1) * (mma > epi ? mma : epi) + mma + epi, 0, 1};
   // two pairs a tile, while all their clusters fit (four: clusters of eight CTAs with an SM
@@ -1007,7 +1008,7 @@ Choice choose(int R, int F, int C, bool p_mn, bool whole) {
     const double hbm = static_cast<double>(F) * C * 2 / 6.9e6;
     const double stage = nt == 128 ? 0.41 : nt == 64 ? 0.31 : 0.27;
     for (int splits = 1; splits <= 8 && splits <= nk; splits *= 2) {
-      const double w = static_cast<double>((ft * tt * splits + 303) / 304);
+      const double w = static_cast<double>((ft * tt * splits + 2 * kSms - 1) / (2 * kSms));
       const double chain = w * stage * ((nk + splits - 1) / splits);
       double us = l2 > hbm ? l2 : hbm;
       us = (us > chain ? us : chain) + 0.1 * chain + (splits == 8 ? 2.0 : 0.0) +
@@ -1077,7 +1078,7 @@ cudaError_t launch_linear_bwd(const LinearBwdCall& a, cudaStream_t st) {
     const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && (!z || a.ldz % 8 == 0);
     const int blocks = (a.N + (vec ? 1023 : 127)) / (vec ? 1024 : 128);
     // row blocks: about 8 CTAs of 128 threads per SM (4: 53 us)
-    int parts = (152 * 8 + blocks - 1) / blocks;
+    int parts = (kSms * 8 + blocks - 1) / blocks;
     parts = parts > kLinearDbParts ? kLinearDbParts : parts;
     const int per = (a.M + parts - 1) / parts;
     parts = (a.M + per - 1) / per;

@@ -32,7 +32,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kMaxThreads = 512;  // a row's threads: 128 registers each
 constexpr int kRaggedFew = 4;     // columns a thread in rows that are no whole vectors: up to
 constexpr int kRaggedMany = 8;    // 1024 columns, and up to 8192
