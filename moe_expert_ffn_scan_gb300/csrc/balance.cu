@@ -11,8 +11,8 @@
 // One pass over the logits, which stay in the registers of the token's lanes (E <= 1024), so
 // the maximum, the sum, the probabilities and their products are register work.  Both
 // directions are bound by reading (and in the gradient writing) T x E fp32 values, and at the
-// sizes of a training step by what surrounds that: 32768 x 384 takes 16.5 us forward (12 for
-// the pass over 50 MB, the rest the second kernel's chain of dependent loads) and 21.9 us
+// sizes of a training step by what surrounds that: 32768 x 384 takes 16.8 us forward (12 for
+// the pass over 50 MB, the rest the second kernel's chain of dependent loads) and 21.3 us
 // backward (100 MB; 0.70 of the copy bandwidth).
 // No floating-point atomics: partial sums are added in a fixed order, or in fixed point.
 #include "block.cuh"

@@ -13,8 +13,9 @@
 //     64 columns of c a stage in a ring of six, persistent, two accumulators in TMEM so that a
 //     tile's epilogue runs under the next tile's MMAs; with few tiles two pairs share one,
 //     each summing half of c.  Bound by the tensor cores (16384 x 7168 x 7168 with residual:
-//     1.00 ms, 1.68 PFLOP/s) or, for short c, by the epilogue's elementwise work (8192 x 4096
-//     x 1024: 44 us plain, 45 with bias, 52 with SiLU, 65 with GELU).
+//     1.01 to 1.06 ms, 1.59 to 1.67 PFLOP/s under the power cap) or, for short c, by the
+//     epilogue's elementwise work (8192 x 4096 x 1024: 42 us plain, with bias and SiLU 52, with
+//     bias and GELU 65 to 70).
 //   * k_linear_split: for outputs with too few such tiles.  128 features (the MMA's M side:
 //     the weights fill its rows even for one token) x NT tokens a tile, c split among the
 //     CTAs of a cluster, whose partial sums meet in distributed shared memory and are added
