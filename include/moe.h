@@ -502,6 +502,89 @@ int moe_linear_backward(const moe_linear_desc* d, const uint16_t* x, const uint1
                         const uint16_t* z, const uint16_t* dy, uint16_t* dx, uint16_t* dw,
                         float* dbias, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * The routed layer's gradient, for training what is in front of it (and its router) with
+ * the experts' 4-bit weights as they are: they have no gradient of their own.  The same
+ * conventions.  The FP8 quantisations pass their gradient straight through.  In order:
+ *     moe_dispatch           dout's tokens to their packed rows         [Rs][H]
+ *     _w2_backward           dh = dout W2, unweighted                   [Rs][I]
+ *     moe_swiglu_backward    dy13 (with the combine weights), and dw    [Rs][2I]
+ *     _w13_backward          dxp = dy13 W13                             [Rs][H]
+ *     moe_dispatch_backward  dx                                         [T][H]
+ * dw then goes to moe_balance_loss_backward.  Where y2 was kept, moe_combine_backward takes
+ * the first step's place, with the weights applied and dw. */
+
+/* Tokens sorted by expert: xp[inv[t*k+j]] = x[t] for every j, xp[R+t] = x[t] if has_shared.
+ *   x [T][H] bf16, inv [T*k] as moe_route gives it, xp [Rs][H] bf16.  An entry of inv outside
+ *   [0, R) is a slot without a row (a token dropped by its expert): nothing is written for
+ *   it; rows that no slot has are left as they were.  No two slots may have the same row. */
+int moe_dispatch(const moe_dims* d, const uint16_t* x, const int32_t* inv, uint16_t* xp,
+                 void* stream);
+
+/* Its gradient: dx[t] = dx_in[t] + sum_j dxp[inv[t*k+j]] + dxp[R+t] (if has_shared), summed in
+ * fp32 in this order and rounded once.  dxp [Rs][H] bf16; dx, dx_in [T][H] of dx_dtype, dx_in
+ * (the gradient that reaches x by other ways) NULL for none, or dx's own buffer.  Slots
+ * without a row add nothing. */
+int moe_dispatch_backward(const moe_dims* d, const uint16_t* dxp, const int32_t* inv,
+                          const void* dx_in, int32_t dx_dtype, void* dx, void* stream);
+
+/* Gradient of moe_combine:
+ *     dy2[inv[t*k+j]] = bf16(w[t][j] * dout[t]),   dy2[R+t] = dout[t] (if has_shared),
+ *     dw[t][j] = sum_h dout[t][h] * y2[inv[t*k+j]][h]      (fp32, a fixed order).
+ *   dout [T][H] bf16, y2 [Rs][H] bf16 (with dw), w [T][k] fp32 (with dy2).  Outputs, at least
+ *   one: dy2 [Rs][H] bf16, dw [T][k] fp32.  dy2 may be y2's buffer.  Slots without a row (see
+ *   moe_dispatch): dw 0; rows that no slot has are left as they were. */
+int moe_combine_backward(const moe_dims* d, const uint16_t* dout, const uint16_t* y2,
+                         const int32_t* inv, const float* w, uint16_t* dy2, float* dw,
+                         void* stream);
+
+/* moe_swiglu_quant that also saves its input in 8 bits for the gradient: hq, hs as
+ * moe_swiglu_quant gives them, yq [rows][2I] and ys [rows][2I/128] as moe_quant_act gives them
+ * of y13, bit for bit, in one pass.  I % 128 == 0; rows == 0 is a no-op. */
+int moe_swiglu_quant_save(int32_t rows, int32_t I, const uint16_t* y13, uint8_t* hq, uint8_t* hs,
+                          uint8_t* yq, uint8_t* ys, void* stream);
+
+/* Gradient of SwiGLU, from its input in 8 bits (yq, ys) or in bf16 (y13): one of the two.  In
+ * each row, with [g | u] that input, s = 1 / (1 + e^-g) and d = dh times the row's weight:
+ *     dy13 = [ d u s (1 + g (1 - s)) | d g s ]                  (fp32, rounded once to bf16)
+ *   dh [rows][I] bf16: the gradient of the row's unweighted output through W2.  dy13
+ *   [rows][2I] bf16 (may be y13's buffer).
+ *   The first R rows are routed slots: row r has the weight w[perm_src[r]] (w [R] fp32, i.e.
+ *   [T][k]; perm_src [R] as moe_route gives it), the others 1; w NULL: 1 for all.
+ *   dw [R] fp32 or NULL: the combine weights' gradient without y2,
+ *     dw[perm_src[r]] = sum_i dh[r][i] * h[r][i]    (<dout, W2 h> = <W2^T dout, h>; fixed order)
+ *   with h the values of hq, hs (what W2 took) where given, else silu(g) u.  A row whose
+ *   perm_src is outside [0, R) has weight 1 and no dw; entries of dw that no row names are
+ *   left as they were.
+ *   Finite for finite inputs whose formulas are.  rows == 0 is a no-op. */
+typedef struct moe_swiglu_backward_desc {
+  int32_t rows, R, I; /* 0 <= R <= rows, I % 128 == 0 */
+} moe_swiglu_backward_desc;
+int moe_swiglu_backward(const moe_swiglu_backward_desc* d, const uint16_t* dh, const uint16_t* y13,
+                        const uint8_t* yq, const uint8_t* ys, const uint8_t* hq,
+                        const uint8_t* hs, const int32_t* perm_src, const float* w,
+                        uint16_t* dy13, float* dw, void* stream);
+
+/* Gradient products of the two grouped GEMMs, with MXFP4 weights as the forward has them: for
+ * every packed row r of group g
+ *     dh[r][i]  = sum_n dy2[r][n]  * deq(w2[g])[n][i],    dy2 [Rs][H],   dh [Rs][I],
+ *     dxp[r][h] = sum_n dy13[r][n] * deq(w13[g])[n][h],   dy13 [Rs][2I], dxp [Rs][H],
+ * bf16 rows, exact products, fp32 sums, one rounding to bf16.  group_offsets [G+1] as for the
+ * forward: rows outside every group are not read and not written; offsets that decrease or
+ * leave [0, Rs] set the status word and nothing is written.
+ *   ws: moe_gemm_backward_workspace_size bytes, 256-byte aligned.  Its first 4 bytes are a
+ *   status word that these two calls only set bits of: zero it once, before the first use and
+ *   in an order with it, and keep the workspace to them; moe_check_status reads it. */
+size_t moe_gemm_backward_workspace_size(const moe_dims* d);
+int moe_grouped_gemm_w2_backward(const moe_dims* d, const uint16_t* dy2,
+                                 const int32_t* group_offsets, const uint8_t* w2,
+                                 const uint8_t* w2_s, uint16_t* dh, void* ws, size_t ws_bytes,
+                                 void* stream);
+int moe_grouped_gemm_w13_backward(const moe_dims* d, const uint16_t* dy13,
+                                  const int32_t* group_offsets, const uint8_t* w13,
+                                  const uint8_t* w13_s, uint16_t* dxp, void* ws, size_t ws_bytes,
+                                  void* stream);
+
 /* Debug helper (synchronises `stream`): reads the device status word at the start of
  * a workspace used by the calls above.  Returns MOE_OK if no bit is set, else
  * MOE_ERR_DEVICE_CHECK and the bits in *bits_out (if not NULL).  The word is

@@ -54,6 +54,10 @@ class moe_linear_desc(ctypes.Structure):
                 [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldr", "ldy", "ldz")])
 
 
+class moe_swiglu_backward_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "R", "I")]
+
+
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}  # MOE_ACT_*
 
 
@@ -153,6 +157,19 @@ def lib():
         for fn in ("moe_add_rmsnorm", "moe_add_rmsnorm_backward", "moe_balance_loss",
                    "moe_balance_loss_backward", "moe_linear", "moe_linear_backward"):
             getattr(L, fn).restype = ctypes.c_int
+        L.moe_dispatch.argtypes = [_DP] + [_P] * 4
+        L.moe_dispatch_backward.argtypes = [_DP, _P, _P, _P, _I, _P, _P]
+        L.moe_combine_backward.argtypes = [_DP] + [_P] * 7
+        L.moe_swiglu_quant_save.argtypes = [_I, _I] + [_P] * 6
+        L.moe_swiglu_backward.argtypes = ([ctypes.POINTER(moe_swiglu_backward_desc)] + [_P] * 11)
+        L.moe_gemm_backward_workspace_size.argtypes = [_DP]
+        L.moe_gemm_backward_workspace_size.restype = _SZ
+        for fn in ("moe_grouped_gemm_w2_backward", "moe_grouped_gemm_w13_backward"):
+            getattr(L, fn).argtypes = [_DP] + [_P] * 6 + [_SZ, _P]
+        for fn in ("moe_dispatch", "moe_dispatch_backward", "moe_combine_backward",
+                   "moe_swiglu_quant_save", "moe_swiglu_backward",
+                   "moe_grouped_gemm_w2_backward", "moe_grouped_gemm_w13_backward"):
+            getattr(L, fn).restype = ctypes.c_int
         for fn in ("moe_route", "moe_quant_act", "moe_grouped_gemm_w13", "moe_swiglu_quant",
                    "moe_grouped_gemm_w2", "moe_combine", "moe_forward", "moe_forward_timed",
                    "moe_check_status", "moe_forward_nvfp4", "moe_forward_nvfp4_timed",
@@ -201,6 +218,17 @@ def _t(t, dtype, shape, name):
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
+    return _p(t)  # raises
+
+
+def _flat(t, dtype, n, name):
+    """_p of n contiguous values of any shape (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} values of {dtype}, got {t.numel()} of {t.dtype}")
     return _p(t)  # raises
 
 
@@ -618,6 +646,112 @@ def moe_linear_backward(x, w, dy, ws, z=None, act="none", dx=None, dw=None, dbia
         ws.numel(), _raw_stream(stream))
     if rc:
         raise MoeError("moe_linear_backward", rc)
+
+
+# ---------------------------------------------------------------- the layer's gradient
+
+def _packed_rows(d):
+    return d.T * (d.k + d.has_shared)
+
+
+def moe_dispatch(d, x, inv, xp, stream=None):
+    """x [T, H] bf16 to the packed rows of its experts, xp [Rs, H]: row inv[t*k+j] (moe_route's
+    inv, [T*k] int32; an entry outside [0, T*k): no row) and, with a shared expert, row
+    T*k + t."""
+    rc = lib().moe_dispatch(
+        _d(d), _t(x, _BF16, (d.T, d.H), "x"), _flat(inv, _I32, d.T * d.k, "inv"),
+        _t(xp, _BF16, (_packed_rows(d), d.H), "xp"), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_dispatch", rc)
+
+
+def moe_dispatch_backward(d, dxp, inv, dx, dx_in=None, stream=None):
+    """Gradient of moe_dispatch: dx [T, H] (bf16 or fp32) = dx_in (dx's type, or None) + the sum
+    of each token's rows of dxp [Rs, H] bf16."""
+    shape, dt, code = (d.T, d.H), dx.dtype, _dtype_code(dx, "dx")
+    rc = lib().moe_dispatch_backward(
+        _d(d), _t(dxp, _BF16, (_packed_rows(d), d.H), "dxp"),
+        _flat(inv, _I32, d.T * d.k, "inv"), _t(dx_in, dt, shape, "dx_in"),
+        code, _t(dx, dt, shape, "dx"), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_dispatch_backward", rc)
+
+
+def moe_combine_backward(d, dout, y2, inv, w, dy2=None, dw=None, stream=None):
+    """Gradient of moe_combine from dout [T, H] bf16: writes what is given of dy2 [Rs, H] bf16
+    (w [T, k] fp32 times the token's dout) and dw [T, k] fp32 (from y2 [Rs, H] bf16, else
+    None)."""
+    rows = (_packed_rows(d), d.H)
+    rc = lib().moe_combine_backward(
+        _d(d), _t(dout, _BF16, (d.T, d.H), "dout"), _t(y2, _BF16, rows, "y2"),
+        _flat(inv, _I32, d.T * d.k, "inv"), _t(w, _F32, (d.T, d.k), "w"),
+        _t(dy2, _BF16, rows, "dy2"), _t(dw, _F32, (d.T, d.k), "dw"), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_combine_backward", rc)
+
+
+def moe_swiglu_quant_save(y13, hq, hs, yq, ys, stream=None):
+    """moe_swiglu_quant of y13 [rows, 2I] bf16 (hq [rows, I], hs [rows, I/128]) that also saves
+    y13 in 8 bits, yq [rows, 2I] and ys [rows, 2I/128], for moe_swiglu_backward (all uint8)."""
+    rows, two_i = y13.shape
+    I = two_i // 2
+    rc = lib().moe_swiglu_quant_save(
+        rows, I, _t(y13, _BF16, (rows, 2 * I), "y13"), _t(hq, _U8, (rows, I), "hq"),
+        _t(hs, _U8, (rows, I // 128), "hs"), _t(yq, _U8, (rows, 2 * I), "yq"),
+        _t(ys, _U8, (rows, 2 * I // 128), "ys"), _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_swiglu_quant_save", rc)
+
+
+def moe_swiglu_backward(dh, dy13, y13=None, yq=None, ys=None, hq=None, hs=None, perm_src=None,
+                        w=None, dw=None, stream=None):
+    """Gradient of SwiGLU from dh [rows, I] bf16 and its input, either in 8 bits (yq, ys as
+    moe_swiglu_quant_save wrote them) or y13 [rows, 2I] bf16.  Writes dy13 [rows, 2I] bf16, each
+    routed row's (the first perm_src.numel() of them) times its weight of w [T, k] fp32 (None:
+    1), and, if given, dw [T, k] fp32: the weights' gradient, from the values of hq, hs if given,
+    else from silu(g) u."""
+    rows, I = dh.shape
+    R = perm_src.numel() if perm_src is not None else 0
+    wp, dwp = _flat(w, _F32, R, "w"), _flat(dw, _F32, R, "dw")
+    desc = moe_swiglu_backward_desc(rows, R, I)
+    two, blocks = (rows, 2 * I), I // 128
+    rc = lib().moe_swiglu_backward(
+        ctypes.byref(desc), _t(dh, _BF16, (rows, I), "dh"), _t(y13, _BF16, two, "y13"),
+        _t(yq, _U8, two, "yq"), _t(ys, _U8, (rows, 2 * blocks), "ys"),
+        _t(hq, _U8, (rows, I), "hq"), _t(hs, _U8, (rows, blocks), "hs"),
+        _flat(perm_src, _I32, R, "perm_src"), wp, _t(dy13, _BF16, two, "dy13"), dwp,
+        _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_swiglu_backward", rc)
+
+
+def gemm_backward_workspace_size(d) -> int:
+    return lib().moe_gemm_backward_workspace_size(_d(d))
+
+
+def _gemm_backward(name, d, dy, cols_in, group_offsets, w, w_s, dx, cols_out, ws, stream):
+    rows, G = _packed_rows(d), d.E + d.has_shared
+    rc = getattr(lib(), name)(
+        _d(d), _t(dy, _BF16, (rows, cols_in), "dy"),
+        _t(group_offsets, _I32, (G + 1,), "group_offsets"),
+        _t(w, _U8, (G, cols_in, cols_out // 2), "w"),
+        _t(w_s, _U8, (G, cols_in, cols_out // 32), "w_s"),
+        _t(dx, _BF16, (rows, cols_out), "dx"), _p(ws), ws.numel(), _raw_stream(stream))
+    if rc:
+        raise MoeError(name, rc)
+
+
+def moe_grouped_gemm_w2_backward(d, dy2, group_offsets, w2, w2_s, dh, ws, stream=None):
+    """dh [Rs, I] = dy2 [Rs, H] . deq(w2[g]) [H, I] for the packed rows of each group (bf16, MXFP4
+    weights).  ws: gemm_backward_workspace_size(d) bytes, kept to the gradient products."""
+    _gemm_backward("moe_grouped_gemm_w2_backward", d, dy2, d.H, group_offsets, w2, w2_s, dh, d.I,
+                   ws, stream)
+
+
+def moe_grouped_gemm_w13_backward(d, dy13, group_offsets, w13, w13_s, dxp, ws, stream=None):
+    """dxp [Rs, H] = dy13 [Rs, 2I] . deq(w13[g]) [2I, H], as moe_grouped_gemm_w2_backward."""
+    _gemm_backward("moe_grouped_gemm_w13_backward", d, dy13, 2 * d.I, group_offsets, w13, w13_s,
+                   dxp, d.H, ws, stream)
 
 
 def moe_check_status(ws, stream=None) -> int:

@@ -5,7 +5,7 @@
 #include <mutex>
 #include <new>
 
-#include "kernels.cuh"
+#include "grad.cuh"
 
 using namespace moe;
 
@@ -35,6 +35,18 @@ unsigned long long current_context_id() {
   return id;
 }
 
+bool dims_ok(const moe_dims* d) {
+  if (!d) return false;
+  if (d->T < 1 || d->H < 128 || d->I < 128 || d->E < 1 || d->E > 1024 || d->k < 1) return false;
+  if (d->k > 16 || d->k > d->E) return false;
+  if (d->H % 128 || d->I % 128) return false;
+  if (d->has_shared != 0 && d->has_shared != 1) return false;
+  long long R = static_cast<long long>(d->T) * d->k;
+  if (R + d->T >= (1LL << 31)) return false;
+  if (static_cast<long long>(2) * d->I * d->H >= (1LL << 40)) return false;
+  return true;
+}
+
 }  // namespace moe
 
 namespace {
@@ -55,18 +67,6 @@ struct Carver {
     return base ? reinterpret_cast<T*>(base + off) : nullptr;
   }
 };
-
-bool dims_ok(const moe_dims* d) {
-  if (!d) return false;
-  if (d->T < 1 || d->H < 128 || d->I < 128 || d->E < 1 || d->E > 1024 || d->k < 1) return false;
-  if (d->k > 16 || d->k > d->E) return false;
-  if (d->H % 128 || d->I % 128) return false;
-  if (d->has_shared != 0 && d->has_shared != 1) return false;
-  long long R = static_cast<long long>(d->T) * d->k;
-  if (R + d->T >= (1LL << 31)) return false;
-  if (static_cast<long long>(2) * d->I * d->H >= (1LL << 40)) return false;
-  return true;
-}
 
 long long rows_R(const moe_dims* d) { return static_cast<long long>(d->T) * d->k; }
 long long rows_Rs(const moe_dims* d) { return rows_R(d) + (d->has_shared ? d->T : 0); }

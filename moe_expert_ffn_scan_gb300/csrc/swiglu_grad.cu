@@ -1,0 +1,200 @@
+// SwiGLU in training: the activation with an 8-bit checkpoint of its inputs, and its gradient.
+//
+// Forward, y13 = [g | u] in bf16: h = silu(g) u is quantised for W2 as in inference (hq, hs),
+// and in the same pass g and u themselves to E4M3 codes with a power-of-two scale per 128
+// columns (yq, ys): what stays until the backward pass is 2 I + I bytes a row instead of the
+// 4 I of y13 (and the 2 H of y2, which the combine weights' gradient then does not need: see
+// below).  One read of y13 for both (a separate quantisation would read it again).
+//
+// Backward, with s = 1 / (1 + e^-g) and d = w dh (w the row's combine weight):
+//     dg = d u s (1 + g (1 - s)),   du = d g s,   dw = sum_i dh_i h_i.
+// dw is the gradient of the combine weight: y2 = W2 h, so <dout, y2> = <W2^T dout, h> = <dh, h>
+// with dh = W2^T dout of the unweighted row.  h is what W2 took, the values of hq, where they
+// are given, else silu(g) u.  Everything in fp32, one rounding to bf16 at the end.
+#include "grad.cuh"
+
+namespace moe {
+
+namespace {
+
+// The sigmoid from ex2.approx and rcp.approx (each within 2 units of 2^-23), as the other
+// elementwise kernels have it: its error is far below the outputs' bf16 rounding.
+__device__ __forceinline__ float sigmoid_of(float z) {
+  return __fdividef(1.f, 1.f + __expf(-z));
+}
+
+__device__ __forceinline__ void ld_floats16(const uint16_t* p, float (&f)[16]) {
+  uint32_t lo[4], hi[4];
+  ld_bf16x8(p, lo);
+  ld_bf16x8(p + 8, hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(lo[i]), f[2 * i + 1] = bf16_hi(lo[i]);
+    f[8 + 2 * i] = bf16_lo(hi[i]), f[9 + 2 * i] = bf16_hi(hi[i]);
+  }
+}
+
+// The 16 values of one lane of an 8-lane group whose lanes hold a 128-column block: their
+// codes and the block's scale exponent.  All lanes of the warp must call it.
+__device__ __forceinline__ uint4 codes16(const float (&f)[16], int& e) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  e = fp8_scale_exponent(amax);
+  const float s = pow2_neg(e);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3x2(f[4 * i] * s, f[4 * i + 1] * s) |
+           static_cast<uint32_t>(e4m3x2(f[4 * i + 2] * s, f[4 * i + 3] * s)) << 16;
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// 2^(b - 127) of a scale byte, exact (2^-127 is an fp32 subnormal).
+__device__ __forceinline__ float scale_of(uint32_t b) {
+  return b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22);
+}
+
+// The 16 values that codes with a scale byte stand for.
+__device__ __forceinline__ void values16(const uint4& c, uint32_t scale, float (&f)[16]) {
+  const float s = scale_of(scale);
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+    const float2 v = __half22float2(__half2(hr));
+    f[2 * i] = v.x * s, f[2 * i + 1] = v.y * s;
+  }
+}
+
+// Eight lanes per 128-column block, 16 columns a lane; Idx as wide as the lanes need.
+template <typename Idx>
+__global__ void __launch_bounds__(256) k_swiglu_save(const uint16_t* __restrict__ y13, int rows,
+                                                     int I, uint8_t* __restrict__ hq,
+                                                     uint8_t* __restrict__ hs,
+                                                     uint8_t* __restrict__ yq,
+                                                     uint8_t* __restrict__ ys) {
+  pdl_wait();
+  pdl_trigger();
+  const Idx nblk = I / 128;
+  const Idx gid = static_cast<Idx>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const Idx blk = gid >> 3;
+  const int sub = static_cast<int>(gid & 7);
+  const bool live = blk < static_cast<Idx>(rows) * nblk;
+  const Idx r = live ? blk / nblk : 0, b = live ? blk - r * nblk : 0;
+  float g[16], u[16], h[16];
+  const size_t col = static_cast<size_t>(b) * 128 + sub * 16;
+  const size_t at = static_cast<size_t>(r) * 2 * I + col;
+  if (live) {
+    ld_floats16(y13 + at, g);
+    ld_floats16(y13 + at + I, u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = u[i] = 0.f;
+  }
+  // (the same expression as the inference kernel's, so that hq and hs are its, bit for bit)
+#pragma unroll
+  for (int i = 0; i < 16; ++i) h[i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i];
+  int eg, eu, eh;
+  const uint4 cg = codes16(g, eg), cu = codes16(u, eu), ch = codes16(h, eh);
+  if (!live) return;
+  *reinterpret_cast<uint4*>(yq + at) = cg;
+  *reinterpret_cast<uint4*>(yq + at + I) = cu;
+  *reinterpret_cast<uint4*>(hq + static_cast<size_t>(r) * I + col) = ch;
+  if (sub == 0) {
+    uint8_t* s = ys + static_cast<size_t>(r) * 2 * nblk + b;
+    s[0] = static_cast<uint8_t>(eg + 127);
+    s[nblk] = static_cast<uint8_t>(eu + 127);
+    hs[static_cast<size_t>(r) * nblk + b] = static_cast<uint8_t>(eh + 127);
+  }
+}
+
+// A CTA per row, 16 columns a thread at a time.  kCodes: g and u from the checkpoint.
+template <bool kCodes>
+__global__ void __launch_bounds__(512) k_swiglu_bwd(const SwigluBwdCall a) {
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x, I = a.I;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float part[16];
+  const bool routed = r < a.R;
+  int src = 0;
+  bool has = false;  // the row has a combine weight
+  if (routed && a.perm_src) {
+    src = __ldg(a.perm_src + r);
+    has = src >= 0 && src < a.R;
+  }
+  const float w = a.w && has ? __ldg(a.w + src) : 1.f;
+  const size_t row = static_cast<size_t>(r);
+  float dot = 0.f;
+  for (int c = threadIdx.x * 16; c < I; c += blockDim.x * 16) {
+    float d[16], g[16], u[16];
+    ld_floats16(a.dh + row * I + c, d);
+    if (kCodes) {
+      const uint8_t* q = a.yq + row * 2 * I + c;
+      const uint8_t* s = a.ys + (row * 2 * I + c) / 128;
+      values16(*reinterpret_cast<const uint4*>(q), s[0], g);
+      values16(*reinterpret_cast<const uint4*>(q + I), s[I / 128], u);
+    } else {
+      ld_floats16(a.y13 + row * 2 * I + c, g);
+      ld_floats16(a.y13 + row * 2 * I + I + c, u);
+    }
+    if (a.dw && a.hq) {
+      float h[16];
+      values16(*reinterpret_cast<const uint4*>(a.hq + row * I + c),
+               a.hs[(row * I + c) / 128], h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dot = fmaf(d[i], h[i], dot);
+    }
+    uint32_t og[2][4], ou[2][4];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      float dg[2], du[2];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const float s = sigmoid_of(g[i + o]), silu = g[i + o] * s, dd = w * d[i + o];
+        if (a.dw && !a.hq) dot = fmaf(d[i + o], silu * u[i + o], dot);
+        dg[o] = dd * u[i + o] * fmaf(silu, 1.f - s, s);
+        du[o] = dd * silu;
+      }
+      og[i / 8][i / 2 % 4] = bf16x2_of(dg[0], dg[1]);
+      ou[i / 8][i / 2 % 4] = bf16x2_of(du[0], du[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      st_bf16x8(a.dy13 + row * 2 * I + c + 8 * i, og[i]);
+      st_bf16x8(a.dy13 + row * 2 * I + I + c + 8 * i, ou[i]);
+    }
+  }
+  if (!a.dw || !has) return;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  if (lane == 0) part[warp] = dot;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i) dot += part[i];
+    a.dw[src] = dot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu_save(const uint16_t* y13, int rows, int I, uint8_t* hq, uint8_t* hs,
+                               uint8_t* yq, uint8_t* ys, cudaStream_t st) {
+  const long long blocks = static_cast<long long>(rows) * (I / 128), grid = (blocks + 31) / 32;
+  if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  return launch_k(grid * 256 <= 0xFFFFFFFFLL ? k_swiglu_save<uint32_t>
+                                             : k_swiglu_save<unsigned long long>,
+                  static_cast<unsigned>(grid), 256, 0, st, y13, rows, I, hq, hs, yq, ys);
+}
+
+cudaError_t launch_swiglu_bwd(const SwigluBwdCall& a, cudaStream_t st) {
+  const int chunks = a.I / 16, rounds = (chunks + 511) / 512;
+  const int warps = (chunks + rounds * 32 - 1) / (rounds * 32);
+  return launch_k(a.y13 ? k_swiglu_bwd<false> : k_swiglu_bwd<true>, a.rows, warps * 32, 0, st, a);
+}
+
+}  // namespace moe
