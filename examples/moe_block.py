@@ -12,7 +12,8 @@ Forward, for the T tokens of a step (a verify step's few or a prefill chunk):
 
 Training the router (the experts' 4-bit weights stay as they are): balance loss and z loss of
 the step's routing, and from them the gradients of the logits, of the gate weight, of the norm
-and of the projection in front of it.
+and of the projection in front of it; with the gradient of the block's output, that through the
+experts too (their inner activations kept in 8 bits).
 """
 
 import argparse
@@ -50,10 +51,12 @@ class MoEBlock:
             moe.linear_backward_workspace_size(T, N, K),
             moe.linear_backward_workspace_size(T, self.E, self.H)), dev)
         self.ws_norm = moe.alloc_workspace(moe.add_rmsnorm_backward_workspace_size(T, self.H), dev)
+        self.ws_experts = moe.alloc_workspace(moe.gemm_backward_workspace_size(d), dev)
 
-    def forward(self, attn, stream):
+    def forward(self, attn, stream, save=False):
         """attn [T, K] bf16 (the attention's output), stream [T, H] bf16.  Returns the experts'
-        output and everything that the next norm and the training step need."""
+        output and everything that the next norm and the router's training step need; with save
+        also what the gradient through the experts needs (in 8 bits)."""
         T, H, E, k, sh = attn.shape[0], self.H, self.E, self.k, self.layer.has_shared
         d = self.layer.dims(T)
         R, Rs, I = T * k, T * k + T * sh, self.layer.I
@@ -72,15 +75,39 @@ class MoEBlock:
         hs, y2, out = new(Rs, I // 128, dt=torch.uint8), new(Rs, H), new(T, H)
         L = self.layer
         moe.moe_grouped_gemm_w13(d, q, s, perm, offsets, L.w13, L.w13_s, y13, self.ws)
-        moe.moe_swiglu_quant(y13, hq, hs)
+        if save:
+            f.update(perm=perm, inv=inv, offsets=offsets, hq=hq, hs=hs,
+                     yq=new(Rs, 2 * I, dt=torch.uint8), ys=new(Rs, 2 * I // 128, dt=torch.uint8))
+            moe.moe_swiglu_quant_save(y13, hq, hs, f["yq"], f["ys"])
+        else:
+            moe.moe_swiglu_quant(y13, hq, hs)
         moe.moe_grouped_gemm_w2(d, hq, hs, offsets, L.w2, L.w2_s, y2, self.ws)
         moe.moe_combine(d, y2, inv, f["w"], out)
         f["out"] = out
         return f
 
-    def router_step(self, f, seq_offsets=None, token_mask=None, balance=1e-2, z=1e-3):
+    def experts_backward(self, f, dout):
+        """From dout [T, H] bf16, the gradient of the experts' output of a forward step that was
+        saved: that of their input (the norm's output) in fp32 and of the combine weights."""
+        T, H, I, k, L = f["T"], self.H, self.layer.I, self.k, self.layer
+        d, Rs = L.dims(T), T * (k + L.has_shared)
+        new = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=dout.device)  # noqa: E731
+        rows, dh, dy13 = new(Rs, H), new(Rs, I), new(Rs, 2 * I)
+        dw, dy = new(T, k, dt=torch.float32), new(T, H, dt=torch.float32)
+        moe.moe_dispatch(d, dout, f["inv"], rows)
+        moe.moe_grouped_gemm_w2_backward(d, rows, f["offsets"], L.w2, L.w2_s, dh, self.ws_experts)
+        moe.moe_swiglu_backward(dh, dy13, yq=f["yq"], ys=f["ys"], hq=f["hq"], hs=f["hs"],
+                                perm_src=f["perm"], w=f["w"], dw=dw)
+        moe.moe_grouped_gemm_w13_backward(d, dy13, f["offsets"], L.w13, L.w13_s, rows,
+                                          self.ws_experts)
+        moe.moe_dispatch_backward(d, rows, f["inv"], dy)
+        return dy, dw
+
+    def router_step(self, f, seq_offsets=None, token_mask=None, balance=1e-2, z=1e-3, dout=None):
         """Balance and z loss of a forward step, per sequence, and their gradients: of the
-        gate weight, the norm's gain, the projection's weight and the two inputs."""
+        gate weight, the norm's gain, the projection's weight and the two inputs.  With dout,
+        the gradient of stream' = h + out (of a step that was saved), its part is in all of
+        them."""
         T, E, H, S = f["T"], self.E, self.H, self.n_seq
         dev = f["y"].device
         new = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device=dev)  # noqa: E731
@@ -89,18 +116,21 @@ class MoEBlock:
         seqs = dict(seq_offsets=seq_offsets, token_mask=token_mask)
         moe.moe_balance_loss(f["logits"], f["idx"], ws=self.ws_balance, **o, **seqs)
         g = dict(dlogits=new(T, E))
+        dy, dw = self.experts_backward(f, dout) if dout is not None else (None, None)
         moe.moe_balance_loss_backward(
             f["logits"], f["idx"], o["counts"], o["n_tokens"], g["dlogits"],
             dloss=torch.full((S,), balance, device=dev), dz_loss=torch.full((S,), z, device=dev),
-            **seqs)
+            dw=dw, **seqs)
         # the gate projection is one more product, its operands in bf16
         bf = torch.bfloat16
         g["dy"], g["dwg"] = new(T, H, dt=bf), new(E, H, dt=bf)
         moe.moe_linear_backward(f["y"], self.wg.to(bf), g["dlogits"].to(bf), self.ws_grad,
                                 dx=g["dy"], dw=g["dwg"])
+        if dy is not None:  # the norm's output goes to the gate and to the experts
+            g["dy"], g["dy_experts"], g["dw"] = (g["dy"].float() + dy).to(bf), dy, dw
         g["dh"], g["dgain"] = new(T, H, dt=bf), new(H)
         moe.moe_add_rmsnorm_backward(g["dy"], f["h"], self.gain, f["rstd"], self.ws_norm,
-                                     dh=g["dh"], dgain=g["dgain"])
+                                     dh_in=dout, dh=g["dh"], dgain=g["dgain"])
         # h = attn W_o^T + stream: dh goes to the stream as it is
         g["dattn"], g["dw_o"] = torch.empty_like(f["attn"]), torch.empty_like(self.w_o)
         moe.moe_linear_backward(f["attn"], self.w_o, g["dh"], self.ws_grad, dx=g["dattn"],
@@ -109,8 +139,10 @@ class MoEBlock:
 
     def check(self):
         """The device-side checks of the calls since the workspaces were made."""
-        return [moe.moe_check_status(w) for w in (self.ws, self.ws_linear, self.ws_balance,
+        bits = [moe.moe_check_status(w) for w in (self.ws, self.ws_linear, self.ws_balance,
                                                  self.ws_grad)]
+        bits[3] |= moe.moe_check_status(self.ws_experts)
+        return bits
 
 
 def make_block(T, size="tiny", seed=0, n_seq=1, device="cuda"):
@@ -132,8 +164,9 @@ def main():
     ap.add_argument("--tokens", type=int, default=64)
     a = ap.parse_args()
     block, attn, stream = make_block(a.tokens)
-    f = block.forward(attn, stream)
-    o, g = block.router_step(f)
+    f = block.forward(attn, stream, save=True)
+    dout = torch.randn(f["out"].shape, device=attn.device).to(torch.bfloat16)
+    o, g = block.router_step(f, dout=dout)
     torch.cuda.synchronize()
     print(f"{a.tokens} tokens: |out| {f['out'].float().norm():.4g}, balance loss "
           f"{o['loss'].item():.4f}, z loss {o['z_loss'].item():.4f}, |dW_g| "

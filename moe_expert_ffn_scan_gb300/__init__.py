@@ -941,6 +941,89 @@ class MoELayer:
                               debug=debug, stream=stream)
         return out
 
+    def train_workspaces(self, T, stream=None):
+        """The workspaces of forward_train and backward steps of up to T tokens (moe_check_status
+        reads the checks of the last forward_train, and of every backward since they were made)."""
+        if getattr(self, "_tws", None) is None or self._tT < T:
+            d = self.dims(T)
+            sizes = (max(route_workspace_size(d), gemm_workspace_size(d)),
+                     gemm_backward_workspace_size(d))
+            if 0 in sizes:
+                raise ValueError("unsupported dims")
+            self._tws = tuple(alloc_workspace(n, self.w13.device, stream) for n in sizes)
+            self._tT = T
+        return self._tws
+
+    def forward_train(self, x, logits, out=None, checkpoint="fp8", stream=None):
+        """forward by its stages, keeping what backward needs.  Returns the output [T, H] and the
+        step's state: routing (idx, w, inv, perm_src, offsets, counts) and the activations, in
+        one of two forms:
+          checkpoint="fp8"   the experts' inner activations in 8 bits (3 I bytes a row),
+          checkpoint="bf16"  in bf16, with the experts' outputs (4 I + 2 H bytes a row).
+        MXFP4 weights.  Steps of one layer share its workspaces: one at a time, as forward."""
+        self._mxfp4_only("training")
+        if checkpoint not in ("fp8", "bf16"):
+            raise ValueError(f"unknown checkpoint form {checkpoint!r}")
+        T, H, I, k, sh, E = x.shape[0], self.H, self.I, self.k, self.has_shared, self.E
+        d = self.dims(T)
+        R, Rs = T * k, T * (k + sh)
+        with torch.cuda.stream(stream):
+            new = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=x.device)  # noqa: E731
+            if out is None:
+                out = new(T, H)
+            ws = self.train_workspaces(T)[0]
+            s = dict(T=T, idx=new(T, k, dt=_I32), w=new(T, k, dt=_F32), counts=new(E, dt=_I32),
+                     offsets=new(E + sh + 1, dt=_I32), perm_src=new(R, dt=_I32),
+                     inv=new(R, dt=_I32))
+            moe_route(d, logits, s["idx"], s["w"], s["counts"], s["offsets"], s["perm_src"],
+                      s["inv"], ws)
+            xq, xs = new(T, H, dt=_U8), new(T, H // 128, dt=_U8)
+            moe_quant_act(x, xq, xs)
+            y13, y2 = new(Rs, 2 * I), new(Rs, H)
+            moe_grouped_gemm_w13(d, xq, xs, s["perm_src"], s["offsets"], self.w13, self.w13_s, y13,
+                                 ws)
+            hq, hs = new(Rs, I, dt=_U8), new(Rs, I // 128, dt=_U8)
+            if checkpoint == "fp8":
+                s |= dict(hq=hq, hs=hs, yq=new(Rs, 2 * I, dt=_U8),
+                          ys=new(Rs, 2 * I // 128, dt=_U8))
+                moe_swiglu_quant_save(y13, hq, hs, s["yq"], s["ys"])
+            else:
+                s |= dict(y13=y13, y2=y2)
+                moe_swiglu_quant(y13, hq, hs)
+            moe_grouped_gemm_w2(d, hq, hs, s["offsets"], self.w2, self.w2_s, y2, ws)
+            moe_combine(d, y2, s["inv"], s["w"], out)
+        return out, s
+
+    def backward(self, dout, saved, dx=None, dx_in=None, stream=None):
+        """Gradient of forward_train from dout [T, H] bf16 and the state it returned (not
+        changed).  Returns dx [T, H] (of dx's type where it is given, else bf16) = dx_in (the
+        gradient that reaches x by other ways, or None) + the experts' part, and dw [T, k] fp32,
+        the combine weights' gradient, which moe_balance_loss_backward takes to the logits.
+        The experts' weights have none."""
+        self._mxfp4_only("training")
+        T, H, I = saved["T"], self.H, self.I
+        d = self.dims(T)
+        Rs = T * (self.k + self.has_shared)
+        with torch.cuda.stream(stream):
+            new = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=dout.device)  # noqa: E731
+            ws = self.train_workspaces(T)[1]
+            if dx is None:
+                dx = new(T, H)
+            rows, dh, dy13, dw = new(Rs, H), new(Rs, I), new(Rs, 2 * I), new(T, self.k, dt=_F32)
+            if "yq" in saved:
+                moe_dispatch(d, dout, saved["inv"], rows)
+                act = dict(yq=saved["yq"], ys=saved["ys"], hq=saved["hq"], hs=saved["hs"],
+                           perm_src=saved["perm_src"], w=saved["w"], dw=dw)
+            else:
+                moe_combine_backward(d, dout, saved["y2"], saved["inv"], saved["w"], dy2=rows,
+                                     dw=dw)
+                act = dict(y13=saved["y13"])
+            moe_grouped_gemm_w2_backward(d, rows, saved["offsets"], self.w2, self.w2_s, dh, ws)
+            moe_swiglu_backward(dh, dy13, **act)
+            moe_grouped_gemm_w13_backward(d, dy13, saved["offsets"], self.w13, self.w13_s, rows, ws)
+            moe_dispatch_backward(d, rows, saved["inv"], dx, dx_in=dx_in)
+        return dx, dw
+
     CHUNK_CANDIDATES = (224, 208, 192, 176, 160, 144)
 
     def tune_chunk_rows(self, x, logits, candidates=CHUNK_CANDIDATES, steps=10, warmup=3):

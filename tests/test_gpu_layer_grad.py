@@ -1,0 +1,245 @@
+"""The gradient's operators together: MoELayer.forward_train / backward and the example's
+training step against float64 (stage by stage on the saved state, and as a whole), difference
+quotients of the formulas, streams, captured graphs."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_ffn_scan_gb300 as moe
+from examples.moe_block import make_block
+from gen import inputs as gi
+from tests import _block_ref as block_ref
+from tests import _grad_ref as ref
+from tests._parity import assert_float_close, with_gate_logits
+
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _experts(x, w13, w2, chosen, w, I):
+    """sum_j w_j W2_e (silu(g) u) of one token in float64, [g | u] = W13_e x; the shared expert
+    last with weight 1."""
+    out = 0
+    for e, we in zip(chosen, w):
+        y = w13[e] @ x
+        out = out + we * (w2[e] @ (y[:I] * ref.sigmoid(y[:I]) * y[I:]))
+    return out
+
+
+def test_formulas_against_difference_quotients():
+    """The chain that backward runs (dispatch, W2, SwiGLU with the weights, W13, sum), in float64
+    on the CPU, against central differences of the layer's formula."""
+    H, I, E, k = 12, 8, 4, 2
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    w13, w2, x, dout, w = r(E, 2 * I, H) * 0.4, r(E, H, I) * 0.4, r(H), r(H), torch.rand(k, generator=g, dtype=torch.float64)
+    chosen = [2, 0]
+    dx, dw = torch.zeros(H, dtype=torch.float64), []
+    for e, we in zip(chosen, w):
+        y = w13[e] @ x
+        dh = dout @ w2[e]
+        dg, du, _ = ref.swiglu_bwd(y[:I], y[I:], we * dh)
+        dx += torch.cat([dg, du]) @ w13[e]
+        dw.append(torch.dot(dh, y[:I] * ref.sigmoid(y[:I]) * y[I:]))
+    f = lambda xx, ww: torch.dot(dout, _experts(xx, w13, w2, chosen, ww, I))  # noqa: E731
+    eps = 1e-6
+    for i in range(H):
+        s = torch.zeros(H, dtype=torch.float64)
+        s[i] = eps
+        assert abs((f(x + s, w) - f(x - s, w)) / (2 * eps) - dx[i]) < 1e-7 * (1 + abs(dx[i]))
+    for j in range(k):
+        s = torch.zeros(k, dtype=torch.float64)
+        s[j] = eps
+        assert abs((f(x, w + s) - f(x, w - s)) / (2 * eps) - dw[j]) < 1e-7 * (1 + abs(dw[j]))
+
+
+def _layer(T, shared, seed=0):
+    d, t = gi.make_layer("tiny", seed=seed)
+    g = torch.Generator().manual_seed(seed + 5)
+    t = with_gate_logits(t)
+    sh = d.has_shared
+    w = {n: t[n].to(DEV) for n in ("w13", "w13_s", "w2", "w2_s")}
+    if shared and not sh:  # one more group from the first
+        w = {n: torch.cat([v, v[:1].flip(1)]) for n, v in w.items()}
+    layer = moe.MoELayer(d.H, d.I, d.E, d.k, int(shared), *w.values())
+    x = torch.randn(T, d.H, generator=g).to(BF).to(DEV)
+    logits = torch.randn(T, d.E, generator=g).to(DEV)
+    dout = torch.randn(T, d.H, generator=g).to(BF).to(DEV)
+    return layer, x, logits, dout
+
+
+def _whole(layer, s, dout, dx_in=None, dx_bf16=True):
+    """dx and dw in float64 from the saved state, each with a bound of the kernels' error: the
+    roundings of the steps (half a step of bf16 of dh, dy13, each row of dxp and dx; 2^-22 a
+    step of 16 of the products' sums; the sigmoid's c; fp32 sums), each carried through the
+    magnitudes of the steps behind it."""
+    T, k, I, H = s["T"], layer.k, layer.I, layer.H
+    R, sh = T * k, layer.has_shared
+    perm, off = s["perm_src"].long(), s["offsets"]
+    Rs = R + T * sh
+    rows = torch.zeros(Rs, H, dtype=torch.float64, device=DEV)
+    rows[:R] = dout.double()[perm // k]
+    if sh:
+        rows[R:] = dout.double()
+    wr = torch.ones(Rs, 1, dtype=torch.float64, device=DEV)
+    wr[:R, 0] = s["w"].double().view(-1)[perm]
+    dh, size = ref.expert_grad(rows, off, layer.w2, layer.w2_s, Rs, I)
+    # (with bf16 the weight comes in front of the product and its rounding, in that of dy2)
+    e_dh = ref.U16 * dh.abs() + (H / 16 + 1) * 2.0 ** -22 * size
+    if "yq" not in s:
+        e_dh += ref.U16 * size
+    y = ref.fp8_values(s["yq"], s["ys"]) if "yq" in s else s["y13"].double()
+    g, u = y[:, :I], y[:, I:]
+    dg, du, scale = ref.swiglu_bwd(g, u, dh * wr)
+    c = (g.abs() + 16) * 2.0 ** -22
+    sg = ref.sigmoid(g)
+    e_g = (u * sg * (1 + g * (1 - sg))).abs() * wr * e_dh + ref.U16 * dg.abs() + c * scale
+    e_u = (g * sg).abs() * wr * e_dh + (ref.U16 + c) * du.abs()
+    dy, e_dy = torch.cat([dg, du], 1), torch.cat([e_g, e_u], 1)
+    rows, size = ref.expert_grad(dy, off, layer.w13, layer.w13_s, Rs, H)
+    e_rows = ref.U16 * rows.abs() + (2 * I / 16 + 1) * 2.0 ** -22 * size
+    e_rows += ref.expert_grad(e_dy, off, layer.w13, layer.w13_s, Rs, H)[1]
+    dx, size = ref.dispatch_bwd(rows, s["inv"], T, k, R, sh, dx_in)
+    e_dx = (k + 2) * ref.U32 * size + ref.dispatch_bwd(e_rows, s["inv"], T, k, R, sh)[0]
+    if dx_bf16:
+        e_dx += ref.U16 * dx.abs()
+    dw = torch.zeros(2, R, dtype=torch.float64, device=DEV)
+    if "yq" in s:
+        h = ref.fp8_values(s["hq"], s["hs"])
+        dw[0, perm] = (dh * h)[:R].sum(1)
+        dw[1, perm] = ((e_dh + 96 * ref.U32 * dh.abs()) * h.abs())[:R].sum(1)
+    else:
+        prod = dout.double()[perm // k] * s["y2"][:R].double()
+        dw[0, perm], dw[1, perm] = prod.sum(1), 64 * ref.U32 * prod.abs().sum(1)
+    # second-order terms: a percent of the bound
+    return dx, 1.01 * e_dx, dw[0].view(T, k), 1.01 * dw[1].view(T, k)
+
+
+def _close(got, want, bound, name):
+    """Within the bound everywhere, and in norm within five roundings to bf16: each moves its
+    step's values by at most 2^-8 of their norm, and the steps behind it carry that and the
+    values alike (random signs)."""
+    err = (got.double() - want).abs()
+    assert torch.all(err <= bound), (name, (err - bound).max().item())
+    assert err.norm() <= 5 * ref.U16 * want.norm(), (name, (err.norm() / want.norm()).item())
+
+
+_np = lambda t: t.detach().double().cpu().numpy()  # noqa: E731
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 64, 300, 1500])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("form", ["fp8", "bf16"])
+def test_layer(T, shared, form):
+    layer, x, logits, dout = _layer(T, shared)
+    out, s = layer.forward_train(x, logits, checkpoint=form)
+    assert torch.equal(out, layer.forward(x, logits))
+    dx, dw = layer.backward(dout, s)
+    assert [moe.moe_check_status(w) for w in layer.train_workspaces(T)] == [0, 0]
+    want_dx, e_dx, want_dw, e_dw = _whole(layer, s, dout)
+    _close(dx, want_dx, e_dx, "dx")
+    _close(dw, want_dw, e_dw, "dw")
+    # with another gradient of x, in fp32
+    more = torch.randn(T, layer.H, device=DEV)
+    dx32, dw2 = layer.backward(dout, s, dx=torch.empty_like(more), dx_in=more)
+    assert torch.equal(dw, dw2)
+    want, bound = _whole(layer, s, dout, more, False)[:2]
+    _close(dx32, want, bound, "dx + dx_in")
+
+
+@pytest.mark.gpu
+def test_the_two_checkpoints_agree():
+    """The 8-bit checkpoint's rounding (half a step: 2^-4) is in dx of one and not the other, its
+    sign random from value to value."""
+    layer, x, logits, dout = _layer(300, True)
+    grads = [layer.backward(dout, layer.forward_train(x, logits, checkpoint=f)[1])
+             for f in ("fp8", "bf16")]
+    for a, b in zip(*grads):
+        err = (a.double() - b.double()).norm() / b.double().norm()
+        assert err < 2.0 ** -4
+
+
+@pytest.mark.gpu
+def test_refusals_of_the_layer():
+    layer, x, logits, dout = _layer(4, False)
+    with pytest.raises(ValueError, match="checkpoint"):
+        layer.forward_train(x, logits, checkpoint="int8")
+    layer.fmt = "nvfp4"
+    with pytest.raises(NotImplementedError):
+        layer.forward_train(x, logits)
+    with pytest.raises(NotImplementedError):
+        layer.backward(dout, {})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["fp8", "bf16"])
+def test_captured_and_replayed_on_new_inputs(form):
+    T = 130
+    layer, x, logits, dout = _layer(T, True)
+    layer.train_workspaces(T)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.backward(dout, layer.forward_train(x, logits, checkpoint=form)[1])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, s = layer.forward_train(x, logits, checkpoint=form)
+        dx, dw = layer.backward(dout, s)
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        x.copy_(torch.randn(x.shape, generator=g).to(BF))
+        logits.copy_(torch.randn(logits.shape, generator=g))
+        dout.copy_(torch.randn(dout.shape, generator=g).to(BF))
+        graph.replay()
+        got = [t.clone() for t in (out, dx, dw)]
+        own, s2 = layer.forward_train(x, logits, checkpoint=form)
+        want = [own, *layer.backward(dout, s2)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_on_a_stream_of_its_own():
+    T = 64
+    layer, x, logits, dout = _layer(T, True)
+    out, s = layer.forward_train(x, logits)
+    want = layer.backward(dout, s)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    o2, s2 = layer.forward_train(x, logits, stream=st)
+    got = layer.backward(dout, s2, stream=st)
+    st.synchronize()
+    assert torch.equal(out, o2) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_block_training_step():
+    T = 130
+    block, attn, stream = make_block(T)
+    f = block.forward(attn, stream, save=True)
+    dout = torch.randn(f["out"].shape, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    o, g = block.router_step(f, dout=dout, balance=1.0, z=0.1)
+    assert block.check() == [0, 0, 0, 0]
+    s = dict(T=T, perm_src=f["perm"], offsets=f["offsets"], inv=f["inv"], w=f["w"],
+             **{n: f[n] for n in ("yq", "ys", "hq", "hs")})
+    dy, e_dy, dw, e_dw = _whole(block.layer, s, dout, dx_bf16=False)
+    _close(g["dy_experts"], dy, e_dy, "dy of the experts")
+    _close(g["dw"], dw, e_dw, "dw")
+    dl = block_ref.balance_bwd(_np(f["logits"]), f["idx"].cpu().numpy(), None, None, 1, np.ones(1),
+                               np.full(1, 0.1), _np(g["dw"]))[0]
+    assert_float_close(_np(g["dlogits"]), dl, "dlogits", rel=1e-4)
+    # through the gate and the norm, the residual stream's own gradient added
+    wg16, dl16 = _np(block.wg.to(BF)), _np(g["dlogits"].to(BF))
+    assert_float_close(_np(g["dy"]), dl16 @ wg16 + _np(g["dy_experts"]), "dy")
+    dh, _ = block_ref.norm_bwd(_np(g["dy"]), _np(f["h"]), _np(f["rstd"]), _np(block.gain), _np(dout))
+    # one rounding to bf16 behind fp32 sums over a row of terms of dh's size
+    assert np.all(np.abs(_np(g["dh"]) - dh) <= ref.U16 * np.abs(dh) + 1e-4 * np.abs(dh).max(1, keepdims=True))
+
+
+@pytest.mark.gpu
+def test_saving_changes_no_output():
+    block, attn, stream = make_block(64)
+    a, b = block.forward(attn, stream), block.forward(attn, stream, save=True)
+    assert torch.equal(a["out"], b["out"])
