@@ -9,17 +9,28 @@
 // kernel multiplies in bf16 instead: E2M1 times a power of two is exact there (2 significant
 // bits), dy is bf16 as it comes, the products are exact in fp32 and are summed in fp32.
 //
-// A tile is 128 features (the MMA's M side) x up to 256 rows of one group (its N side, a
-// multiple of 16); a stage is 64 values of c:
+// The codes become bf16 straight in tensor memory, the MMA's A operand: the features are its M
+// side, one per TMEM lane.  The weights lie with the features contiguous, so a transpose is
+// needed, and ldmatrix makes it on the codes: read as 16-bit values (four features of one c),
+// transposed, a thread's 32-bit register holds four features of two consecutive c, and the codes
+// of one feature are 16 bits apart: a shift and two masks put them into the two halves of one
+// TMEM column, one multiplication by the two c's scales finishes them.  (Through shared memory
+// the converted weights cost 328 of a stage's 773 cycles of its bandwidth, and bound it.)
+//
+// Two forms of one kernel, P CTAs a tile:
+//   * P = 2, SM pairs (cta_group::2 MMAs of M = 256): 256 features x up to 192 rows of one group.
+//     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
+//     of the shared-memory traffic for dy that a tile of its own would.
+//   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
+//     weights' way from HBM and their conversion are the work.
+// A stage is 64 values of c, in each CTA:
 //   * warp 2 brings the codes of 64 weight rows x 128 features (4 KB, TMA) and their scales
-//     (cp.async: 4 bytes a row) into a ring of their own, so that many stages of the weights
-//     are on their way from HBM;
-//   * eight converter warps turn them into bf16 in shared memory, MN-major with the 128-byte
-//     swizzle (64 features of one c are a 128-byte row): a thread has 32 codes of one weight
-//     row and so one scale;
-//   * warp 0 brings dy's rows (K-major, TMA), warp 1 issues the MMAs;
+//     (cp.async: 4 bytes a row) into a ring, so that many stages of the weights are on their way;
+//   * groups of four converter warps, a stage each in turn; a warp has 32 features, so one
+//     scale a row;
+//   * warp 0 brings dy's rows (K-major, TMA), warp 1 (of the pair's first CTA) issues the MMAs;
 //   * four warps store the fp32 sums of the last tile from TMEM under the next one's MMAs.
-// Persistent CTAs; every CTA finds its tiles from the group offsets by itself (no plan kernel).
+// Persistent; every CTA finds its tiles from the group offsets by itself (no plan kernel).
 // Every wait is bounded; one that expires sets the workspace's status word.
 #include "grad.cuh"
 
@@ -28,27 +39,37 @@ namespace moe {
 namespace {
 
 constexpr int kBK = 64;          // c per stage: one 128-byte row of dy
-constexpr int kFeat = 128;       // features per tile
-constexpr int kRowsMax = 256;    // rows per tile
+constexpr int kFeat = 128;       // features per CTA
 constexpr int kMaxGroups = 1025;
-constexpr int kConvWarps = 8;
-constexpr int kThreads = 32 * (8 + kConvWarps);
-
-constexpr int kABytes = kFeat * kBK * 2;
-constexpr int kBBytes = kRowsMax * kBK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 3;
 constexpr int kRawCodes = kFeat / 2 * kBK;
 constexpr int kRawScales = kFeat / 32 * kBK;
-constexpr int kRaw = 12;
-constexpr int kOffRaw = kStages * kStageBytes;
-constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
-constexpr int kOffBar = kOffScale + kRaw * kRawScales;
-// full[S], empty[S], raw_full[R], raw_empty[R], acc_full[2], acc_empty[2], drain
-constexpr int kOffMisc = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8;
-constexpr int kOffGroups = kOffMisc + 16;  // tmem slot, abort flag; then off[], first[]
-constexpr int kSmem = kOffGroups + 2 * (kMaxGroups + 1) * 4 + 64;
-static_assert(kSmem <= kSmemMax, "dynamic shared memory of one CTA");
+constexpr int kACols = kBK / 2;  // TMEM columns of a stage of A
+
+template <int P>
+struct Cfg {
+  static constexpr int kOcc = P == 2 ? 1 : 2;         // CTAs per SM
+  static constexpr int kGroups = P == 2 ? 4 : 2;      // converter groups of four warps
+  static constexpr int kThreads = 32 * (8 + 4 * kGroups);
+  static constexpr int kRowsMax = P == 2 ? 192 : 32;  // rows per tile
+  static constexpr int kUnit = 16 * P;                // its N is a multiple of this
+  static constexpr int kBox = P == 2 ? 96 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
+  static constexpr int kBBytes = kRowsMax / P * kBK * 2;
+  static constexpr int kA = P == 2 ? 4 : 6;           // stages of A in TMEM
+  static constexpr int kB = P == 2 ? 8 : 6;           // of dy
+  static constexpr int kRaw = 16;                     // of codes and scales
+  static constexpr int kTmemCols = P == 2 ? 512 : 256;
+  static constexpr int kTmemA = 2 * kRowsMax;         // behind the two accumulators
+  static constexpr int kOffRaw = kB * kBBytes;
+  static constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
+  static constexpr int kOffBar = kOffScale + kRaw * kRawScales;
+  // a_full, a_empty [A], b_full, b_empty [B], raw_full, raw_empty [R], acc_full, acc_empty [2],
+  // drain
+  static constexpr int kOffMisc = kOffBar + (2 * (kA + kB + kRaw) + 5) * 8;
+  static constexpr int kOffGroups = kOffMisc + 16;  // tmem slot, abort flag; then off[], first[]
+  static constexpr int kSmem = kOffGroups + 2 * (kMaxGroups + 1) * 4 + kThreads / 32 * 4;
+  static_assert(kTmemA + kA * kACols <= kTmemCols, "tensor memory");
+  static_assert(kSmem <= kSmemMax / kOcc, "dynamic shared memory");
+};
 
 struct GradParams {
   const int32_t* offsets;
@@ -63,16 +84,85 @@ struct GradTile {
   int g, row0, rows, f0;
 };
 
-__device__ __forceinline__ uint32_t idesc_a_mn(int n) {  // bf16, A MN-major, M = 128
-  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(128 >> 4) << 24);
+// Instruction descriptor, kind::f16: D fp32, A and B bf16 and K-major, M x n.
+__device__ __forceinline__ uint32_t idesc_bf16(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// Rows of a group in chunks of at most kRowsMax, near-equal multiples of 16.
-__device__ __forceinline__ int chunks_of(int m) { return (m + kRowsMax - 1) / kRowsMax; }
+// kind::f16 MMA of an SM pair with A (each CTA's 128 rows) in tensor memory.
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
-// Tile L: items chunk by chunk inside a group, for one block of features after the other, so
-// that a weight tile is read for all of its group's chunks at about the same time.
+// Four 8 x 8 matrices of 16-bit values, transposed: lane l gives the address of row l % 8 of
+// matrix l / 8; its register m then holds (low, high) rows 2 (l % 4), + 1 of column l / 4.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 TMEM lanes x 16 columns: lane l's registers 2 m, 2 m + 1 go to lanes l / 4, l / 4 + 8 of
+// column 4 m + l % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// Arrive on an mbarrier of the pair's other CTA.  What it announces is in tensor memory,
+// complete since tcgen05.wait, so the arrival orders no more than this thread's CTA sees: with a
+// release for the cluster each took 1700 cycles.
+__device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// One lane of a converged warp, always the same.  The warps that issue TMA loads and MMAs run
+// their loops as a whole and branch to one lane for the issue alone: their addresses and
+// descriptors then live in uniform registers, as those instructions take them.  (A loop that one
+// lane runs alone spent 660 cycles a stage on four MMAs and their commit.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      :
+      : "memory");
+  return r != 0;
+}
+
+// A ring's slot and its phase, every `step`-th from `s` on (N a multiple of it).
+template <int N, int step = 1>
+struct Ring {
+  static_assert(N % step == 0, "the same slots in every round");
+  uint32_t s, phase = 0, round = 0;  // round: 0 while the slots are used for the first time
+  __device__ __forceinline__ explicit Ring(uint32_t first = 0) : s(first) {}
+  __device__ __forceinline__ void next() {
+    s += step;
+    if (s >= N) s -= N, phase ^= 1u, round = 1;
+  }
+};
+
+// Tile L: chunks of a group's rows (at most kRowsMax, near-equal multiples of kUnit) inside a
+// block of features, so that a weight tile is read for all of its group's chunks at about the
+// same time.
+template <int P>
+__device__ __forceinline__ int chunks_of(int m) {
+  return (m + Cfg<P>::kRowsMax - 1) / Cfg<P>::kRowsMax;
+}
+template <int P>
 __device__ __forceinline__ GradTile tile_at(long long L, int f_tiles, int G, const int* off,
                                             const int* first) {
   const int item = static_cast<int>(L / f_tiles);
@@ -84,64 +174,92 @@ __device__ __forceinline__ GradTile tile_at(long long L, int f_tiles, int G, con
   }
   const int m = off[lo + 1] - off[lo], nch = first[lo + 1] - first[lo];
   const int in = static_cast<int>(L - static_cast<long long>(first[lo]) * f_tiles);
-  const int per = ((m + nch - 1) / nch + 15) & ~15;
+  constexpr int U = Cfg<P>::kUnit;
+  const int per = ((m + nch - 1) / nch + U - 1) / U * U;
   const int chunk = in % nch;
   GradTile t;
   t.g = lo;
   t.row0 = off[lo] + chunk * per;
   t.rows = m - chunk * per < per ? m - chunk * per : per;
-  t.f0 = in / nch * kFeat;
+  t.f0 = in / nch * (kFeat * P);
   return t;
 }
 
-// Eight codes (a word, the code of feature i in bits 4 i..) to bf16 at memory positions
-// 0..7 = features 0, 4, 1, 5, 2, 6, 3, 7 (codes 16 bits apart share a register).  A code
-// s e e m put at bits 15 and 8..6 of a bf16 is its value times 2^-126, subnormals included;
-// mul is the scale times 2^126.
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, __nv_bfloat162 mul, uint32_t (&o)[4]) {
-  const uint32_t s[4] = {w << 12, w << 8, w << 4, w};
-  const uint32_t m[4] = {w << 6, w << 2, w >> 2, w >> 6};
+// A register of ldmatrix: feature i's codes of two c at bits 4 i and 4 i + 16, scales s the two
+// c's bytes (low, high half).  A code s e e m at bits 15 and 8..6 of a bf16 is its value times
+// 2^-126, subnormals included; the factor 2^(s - 127 + 126) is a bf16 up to s = 128.
+// (Shifts to the left as products, and the two parts joined by a product's addend: the shifts,
+// masks and joins of a stage would otherwise all fall on one pipe.)
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t factor, uint32_t (&o)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t v = (s[j] & 0x80008000u) | (m[j] & 0x01C001C0u);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&v), mul);
-    o[j] = *reinterpret_cast<const uint32_t*>(&r);
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t x = i ? w >> 8 : w;
+    uint32_t v[2];
+    v[0] = (x & 0x00070007u) * 64 + ((x * 4096) & 0x80008000u);
+    v[1] = (x & 0x00700070u) * 4 + ((x * 256) & 0x80008000u);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&v[j]),
+                                       *reinterpret_cast<__nv_bfloat162*>(&factor));
+      o[i + j] = *reinterpret_cast<const uint32_t*>(&r);
+    }
   }
 }
-// Position p of those eight holds feature:
-__device__ __forceinline__ int feature_at(int p) {
-  return (p & ~7) | ((p & 1) << 2) | ((p & 7) >> 1);
+// The factor where a scale byte is above 128: 2^127 in its place, and what is left of it
+// (255: NaN).
+__device__ __forceinline__ uint32_t factor_most(uint32_t s) {
+  const uint32_t lo = s & 0xFFFFu, hi = s >> 16;
+  return (((lo < 128 ? lo : 128) + 126) << 7) | (((hi < 128 ? hi : 128) + 126) << 23);
 }
+__device__ __forceinline__ uint32_t factor_rest(uint32_t s) {
+  const uint32_t lo = s & 0xFFFFu, hi = s >> 16;
+  const uint32_t a = lo == 255 ? 0x7FC0u : (lo < 128 ? 127u : lo - 1) << 7;
+  const uint32_t b = hi == 255 ? 0x7FC0u : (hi < 128 ? 127u : hi - 1) << 7;
+  return a | (b << 16);
+}
+// TMEM lane l of a warp's 32 holds feature:
+__device__ __forceinline__ int feature_at(int l) { return 4 * (l & 7) + (l >> 3); }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int P>
+__global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     k_expert_grad(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmBs, const GradParams p) {
+  using C = Cfg<P>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* empty = full + kStages;
-  uint64_t* raw_full = empty + kStages;
-  uint64_t* raw_empty = raw_full + kRaw;
-  uint64_t* acc_full = raw_empty + kRaw;
+  const uint32_t rank = P == 2 ? cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* a_empty = a_full + C::kA;
+  uint64_t* b_full = a_empty + C::kA;
+  uint64_t* b_empty = b_full + C::kB;
+  uint64_t* raw_full = b_empty + C::kB;
+  uint64_t* raw_empty = raw_full + C::kRaw;
+  uint64_t* acc_full = raw_empty + C::kRaw;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* off = reinterpret_cast<int*>(smem + kOffGroups);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  int* off = reinterpret_cast<int*>(smem + C::kOffGroups);
   int* first = off + kMaxGroups + 1;
-  int* sums = first + kMaxGroups + 1;  // of 16 warps
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* sums = first + kMaxGroups + 1;  // a warp's
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1 + kConvWarps);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < C::kA; ++s) {
+      mbar_init(&a_full[s], 4 * P);  // the stage's converter warps
+      mbar_init(&a_empty[s], 1);
     }
-    for (int s = 0; s < kRaw; ++s) {
+    for (int s = 0; s < C::kB; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(&raw_full[s], 1 + 32);
-      mbar_init(&raw_empty[s], kConvWarps);
+      mbar_init(&raw_empty[s], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);
+      mbar_init(&acc_empty[b], 4 * P);
     }
     mbar_init(drain, 1);
     const bool bad = (smem_u32(smem) & 1023u) != 0;
@@ -152,14 +270,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmBs);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  if (warp == 1) {
+    if (P == 2) tmem_alloc_pair(tmem_slot, C::kTmemCols);
+    else tmem_alloc(tmem_slot, C::kTmemCols);
+  }
   pdl_wait();
   // group offsets, and the number of chunks in front of each group
   const int G = p.G;
-  for (int g = threadIdx.x; g <= G; g += kThreads) off[g] = p.offsets[g];
+  for (int g = threadIdx.x; g <= G; g += C::kThreads) off[g] = p.offsets[g];
   __syncthreads();
   {
-    constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+    constexpr int kPer = (kMaxGroups + C::kThreads) / C::kThreads;
     int n[kPer], total = 0;
     bool bad = false;
 #pragma unroll
@@ -169,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g < G) {
         const int a = off[g], b = off[g + 1];
         if (a < 0 || b < a || b > p.rows) bad = true;
-        else total += chunks_of(b - a);
+        else total += chunks_of<P>(b - a);
       }
     }
     int scan = total;
@@ -195,204 +316,262 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (P == 2) cluster_sync();
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  const int f_tiles = p.F / kFeat, nk = p.C / kBK;
+  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P), nk = p.C / kBK;
   const long long total = *abort_flag ? 0 : static_cast<long long>(first[G]) * f_tiles;
+  const int cl = blockIdx.x / P, ncl = gridDim.x / P;
+  auto leader_addr = [&](const uint64_t* b) -> uint32_t { return mapa_shared(smem_u32(b), 0); };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- dy
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (long long L = blockIdx.x; L < total && ok; L += gridDim.x) {
-        const GradTile t = tile_at(L, f_tiles, G, off, first);
-        const bool small = t.rows <= 64;  // boxes of 32 rows, else of 128
-        const int box = small ? 32 : 128, boxes = (t.rows + box - 1) / box;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (it >= kStages &&
-              !mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, p.status, abort_flag)) {
-            ok = false;
-            break;
+    Ring<C::kB> st;
+    bool ok = true;
+    uint32_t issued = 0;
+    const uint32_t bar0 = P == 2 ? leader_addr(&b_full[0]) : 0;
+    for (long long L = cl; L < total && ok; L += ncl) {
+      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const int mine = (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit / P;  // rows in this CTA
+      const int row0 = t.row0 + static_cast<int>(rank) * mine;
+      const bool small = mine <= 2 * C::kBoxSmall;
+      const int box = small ? C::kBoxSmall : C::kBox, boxes = (mine + box - 1) / box;
+      const CUtensorMap* map = small ? &tmBs : &tmB;
+      const uint32_t bytes = P * boxes * box * kBK * 2;
+      for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
+        if (st.round && !mbar_wait(&b_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* b = smem + st.s * C::kBBytes;
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&b_full[st.s], bytes);
+          if (P == 2) {
+            tma_load_2d_pair(b, map, bar0 + st.s * 8, kb * kBK, row0);
+            if (boxes > 1)
+              tma_load_2d_pair(b + box * kBK * 2, map, bar0 + st.s * 8, kb * kBK, row0 + box);
+          } else {
+            tma_load_2d(b, map, &b_full[st.s], kb * kBK, row0);
+            if (boxes > 1)
+              tma_load_2d(b + box * kBK * 2, map, &b_full[st.s], kb * kBK, row0 + box);
           }
-          mbar_arrive_expect_tx(&full[s], boxes * box * kBK * 2);
-          uint8_t* b = smem + s * kStageBytes + kABytes;
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(b + i * box * kBK * 2, small ? &tmBs : &tmB, &full[s], kb * kBK,
-                        t.row0 + i * box);
         }
       }
-      if (*abort_flag) {
-        const uint32_t from = it > kStages ? it - kStages : 0;
-        for (uint32_t i = from; i < it; ++i) mbar_wait_drain(&full[i % kStages], (i / kStages) & 1u);
-      }
+    }
+    // after an abort: the loads still in flight (all counted on the first CTA's barriers)
+    if (leader && *abort_flag) {
+      const uint32_t from = issued > C::kB ? issued - C::kB : 0;
+      for (uint32_t i = from; i < issued; ++i)
+        mbar_wait_drain(&b_full[i % C::kB], (i / C::kB) & 1u);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      uint32_t it = 0, tc = 0;
+    if (leader) {
+      Ring<C::kA> ra;
+      Ring<C::kB> rb;
+      uint32_t tc = 0;
       bool ok = true;
-      for (long long L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
-        const GradTile t = tile_at(L, f_tiles, G, off, first);
-        const uint32_t idesc = idesc_a_mn((t.rows + 15) & ~15);
+      // (of a descriptor only the address, the low 14 bits, moves)
+      const uint64_t db0 = smem_desc(smem_u32(smem), 0, 1024, kLayoutSw128);
+      for (long long L = cl; L < total && ok; L += ncl, ++tc) {
+        const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+        const uint32_t idesc =
+            idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit);
         const uint32_t b = tc & 1u, use = tc >> 1;
         if (tc >= 2 && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
         tc_fence_after();
-        const uint32_t d = tmem + b * kRowsMax;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(&full[s], (it / kStages) & 1u, p.status, abort_flag)) {
-            ok = false;
-            break;
-          }
+        const uint32_t d = tmem + b * C::kRowsMax;
+        for (int kb = 0; kb < nk; ++kb, ra.next(), rb.next()) {
+          ok = mbar_wait(&b_full[rb.s], rb.phase, p.status, abort_flag) &&
+               mbar_wait(&a_full[ra.s], ra.phase, p.status, abort_flag);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + s * kStageBytes);
+          const uint32_t at = tmem + C::kTmemA + ra.s * kACols;
+          const uint64_t db = db0 + rb.s * (C::kBBytes / 16);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ss(d, smem_desc(a0 + kk * 2048, kBK * 128, 1024, kLayoutSw128),
-                        smem_desc(a0 + kABytes + kk * 32, 0, 1024, kLayoutSw128), idesc,
-                        kb > 0 || kk > 0);
-          tc_commit(&empty[s]);
+            for (int kk = 0; kk < 4; ++kk) {
+              if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
+              else mma_bf16_ts(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
+            }
+            if (P == 2) {
+              tc_commit_pair_mc(&a_empty[ra.s], 3);
+              tc_commit_pair_mc(&b_empty[rb.s], 3);
+            } else {
+              tc_commit(&a_empty[ra.s]);
+              tc_commit(&b_empty[rb.s]);
+            }
+          }
+          __syncwarp();
         }
-        if (ok) tc_commit(&acc_full[b]);
+        if (ok && elect_one()) {
+          if (P == 2) tc_commit_pair_mc(&acc_full[b], 3);
+          else tc_commit(&acc_full[b]);
+        }
+        __syncwarp();
       }
+      // after an abort: the MMAs already issued
       if (*abort_flag) {
-        tc_commit(drain);
+        if (elect_one()) {
+          if (P == 2) tc_commit_pair_mc(drain, 1);
+          else tc_commit(drain);
+        }
         mbar_wait_drain(drain, 0);
       }
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- codes and scales
-    uint32_t it = 0;
+    Ring<C::kRaw> st;
     bool ok = true;
-    for (long long L = blockIdx.x; L < total && ok; L += gridDim.x) {
-      const GradTile t = tile_at(L, f_tiles, G, off, first);
-      const uint8_t* sc = p.scales + static_cast<size_t>(t.g) * p.C * (p.F / 32) + t.f0 / 32;
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        const int s = it % kRaw;
-        int w_ok = 1;
-        if (it >= kRaw) {
-          if (lane == 0)
-            w_ok = mbar_wait(&raw_empty[s], ((it / kRaw) & 1u) ^ 1u, p.status, abort_flag);
-          w_ok = __shfl_sync(0xFFFFFFFFu, w_ok, 0);
-        }
-        if (!w_ok) {
+    uint32_t issued = 0;
+    const size_t row = p.F / 32;
+    for (long long L = cl; L < total && ok; L += ncl) {
+      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
+      const bool there = f0 < p.F;  // (the pair's second half may lie past the last feature)
+      const uint8_t* sc = p.scales + (static_cast<size_t>(t.g) * p.C + lane) * row + f0 / 32;
+      for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
+        if (st.round && !mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) ok = false;
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&raw_full[s], kRawCodes);
-          tma_load_2d(smem + kOffRaw + s * kRawCodes, &tmW, &raw_full[s], t.f0 / 2,
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&raw_full[st.s], kRawCodes);
+          tma_load_2d(smem + C::kOffRaw + st.s * kRawCodes, &tmW, &raw_full[st.s], f0 / 2,
                       t.g * p.C + kb * kBK);
         }
-        uint8_t* ds = smem + kOffScale + s * kRawScales;
-#pragma unroll
-        for (int i = 0; i < kBK; i += 32)
-          cp_async4(ds + (i + lane) * 4, sc + static_cast<size_t>(kb * kBK + i + lane) * (p.F / 32));
+        __syncwarp();
+        if (there) {
+          uint8_t* ds = smem + C::kOffScale + st.s * kRawScales + lane * 4;
+          cp_async4(ds, sc);
+          cp_async4(ds + 128, sc + 32 * row);
+          sc += kBK * row;
+        }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_u32(&raw_full[s]))
+                         smem_u32(&raw_full[st.s]))
                      : "memory");
       }
     }
     cp_async_commit();
     cp_async_wait<0>();
     __syncwarp();
-    if (lane == 0 && *abort_flag) {
-      const uint32_t from = it > kRaw ? it - kRaw : 0;
-      for (uint32_t i = from; i < it; ++i) mbar_wait_drain(&raw_full[i % kRaw], (i / kRaw) & 1u);
+    if (*abort_flag) {
+      const uint32_t from = issued > C::kRaw ? issued - C::kRaw : 0;
+      for (uint32_t i = from; i < issued; ++i)
+        mbar_wait_drain(&raw_full[i % C::kRaw], (i / C::kRaw) & 1u);
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- converters
-    // A warp has 32 weight rows x 32 features of the stage: with a row a lane, a quarter
-    // warp's 16-byte accesses fall on all the banks on both sides.
-    const int cw = warp - 8, q = cw & 3, row = (cw >> 2) * 32 + lane;
-    const uint32_t src = row * 64 + ((q ^ ((row >> 1) & 3)) << 4);  // 64-byte swizzle
-    const uint32_t dst = (q >> 1) * (kBK * 128) + row * 128;
-    const int j0 = (q & 1) * 4;
-    const uint32_t steps_per_tile = nk;
-    uint32_t it = 0;
-    bool ok = true;
-    for (long long L = blockIdx.x; L < total && ok; L += gridDim.x) {
-      for (uint32_t kb = 0; kb < steps_per_tile; ++kb, ++it) {
-        const int rs = it % kRaw, s = it % kStages;
-        bool w_ok = mbar_wait(&raw_full[rs], (it / kRaw) & 1u, p.status, abort_flag);
-        if (w_ok && it >= kStages)
-          w_ok = mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u, p.status, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, w_ok)) {
-          ok = false;
-          break;
+    const int q = warp & 3;  // its features' quarter, and TMEM lanes
+    // (64-byte swizzle: eight rows' 16-byte chunks fall on all the banks)
+    const uint32_t src =
+        smem_u32(smem + C::kOffRaw) + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+    const uint8_t* scales = smem + C::kOffScale + (lane & 3) * 8;  // of c = 2 (lane % 4), + 1
+    const uint32_t pick = q | (4 + q) << 8;  // bytes q of two words, to the two halves
+    const uint32_t dst = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::kTmemA;
+    const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
+    const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
+    const uint32_t group = (warp - 8) >> 2;
+    const uint32_t full0 = P == 2 ? leader_addr(&a_full[0]) : 0;
+    Ring<C::kA, C::kGroups> ra(group);
+    Ring<C::kRaw, C::kGroups> rr(group);
+    for (unsigned long long n = group; n < end; n += C::kGroups, ra.next(), rr.next()) {
+      bool w_ok = mbar_wait(&raw_full[rr.s], rr.phase, p.status, abort_flag);
+      if (w_ok && ra.round) w_ok = mbar_wait(&a_empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // 32 c each
+        uint32_t w[4], sc[4], over = 0;
+        ldmatrix_x4_trans(src + rr.s * kRawCodes + h * 2048, w);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint2 b = *reinterpret_cast<const uint2*>(scales + rr.s * kRawScales + h * 128 + m * 32);
+          sc[m] = __byte_perm(b.x, b.y, pick) & 0x00FF00FFu;
+          over |= sc[m] + 0x007F007Fu;
         }
-        const uint4 c = *reinterpret_cast<const uint4*>(smem + kOffRaw + rs * kRawCodes + src);
-        const uint32_t sb = smem[kOffScale + rs * kRawScales + row * 4 + q];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[rs]);
-        // 2^(sb - 127) * 2^126 as one bf16 factor up to sb = 128; what is above goes into a
-        // second one (255: NaN)
-        const uint32_t e1 = sb + 126 < 254 ? sb + 126 : 254;
-        const __nv_bfloat162 mul = __bfloat162bfloat162(__ushort_as_bfloat16(e1 << 7));
-        const uint32_t cw4[4] = {c.x, c.y, c.z, c.w};
-        uint32_t o[4][4];
+        if (h == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
+        }
+        uint32_t lo[8], hi[8];  // features 0, 1 and 2, 3 of the thread's four
 #pragma unroll
-        for (int i = 0; i < 4; ++i) codes_to_bf16(cw4[i], mul, o[i]);
-        if (sb > 128) {
-          const uint32_t e2 = sb == 255 ? 0x7FC0u : (sb - 128 + 127) << 7;
-          const __nv_bfloat162 more = __bfloat162bfloat162(__ushort_as_bfloat16(e2));
+        for (int m = 0; m < 4; ++m) {
+          uint32_t o[4];
+          codes_to_bf16(w[m], sc[m] * 128 + 0x3F003F00u, o);
+          lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
+        }
+        if (over & 0x01000100u) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int m = 0; m < 4; ++m) {
+            uint32_t o[4];
+            codes_to_bf16(w[m], factor_most(sc[m]), o);
+            uint32_t f = factor_rest(sc[m]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 r =
-                  __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i][j]), more);
-              o[i][j] = *reinterpret_cast<const uint32_t*>(&r);
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]),
+                                               *reinterpret_cast<__nv_bfloat162*>(&f));
+              o[i] = *reinterpret_cast<const uint32_t*>(&r);
             }
+            lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
+          }
         }
-        uint8_t* a = smem + s * kStageBytes + dst;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(a + (((j0 + i) ^ (row & 7)) << 4)) =
-              make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
+        tmem_st_16x128b_x4(dst + ra.s * kACols + h * 16, lo);
+        tmem_st_16x128b_x4(dst + ra.s * kACols + h * 16 + (16u << 16), hi);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (P == 2 && !leader) mbar_arrive_other(full0 + ra.s * 8);
+        else mbar_arrive(&a_full[ra.s]);
       }
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
     uint32_t tc = 0;
-    for (long long L = blockIdx.x; L < total; L += gridDim.x, ++tc) {
-      const GradTile t = tile_at(L, f_tiles, G, off, first);
+    for (long long L = cl; L < total; L += ncl, ++tc) {
+      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
       const uint32_t b = tc & 1u, use = tc >> 1;
       int w_ok = 1;
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kRowsMax;
-      uint16_t* out = p.dx + static_cast<size_t>(t.row0) * p.F + t.f0 + q * 32 + feature_at(lane);
-      for (int c = 0; c < t.rows; c += 16) {
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kRowsMax;
+      const int f = t.f0 + static_cast<int>(rank) * kFeat + q * 32;
+      uint16_t* out = p.dx + static_cast<size_t>(t.row0) * p.F + f + feature_at(lane);
+      const int rows = f < p.F ? t.rows : 0;
+      for (int c = 0; c < rows; c += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(acc + c, v);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (c + i < t.rows)
+          if (c + i < rows)
             out[static_cast<size_t>(c + i) * p.F] =
                 __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[i])));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (lane == 0) {
+        if (P == 2 && !leader) mbar_arrive_other(leader_addr(&acc_empty[b]));
+        else mbar_arrive(&acc_empty[b]);
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (P == 2) cluster_sync();  // neither CTA releases what the pair still uses
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (P == 2) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -420,16 +599,59 @@ bool encode_dy(CUtensorMap* m, const ExpertGradCall& a, int box_rows) {
          CUDA_SUCCESS;
 }
 
+template <int P>
+cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
+  using C = Cfg<P>;
+  static OncePerContext once;  // how many of its clusters fit the GPU at once
+  int dev = 0, clusters = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= OncePerContext::kDevices) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = P;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  if (once.ready(dev, current_context_id())) {
+    clusters = once.value(dev);
+  } else {
+    e = cudaFuncSetAttribute(k_expert_grad<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem);
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (P == 2) {
+      cfg.gridDim = dim3(sms / P * P);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&clusters, k_expert_grad<P>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (clusters < 1) return cudaErrorInvalidConfiguration;
+    } else {
+      clusters = sms * C::kOcc;  // (the query says one CTA per SM of any kernel with tensor memory)
+    }
+    once.set(dev, clusters);
+  }
+  CUtensorMap tmW, tmB, tmBs;
+  if (!encode_w(&tmW, a) || !encode_dy(&tmB, a, C::kBox) || !encode_dy(&tmBs, a, C::kBoxSmall))
+    return cudaErrorInvalidValue;
+  const GradParams p = {a.offsets, a.w_s, a.dx, a.G, a.rows, a.C, a.F, a.status};
+  cfg.gridDim = dim3(clusters * P);
+  cfg.attrs = attr;
+  cfg.numAttrs = P == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_expert_grad<P>, tmW, tmB, tmBs, p);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_grad(const ExpertGradCall& a, cudaStream_t st) {
-  cudaError_t e = allow_smem<k_expert_grad>();
-  if (e != cudaSuccess) return e;
-  CUtensorMap tmW, tmB, tmBs;
-  if (!encode_w(&tmW, a) || !encode_dy(&tmB, a, 128) || !encode_dy(&tmBs, a, 32))
-    return cudaErrorInvalidValue;
-  const GradParams p = {a.offsets, a.w_s, a.dx, a.G, a.rows, a.C, a.F, a.status};
-  return launch_k(k_expert_grad, kSms, kThreads, kSmem, st, tmW, tmB, tmBs, p);
+  return a.rows <= 32LL * a.G ? launch_grad<1>(a, st) : launch_grad<2>(a, st);
 }
 
 }  // namespace moe
