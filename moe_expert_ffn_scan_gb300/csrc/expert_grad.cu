@@ -26,6 +26,7 @@
 // A stage is 64 values of c, in each CTA:
 //   * warp 2 brings the codes of 64 weight rows x 128 features (4 KB, TMA) and their scales
 //     (cp.async: 4 bytes a row) into a ring, so that many stages of the weights are on their way;
+//   * warp 3 makes the scales what the converters multiply by;
 //   * groups of four converter warps, a stage each in turn; a warp has 32 features, so one
 //     scale a row;
 //   * warp 0 brings dy's rows (K-major, TMA), warp 1 (of the pair's first CTA) issues the MMAs;
@@ -43,32 +44,40 @@ constexpr int kFeat = 128;       // features per CTA
 constexpr int kMaxGroups = 1025;
 constexpr int kRawCodes = kFeat / 2 * kBK;
 constexpr int kRawScales = kFeat / 32 * kBK;
+// The scales of a stage as the converters multiply by them: [32 c][quarter of the features]
+// [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a scale byte is above 128.
+constexpr int kFactors = kRawScales * 2 + 16;
 constexpr int kACols = kBK / 2;  // TMEM columns of a stage of A
 
 template <int P>
 struct Cfg {
   static constexpr int kOcc = P == 2 ? 1 : 2;         // CTAs per SM
-  static constexpr int kGroups = P == 2 ? 4 : 2;      // converter groups of four warps
-  static constexpr int kThreads = 32 * (8 + 4 * kGroups);
-  static constexpr int kRowsMax = P == 2 ? 192 : 32;  // rows per tile
+  static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
+  static constexpr int kGroups = P == 2 ? 3 : 2;      // converter groups of four warps
+  static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
+  static constexpr int kRowsMax = P == 2 ? 256 : 32;  // rows per tile
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
-  static constexpr int kBox = P == 2 ? 96 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
+  static constexpr int kBox = P == 2 ? 128 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
+  static constexpr int kAcc = P == 2 ? 1 : 2;         // accumulators
+  static constexpr int kA = P == 2 ? 6 : 2;           // stages of A
+  static constexpr int kB = P == 2 ? 7 : 4;           // of dy
+  static constexpr int kRaw = P == 2 ? 15 : 12;       // of codes and scales
+  static constexpr int kTmemCols = P == 2 ? 512 : 64;
+  static constexpr int kTmemA = kAcc * kRowsMax;      // P = 2: A behind the accumulator
   static constexpr int kBBytes = kRowsMax / P * kBK * 2;
-  static constexpr int kA = P == 2 ? 4 : 6;           // stages of A in TMEM
-  static constexpr int kB = P == 2 ? 8 : 6;           // of dy
-  static constexpr int kRaw = 16;                     // of codes and scales
-  static constexpr int kTmemCols = P == 2 ? 512 : 256;
-  static constexpr int kTmemA = 2 * kRowsMax;         // behind the two accumulators
-  static constexpr int kOffRaw = kB * kBBytes;
+  static constexpr int kABytes = P == 2 ? 0 : kFeat * kBK * 2;  // P = 1: in shared memory
+  static constexpr int kOffA = kB * kBBytes;
+  static constexpr int kOffRaw = kOffA + kA * kABytes;
   static constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
-  static constexpr int kOffBar = kOffScale + kRaw * kRawScales;
-  // a_full, a_empty [A], b_full, b_empty [B], raw_full, raw_empty [R], acc_full, acc_empty [2],
-  // drain
-  static constexpr int kOffMisc = kOffBar + (2 * (kA + kB + kRaw) + 5) * 8;
+  static constexpr int kOffFactor = kOffScale + kRaw * kRawScales;
+  static constexpr int kOffBar = kOffFactor + (P == 2 ? kRaw * kFactors : 0);
+  // a_full, a_empty [A], b_full, b_empty [B], raw_full, raw_empty, fac_full [R], acc_full,
+  // acc_empty [2], drain
+  static constexpr int kOffMisc = kOffBar + (2 * kA + 2 * kB + 3 * kRaw + 5) * 8;
   static constexpr int kOffGroups = kOffMisc + 16;  // tmem slot, abort flag; then off[], first[]
   static constexpr int kSmem = kOffGroups + 2 * (kMaxGroups + 1) * 4 + kThreads / 32 * 4;
-  static_assert(kTmemA + kA * kACols <= kTmemCols, "tensor memory");
-  static_assert(kSmem <= kSmemMax / kOcc, "dynamic shared memory");
+  static_assert(kTmemA + (P == 2 ? kA * kACols : 0) <= kTmemCols, "tensor memory");
+  static_assert(kOffBar % 8 == 0 && kSmem <= kSmemMax / kOcc, "dynamic shared memory");
 };
 
 struct GradParams {
@@ -84,10 +93,10 @@ struct GradTile {
   int g, row0, rows, f0;
 };
 
-// Instruction descriptor, kind::f16: D fp32, A and B bf16 and K-major, M x n.
-__device__ __forceinline__ uint32_t idesc_bf16(int m, int n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(m >> 4) << 24);
+// Instruction descriptor, kind::f16: D fp32, A and B bf16, M x n, A MN-major or not.
+__device__ __forceinline__ uint32_t idesc_bf16(int m, int n, bool a_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // kind::f16 MMA of an SM pair with A (each CTA's 128 rows) in tensor memory.
@@ -217,8 +226,37 @@ __device__ __forceinline__ uint32_t factor_rest(uint32_t s) {
   const uint32_t b = hi == 255 ? 0x7FC0u : (hi < 128 ? 127u : hi - 1) << 7;
   return a | (b << 16);
 }
-// TMEM lane l of a warp's 32 holds feature:
-__device__ __forceinline__ int feature_at(int l) { return 4 * (l & 7) + (l >> 3); }
+// TMEM lane l of a warp's 32 holds feature (codes_to_bf16's order of a lane's four, or of the
+// eight of a word in shared memory):
+template <int P>
+__device__ __forceinline__ int feature_at(int l) {
+  return P == 2 ? 4 * (l & 7) + (l >> 3) : (l & ~7) | ((l & 1) << 2) | ((l & 7) >> 1);
+}
+
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A tile's scales, 64 rows of four bytes a stage: lane l has rows l and l + 32.  Their arrival
+// counts on the stage's barrier.
+struct ScaleLoad {
+  const uint8_t* at;
+  size_t row;
+  bool there;  // (a pair's second half may lie past the last feature)
+  __device__ __forceinline__ ScaleLoad(const GradParams& p, const GradTile& t, int f0, int lane)
+      : row(p.F / 32), there(f0 < p.F) {
+    at = p.scales + (static_cast<size_t>(t.g) * p.C + lane) * row + f0 / 32;
+  }
+  __device__ __forceinline__ void stage(uint8_t* to, uint64_t* bar, int lane) {
+    if (there) {
+      cp_async4(to + lane * 4, at);
+      cp_async4(to + 128 + lane * 4, at + 32 * row);
+      at += kBK * row;
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+  }
+};
 
 template <int P>
 __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
@@ -234,7 +272,8 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
   uint64_t* b_empty = b_full + C::kB;
   uint64_t* raw_full = b_empty + C::kB;
   uint64_t* raw_empty = raw_full + C::kRaw;
-  uint64_t* acc_full = raw_empty + C::kRaw;
+  uint64_t* fac_full = raw_empty + C::kRaw;
+  uint64_t* acc_full = fac_full + C::kRaw;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -256,10 +295,11 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(&raw_full[s], 1 + 32);
       mbar_init(&raw_empty[s], 4);
+      mbar_init(&fac_full[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4 * P);
+      mbar_init(&acc_empty[b], C::kEpi * P);
     }
     mbar_init(drain, 1);
     const bool bad = (smem_u32(smem) & 1023u) != 0;
@@ -374,12 +414,13 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       bool ok = true;
       // (of a descriptor only the address, the low 14 bits, moves)
       const uint64_t db0 = smem_desc(smem_u32(smem), 0, 1024, kLayoutSw128);
+      const uint64_t da0 = smem_desc(smem_u32(smem) + C::kOffA, kBK * 128, 1024, kLayoutSw128);
       for (long long L = cl; L < total && ok; L += ncl, ++tc) {
         const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
         const uint32_t idesc =
-            idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit);
-        const uint32_t b = tc & 1u, use = tc >> 1;
-        if (tc >= 2 && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
+            idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit, P == 1);
+        const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
+        if (use && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + b * C::kRowsMax;
         for (int kb = 0; kb < nk; ++kb, ra.next(), rb.next()) {
@@ -388,12 +429,13 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = tmem + C::kTmemA + ra.s * kACols;
+          const uint64_t da = da0 + ra.s * (C::kABytes / 16);
           const uint64_t db = db0 + rb.s * (C::kBBytes / 16);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
-              else mma_bf16_ts(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
+              else mma_bf16_ss(d, da + kk * (2048 / 16), db + kk * 2, idesc, kb > 0 || kk > 0);
             }
             if (P == 2) {
               tc_commit_pair_mc(&a_empty[ra.s], 3);
@@ -421,16 +463,14 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       }
     }
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- codes and scales
+    // ---------------------------------------------------------------- codes (P = 2: and scales)
     Ring<C::kRaw> st;
     bool ok = true;
     uint32_t issued = 0;
-    const size_t row = p.F / 32;
     for (long long L = cl; L < total && ok; L += ncl) {
       const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
       const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
-      const bool there = f0 < p.F;  // (the pair's second half may lie past the last feature)
-      const uint8_t* sc = p.scales + (static_cast<size_t>(t.g) * p.C + lane) * row + f0 / 32;
+      ScaleLoad sc(p, t, f0, lane);
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
         if (st.round && !mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) ok = false;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -443,76 +483,126 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
                       t.g * p.C + kb * kBK);
         }
         __syncwarp();
-        if (there) {
-          uint8_t* ds = smem + C::kOffScale + st.s * kRawScales + lane * 4;
-          cp_async4(ds, sc);
-          cp_async4(ds + 128, sc + 32 * row);
-          sc += kBK * row;
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_u32(&raw_full[st.s]))
-                     : "memory");
+        if (P == 2) sc.stage(smem + C::kOffScale + st.s * kRawScales, &raw_full[st.s], lane);
       }
     }
-    cp_async_commit();
-    cp_async_wait<0>();
+    if (P == 2) cp_async_wait_all();
     __syncwarp();
     if (*abort_flag) {
       const uint32_t from = issued > C::kRaw ? issued - C::kRaw : 0;
       for (uint32_t i = from; i < issued; ++i)
         mbar_wait_drain(&raw_full[i % C::kRaw], (i / C::kRaw) & 1u);
     }
-  } else if (warp >= 8) {
-    // ---------------------------------------------------------------- converters
+  } else if (warp == 3 && P == 1) {
+    // ---------------------------------------------------------------- scales
+    Ring<C::kRaw> st;
+    bool ok = true;
+    for (long long L = cl; L < total && ok; L += ncl) {
+      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      ScaleLoad sc(p, t, t.f0, lane);
+      for (int kb = 0; kb < nk; ++kb, st.next()) {
+        if (st.round && !mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) ok = false;
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        sc.stage(smem + C::kOffScale + st.s * kRawScales, &raw_full[st.s], lane);
+      }
+    }
+    cp_async_wait_all();
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- factors
+    // lane l has c = 2 l, 2 l + 1: factors 2^(s - 127 + 126), a bf16 each, for every quarter
+    Ring<C::kRaw> st;
+    bool ok = true;
+    uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::kOffFactor) + (lane >> 4) * 64 +
+                   (lane & 3) * 4 + ((lane >> 2) & 3);
+    for (long long L = cl; L < total && ok; L += ncl)
+      for (int kb = 0; kb < nk; ++kb, st.next()) {
+        ok = mbar_wait(&raw_full[st.s], st.phase, p.status, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint2 b = *reinterpret_cast<const uint2*>(smem + C::kOffScale + st.s * kRawScales +
+                                                        lane * 8);
+        uint32_t over = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t v = __byte_perm(b.x, b.y, q | (4 + q) << 8) & 0x00FF00FFu;
+          over |= v + 0x007F007Fu;
+          to[st.s * (kFactors / 4) + q * 16] = v * 128 + 0x3F003F00u;
+        }
+        const bool any = __any_sync(0xFFFFFFFFu, (over & 0x01000100u) != 0);
+        if (lane == 0) {
+          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * kFactors + kRawScales * 2) =
+              any;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&fac_full[st.s]);
+      }
+  } else if (P == 2 && warp >= 4 + C::kEpi) {
+    // ---------------------------------------------------------------- converters, P = 2
     const int q = warp & 3;  // its features' quarter, and TMEM lanes
     // (64-byte swizzle: eight rows' 16-byte chunks fall on all the banks)
     const uint32_t src =
         smem_u32(smem + C::kOffRaw) + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
-    const uint8_t* scales = smem + C::kOffScale + (lane & 3) * 8;  // of c = 2 (lane % 4), + 1
-    const uint32_t pick = q | (4 + q) << 8;  // bytes q of two words, to the two halves
+    const uint8_t* factors = smem + C::kOffFactor + q * 64 + (lane & 3) * 16;
     const uint32_t dst = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::kTmemA;
     const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
     const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
-    const uint32_t group = (warp - 8) >> 2;
+    const uint32_t group = (warp - 4 - C::kEpi) >> 2;
     const uint32_t full0 = P == 2 ? leader_addr(&a_full[0]) : 0;
     Ring<C::kA, C::kGroups> ra(group);
     Ring<C::kRaw, C::kGroups> rr(group);
     for (unsigned long long n = group; n < end; n += C::kGroups, ra.next(), rr.next()) {
-      bool w_ok = mbar_wait(&raw_full[rr.s], rr.phase, p.status, abort_flag);
+      bool w_ok = mbar_wait(&fac_full[rr.s], rr.phase, p.status, abort_flag);
       if (w_ok && ra.round) w_ok = mbar_wait(&a_empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       tc_fence_after();
+      const uint32_t over = *reinterpret_cast<const uint32_t*>(
+          smem + C::kOffFactor + rr.s * kFactors + kRawScales * 2);
+      uint32_t w[2][4];
+      uint4 fac[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ldmatrix_x4_trans(src + rr.s * kRawCodes + h * 2048, w[h]);
+        fac[h] = *reinterpret_cast<const uint4*>(factors + rr.s * kFactors + h * 256);
+      }
+      uint32_t sc[2][4];
+      if (over) {  // the bytes themselves
+        const int q8 = q * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint2 b = *reinterpret_cast<const uint2*>(
+                smem + C::kOffScale + rr.s * kRawScales + h * 128 + m * 32 + (lane & 3) * 8);
+            sc[h][m] = ((b.x >> q8) & 255u) | (((b.y >> q8) & 255u) << 16);
+          }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // 32 c each
-        uint32_t w[4], sc[4], over = 0;
-        ldmatrix_x4_trans(src + rr.s * kRawCodes + h * 2048, w);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint2 b = *reinterpret_cast<const uint2*>(scales + rr.s * kRawScales + h * 128 + m * 32);
-          sc[m] = __byte_perm(b.x, b.y, pick) & 0x00FF00FFu;
-          over |= sc[m] + 0x007F007Fu;
-        }
-        if (h == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
-        }
         uint32_t lo[8], hi[8];  // features 0, 1 and 2, 3 of the thread's four
+        const uint32_t f[4] = {fac[h].x, fac[h].y, fac[h].z, fac[h].w};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           uint32_t o[4];
-          codes_to_bf16(w[m], sc[m] * 128 + 0x3F003F00u, o);
+          codes_to_bf16(w[h][m], f[m], o);
           lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
         }
-        if (over & 0x01000100u) {
+        if (over) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             uint32_t o[4];
-            codes_to_bf16(w[m], factor_most(sc[m]), o);
-            uint32_t f = factor_rest(sc[m]);
+            codes_to_bf16(w[h][m], factor_most(sc[h][m]), o);
+            uint32_t rest = factor_rest(sc[h][m]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]),
-                                               *reinterpret_cast<__nv_bfloat162*>(&f));
+                                               *reinterpret_cast<__nv_bfloat162*>(&rest));
               o[i] = *reinterpret_cast<const uint32_t*>(&r);
             }
             lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
@@ -530,37 +620,107 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         else mbar_arrive(&a_full[ra.s]);
       }
     }
+  } else if (P == 1 && warp >= 4 + C::kEpi) {
+    // ---------------------------------------------------------------- converters, P = 1
+    // A lane has the warp's 32 features of two weight rows: one scale each, and a quarter
+    // warp's 16-byte accesses fall on all the banks on both sides.
+    const int q = warp & 3;
+    const uint8_t* src = smem + C::kOffRaw + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+    const uint8_t* scales = smem + C::kOffScale + lane * 4 + q;
+    uint8_t* dst = smem + C::kOffA + (q >> 1) * (kBK * 128) + lane * 128;
+    const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
+    const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
+    const uint32_t group = (warp - 4 - C::kEpi) >> 2;
+    Ring<C::kA, C::kGroups> ra(group);
+    Ring<C::kRaw, C::kGroups> rr(group);
+    for (unsigned long long n = group; n < end; n += C::kGroups, ra.next(), rr.next()) {
+      bool w_ok = mbar_wait(&raw_full[rr.s], rr.phase, p.status, abort_flag);
+      if (w_ok && ra.round) w_ok = mbar_wait(&a_empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
+      uint4 c[2];
+      uint32_t sb[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        c[h] = *reinterpret_cast<const uint4*>(src + rr.s * kRawCodes + h * 2048);
+        sb[h] = scales[rr.s * kRawScales + h * 128];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s2 = sb[h] * 0x00010001u, w4[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
+        uint32_t o[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          codes_to_bf16(w4[i], sb[h] > 128 ? factor_most(s2) : s2 * 128 + 0x3F003F00u, o[i]);
+        if (sb[h] > 128) {
+          uint32_t rest = factor_rest(s2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i][j]),
+                                               *reinterpret_cast<__nv_bfloat162*>(&rest));
+              o[i][j] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(dst + ra.s * C::kABytes + h * 4096 +
+                                    ((((q & 1) * 4 + i) ^ (lane & 7)) << 4)) =
+              make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[ra.s]);
+    }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
+    // P = 2: one accumulator, so the sums are first all taken to registers (eight warps, two
+    // for the same lanes with half of the rows each) and stored under the next tile's MMAs.
     const int q = warp & 3;
+    constexpr int kCols = P == 2 ? C::kRowsMax / (C::kEpi / 4) : 16;
     uint32_t tc = 0;
     for (long long L = cl; L < total; L += ncl, ++tc) {
       const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
-      const uint32_t b = tc & 1u, use = tc >> 1;
+      const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
       int w_ok = 1;
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kRowsMax;
+      const int c0 = P == 2 ? ((warp - 4) >> 2) * kCols : 0;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kRowsMax + c0;
       const int f = t.f0 + static_cast<int>(rank) * kFeat + q * 32;
-      uint16_t* out = p.dx + static_cast<size_t>(t.row0) * p.F + f + feature_at(lane);
-      const int rows = f < p.F ? t.rows : 0;
-      for (int c = 0; c < rows; c += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(acc + c, v);
-        tmem_ld_wait();
+      const int rows = f < p.F ? t.rows - c0 : 0;
+      uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0) * p.F + f + feature_at<P>(lane);
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (P == 2 && !leader) mbar_arrive_other(leader_addr(&acc_empty[b]));
+          else mbar_arrive(&acc_empty[b]);
+        }
+      };
+      uint32_t v[kCols / 2];  // two rows a register
+      for (int r0 = 0; r0 < (P == 2 ? 1 : rows); r0 += kCols) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < rows)
-            out[static_cast<size_t>(c + i) * p.F] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[i])));
+        for (int c = 0; c < kCols; c += 8) {
+          if (r0 + c < rows) {
+            uint32_t x[8];
+            tmem_ld_32x32b_x8(acc + r0 + c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[c / 2 + i] = bf16x2_of(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+          }
+        }
+        if (P == 2) release();
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (r0 + c < rows)
+            out[static_cast<size_t>(r0 + c) * p.F] = static_cast<uint16_t>(v[c / 2] >> (16 * (c & 1)));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (P == 2 && !leader) mbar_arrive_other(leader_addr(&acc_empty[b]));
-        else mbar_arrive(&acc_empty[b]);
-      }
+      if (P == 1) release();
     }
   }
   __syncwarp();
