@@ -59,24 +59,22 @@ struct Cfg {
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
   static constexpr int kBox = P == 2 ? 128 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
   static constexpr int kAcc = P == 2 ? 1 : 2;         // accumulators
-  static constexpr int kA = P == 2 ? 6 : 2;           // stages of A
-  static constexpr int kB = P == 2 ? 7 : 4;           // of dy
-  static constexpr int kRaw = P == 2 ? 15 : 12;       // of codes and scales
+  static constexpr int kSt = P == 2 ? 6 : 4;          // stages of both operands
+  static constexpr int kRaw = P == 2 ? 18 : 5;        // of codes and scales
   static constexpr int kTmemCols = P == 2 ? 512 : 64;
   static constexpr int kTmemA = kAcc * kRowsMax;      // P = 2: A behind the accumulator
   static constexpr int kBBytes = kRowsMax / P * kBK * 2;
   static constexpr int kABytes = P == 2 ? 0 : kFeat * kBK * 2;  // P = 1: in shared memory
-  static constexpr int kOffA = kB * kBBytes;
-  static constexpr int kOffRaw = kOffA + kA * kABytes;
+  static constexpr int kOffA = kSt * kBBytes;
+  static constexpr int kOffRaw = kOffA + kSt * kABytes;
   static constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
   static constexpr int kOffFactor = kOffScale + kRaw * kRawScales;
   static constexpr int kOffBar = kOffFactor + (P == 2 ? kRaw * kFactors : 0);
-  // a_full, a_empty [A], b_full, b_empty [B], raw_full, raw_empty, fac_full [R], acc_full,
-  // acc_empty [2], drain
-  static constexpr int kOffMisc = kOffBar + (2 * kA + 2 * kB + 3 * kRaw + 5) * 8;
+  // full, empty [St], raw_full, raw_empty, fac_full [R], acc_full, acc_empty [2], drain
+  static constexpr int kOffMisc = kOffBar + (2 * kSt + 3 * kRaw + 5) * 8;
   static constexpr int kOffGroups = kOffMisc + 16;  // tmem slot, abort flag; then off[], first[]
   static constexpr int kSmem = kOffGroups + 2 * (kMaxGroups + 1) * 4 + kThreads / 32 * 4;
-  static_assert(kTmemA + (P == 2 ? kA * kACols : 0) <= kTmemCols, "tensor memory");
+  static_assert(kTmemA + (P == 2 ? kSt * kACols : 0) <= kTmemCols, "tensor memory");
   static_assert(kOffBar % 8 == 0 && kSmem <= kSmemMax / kOcc, "dynamic shared memory");
 };
 
@@ -152,10 +150,10 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// A ring's slot and its phase, every `step`-th from `s` on (N a multiple of it).
+// A ring's slot and its phase, every `step`-th from `first` on.
 template <int N, int step = 1>
 struct Ring {
-  static_assert(N % step == 0, "the same slots in every round");
+  static_assert(N >= step, "at most one round a step");
   uint32_t s, phase = 0, round = 0;  // round: 0 while the slots are used for the first time
   __device__ __forceinline__ explicit Ring(uint32_t first = 0) : s(first) {}
   __device__ __forceinline__ void next() {
@@ -266,11 +264,9 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t rank = P == 2 ? cluster_ctarank() : 0;
   const bool leader = rank == 0;
-  uint64_t* a_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* a_empty = a_full + C::kA;
-  uint64_t* b_full = a_empty + C::kA;
-  uint64_t* b_empty = b_full + C::kB;
-  uint64_t* raw_full = b_empty + C::kB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + C::kSt;
+  uint64_t* raw_full = empty + C::kSt;
   uint64_t* raw_empty = raw_full + C::kRaw;
   uint64_t* fac_full = raw_empty + C::kRaw;
   uint64_t* acc_full = fac_full + C::kRaw;
@@ -284,13 +280,9 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kA; ++s) {
-      mbar_init(&a_full[s], 4 * P);  // the stage's converter warps
-      mbar_init(&a_empty[s], 1);
-    }
-    for (int s = 0; s < C::kB; ++s) {
-      mbar_init(&b_full[s], 1);
-      mbar_init(&b_empty[s], 1);
+    for (int s = 0; s < C::kSt; ++s) {
+      mbar_init(&full[s], 1 + 4 * P);  // dy's loads, the stage's converter warps
+      mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(&raw_full[s], 1 + 32);
@@ -367,10 +359,10 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- dy
-    Ring<C::kB> st;
+    Ring<C::kSt> st;
     bool ok = true;
     uint32_t issued = 0;
-    const uint32_t bar0 = P == 2 ? leader_addr(&b_full[0]) : 0;
+    const uint32_t bar0 = P == 2 ? leader_addr(&full[0]) : 0;
     for (long long L = cl; L < total && ok; L += ncl) {
       const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
       const int mine = (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit / P;  // rows in this CTA
@@ -380,36 +372,35 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const CUtensorMap* map = small ? &tmBs : &tmB;
       const uint32_t bytes = P * boxes * box * kBK * 2;
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
-        if (st.round && !mbar_wait(&b_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) {
+        if (st.round && !mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag)) {
           ok = false;
           break;
         }
         uint8_t* b = smem + st.s * C::kBBytes;
         if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(&b_full[st.s], bytes);
+          if (leader) mbar_arrive_expect_tx(&full[st.s], bytes);
           if (P == 2) {
             tma_load_2d_pair(b, map, bar0 + st.s * 8, kb * kBK, row0);
             if (boxes > 1)
               tma_load_2d_pair(b + box * kBK * 2, map, bar0 + st.s * 8, kb * kBK, row0 + box);
           } else {
-            tma_load_2d(b, map, &b_full[st.s], kb * kBK, row0);
+            tma_load_2d(b, map, &full[st.s], kb * kBK, row0);
             if (boxes > 1)
-              tma_load_2d(b + box * kBK * 2, map, &b_full[st.s], kb * kBK, row0 + box);
+              tma_load_2d(b + box * kBK * 2, map, &full[st.s], kb * kBK, row0 + box);
           }
         }
       }
     }
     // after an abort: the loads still in flight (all counted on the first CTA's barriers)
     if (leader && *abort_flag) {
-      const uint32_t from = issued > C::kB ? issued - C::kB : 0;
+      const uint32_t from = issued > C::kSt ? issued - C::kSt : 0;
       for (uint32_t i = from; i < issued; ++i)
-        mbar_wait_drain(&b_full[i % C::kB], (i / C::kB) & 1u);
+        mbar_wait_drain(&full[i % C::kSt], (i / C::kSt) & 1u);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
     if (leader) {
-      Ring<C::kA> ra;
-      Ring<C::kB> rb;
+      Ring<C::kSt> st;
       uint32_t tc = 0;
       bool ok = true;
       // (of a descriptor only the address, the low 14 bits, moves)
@@ -423,27 +414,20 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         if (use && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + b * C::kRowsMax;
-        for (int kb = 0; kb < nk; ++kb, ra.next(), rb.next()) {
-          ok = mbar_wait(&b_full[rb.s], rb.phase, p.status, abort_flag) &&
-               mbar_wait(&a_full[ra.s], ra.phase, p.status, abort_flag);
+        for (int kb = 0; kb < nk; ++kb, st.next()) {
+          ok = mbar_wait(&full[st.s], st.phase, p.status, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = tmem + C::kTmemA + ra.s * kACols;
-          const uint64_t da = da0 + ra.s * (C::kABytes / 16);
-          const uint64_t db = db0 + rb.s * (C::kBBytes / 16);
+          const uint32_t at = tmem + C::kTmemA + st.s * kACols;
+          const uint64_t da = da0 + st.s * (C::kABytes / 16), db = db0 + st.s * (C::kBBytes / 16);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
               else mma_bf16_ss(d, da + kk * (2048 / 16), db + kk * 2, idesc, kb > 0 || kk > 0);
             }
-            if (P == 2) {
-              tc_commit_pair_mc(&a_empty[ra.s], 3);
-              tc_commit_pair_mc(&b_empty[rb.s], 3);
-            } else {
-              tc_commit(&a_empty[ra.s]);
-              tc_commit(&b_empty[rb.s]);
-            }
+            if (P == 2) tc_commit_pair_mc(&empty[st.s], 3);
+            else tc_commit(&empty[st.s]);
           }
           __syncwarp();
         }
@@ -552,12 +536,12 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
     const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
     const uint32_t group = (warp - 4 - C::kEpi) >> 2;
-    const uint32_t full0 = P == 2 ? leader_addr(&a_full[0]) : 0;
-    Ring<C::kA, C::kGroups> ra(group);
+    const uint32_t full0 = P == 2 ? leader_addr(&full[0]) : 0;
+    Ring<C::kSt, C::kGroups> ra(group);
     Ring<C::kRaw, C::kGroups> rr(group);
     for (unsigned long long n = group; n < end; n += C::kGroups, ra.next(), rr.next()) {
       bool w_ok = mbar_wait(&fac_full[rr.s], rr.phase, p.status, abort_flag);
-      if (w_ok && ra.round) w_ok = mbar_wait(&a_empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
+      if (w_ok && ra.round) w_ok = mbar_wait(&empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       tc_fence_after();
       const uint32_t over = *reinterpret_cast<const uint32_t*>(
@@ -617,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       __syncwarp();
       if (lane == 0) {
         if (P == 2 && !leader) mbar_arrive_other(full0 + ra.s * 8);
-        else mbar_arrive(&a_full[ra.s]);
+        else mbar_arrive(&full[ra.s]);
       }
     }
   } else if (P == 1 && warp >= 4 + C::kEpi) {
@@ -631,11 +615,11 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
     const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
     const uint32_t group = (warp - 4 - C::kEpi) >> 2;
-    Ring<C::kA, C::kGroups> ra(group);
+    Ring<C::kSt, C::kGroups> ra(group);
     Ring<C::kRaw, C::kGroups> rr(group);
     for (unsigned long long n = group; n < end; n += C::kGroups, ra.next(), rr.next()) {
       bool w_ok = mbar_wait(&raw_full[rr.s], rr.phase, p.status, abort_flag);
-      if (w_ok && ra.round) w_ok = mbar_wait(&a_empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
+      if (w_ok && ra.round) w_ok = mbar_wait(&empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       uint4 c[2];
       uint32_t sb[2];
@@ -672,7 +656,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&a_full[ra.s]);
+      if (lane == 0) mbar_arrive(&full[ra.s]);
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
