@@ -195,15 +195,15 @@ __device__ __forceinline__ GradTile tile_at(long long L, int f_tiles, int G, con
 // A register of ldmatrix: feature i's codes of two c at bits 4 i and 4 i + 16, scales s the two
 // c's bytes (low, high half).  A code s e e m at bits 15 and 8..6 of a bf16 is its value times
 // 2^-126, subnormals included; the factor 2^(s - 127 + 126) is a bf16 up to s = 128.
-// (Shifts to the left as products, and the two parts joined by a product's addend: the shifts,
-// masks and joins of a stage would otherwise all fall on one pipe.)
+// (The product puts a copy of the code below bit 15 and one below bit 9; what the two leave
+// besides sign and magnitude is masked.  Shifts and joins would double the instructions.)
 __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t factor, uint32_t (&o)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
     const uint32_t x = i ? w >> 8 : w;
     uint32_t v[2];
-    v[0] = (x & 0x00070007u) * 64 + ((x * 4096) & 0x80008000u);
-    v[1] = (x & 0x00700070u) * 4 + ((x * 256) & 0x80008000u);
+    v[0] = ((x & 0x000F000Fu) * (64 + 4096)) & 0x81C081C0u;
+    v[1] = ((x & 0x00F000F0u) * (4 + 256)) & 0x81C081C0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&v[j]),
