@@ -59,22 +59,20 @@ struct Cfg {
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
   static constexpr int kBox = P == 2 ? 128 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
   static constexpr int kAcc = P == 2 ? 1 : 2;         // accumulators
-  static constexpr int kSt = P == 2 ? 6 : 4;          // stages of both operands
-  static constexpr int kRaw = P == 2 ? 18 : 5;        // of codes and scales
-  static constexpr int kTmemCols = P == 2 ? 512 : 64;
-  static constexpr int kTmemA = kAcc * kRowsMax;      // P = 2: A behind the accumulator
+  static constexpr int kSt = 6;                       // stages of both operands
+  static constexpr int kRaw = P == 2 ? 18 : 14;       // of codes and scales
+  static constexpr int kTmemCols = P == 2 ? 512 : 256;
+  static constexpr int kTmemA = kAcc * kRowsMax;      // A's stages behind the accumulators
   static constexpr int kBBytes = kRowsMax / P * kBK * 2;
-  static constexpr int kABytes = P == 2 ? 0 : kFeat * kBK * 2;  // P = 1: in shared memory
-  static constexpr int kOffA = kSt * kBBytes;
-  static constexpr int kOffRaw = kOffA + kSt * kABytes;
+  static constexpr int kOffRaw = kSt * kBBytes;
   static constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
   static constexpr int kOffFactor = kOffScale + kRaw * kRawScales;
-  static constexpr int kOffBar = kOffFactor + (P == 2 ? kRaw * kFactors : 0);
+  static constexpr int kOffBar = kOffFactor + kRaw * kFactors;
   // full, empty [St], raw_full, raw_empty, fac_full [R], acc_full, acc_empty [2], drain
   static constexpr int kOffMisc = kOffBar + (2 * kSt + 3 * kRaw + 5) * 8;
   static constexpr int kOffGroups = kOffMisc + 16;  // tmem slot, abort flag; then off[], first[]
   static constexpr int kSmem = kOffGroups + 2 * (kMaxGroups + 1) * 4 + kThreads / 32 * 4;
-  static_assert(kTmemA + (P == 2 ? kSt * kACols : 0) <= kTmemCols, "tensor memory");
+  static_assert(kTmemA + kSt * kACols <= kTmemCols, "tensor memory");
   static_assert(kOffBar % 8 == 0 && kSmem <= kSmemMax / kOcc, "dynamic shared memory");
 };
 
@@ -91,10 +89,10 @@ struct GradTile {
   int g, row0, rows, f0;
 };
 
-// Instruction descriptor, kind::f16: D fp32, A and B bf16, M x n, A MN-major or not.
-__device__ __forceinline__ uint32_t idesc_bf16(int m, int n, bool a_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+// Instruction descriptor, kind::f16: D fp32, A and B bf16 and K-major, M x n.
+__device__ __forceinline__ uint32_t idesc_bf16(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // kind::f16 MMA of an SM pair with A (each CTA's 128 rows) in tensor memory.
@@ -224,12 +222,8 @@ __device__ __forceinline__ uint32_t factor_rest(uint32_t s) {
   const uint32_t b = hi == 255 ? 0x7FC0u : (hi < 128 ? 127u : hi - 1) << 7;
   return a | (b << 16);
 }
-// TMEM lane l of a warp's 32 holds feature (codes_to_bf16's order of a lane's four, or of the
-// eight of a word in shared memory):
-template <int P>
-__device__ __forceinline__ int feature_at(int l) {
-  return P == 2 ? 4 * (l & 7) + (l >> 3) : (l & ~7) | ((l & 1) << 2) | ((l & 7) >> 1);
-}
+// TMEM lane l of a warp's 32 holds feature:
+__device__ __forceinline__ int feature_at(int l) { return 4 * (l & 7) + (l >> 3); }
 
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -405,11 +399,10 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       bool ok = true;
       // (of a descriptor only the address, the low 14 bits, moves)
       const uint64_t db0 = smem_desc(smem_u32(smem), 0, 1024, kLayoutSw128);
-      const uint64_t da0 = smem_desc(smem_u32(smem) + C::kOffA, kBK * 128, 1024, kLayoutSw128);
       for (long long L = cl; L < total && ok; L += ncl, ++tc) {
         const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
         const uint32_t idesc =
-            idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit, P == 1);
+            idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit);
         const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
         if (use && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
         tc_fence_after();
@@ -419,12 +412,12 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = tmem + C::kTmemA + st.s * kACols;
-          const uint64_t da = da0 + st.s * (C::kABytes / 16), db = db0 + st.s * (C::kBBytes / 16);
+          const uint64_t db = db0 + st.s * (C::kBBytes / 16);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
-              else mma_bf16_ss(d, da + kk * (2048 / 16), db + kk * 2, idesc, kb > 0 || kk > 0);
+              else mma_bf16_ts(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
             }
             if (P == 2) tc_commit_pair_mc(&empty[st.s], 3);
             else tc_commit(&empty[st.s]);
@@ -447,7 +440,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       }
     }
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- codes (P = 2: and scales)
+    // ---------------------------------------------------------------- codes and scales
     Ring<C::kRaw> st;
     bool ok = true;
     uint32_t issued = 0;
@@ -467,33 +460,16 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
                       t.g * p.C + kb * kBK);
         }
         __syncwarp();
-        if (P == 2) sc.stage(smem + C::kOffScale + st.s * kRawScales, &raw_full[st.s], lane);
+        sc.stage(smem + C::kOffScale + st.s * kRawScales, &raw_full[st.s], lane);
       }
     }
-    if (P == 2) cp_async_wait_all();
+    cp_async_wait_all();
     __syncwarp();
     if (*abort_flag) {
       const uint32_t from = issued > C::kRaw ? issued - C::kRaw : 0;
       for (uint32_t i = from; i < issued; ++i)
         mbar_wait_drain(&raw_full[i % C::kRaw], (i / C::kRaw) & 1u);
     }
-  } else if (warp == 3 && P == 1) {
-    // ---------------------------------------------------------------- scales
-    Ring<C::kRaw> st;
-    bool ok = true;
-    for (long long L = cl; L < total && ok; L += ncl) {
-      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
-      ScaleLoad sc(p, t, t.f0, lane);
-      for (int kb = 0; kb < nk; ++kb, st.next()) {
-        if (st.round && !mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) ok = false;
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
-        sc.stage(smem + C::kOffScale + st.s * kRawScales, &raw_full[st.s], lane);
-      }
-    }
-    cp_async_wait_all();
   } else if (warp == 3) {
     // ---------------------------------------------------------------- factors
     // lane l has c = 2 l, 2 l + 1: factors 2^(s - 127 + 126), a bf16 each, for every quarter
@@ -525,8 +501,8 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         __syncwarp();
         if (lane == 0) mbar_arrive(&fac_full[st.s]);
       }
-  } else if (P == 2 && warp >= 4 + C::kEpi) {
-    // ---------------------------------------------------------------- converters, P = 2
+  } else if (warp >= 4 + C::kEpi) {
+    // ---------------------------------------------------------------- converters
     const int q = warp & 3;  // its features' quarter, and TMEM lanes
     // (64-byte swizzle: eight rows' 16-byte chunks fall on all the banks)
     const uint32_t src =
@@ -604,60 +580,6 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         else mbar_arrive(&full[ra.s]);
       }
     }
-  } else if (P == 1 && warp >= 4 + C::kEpi) {
-    // ---------------------------------------------------------------- converters, P = 1
-    // A lane has the warp's 32 features of two weight rows: one scale each, and a quarter
-    // warp's 16-byte accesses fall on all the banks on both sides.
-    const int q = warp & 3;
-    const uint8_t* src = smem + C::kOffRaw + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
-    const uint8_t* scales = smem + C::kOffScale + lane * 4 + q;
-    uint8_t* dst = smem + C::kOffA + (q >> 1) * (kBK * 128) + lane * 128;
-    const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
-    const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
-    const uint32_t group = (warp - 4 - C::kEpi) >> 2;
-    Ring<C::kSt, C::kGroups> ra(group);
-    Ring<C::kRaw, C::kGroups> rr(group);
-    for (unsigned long long n = group; n < end; n += C::kGroups, ra.next(), rr.next()) {
-      bool w_ok = mbar_wait(&raw_full[rr.s], rr.phase, p.status, abort_flag);
-      if (w_ok && ra.round) w_ok = mbar_wait(&empty[ra.s], ra.phase ^ 1u, p.status, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
-      uint4 c[2];
-      uint32_t sb[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        c[h] = *reinterpret_cast<const uint4*>(src + rr.s * kRawCodes + h * 2048);
-        sb[h] = scales[rr.s * kRawScales + h * 128];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t s2 = sb[h] * 0x00010001u, w4[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
-        uint32_t o[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          codes_to_bf16(w4[i], sb[h] > 128 ? factor_most(s2) : s2 * 128 + 0x3F003F00u, o[i]);
-        if (sb[h] > 128) {
-          uint32_t rest = factor_rest(s2);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i][j]),
-                                               *reinterpret_cast<__nv_bfloat162*>(&rest));
-              o[i][j] = *reinterpret_cast<const uint32_t*>(&r);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(dst + ra.s * C::kABytes + h * 4096 +
-                                    ((((q & 1) * 4 + i) ^ (lane & 7)) << 4)) =
-              make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[ra.s]);
-    }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     // P = 2: one accumulator, so the sums are first all taken to registers (eight warps, two
@@ -676,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kRowsMax + c0;
       const int f = t.f0 + static_cast<int>(rank) * kFeat + q * 32;
       const int rows = f < p.F ? t.rows - c0 : 0;
-      uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0) * p.F + f + feature_at<P>(lane);
+      uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0) * p.F + f + feature_at(lane);
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
