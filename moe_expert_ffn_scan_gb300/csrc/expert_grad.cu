@@ -39,19 +39,20 @@ namespace moe {
 
 namespace {
 
-constexpr int kBK = 64;          // c per stage: one 128-byte row of dy
 constexpr int kFeat = 128;       // features per CTA
 constexpr int kMaxGroups = 1025;
-constexpr int kRawCodes = kFeat / 2 * kBK;
-constexpr int kRawScales = kFeat / 32 * kBK;
-// The scales of a stage as the converters multiply by them: [32 c][quarter of the features]
-// [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a scale byte is above 128.
-constexpr int kFactors = kRawScales * 2 + 16;
-constexpr int kACols = kBK / 2;  // TMEM columns of a stage of A
 
 template <int P>
 struct Cfg {
   static constexpr int kOcc = P == 2 ? 1 : 2;         // CTAs per SM
+  // c per stage.  Few rows: the barriers' and loops' instructions weigh, so a longer stage.
+  static constexpr int kBK = P == 2 ? 64 : 128;
+  static constexpr int kACols = kBK / 2;              // TMEM columns of a stage of A
+  static constexpr int kRawCodes = kFeat / 2 * kBK;
+  static constexpr int kRawScales = kFeat / 32 * kBK;
+  // The scales of a stage as the converters multiply by them: [32 c][quarter of the features]
+  // [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a byte is above 128.
+  static constexpr int kFactors = kRawScales * 2 + 16;
   static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
   static constexpr int kGroups = P == 2 ? 3 : 2;      // converter groups of four warps
   static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
@@ -59,8 +60,8 @@ struct Cfg {
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
   static constexpr int kBox = P == 2 ? 128 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
   static constexpr int kAcc = P == 2 ? 1 : 2;         // accumulators
-  static constexpr int kSt = 6;                       // stages of both operands
-  static constexpr int kRaw = P == 2 ? 18 : 14;       // of codes and scales
+  static constexpr int kSt = P == 2 ? 6 : 3;          // stages of both operands
+  static constexpr int kRaw = P == 2 ? 18 : 7;        // of codes and scales
   static constexpr int kTmemCols = P == 2 ? 512 : 256;
   static constexpr int kTmemA = kAcc * kRowsMax;      // A's stages behind the accumulators
   static constexpr int kBBytes = kRowsMax / P * kBK * 2;
@@ -229,8 +230,9 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A tile's scales, 64 rows of four bytes a stage: lane l has rows l and l + 32.  Their arrival
+// A tile's scales, kBK rows of four bytes a stage: lane l has rows l, l + 32, ...  Their arrival
 // counts on the stage's barrier.
+template <int P>
 struct ScaleLoad {
   const uint8_t* at;
   size_t row;
@@ -241,9 +243,11 @@ struct ScaleLoad {
   }
   __device__ __forceinline__ void stage(uint8_t* to, uint64_t* bar, int lane) {
     if (there) {
-      cp_async4(to + lane * 4, at);
-      cp_async4(to + 128 + lane * 4, at + 32 * row);
-      at += kBK * row;
+#pragma unroll
+      for (int i = 0; i < Cfg<P>::kBK / 32; ++i) {
+        cp_async4(to + (32 * i + lane) * 4, at);
+        at += 32 * row;
+      }
     }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P), nk = p.C / kBK;
+  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P), nk = p.C / C::kBK;
   const long long total = *abort_flag ? 0 : static_cast<long long>(first[G]) * f_tiles;
   const int cl = blockIdx.x / P, ncl = gridDim.x / P;
   auto leader_addr = [&](const uint64_t* b) -> uint32_t { return mapa_shared(smem_u32(b), 0); };
@@ -364,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const bool small = mine <= 2 * C::kBoxSmall;
       const int box = small ? C::kBoxSmall : C::kBox, boxes = (mine + box - 1) / box;
       const CUtensorMap* map = small ? &tmBs : &tmB;
-      const uint32_t bytes = P * boxes * box * kBK * 2;
+      const uint32_t bytes = P * boxes * box * C::kBK * 2;
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
         if (st.round && !mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag)) {
           ok = false;
@@ -373,15 +377,15 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         uint8_t* b = smem + st.s * C::kBBytes;
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[st.s], bytes);
-          if (P == 2) {
-            tma_load_2d_pair(b, map, bar0 + st.s * 8, kb * kBK, row0);
-            if (boxes > 1)
-              tma_load_2d_pair(b + box * kBK * 2, map, bar0 + st.s * 8, kb * kBK, row0 + box);
-          } else {
-            tma_load_2d(b, map, &full[st.s], kb * kBK, row0);
-            if (boxes > 1)
-              tma_load_2d(b + box * kBK * 2, map, &full[st.s], kb * kBK, row0 + box);
-          }
+#pragma unroll
+          for (int h = 0; h < C::kBK / 64; ++h)  // 64 c, one 128-byte swizzle row, each
+            for (int i = 0; i < boxes; ++i) {
+              uint8_t* to = b + (h * (C::kRowsMax / P) + i * box) * 128;
+              if (P == 2)
+                tma_load_2d_pair(to, map, bar0 + st.s * 8, kb * C::kBK + h * 64, row0 + i * box);
+              else
+                tma_load_2d(to, map, &full[st.s], kb * C::kBK + h * 64, row0 + i * box);
+            }
         }
       }
     }
@@ -411,13 +415,14 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           ok = mbar_wait(&full[st.s], st.phase, p.status, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = tmem + C::kTmemA + st.s * kACols;
+          const uint32_t at = tmem + C::kTmemA + st.s * C::kACols;
           const uint64_t db = db0 + st.s * (C::kBBytes / 16);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
-              else mma_bf16_ts(d, at + kk * 8, db + kk * 2, idesc, kb > 0 || kk > 0);
+            for (int kk = 0; kk < C::kBK / 16; ++kk) {
+              const uint64_t dk = db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2;
+              if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
+              else mma_bf16_ts(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
             }
             if (P == 2) tc_commit_pair_mc(&empty[st.s], 3);
             else tc_commit(&empty[st.s]);
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     for (long long L = cl; L < total && ok; L += ncl) {
       const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
       const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
-      ScaleLoad sc(p, t, f0, lane);
+      ScaleLoad<P> sc(p, t, f0, lane);
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
         if (st.round && !mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) ok = false;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -455,12 +460,12 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           break;
         }
         if (elect_one()) {
-          mbar_arrive_expect_tx(&raw_full[st.s], kRawCodes);
-          tma_load_2d(smem + C::kOffRaw + st.s * kRawCodes, &tmW, &raw_full[st.s], f0 / 2,
-                      t.g * p.C + kb * kBK);
+          mbar_arrive_expect_tx(&raw_full[st.s], C::kRawCodes);
+          tma_load_2d(smem + C::kOffRaw + st.s * C::kRawCodes, &tmW, &raw_full[st.s], f0 / 2,
+                      t.g * p.C + kb * C::kBK);
         }
         __syncwarp();
-        sc.stage(smem + C::kOffScale + st.s * kRawScales, &raw_full[st.s], lane);
+        sc.stage(smem + C::kOffScale + st.s * C::kRawScales, &raw_full[st.s], lane);
       }
     }
     cp_async_wait_all();
@@ -472,7 +477,8 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- factors
-    // lane l has c = 2 l, 2 l + 1: factors 2^(s - 127 + 126), a bf16 each, for every quarter
+    // lane l has c = 2 l, 2 l + 1 of every 64: factors 2^(s - 127 + 126), a bf16 each, for every
+    // quarter
     Ring<C::kRaw> st;
     bool ok = true;
     uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::kOffFactor) + (lane >> 4) * 64 +
@@ -484,19 +490,22 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           ok = false;
           break;
         }
-        const uint2 b = *reinterpret_cast<const uint2*>(smem + C::kOffScale + st.s * kRawScales +
-                                                        lane * 8);
         uint32_t over = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t v = __byte_perm(b.x, b.y, q | (4 + q) << 8) & 0x00FF00FFu;
-          over |= v + 0x007F007Fu;
-          to[st.s * (kFactors / 4) + q * 16] = v * 128 + 0x3F003F00u;
+        for (int h = 0; h < C::kBK / 64; ++h) {
+          const uint2 b = *reinterpret_cast<const uint2*>(
+              smem + C::kOffScale + st.s * C::kRawScales + h * 256 + lane * 8);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t v = __byte_perm(b.x, b.y, q | (4 + q) << 8) & 0x00FF00FFu;
+            over |= v + 0x007F007Fu;
+            to[st.s * (C::kFactors / 4) + h * 128 + q * 16] = v * 128 + 0x3F003F00u;
+          }
         }
         const bool any = __any_sync(0xFFFFFFFFu, (over & 0x01000100u) != 0);
         if (lane == 0) {
-          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * kFactors + kRawScales * 2) =
-              any;
+          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors +
+                                       C::kRawScales * 2) = any;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&fac_full[st.s]);
@@ -521,44 +530,41 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       tc_fence_after();
       const uint32_t over = *reinterpret_cast<const uint32_t*>(
-          smem + C::kOffFactor + rr.s * kFactors + kRawScales * 2);
-      uint32_t w[2][4];
-      uint4 fac[2];
+          smem + C::kOffFactor + rr.s * C::kFactors + C::kRawScales * 2);
+      constexpr int kH = C::kBK / 32;  // 32 c each
+      const uint32_t to = dst + ra.s * C::kACols;
+      if (!over) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ldmatrix_x4_trans(src + rr.s * kRawCodes + h * 2048, w[h]);
-        fac[h] = *reinterpret_cast<const uint4*>(factors + rr.s * kFactors + h * 256);
-      }
-      uint32_t sc[2][4];
-      if (over) {  // the bytes themselves
-        const int q8 = q * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint2 b = *reinterpret_cast<const uint2*>(
-                smem + C::kOffScale + rr.s * kRawScales + h * 128 + m * 32 + (lane & 3) * 8);
-            sc[h][m] = ((b.x >> q8) & 255u) | (((b.y >> q8) & 255u) << 16);
+        for (int h = 0; h < kH; ++h) {
+          uint32_t w[4], lo[8], hi[8];  // features 0, 1 and 2, 3 of the thread's four
+          ldmatrix_x4_trans(src + rr.s * C::kRawCodes + h * 2048, w);
+          const uint4 f = *reinterpret_cast<const uint4*>(factors + rr.s * C::kFactors + h * 256);
+          if (h == kH - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
           }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // 32 c each
-        uint32_t lo[8], hi[8];  // features 0, 1 and 2, 3 of the thread's four
-        const uint32_t f[4] = {fac[h].x, fac[h].y, fac[h].z, fac[h].w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          uint32_t o[4];
-          codes_to_bf16(w[h][m], f[m], o);
-          lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
-        }
-        if (over) {
+          const uint32_t f4[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             uint32_t o[4];
-            codes_to_bf16(w[h][m], factor_most(sc[h][m]), o);
-            uint32_t rest = factor_rest(sc[h][m]);
+            codes_to_bf16(w[m], f4[m], o);
+            lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
+          }
+          tmem_st_16x128b_x4(to + h * 16, lo);
+          tmem_st_16x128b_x4(to + h * 16 + (16u << 16), hi);
+        }
+      } else {  // a scale byte above 128: two factors, from the bytes
+#pragma unroll 1
+        for (int h = 0; h < kH; ++h) {
+          uint32_t w[4], lo[8], hi[8];
+          ldmatrix_x4_trans(src + rr.s * C::kRawCodes + h * 2048, w);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint2 b = *reinterpret_cast<const uint2*>(
+                smem + C::kOffScale + rr.s * C::kRawScales + h * 128 + m * 32 + (lane & 3) * 8);
+            const uint32_t sc = ((b.x >> (8 * q)) & 255u) | (((b.y >> (8 * q)) & 255u) << 16);
+            uint32_t o[4], rest = factor_rest(sc);
+            codes_to_bf16(w[m], factor_most(sc), o);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]),
@@ -567,10 +573,11 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
             }
             lo[2 * m] = o[0], lo[2 * m + 1] = o[1], hi[2 * m] = o[2], hi[2 * m + 1] = o[3];
           }
+          __syncwarp();
+          tmem_st_16x128b_x4(to + h * 16, lo);
+          tmem_st_16x128b_x4(to + h * 16 + (16u << 16), hi);
         }
-        __syncwarp();
-        tmem_st_16x128b_x4(dst + ra.s * kACols + h * 16, lo);
-        tmem_st_16x128b_x4(dst + ra.s * kACols + h * 16 + (16u << 16), hi);
+        if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -641,12 +648,12 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
   }
 }
 
-bool encode_w(CUtensorMap* m, const ExpertGradCall& a) {
+bool encode_w(CUtensorMap* m, const ExpertGradCall& a, int box_rows) {
   EncodeTiledFn enc = get_encode_tiled_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.F) / 2, static_cast<cuuint64_t>(a.G) * a.C};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.F) / 2};
-  cuuint32_t box[2] = {kFeat / 2, kBK}, es[2] = {1, 1};
+  cuuint32_t box[2] = {kFeat / 2, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.w), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
@@ -658,7 +665,7 @@ bool encode_dy(CUtensorMap* m, const ExpertGradCall& a, int box_rows) {
   if (!enc) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.C), static_cast<cuuint64_t>(a.rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.C) * 2};
-  cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(a.dy), dims, strides,
              box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
@@ -705,7 +712,7 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
     once.set(dev, clusters);
   }
   CUtensorMap tmW, tmB, tmBs;
-  if (!encode_w(&tmW, a) || !encode_dy(&tmB, a, C::kBox) || !encode_dy(&tmBs, a, C::kBoxSmall))
+  if (!encode_w(&tmW, a, C::kBK) || !encode_dy(&tmB, a, C::kBox) || !encode_dy(&tmBs, a, C::kBoxSmall))
     return cudaErrorInvalidValue;
   const GradParams p = {a.offsets, a.w_s, a.dx, a.G, a.rows, a.C, a.F, a.status};
   cfg.gridDim = dim3(clusters * P);
