@@ -57,17 +57,21 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
   return b ? __uint_as_float(b << 23) : __uint_as_float(1u << 22);
 }
 
-// The 16 values that codes with a scale byte stand for.
-__device__ __forceinline__ void values16(const uint4& c, uint32_t scale, float (&f)[16]) {
-  const float s = scale_of(scale);
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// Four codes (a word) as fp32, without their scale.
+__device__ __forceinline__ void codes4(uint32_t w, float (&f)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+        static_cast<__nv_fp8x2_storage_t>((w >> (16 * i)) & 0xFFFFu), __NV_E4M3);
     const float2 v = __half22float2(__half2(hr));
-    f[2 * i] = v.x * s, f[2 * i + 1] = v.y * s;
+    f[2 * i] = v.x, f[2 * i + 1] = v.y;
   }
+}
+__device__ __forceinline__ void bf16x4(uint32_t lo, uint32_t hi, float (&f)[4]) {
+  f[0] = bf16_lo(lo), f[1] = bf16_hi(lo), f[2] = bf16_lo(hi), f[3] = bf16_hi(hi);
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // Eight lanes per 128-column block, 16 columns a lane; Idx as wide as the lanes need.
@@ -112,18 +116,20 @@ __global__ void __launch_bounds__(256) k_swiglu_save(const uint16_t* __restrict_
   }
 }
 
-// A CTA per row, 16 columns a thread at a time.  kCodes: g and u from the checkpoint.
-template <bool kCodes>
-__global__ void __launch_bounds__(512) k_swiglu_bwd(const SwigluBwdCall a) {
+// A CTA per row, 16 columns a thread at a time; all of a thread's loads are in flight before
+// the first is used, and what they bring stays packed until its four columns' turn, so that
+// registers leave room for enough rows in flight.  kCodes: g and u from the checkpoint; kH: h
+// from hq.
+template <bool kCodes, bool kH>
+__global__ void __launch_bounds__(512, 2) k_swiglu_bwd(const SwigluBwdCall a) {
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, I = a.I;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ float part[16];
-  const bool routed = r < a.R;
   int src = 0;
   bool has = false;  // the row has a combine weight
-  if (routed && a.perm_src) {
+  if (r < a.R && a.perm_src) {
     src = __ldg(a.perm_src + r);
     has = src >= 0 && src < a.R;
   }
@@ -131,43 +137,56 @@ __global__ void __launch_bounds__(512) k_swiglu_bwd(const SwigluBwdCall a) {
   const size_t row = static_cast<size_t>(r);
   float dot = 0.f;
   for (int c = threadIdx.x * 16; c < I; c += blockDim.x * 16) {
-    float d[16], g[16], u[16];
-    ld_floats16(a.dh + row * I + c, d);
+    const uint4* dp = reinterpret_cast<const uint4*>(a.dh + row * I + c);
+    const uint4 d0 = dp[0], d1 = dp[1];
+    uint4 g0, g1, u0, u1, h0 = make_uint4(0, 0, 0, 0);
+    float sg = 1.f, su = 1.f, sh = 1.f;
     if (kCodes) {
       const uint8_t* q = a.yq + row * 2 * I + c;
       const uint8_t* s = a.ys + (row * 2 * I + c) / 128;
-      values16(*reinterpret_cast<const uint4*>(q), s[0], g);
-      values16(*reinterpret_cast<const uint4*>(q + I), s[I / 128], u);
+      g0 = *reinterpret_cast<const uint4*>(q);
+      u0 = *reinterpret_cast<const uint4*>(q + I);
+      sg = scale_of(s[0]), su = scale_of(s[I / 128]);
     } else {
-      ld_floats16(a.y13 + row * 2 * I + c, g);
-      ld_floats16(a.y13 + row * 2 * I + I + c, u);
+      const uint4* q = reinterpret_cast<const uint4*>(a.y13 + row * 2 * I + c);
+      g0 = q[0], g1 = q[1], u0 = q[I / 8], u1 = q[I / 8 + 1];
     }
-    if (a.dw && a.hq) {
-      float h[16];
-      values16(*reinterpret_cast<const uint4*>(a.hq + row * I + c),
-               a.hs[(row * I + c) / 128], h);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) dot = fmaf(d[i], h[i], dot);
+    if (kH) {
+      h0 = *reinterpret_cast<const uint4*>(a.hq + row * I + c);
+      sh = scale_of(a.hs[(row * I + c) / 128]);
     }
-    uint32_t og[2][4], ou[2][4];
+    float sum = 0.f;
+    uint32_t og[8], ou[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      float dg[2], du[2];
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const float s = sigmoid_of(g[i + o]), silu = g[i + o] * s, dd = w * d[i + o];
-        if (a.dw && !a.hq) dot = fmaf(d[i + o], silu * u[i + o], dot);
-        dg[o] = dd * u[i + o] * fmaf(silu, 1.f - s, s);
-        du[o] = dd * silu;
+    for (int i = 0; i < 4; ++i) {  // four columns
+      float d[4], g[4], u[4], h[4], dg[4], du[4];
+      const uint4& dv = i < 2 ? d0 : d1;
+      bf16x4(word(dv, 2 * i & 3), word(dv, (2 * i & 3) + 1), d);
+      if (kCodes) {
+        codes4(word(g0, i), g);
+        codes4(word(u0, i), u);
+      } else {
+        const uint4 &gv = i < 2 ? g0 : g1, &uv = i < 2 ? u0 : u1;
+        bf16x4(word(gv, 2 * i & 3), word(gv, (2 * i & 3) + 1), g);
+        bf16x4(word(uv, 2 * i & 3), word(uv, (2 * i & 3) + 1), u);
       }
-      og[i / 8][i / 2 % 4] = bf16x2_of(dg[0], dg[1]);
-      ou[i / 8][i / 2 % 4] = bf16x2_of(du[0], du[1]);
-    }
+      if (kH) codes4(word(h0, i), h);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      st_bf16x8(a.dy13 + row * 2 * I + c + 8 * i, og[i]);
-      st_bf16x8(a.dy13 + row * 2 * I + I + c + 8 * i, ou[i]);
+      for (int j = 0; j < 4; ++j) {
+        const float gj = kCodes ? g[j] * sg : g[j], uj = kCodes ? u[j] * su : u[j];
+        const float s = sigmoid_of(gj), silu = gj * s, dd = w * d[j];
+        sum = fmaf(d[j], kH ? h[j] : silu * uj, sum);
+        dg[j] = dd * uj * fmaf(silu, 1.f - s, s);
+        du[j] = dd * silu;
+      }
+      og[2 * i] = bf16x2_of(dg[0], dg[1]), og[2 * i + 1] = bf16x2_of(dg[2], dg[3]);
+      ou[2 * i] = bf16x2_of(du[0], du[1]), ou[2 * i + 1] = bf16x2_of(du[2], du[3]);
     }
+    dot = fmaf(sum, sh, dot);  // (h's scale is a power of two)
+    uint4* o = reinterpret_cast<uint4*>(a.dy13 + row * 2 * I + c);
+    o[0] = make_uint4(og[0], og[1], og[2], og[3]), o[1] = make_uint4(og[4], og[5], og[6], og[7]);
+    o[I / 8] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    o[I / 8 + 1] = make_uint4(ou[4], ou[5], ou[6], ou[7]);
   }
   if (!a.dw || !has) return;
 #pragma unroll
@@ -194,7 +213,10 @@ cudaError_t launch_swiglu_save(const uint16_t* y13, int rows, int I, uint8_t* hq
 cudaError_t launch_swiglu_bwd(const SwigluBwdCall& a, cudaStream_t st) {
   const int chunks = a.I / 16, rounds = (chunks + 511) / 512;
   const int warps = (chunks + rounds * 32 - 1) / (rounds * 32);
-  return launch_k(a.y13 ? k_swiglu_bwd<false> : k_swiglu_bwd<true>, a.rows, warps * 32, 0, st, a);
+  const bool h = a.dw && a.hq;
+  return launch_k(a.y13 ? (h ? k_swiglu_bwd<false, true> : k_swiglu_bwd<false, false>)
+                        : (h ? k_swiglu_bwd<true, true> : k_swiglu_bwd<true, false>),
+                  a.rows, warps * 32, 0, st, a);
 }
 
 }  // namespace moe
