@@ -70,9 +70,8 @@ __device__ __forceinline__ void codes4(uint32_t w, float (&f)[4]) {
 __device__ __forceinline__ void bf16x4(uint32_t lo, uint32_t hi, float (&f)[4]) {
   f[0] = bf16_lo(lo), f[1] = bf16_hi(lo), f[2] = bf16_lo(hi), f[3] = bf16_hi(hi);
 }
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
+// The gradient's CTAs: at most so many threads, and so many CTAs of that size per SM.
+constexpr int kBwdThreads = 512, kBwdCtas = 4;
 
 // Eight lanes per 128-column block, 16 columns a lane; Idx as wide as the lanes need.
 template <typename Idx>
@@ -116,17 +115,17 @@ __global__ void __launch_bounds__(256) k_swiglu_save(const uint16_t* __restrict_
   }
 }
 
-// A CTA per row, 16 columns a thread at a time; all of a thread's loads are in flight before
-// the first is used, and what they bring stays packed until its four columns' turn, so that
-// registers leave room for enough rows in flight.  kCodes: g and u from the checkpoint; kH: h
-// from hq.
+// A CTA per row, 8 columns a thread at a time; all of a thread's loads are in flight before the
+// first is used, and what they bring stays packed until its four columns' turn, so that
+// registers leave room for full occupancy (73728 rows of 2048: 225 us, 0.90 of HBM; with 40
+// registers a thread 272, with 16 columns and 64 registers 254).  kCodes: g and u from the checkpoint; kH: h from hq.
 template <bool kCodes, bool kH>
-__global__ void __launch_bounds__(512, 2) k_swiglu_bwd(const SwigluBwdCall a) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) k_swiglu_bwd(const SwigluBwdCall a) {
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, I = a.I;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float part[16];
+  __shared__ float part[kBwdThreads / 32];
   int src = 0;
   bool has = false;  // the row has a combine weight
   if (r < a.R && a.perm_src) {
@@ -136,41 +135,39 @@ __global__ void __launch_bounds__(512, 2) k_swiglu_bwd(const SwigluBwdCall a) {
   const float w = a.w && has ? __ldg(a.w + src) : 1.f;
   const size_t row = static_cast<size_t>(r);
   float dot = 0.f;
-  for (int c = threadIdx.x * 16; c < I; c += blockDim.x * 16) {
-    const uint4* dp = reinterpret_cast<const uint4*>(a.dh + row * I + c);
-    const uint4 d0 = dp[0], d1 = dp[1];
-    uint4 g0, g1, u0, u1, h0 = make_uint4(0, 0, 0, 0);
+  for (int c = threadIdx.x * 8; c < I; c += blockDim.x * 8) {
+    uint32_t dv[4], gv[4], uv[4], hv[2] = {0, 0};
+    ld_bf16x8(a.dh + row * I + c, dv);
     float sg = 1.f, su = 1.f, sh = 1.f;
     if (kCodes) {
       const uint8_t* q = a.yq + row * 2 * I + c;
       const uint8_t* s = a.ys + (row * 2 * I + c) / 128;
-      g0 = *reinterpret_cast<const uint4*>(q);
-      u0 = *reinterpret_cast<const uint4*>(q + I);
+      const uint2 g = *reinterpret_cast<const uint2*>(q), u = *reinterpret_cast<const uint2*>(q + I);
+      gv[0] = g.x, gv[1] = g.y, uv[0] = u.x, uv[1] = u.y;
       sg = scale_of(s[0]), su = scale_of(s[I / 128]);
     } else {
-      const uint4* q = reinterpret_cast<const uint4*>(a.y13 + row * 2 * I + c);
-      g0 = q[0], g1 = q[1], u0 = q[I / 8], u1 = q[I / 8 + 1];
+      ld_bf16x8(a.y13 + row * 2 * I + c, gv);
+      ld_bf16x8(a.y13 + row * 2 * I + I + c, uv);
     }
     if (kH) {
-      h0 = *reinterpret_cast<const uint4*>(a.hq + row * I + c);
+      const uint2 h = *reinterpret_cast<const uint2*>(a.hq + row * I + c);
+      hv[0] = h.x, hv[1] = h.y;
       sh = scale_of(a.hs[(row * I + c) / 128]);
     }
     float sum = 0.f;
-    uint32_t og[8], ou[8];
+    uint32_t og[4], ou[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // four columns
+    for (int i = 0; i < 2; ++i) {  // four columns
       float d[4], g[4], u[4], h[4], dg[4], du[4];
-      const uint4& dv = i < 2 ? d0 : d1;
-      bf16x4(word(dv, 2 * i & 3), word(dv, (2 * i & 3) + 1), d);
+      bf16x4(dv[2 * i], dv[2 * i + 1], d);
       if (kCodes) {
-        codes4(word(g0, i), g);
-        codes4(word(u0, i), u);
+        codes4(gv[i], g);
+        codes4(uv[i], u);
       } else {
-        const uint4 &gv = i < 2 ? g0 : g1, &uv = i < 2 ? u0 : u1;
-        bf16x4(word(gv, 2 * i & 3), word(gv, (2 * i & 3) + 1), g);
-        bf16x4(word(uv, 2 * i & 3), word(uv, (2 * i & 3) + 1), u);
+        bf16x4(gv[2 * i], gv[2 * i + 1], g);
+        bf16x4(uv[2 * i], uv[2 * i + 1], u);
       }
-      if (kH) codes4(word(h0, i), h);
+      if (kH) codes4(hv[i], h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float gj = kCodes ? g[j] * sg : g[j], uj = kCodes ? u[j] * su : u[j];
@@ -183,10 +180,8 @@ __global__ void __launch_bounds__(512, 2) k_swiglu_bwd(const SwigluBwdCall a) {
       ou[2 * i] = bf16x2_of(du[0], du[1]), ou[2 * i + 1] = bf16x2_of(du[2], du[3]);
     }
     dot = fmaf(sum, sh, dot);  // (h's scale is a power of two)
-    uint4* o = reinterpret_cast<uint4*>(a.dy13 + row * 2 * I + c);
-    o[0] = make_uint4(og[0], og[1], og[2], og[3]), o[1] = make_uint4(og[4], og[5], og[6], og[7]);
-    o[I / 8] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-    o[I / 8 + 1] = make_uint4(ou[4], ou[5], ou[6], ou[7]);
+    st_bf16x8(a.dy13 + row * 2 * I + c, og);
+    st_bf16x8(a.dy13 + row * 2 * I + I + c, ou);
   }
   if (!a.dw || !has) return;
 #pragma unroll
@@ -211,7 +206,7 @@ cudaError_t launch_swiglu_save(const uint16_t* y13, int rows, int I, uint8_t* hq
 }
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdCall& a, cudaStream_t st) {
-  const int chunks = a.I / 16, rounds = (chunks + 511) / 512;
+  const int chunks = a.I / 8, rounds = (chunks + kBwdThreads - 1) / kBwdThreads;
   const int warps = (chunks + rounds * 32 - 1) / (rounds * 32);
   const bool h = a.dw && a.hq;
   return launch_k(a.y13 ? (h ? k_swiglu_bwd<false, true> : k_swiglu_bwd<false, false>)
