@@ -31,7 +31,8 @@ int expert_grad(const moe_dims* d, int C, int F, const uint16_t* dy, const int32
   if (ws_bytes < moe_gemm_backward_workspace_size(d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   ExpertGradCall a = {};
   a.dy = dy, a.offsets = offsets, a.w = w, a.w_s = w_s, a.dx = dx;
-  a.G = d->E + d->has_shared, a.rows = rows_Rs(d), a.C = C, a.F = F;
+  a.E = d->E, a.G = d->E + d->has_shared, a.routed = rows_R(d), a.rows = rows_Rs(d);
+  a.C = C, a.F = F;
   a.status = static_cast<uint32_t*>(ws);
   return cuda_rc(launch_expert_grad(a, static_cast<cudaStream_t>(stream)));
 }

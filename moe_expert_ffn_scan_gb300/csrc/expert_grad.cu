@@ -35,6 +35,8 @@
 // Every wait is bounded; one that expires sets the workspace's status word.
 #include "grad.cuh"
 
+#include <math.h>
+
 namespace moe {
 
 namespace {
@@ -49,10 +51,10 @@ struct Cfg {
   static constexpr int kBK = P == 2 ? 64 : 128;
   static constexpr int kACols = kBK / 2;              // TMEM columns of a stage of A
   static constexpr int kRawCodes = kFeat / 2 * kBK;
-  static constexpr int kRawScales = kFeat / 32 * kBK;
+  static constexpr int kRawScales = 16 * kBK;         // 16 bytes a weight row, 4 of them the CTA's
   // The scales of a stage as the converters multiply by them: [32 c][quarter of the features]
   // [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a byte is above 128.
-  static constexpr int kFactors = kRawScales * 2 + 16;
+  static constexpr int kFactors = kBK * 8 + 16;
   static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
   static constexpr int kGroups = P == 2 ? 3 : 2;      // converter groups of four warps
   static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
@@ -230,8 +232,10 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A tile's scales, kBK rows of four bytes a stage: lane l has rows l, l + 32, ...  Their arrival
-// counts on the stage's barrier.
+// A tile's scales, kBK weight rows a stage: lane l has rows l, l + 32, ...  Of each row the CTA's
+// four bytes are loaded with the aligned 16 around them (which end inside the tensor: its size
+// is a multiple of 512 bytes), because copies of 16 bytes pass L1 by: with 4 bytes a row 32 groups
+// of one row took 158 us in place of 132.  Their arrival counts on the stage's barrier.
 template <int P>
 struct ScaleLoad {
   const uint8_t* at;
@@ -245,7 +249,8 @@ struct ScaleLoad {
     if (there) {
 #pragma unroll
       for (int i = 0; i < Cfg<P>::kBK / 32; ++i) {
-        cp_async4(to + (32 * i + lane) * 4, at);
+        cp_async16(to + (32 * i + lane) * 16,
+                   reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15)));
         at += 32 * row;
       }
     }
@@ -253,6 +258,11 @@ struct ScaleLoad {
                  : "memory");
   }
 };
+// Where row c of a stage has the four bytes: a stage's first row, and so a group's, starts at a
+// multiple of 16 bytes.
+__device__ __forceinline__ int scale_at(int c, int f0, int F) {
+  return c * 16 + ((c * (F / 128) + f0 / 128) & 3) * 4;
+}
 
 template <int P>
 __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
@@ -483,7 +493,11 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     bool ok = true;
     uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::kOffFactor) + (lane >> 4) * 64 +
                    (lane & 3) * 4 + ((lane >> 2) & 3);
-    for (long long L = cl; L < total && ok; L += ncl)
+    for (long long L = cl; L < total && ok; L += ncl) {
+      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
+      const uint8_t* lo = smem + C::kOffScale + scale_at(2 * lane, f0, p.F);
+      const uint8_t* hi = smem + C::kOffScale + scale_at(2 * lane + 1, f0, p.F);
       for (int kb = 0; kb < nk; ++kb, st.next()) {
         ok = mbar_wait(&raw_full[st.s], st.phase, p.status, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -493,23 +507,25 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         uint32_t over = 0;
 #pragma unroll
         for (int h = 0; h < C::kBK / 64; ++h) {
-          const uint2 b = *reinterpret_cast<const uint2*>(
-              smem + C::kOffScale + st.s * C::kRawScales + h * 256 + lane * 8);
+          // (64 rows further the bytes' place in their 16 is the same)
+          const int at = st.s * C::kRawScales + h * 1024;
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(lo + at);
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(hi + at);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t v = __byte_perm(b.x, b.y, q | (4 + q) << 8) & 0x00FF00FFu;
+            const uint32_t v = __byte_perm(x, y, q | (4 + q) << 8) & 0x00FF00FFu;
             over |= v + 0x007F007Fu;
             to[st.s * (C::kFactors / 4) + h * 128 + q * 16] = v * 128 + 0x3F003F00u;
           }
         }
         const bool any = __any_sync(0xFFFFFFFFu, (over & 0x01000100u) != 0);
         if (lane == 0) {
-          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors +
-                                       C::kRawScales * 2) = any;
+          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + C::kBK * 8) = any;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&fac_full[st.s]);
       }
+    }
   } else if (warp >= 4 + C::kEpi) {
     // ---------------------------------------------------------------- converters
     const int q = warp & 3;  // its features' quarter, and TMEM lanes
@@ -530,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       tc_fence_after();
       const uint32_t over = *reinterpret_cast<const uint32_t*>(
-          smem + C::kOffFactor + rr.s * C::kFactors + C::kRawScales * 2);
+          smem + C::kOffFactor + rr.s * C::kFactors + C::kBK * 8);
       constexpr int kH = C::kBK / 32;  // 32 c each
       const uint32_t to = dst + ra.s * C::kACols;
       if (!over) {
@@ -560,9 +576,10 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           ldmatrix_x4_trans(src + rr.s * C::kRawCodes + h * 2048, w);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const uint2 b = *reinterpret_cast<const uint2*>(
-                smem + C::kOffScale + rr.s * C::kRawScales + h * 128 + m * 32 + (lane & 3) * 8);
-            const uint32_t sc = ((b.x >> (8 * q)) & 255u) | (((b.y >> (8 * q)) & 255u) << 16);
+            // the two bytes again, of what the factor's arithmetic made of them
+            const uint32_t f = *reinterpret_cast<const uint32_t*>(
+                factors + rr.s * C::kFactors + h * 256 + m * 4);
+            const uint32_t sc = ((f - 0x3F003F00u) >> 7) & 0x01FF01FFu;
             uint32_t o[4], rest = factor_rest(sc);
             codes_to_bf16(w[m], factor_most(sc), o);
 #pragma unroll
@@ -721,10 +738,29 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_expert_grad<P>, tmW, tmB, tmBs, p);
 }
 
+// The form that should take less time, from what the host knows: the dims, not the routing.  Of
+// a form's tiles `slots` run at once, each a stage's time per stage and a tile's own besides.  A
+// group of R / E rows is taken to have one chunk up to three quarters of a tile's rows, above
+// that what its rows fill and 0.4 (the groups' sizes vary).  Costs as measured on GB300 (us; both
+// sides, P = 1 and 2): w13 of 7168 x 2048, 32 groups: 1 row 158, 218; 32 rows 165, 218; 64 rows 330,
+// 218; 2 groups of 32, 100, 250 rows: 29, 47, 81 and 33, 36, 39; 1024 x 1024, 64 groups of 20, 40,
+// 80 rows: 27, 36, 44 and 40, 44, 48.
+template <int P>
+double cost_us(const ExpertGradCall& a) {
+  const double M = Cfg<P>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
+  auto chunks = [&](double rows) { return rows <= 0.75 * M ? 1.0 : rows / M + 0.4; };
+  double items = groups * chunks(a.routed / groups);
+  if (a.G > a.E) items += chunks(a.rows - a.routed);
+  const double tiles = items * ((a.F + kFeat * P - 1) / (kFeat * P));
+  const double waves = ceil(tiles * P / (kSms * Cfg<P>::kOcc));
+  const double stages = a.C / Cfg<P>::kBK;
+  return P == 1 ? 8.0 + waves * (0.82 * stages + 0.7) : 14.0 + waves * (0.30 * stages + 3.0);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_grad(const ExpertGradCall& a, cudaStream_t st) {
-  return a.rows <= 32LL * a.G ? launch_grad<1>(a, st) : launch_grad<2>(a, st);
+  return cost_us<1>(a) <= cost_us<2>(a) ? launch_grad<1>(a, st) : launch_grad<2>(a, st);
 }
 
 }  // namespace moe

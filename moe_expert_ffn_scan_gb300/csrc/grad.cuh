@@ -60,7 +60,7 @@ struct ExpertGradCall {
   const int32_t* offsets;   // [G + 1]
   const uint8_t *w, *w_s;
   uint16_t* dx;             // [rows][F]
-  int G, rows, C, F;
+  int E, G, routed, rows, C, F;  // G = E, or E + 1 with a shared expert; routed: rows of the E
   uint32_t* status;
 };
 cudaError_t launch_expert_grad(const ExpertGradCall& a, cudaStream_t st);

@@ -57,8 +57,11 @@ def _check(dy, off, w, w_s, dx, ints):
         assert torch.all((dx.double() - want).abs()[~out] <= tol[~out])
 
 
+# (the first five shapes run on single CTAs, the others on SM pairs: longer contractions, and
+# features that end in a pair's first half)
 @pytest.mark.parametrize("which", ["w2", "w13"])
-@pytest.mark.parametrize("H,I", [(128, 128), (256, 384), (640, 128), (1152, 256), (384, 640)])
+@pytest.mark.parametrize("H,I", [(128, 128), (256, 384), (640, 128), (1152, 256), (384, 640),
+                                 (4096, 1152), (1152, 2048), (2048, 2048)])
 @pytest.mark.parametrize("ints", [True, False])
 def test_group_lengths(which, H, I, ints):
     _check(*_call(which, EDGES, H, I, ints=ints), ints)
