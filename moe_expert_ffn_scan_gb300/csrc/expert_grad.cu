@@ -56,7 +56,7 @@ struct Cfg {
   // [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a byte is above 128.
   static constexpr int kFactors = kBK * 8 + 16;
   static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
-  static constexpr int kGroups = P == 2 ? 3 : 2;      // converter groups of four warps
+  static constexpr int kGroups = 3;                   // converter groups of four warps
   static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
   static constexpr int kRowsMax = P == 2 ? 256 : 32;  // rows per tile
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
@@ -739,12 +739,13 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
 }
 
 // The form that should take less time, from what the host knows: the dims, not the routing.  Of
-// a form's tiles `slots` run at once, each a stage's time per stage and a tile's own besides.  A
-// group of R / E rows is taken to have one chunk up to three quarters of a tile's rows, above
-// that what its rows fill and 0.4 (the groups' sizes vary).  Costs as measured on GB300 (us; both
-// sides, P = 1 and 2): w13 of 7168 x 2048, 32 groups: 1 row 158, 218; 32 rows 165, 218; 64 rows 330,
-// 218; 2 groups of 32, 100, 250 rows: 29, 47, 81 and 33, 36, 39; 1024 x 1024, 64 groups of 20, 40,
-// 80 rows: 27, 36, 44 and 40, 44, 48.
+// a form's tiles as many run at once as CTAs or pairs fit, each a stage's time per stage and a
+// tile's own besides.  A group of R / E rows is taken to have one chunk up to three quarters of a
+// tile's rows, above that what its rows fill and 0.4 (the groups' sizes vary).  Costs as measured
+// on GB300, weights from HBM (us; P = 1 and 2): w13 of 7168 x 2048, 32 groups of 16, 64, 128 rows:
+// 127, 251, 490 and 222, 229, 246; 2 groups of 32, 100, 250: 18, 45, 67 and 26, 28, 32; w13 and w2
+// of 2048 x 1024, 16 groups of 50: 27, 16 and 29, 18, of 150: 52, 31 and 33, 21; w2 of 1024 x 1024,
+// 64 groups of 20, 80: 18, 37 and 33, 43.
 template <int P>
 double cost_us(const ExpertGradCall& a) {
   const double M = Cfg<P>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
@@ -754,7 +755,10 @@ double cost_us(const ExpertGradCall& a) {
   const double tiles = items * ((a.F + kFeat * P - 1) / (kFeat * P));
   const double waves = ceil(tiles * P / (kSms * Cfg<P>::kOcc));
   const double stages = a.C / Cfg<P>::kBK;
-  return P == 1 ? 8.0 + waves * (0.82 * stages + 0.7) : 14.0 + waves * (0.30 * stages + 3.0);
+  // (a CTA that has its SM for itself is faster; a pair's MMAs take longer for more rows)
+  if (P == 1) return 3.5 + waves * (stages * (tiles <= kSms ? 0.45 : 0.65) + 1.2);
+  const double rows = a.rows / items;
+  return 7.0 + waves * (stages * (0.28 + 0.07 * (rows < M ? rows / M : 1.0)) + 1.0);
 }
 
 }  // namespace
