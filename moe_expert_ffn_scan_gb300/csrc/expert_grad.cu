@@ -225,8 +225,21 @@ __device__ __forceinline__ uint32_t factor_rest(uint32_t s) {
   const uint32_t b = hi == 255 ? 0x7FC0u : (hi < 128 ? 127u : hi - 1) << 7;
   return a | (b << 16);
 }
-// TMEM lane l of a warp's 32 holds feature:
-__device__ __forceinline__ int feature_at(int l) { return 4 * (l & 7) + (l >> 3); }
+// TMEM lane l of a warp's 32 holds feature 4 (l % 8) + l / 8, so lanes l, l + 8, l + 16, l + 24
+// have four neighbours.  Of rows (r0, r0 + 1) and (r0 + 2, r0 + 3) of its feature each lane gets
+// row r0 + l / 8 of all four, for one store of 8 bytes (a store of 2 bytes a row and lane made
+// the epilogue of a tile 8 us).
+__device__ __forceinline__ uint2 four_rows(uint32_t r01, uint32_t r23, int lane) {
+  const bool high = lane & 16, odd = lane & 8;
+  const uint32_t own = high ? r23 : r01;
+  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? r01 : r23, 16);
+  // features (l / 8) % 2 and that + 2 of the same two rows
+  const uint32_t f0 = high ? got : own, f2 = high ? own : got;
+  const uint32_t mine = __byte_perm(f0, f2, odd ? 0x7632 : 0x5410);
+  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, __byte_perm(f0, f2, odd ? 0x5410 : 0x7632), 8);
+  const uint32_t even = odd ? other : mine, odds = odd ? mine : other;
+  return make_uint2(__byte_perm(even, odds, 0x5410), __byte_perm(even, odds, 0x7632));
+}
 
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -622,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kRowsMax + c0;
       const int f = t.f0 + static_cast<int>(rank) * kFeat + q * 32;
       const int rows = f < p.F ? t.rows - c0 : 0;
-      uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0) * p.F + f + feature_at(lane);
+      uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0 + (lane >> 3)) * p.F + f + 4 * (lane & 7);
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
@@ -646,9 +659,12 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         }
         if (P == 2) release();
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (r0 + c < rows)
-            out[static_cast<size_t>(r0 + c) * p.F] = static_cast<uint16_t>(v[c / 2] >> (16 * (c & 1)));
+        for (int c = 0; c < kCols; c += 4)
+          if (r0 + c < rows) {
+            const uint2 o = four_rows(v[c / 2], v[c / 2 + 1], lane);
+            if (r0 + c + (lane >> 3) < rows)
+              *reinterpret_cast<uint2*>(out + static_cast<size_t>(r0 + c) * p.F) = o;
+          }
       }
       if (P == 1) release();
     }

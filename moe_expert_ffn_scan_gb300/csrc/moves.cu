@@ -33,20 +33,30 @@ struct TokenChunk {
   }
 };
 
+// kWeights: the combine's gradient without the weights' own, dy2 of dout (rounded once; the
+// shared row as it is).
+template <bool kWeights>
 __global__ void __launch_bounds__(256) k_dispatch(const uint16_t* __restrict__ x,
-                                                  const int32_t* __restrict__ inv, int T, int k,
-                                                  int H, int R, int shared,
-                                                  uint16_t* __restrict__ xp) {
+                                                  const int32_t* __restrict__ inv,
+                                                  const float* __restrict__ w, int T, int k, int H,
+                                                  int R, int shared, uint16_t* __restrict__ xp) {
   pdl_wait();
   pdl_trigger();
   const TokenChunk at(T, H / 8);
   if (!at.live) return;
   uint32_t v[4];
   ld_bf16x8(x + static_cast<size_t>(at.t) * H + at.c * 8, v);
-  const int32_t* slot = inv + static_cast<size_t>(at.t) * k;
+  const size_t slot = static_cast<size_t>(at.t) * k;
   for (int j = 0; j < k; ++j) {
-    const int r = __ldg(slot + j);
-    if (r >= 0 && r < R) st_bf16x8(xp + static_cast<size_t>(r) * H + at.c * 8, v);
+    const int r = __ldg(inv + slot + j);
+    if (r < 0 || r >= R) continue;
+    uint32_t o[4];
+    if (kWeights) {
+      const float wj = __ldg(w + slot + j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = bf16x2_of(wj * bf16_lo(v[i]), wj * bf16_hi(v[i]));
+    }
+    st_bf16x8(xp + static_cast<size_t>(r) * H + at.c * 8, kWeights ? o : v);
   }
   if (shared) st_bf16x8(xp + (static_cast<size_t>(R) + at.t) * H + at.c * 8, v);
 }
@@ -116,24 +126,28 @@ __global__ void __launch_bounds__(256) k_dispatch_bwd(const uint16_t* __restrict
   }
 }
 
-// A CTA per token.  dy2 and dw may each be null; y2 is read for dw only, and may be dy2's buffer.
-__global__ void __launch_bounds__(512) k_combine_bwd(const uint16_t* __restrict__ dout,
-                                                     const uint16_t* y2,
-                                                     const int32_t* __restrict__ inv,
-                                                     const float* __restrict__ w, int T, int k,
-                                                     int H, int R, int shared, uint16_t* dy2,
-                                                     float* __restrict__ dw) {
+// dw, and dy2 if it is not null (it may be y2's buffer).  A CTA per token, or with kPack `warps`
+// warps per token and as many tokens as the CTA's warps do for.
+template <bool kPack>
+__global__ void __launch_bounds__(kPack ? 256 : 512)
+    k_combine_bwd(const uint16_t* __restrict__ dout, const uint16_t* y2,
+                  const int32_t* __restrict__ inv, const float* __restrict__ w, int T, int k, int H,
+                  int R, int shared, int pack, uint16_t* dy2, float* __restrict__ dw) {
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (kPack: the CTA's token, the warp's part of its row)
+  const int of = kPack ? warp / pack : 0, part_of = kPack ? warp - of * pack : warp;
+  const int t = kPack ? blockIdx.x * (blockDim.x / 32 / pack) + of : blockIdx.x;
+  const int first = kPack ? (part_of * 32 + lane) * 8 : threadIdx.x * 8;
   __shared__ float part[16][kMaxK];
+  const bool live = !kPack || t < T;
   const int32_t* slot = inv + static_cast<size_t>(t) * k;
   const float* wt = w + static_cast<size_t>(t) * k;
   float dot[kMaxK];
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) dot[j] = 0.f;
-  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+  for (int c = first; live && c < H; c += kPack ? pack * 256 : blockDim.x * 8) {
     uint32_t g[4];
     ld_bf16x8(dout + static_cast<size_t>(t) * H + c, g);
 #pragma unroll
@@ -148,7 +162,7 @@ __global__ void __launch_bounds__(512) k_combine_bwd(const uint16_t* __restrict_
         if (r[jj] >= R) r[jj] = -1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[jj][i] = 0;
-        if (dw && r[jj] >= 0) ld_bf16x8(y2 + static_cast<size_t>(r[jj]) * H + c, y[jj]);
+        if (r[jj] >= 0) ld_bf16x8(y2 + static_cast<size_t>(r[jj]) * H + c, y[jj]);
       }
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
@@ -160,20 +174,17 @@ __global__ void __launch_bounds__(512) k_combine_bwd(const uint16_t* __restrict_
           for (int i = 0; i < 4; ++i) o[i] = bf16x2_of(wj * bf16_lo(g[i]), wj * bf16_hi(g[i]));
           st_bf16x8(dy2 + static_cast<size_t>(r[jj]) * H + c, o);
         }
-        if (dw) {
-          float s = 0.f;
+        float s = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s = fmaf(bf16_lo(g[i]), bf16_lo(y[jj][i]), s);
-            s = fmaf(bf16_hi(g[i]), bf16_hi(y[jj][i]), s);
-          }
-          dot[j0 + jj] += s;
+        for (int i = 0; i < 4; ++i) {
+          s = fmaf(bf16_lo(g[i]), bf16_lo(y[jj][i]), s);
+          s = fmaf(bf16_hi(g[i]), bf16_hi(y[jj][i]), s);
         }
+        dot[j0 + jj] += s;
       }
     }
     if (dy2 && shared) st_bf16x8(dy2 + (static_cast<size_t>(R) + t) * H + c, g);
   }
-  if (!dw) return;
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
     if (j >= k) break;
@@ -183,10 +194,11 @@ __global__ void __launch_bounds__(512) k_combine_bwd(const uint16_t* __restrict_
     if (lane == 0) part[warp][j] = s;
   }
   __syncthreads();
-  if (threadIdx.x < k) {
+  if (live && part_of == 0 && lane < k) {
     float s = 0.f;
-    for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s += part[i][threadIdx.x];
-    dw[static_cast<size_t>(t) * k + threadIdx.x] = s;
+    const int n = kPack ? pack : blockDim.x / 32;
+    for (int i = 0; i < n; ++i) s += part[warp + i][lane];
+    dw[static_cast<size_t>(t) * k + lane] = s;
   }
 }
 
@@ -204,7 +216,7 @@ cudaError_t launch_dispatch(const uint16_t* x, const int32_t* inv, int T, int k,
   unsigned grid;
   const cudaError_t e = chunk_grid(T, H, &grid);
   if (e != cudaSuccess) return e;
-  return launch_k(k_dispatch, grid, 256, 0, st, x, inv, T, k, H, R, shared, xp);
+  return launch_k(k_dispatch<false>, grid, 256, 0, st, x, inv, nullptr, T, k, H, R, shared, xp);
 }
 
 cudaError_t launch_dispatch_bwd(const uint16_t* dxp, const int32_t* inv, const void* dx_in,
@@ -220,11 +232,20 @@ cudaError_t launch_dispatch_bwd(const uint16_t* dxp, const int32_t* inv, const v
 cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y2, const int32_t* inv,
                                const float* w, int T, int k, int H, int R, int shared,
                                uint16_t* dy2, float* dw, cudaStream_t st) {
-  // as many warps as a token's row has chunks for, in as few rounds as 16 warps allow
+  if (!dw) {
+    unsigned grid;
+    const cudaError_t e = chunk_grid(T, H, &grid);
+    if (e != cudaSuccess) return e;
+    return launch_k(k_dispatch<true>, grid, 256, 0, st, dout, inv, w, T, k, H, R, shared, dy2);
+  }
+  // as many warps as a token's row has chunks for, in as few rounds as 16 warps allow; of short
+  // rows several share a CTA
   const int chunks = H / 8, rounds = (chunks + 511) / 512;
   const int warps = (chunks + rounds * 32 - 1) / (rounds * 32);
-  return launch_k(k_combine_bwd, T, warps * 32, 0, st, dout, y2, inv, w, T, k, H, R, shared, dy2,
-                  dw);
+  const int tokens = warps < 8 ? 8 / warps : 1;
+  return launch_k(tokens > 1 ? k_combine_bwd<true> : k_combine_bwd<false>,
+                  (T + tokens - 1) / tokens, warps * tokens * 32, 0, st, dout, y2, inv, w, T, k, H, R,
+                  shared, warps, dy2, dw);
 }
 
 }  // namespace moe

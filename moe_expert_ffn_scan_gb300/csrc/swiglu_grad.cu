@@ -115,16 +115,21 @@ __global__ void __launch_bounds__(256) k_swiglu_save(const uint16_t* __restrict_
   }
 }
 
-// A CTA per row, 8 columns a thread at a time; all of a thread's loads are in flight before the
+// A CTA per row, or with kPack `pack` warps per row and as many rows as the CTA's warps do for; 8
+// columns a thread at a time; all of a thread's loads are in flight before the
 // first is used, and what they bring stays packed until its four columns' turn, so that
 // registers leave room for full occupancy (73728 rows of 2048: 225 us, 0.90 of HBM; with 40
 // registers a thread 272, with 16 columns and 64 registers 254).  kCodes: g and u from the checkpoint; kH: h from hq.
-template <bool kCodes, bool kH>
-__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) k_swiglu_bwd(const SwigluBwdCall a) {
+template <bool kCodes, bool kH, bool kPack>
+__global__ void __launch_bounds__(kPack ? 256 : kBwdThreads, kPack ? 6 : kBwdCtas)
+    k_swiglu_bwd(const SwigluBwdCall a, int pack) {
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x, I = a.I;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int I = a.I, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (kPack: the CTA's row, the warp's part of it)
+  const int of = kPack ? warp / pack : 0, part_of = kPack ? warp - of * pack : warp;
+  const int r = kPack ? blockIdx.x * (blockDim.x / 32 / pack) + of : blockIdx.x;
+  const int first = kPack ? (part_of * 32 + lane) * 8 : threadIdx.x * 8;
   __shared__ float part[kBwdThreads / 32];
   int src = 0;
   bool has = false;  // the row has a combine weight
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) k_swiglu_bwd(const Swig
   const float w = a.w && has ? __ldg(a.w + src) : 1.f;
   const size_t row = static_cast<size_t>(r);
   float dot = 0.f;
-  for (int c = threadIdx.x * 8; c < I; c += blockDim.x * 8) {
+  for (int c = first; (!kPack || r < a.rows) && c < I; c += kPack ? pack * 256 : blockDim.x * 8) {
     uint32_t dv[4], gv[4], uv[4], hv[2] = {0, 0};
     ld_bf16x8(a.dh + row * I + c, dv);
     float sg = 1.f, su = 1.f, sh = 1.f;
@@ -183,13 +188,14 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) k_swiglu_bwd(const Swig
     st_bf16x8(a.dy13 + row * 2 * I + c, og);
     st_bf16x8(a.dy13 + row * 2 * I + I + c, ou);
   }
-  if (!a.dw || !has) return;
+  if (!a.dw || (!kPack && !has)) return;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
   if (lane == 0) part[warp] = dot;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i) dot += part[i];
+  if (has && part_of == 0 && lane == 0) {
+    const int n = kPack ? pack : blockDim.x / 32;
+    for (int i = 1; i < n; ++i) dot += part[warp + i];
     a.dw[src] = dot;
   }
 }
@@ -208,10 +214,16 @@ cudaError_t launch_swiglu_save(const uint16_t* y13, int rows, int I, uint8_t* hq
 cudaError_t launch_swiglu_bwd(const SwigluBwdCall& a, cudaStream_t st) {
   const int chunks = a.I / 8, rounds = (chunks + kBwdThreads - 1) / kBwdThreads;
   const int warps = (chunks + rounds * 32 - 1) / (rounds * 32);
-  const bool h = a.dw && a.hq;
-  return launch_k(a.y13 ? (h ? k_swiglu_bwd<false, true> : k_swiglu_bwd<false, false>)
-                        : (h ? k_swiglu_bwd<true, true> : k_swiglu_bwd<true, false>),
-                  a.rows, warps * 32, 0, st, a);
+  const int rows = warps < 8 ? 8 / warps : 1;  // of short rows several share a CTA
+  using Kernel = void (*)(const SwigluBwdCall, int);
+  static const Kernel kernels[2][2][2] = {
+      {{k_swiglu_bwd<false, false, false>, k_swiglu_bwd<false, false, true>},
+       {k_swiglu_bwd<false, true, false>, k_swiglu_bwd<false, true, true>}},
+      {{k_swiglu_bwd<true, false, false>, k_swiglu_bwd<true, false, true>},
+       {k_swiglu_bwd<true, true, false>, k_swiglu_bwd<true, true, true>}}};
+  const Kernel kern = kernels[a.y13 == nullptr][a.dw && a.hq][rows > 1];
+  return launch_k(kern, static_cast<unsigned>((static_cast<long long>(a.rows) + rows - 1) / rows),
+                  warps * rows * 32, 0, st, a, warps);
 }
 
 }  // namespace moe
