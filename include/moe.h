@@ -517,7 +517,8 @@ int moe_linear_backward(const moe_linear_desc* d, const uint16_t* x, const uint1
 /* Tokens sorted by expert: xp[inv[t*k+j]] = x[t] for every j, xp[R+t] = x[t] if has_shared.
  *   x [T][H] bf16, inv [T*k] as moe_route gives it, xp [Rs][H] bf16.  An entry of inv outside
  *   [0, R) is a slot without a row (a token dropped by its expert): nothing is written for
- *   it; rows that no slot has are left as they were.  No two slots may have the same row. */
+ *   it; rows that no slot has are left as they were.  No two slots may have the same row.  xp
+ *   and x must not overlap. */
 int moe_dispatch(const moe_dims* d, const uint16_t* x, const int32_t* inv, uint16_t* xp,
                  void* stream);
 
@@ -540,7 +541,7 @@ int moe_combine_backward(const moe_dims* d, const uint16_t* dout, const uint16_t
 
 /* moe_swiglu_quant that also saves its input in 8 bits for the gradient: hq, hs as
  * moe_swiglu_quant gives them, yq [rows][2I] and ys [rows][2I/128] as moe_quant_act gives them
- * of y13, bit for bit, in one pass.  I % 128 == 0; rows == 0 is a no-op. */
+ * of y13, bit for bit, in one pass.  I % 128 == 0, I <= 2^29; 0 <= rows <= 2^30 (0: no-op). */
 int moe_swiglu_quant_save(int32_t rows, int32_t I, const uint16_t* y13, uint8_t* hq, uint8_t* hs,
                           uint8_t* yq, uint8_t* ys, void* stream);
 
@@ -558,7 +559,7 @@ int moe_swiglu_quant_save(int32_t rows, int32_t I, const uint16_t* y13, uint8_t*
  *   left as they were.
  *   Finite for finite inputs whose formulas are.  rows == 0 is a no-op. */
 typedef struct moe_swiglu_backward_desc {
-  int32_t rows, R, I; /* 0 <= R <= rows, I % 128 == 0 */
+  int32_t rows, R, I; /* 0 <= R <= rows <= 2^30; I % 128 == 0, I <= 2^29 */
 } moe_swiglu_backward_desc;
 int moe_swiglu_backward(const moe_swiglu_backward_desc* d, const uint16_t* dh, const uint16_t* y13,
                         const uint8_t* yq, const uint8_t* ys, const uint8_t* hq,

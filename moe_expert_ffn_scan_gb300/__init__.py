@@ -654,10 +654,17 @@ def _packed_rows(d):
     return d.T * (d.k + d.has_shared)
 
 
+def _here(t, name):
+    """The call runs on the current device: so must its tensors (checked on its main one)."""
+    if t.is_cuda and t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+
+
 def moe_dispatch(d, x, inv, xp, stream=None):
     """x [T, H] bf16 to the packed rows of its experts, xp [Rs, H]: row inv[t*k+j] (moe_route's
     inv, [T*k] int32; an entry outside [0, T*k): no row) and, with a shared expert, row
     T*k + t."""
+    _here(x, "x")
     rc = lib().moe_dispatch(
         _d(d), _t(x, _BF16, (d.T, d.H), "x"), _flat(inv, _I32, d.T * d.k, "inv"),
         _t(xp, _BF16, (_packed_rows(d), d.H), "xp"), _raw_stream(stream))
@@ -668,6 +675,7 @@ def moe_dispatch(d, x, inv, xp, stream=None):
 def moe_dispatch_backward(d, dxp, inv, dx, dx_in=None, stream=None):
     """Gradient of moe_dispatch: dx [T, H] (bf16 or fp32) = dx_in (dx's type, or None) + the sum
     of each token's rows of dxp [Rs, H] bf16."""
+    _here(dx, "dx")
     shape, dt, code = (d.T, d.H), dx.dtype, _dtype_code(dx, "dx")
     rc = lib().moe_dispatch_backward(
         _d(d), _t(dxp, _BF16, (_packed_rows(d), d.H), "dxp"),
@@ -681,6 +689,7 @@ def moe_combine_backward(d, dout, y2, inv, w, dy2=None, dw=None, stream=None):
     """Gradient of moe_combine from dout [T, H] bf16: writes what is given of dy2 [Rs, H] bf16
     (w [T, k] fp32 times the token's dout) and dw [T, k] fp32 (from y2 [Rs, H] bf16, else
     None)."""
+    _here(dout, "dout")
     rows = (_packed_rows(d), d.H)
     rc = lib().moe_combine_backward(
         _d(d), _t(dout, _BF16, (d.T, d.H), "dout"), _t(y2, _BF16, rows, "y2"),
@@ -693,6 +702,7 @@ def moe_combine_backward(d, dout, y2, inv, w, dy2=None, dw=None, stream=None):
 def moe_swiglu_quant_save(y13, hq, hs, yq, ys, stream=None):
     """moe_swiglu_quant of y13 [rows, 2I] bf16 (hq [rows, I], hs [rows, I/128]) that also saves
     y13 in 8 bits, yq [rows, 2I] and ys [rows, 2I/128], for moe_swiglu_backward (all uint8)."""
+    _here(y13, "y13")
     rows, two_i = y13.shape
     I = two_i // 2
     rc = lib().moe_swiglu_quant_save(
@@ -710,6 +720,7 @@ def moe_swiglu_backward(dh, dy13, y13=None, yq=None, ys=None, hq=None, hs=None, 
     routed row's (the first perm_src.numel() of them) times its weight of w [T, k] fp32 (None:
     1), and, if given, dw [T, k] fp32: the weights' gradient, from the values of hq, hs if given,
     else from silu(g) u."""
+    _here(dh, "dh")
     rows, I = dh.shape
     R = perm_src.numel() if perm_src is not None else 0
     wp, dwp = _flat(w, _F32, R, "w"), _flat(dw, _F32, R, "dw")
@@ -730,6 +741,7 @@ def gemm_backward_workspace_size(d) -> int:
 
 
 def _gemm_backward(name, d, dy, cols_in, group_offsets, w, w_s, dx, cols_out, ws, stream):
+    _here(dy, "dy")
     rows, G = _packed_rows(d), d.E + d.has_shared
     rc = getattr(lib(), name)(
         _d(d), _t(dy, _BF16, (rows, cols_in), "dy"),

@@ -15,6 +15,11 @@ bool null_or(const void* p, size_t a) { return !p || aligned(p, a); }
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// (limits that leave room in 32-bit row and column arithmetic)
+bool swiglu_ok(int rows, int I) {
+  return rows >= 0 && rows <= (1 << 30) && I >= 128 && I % 128 == 0 && I <= (1 << 29);
+}
+
 int rows_R(const moe_dims* d) { return d->T * d->k; }
 int rows_Rs(const moe_dims* d) { return rows_R(d) + (d->has_shared ? d->T : 0); }
 
@@ -76,7 +81,7 @@ int moe_combine_backward(const moe_dims* d, const uint16_t* dout, const uint16_t
 
 int moe_swiglu_quant_save(int32_t rows, int32_t I, const uint16_t* y13, uint8_t* hq, uint8_t* hs,
                           uint8_t* yq, uint8_t* ys, void* stream) {
-  if (rows < 0 || I < 128 || I % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!swiglu_ok(rows, I)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!y13 || !hq || !hs || !yq || !ys || !aligned(y13, 16) || !aligned(hq, 16) ||
       !aligned(yq, 16))
@@ -89,7 +94,7 @@ int moe_swiglu_backward(const moe_swiglu_backward_desc* d, const uint16_t* dh, c
                         const uint8_t* yq, const uint8_t* ys, const uint8_t* hq,
                         const uint8_t* hs, const int32_t* perm_src, const float* w,
                         uint16_t* dy13, float* dw, void* stream) {
-  if (!d || d->rows < 0 || d->R < 0 || d->R > d->rows || d->I < 128 || d->I % 128)
+  if (!d || !swiglu_ok(d->rows, d->I) || d->R < 0 || d->R > d->rows)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (d->rows == 0) return MOE_OK;
   // the activations in exactly one form; codes with their scales

@@ -41,14 +41,16 @@ namespace moe {
 
 namespace {
 
+// c per stage.  With 64 the warps that issue and wait spend twice the instructions on it (SM
+// pairs, 32 groups of w13, 7168 x 2048: 64 rows each 214 us in place of 170, 128 rows 229 in place
+// of 194; 256 rows 262 in place of 268; few rows on single CTAs 156 in place of 127).
+constexpr int kBK = 128;
 constexpr int kFeat = 128;       // features per CTA
 constexpr int kMaxGroups = 1025;
 
 template <int P>
 struct Cfg {
   static constexpr int kOcc = P == 2 ? 1 : 2;         // CTAs per SM
-  // c per stage.  Few rows: the barriers' and loops' instructions weigh, so a longer stage.
-  static constexpr int kBK = P == 2 ? 64 : 128;
   static constexpr int kACols = kBK / 2;              // TMEM columns of a stage of A
   static constexpr int kRawCodes = kFeat / 2 * kBK;
   static constexpr int kRawScales = 16 * kBK;         // 16 bytes a weight row, 4 of them the CTA's
@@ -62,8 +64,8 @@ struct Cfg {
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
   static constexpr int kBox = P == 2 ? 128 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
   static constexpr int kAcc = P == 2 ? 1 : 2;         // accumulators
-  static constexpr int kSt = P == 2 ? 6 : 3;          // stages of both operands
-  static constexpr int kRaw = P == 2 ? 18 : 7;        // of codes and scales
+  static constexpr int kSt = P == 2 ? 4 : 3;          // stages of both operands
+  static constexpr int kRaw = 7;                      // of codes and scales
   static constexpr int kTmemCols = P == 2 ? 512 : 256;
   static constexpr int kTmemA = kAcc * kRowsMax;      // A's stages behind the accumulators
   static constexpr int kBBytes = kRowsMax / P * kBK * 2;
@@ -261,7 +263,7 @@ struct ScaleLoad {
   __device__ __forceinline__ void stage(uint8_t* to, uint64_t* bar, int lane) {
     if (there) {
 #pragma unroll
-      for (int i = 0; i < Cfg<P>::kBK / 32; ++i) {
+      for (int i = 0; i < kBK / 32; ++i) {
         cp_async16(to + (32 * i + lane) * 16,
                    reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(15)));
         at += 32 * row;
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P), nk = p.C / C::kBK;
+  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P), nk = p.C / kBK;
   const long long total = *abort_flag ? 0 : static_cast<long long>(first[G]) * f_tiles;
   const int cl = blockIdx.x / P, ncl = gridDim.x / P;
   auto leader_addr = [&](const uint64_t* b) -> uint32_t { return mapa_shared(smem_u32(b), 0); };
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const bool small = mine <= 2 * C::kBoxSmall;
       const int box = small ? C::kBoxSmall : C::kBox, boxes = (mine + box - 1) / box;
       const CUtensorMap* map = small ? &tmBs : &tmB;
-      const uint32_t bytes = P * boxes * box * C::kBK * 2;
+      const uint32_t bytes = P * boxes * box * kBK * 2;
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
         if (st.round && !mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag)) {
           ok = false;
@@ -401,13 +403,13 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[st.s], bytes);
 #pragma unroll
-          for (int h = 0; h < C::kBK / 64; ++h)  // 64 c, one 128-byte swizzle row, each
+          for (int h = 0; h < kBK / 64; ++h)  // 64 c, one 128-byte swizzle row, each
             for (int i = 0; i < boxes; ++i) {
               uint8_t* to = b + (h * (C::kRowsMax / P) + i * box) * 128;
               if (P == 2)
-                tma_load_2d_pair(to, map, bar0 + st.s * 8, kb * C::kBK + h * 64, row0 + i * box);
+                tma_load_2d_pair(to, map, bar0 + st.s * 8, kb * kBK + h * 64, row0 + i * box);
               else
-                tma_load_2d(to, map, &full[st.s], kb * C::kBK + h * 64, row0 + i * box);
+                tma_load_2d(to, map, &full[st.s], kb * kBK + h * 64, row0 + i * box);
             }
         }
       }
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           const uint64_t db = db0 + st.s * (C::kBBytes / 16);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < C::kBK / 16; ++kk) {
+            for (int kk = 0; kk < kBK / 16; ++kk) {
               const uint64_t dk = db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2;
               if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
               else mma_bf16_ts(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
@@ -485,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         if (elect_one()) {
           mbar_arrive_expect_tx(&raw_full[st.s], C::kRawCodes);
           tma_load_2d(smem + C::kOffRaw + st.s * C::kRawCodes, &tmW, &raw_full[st.s], f0 / 2,
-                      t.g * p.C + kb * C::kBK);
+                      t.g * p.C + kb * kBK);
         }
         __syncwarp();
         sc.stage(smem + C::kOffScale + st.s * C::kRawScales, &raw_full[st.s], lane);
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         }
         uint32_t over = 0;
 #pragma unroll
-        for (int h = 0; h < C::kBK / 64; ++h) {
+        for (int h = 0; h < kBK / 64; ++h) {
           // (64 rows further the bytes' place in their 16 is the same)
           const int at = st.s * C::kRawScales + h * 1024;
           const uint32_t x = *reinterpret_cast<const uint32_t*>(lo + at);
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         }
         const bool any = __any_sync(0xFFFFFFFFu, (over & 0x01000100u) != 0);
         if (lane == 0) {
-          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + C::kBK * 8) = any;
+          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + kBK * 8) = any;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&fac_full[st.s]);
@@ -559,8 +561,8 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       tc_fence_after();
       const uint32_t over = *reinterpret_cast<const uint32_t*>(
-          smem + C::kOffFactor + rr.s * C::kFactors + C::kBK * 8);
-      constexpr int kH = C::kBK / 32;  // 32 c each
+          smem + C::kOffFactor + rr.s * C::kFactors + kBK * 8);
+      constexpr int kH = kBK / 32;  // 32 c each
       const uint32_t to = dst + ra.s * C::kACols;
       if (!over) {
 #pragma unroll
@@ -745,7 +747,7 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
     once.set(dev, clusters);
   }
   CUtensorMap tmW, tmB, tmBs;
-  if (!encode_w(&tmW, a, C::kBK) || !encode_dy(&tmB, a, C::kBox) || !encode_dy(&tmBs, a, C::kBoxSmall))
+  if (!encode_w(&tmW, a, kBK) || !encode_dy(&tmB, a, C::kBox) || !encode_dy(&tmBs, a, C::kBoxSmall))
     return cudaErrorInvalidValue;
   const GradParams p = {a.offsets, a.w_s, a.dx, a.G, a.rows, a.C, a.F, a.status};
   cfg.gridDim = dim3(clusters * P);
@@ -758,10 +760,11 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
 // a form's tiles as many run at once as CTAs or pairs fit, each a stage's time per stage and a
 // tile's own besides.  A group of R / E rows is taken to have one chunk up to three quarters of a
 // tile's rows, above that what its rows fill and 0.4 (the groups' sizes vary).  Costs as measured
-// on GB300, weights from HBM (us; P = 1 and 2): w13 of 7168 x 2048, 32 groups of 16, 64, 128 rows:
-// 127, 251, 490 and 222, 229, 246; 2 groups of 32, 100, 250: 18, 45, 67 and 26, 28, 32; w13 and w2
-// of 2048 x 1024, 16 groups of 50: 27, 16 and 29, 18, of 150: 52, 31 and 33, 21; w2 of 1024 x 1024,
-// 64 groups of 20, 80: 18, 37 and 33, 43.
+// on GB300, weights from HBM (us; P = 1 and 2): w13 of 7168 x 2048, 32 groups of 16, 40, 64 rows:
+// 114, 224, 220 and 164, 167, 169; 2 groups of 32, 100, 250: 17, 41, 59 and 19, 22, 28; w13 and w2
+// of 2048 x 1024, 16 groups of 50: 25, 15 and 22, 14, of 150: 46, 28 and 26, 17; w2 of 1024 x 1024,
+// 64 groups of 20, 80: 16, 33 and 24, 30; w2 of 1152 x 640, 13 groups of 60, 179: 8.5, 15.8 and
+// 10.8, 13.7.
 template <int P>
 double cost_us(const ExpertGradCall& a) {
   const double M = Cfg<P>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
@@ -770,11 +773,11 @@ double cost_us(const ExpertGradCall& a) {
   if (a.G > a.E) items += chunks(a.rows - a.routed);
   const double tiles = items * ((a.F + kFeat * P - 1) / (kFeat * P));
   const double waves = ceil(tiles * P / (kSms * Cfg<P>::kOcc));
-  const double stages = a.C / Cfg<P>::kBK;
+  const double stages = a.C / kBK;
   // (a CTA that has its SM for itself is faster; a pair's MMAs take longer for more rows)
-  if (P == 1) return 3.5 + waves * (stages * (tiles <= kSms ? 0.45 : 0.65) + 1.2);
+  if (P == 1) return 3.5 + waves * (stages * (tiles <= kSms ? 0.45 : 0.56) + 1.2);
   const double rows = a.rows / items;
-  return 7.0 + waves * (stages * (0.28 + 0.07 * (rows < M ? rows / M : 1.0)) + 1.0);
+  return 7.0 + waves * (stages * (0.36 + 0.28 * (rows < M ? rows / M : 1.0)) + 0.7);
 }
 
 }  // namespace

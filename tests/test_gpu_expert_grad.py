@@ -19,7 +19,7 @@ EDGES = [1, 0, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 0, 96, 127, 128, 129, 191
          256, 257, 300, 511, 512, 513, 0]
 
 
-def _call(which, lens, H, I, seed=0, ints=True, gap=(0, 0)):
+def _call(which, lens, H, I, seed=0, ints=True, gap=(0, 0), scales=(127, 129)):
     """Groups of these lengths (gap: rows in front of the first and behind the last).  Returns
     the inputs and the output, which starts as 7."""
     g = torch.Generator(device=DEV).manual_seed(seed + H + 3 * I + len(lens))
@@ -32,7 +32,7 @@ def _call(which, lens, H, I, seed=0, ints=True, gap=(0, 0)):
         # |dy| <= 2 and weights of whole or half steps up to 6 * 2: sums are multiples of 1/2
         # below 2^23 / 2, exact in fp32
         dy = ri(-2, 3, rows, C).to(BF)
-        w_s = ri(127, 129, G, C, F // 32).to(U8)
+        w_s = ri(*scales, G, C, F // 32).to(U8)
     else:
         dy = torch.randn(rows, C, generator=g, device=DEV).to(BF)
         w_s = ri(110, 130, G, C, F // 32).to(U8)
@@ -78,6 +78,14 @@ def test_few_and_many_groups(which, lens):
 def test_layer_sizes(which):
     _check(*_call(which, [3, 0, 290, 17, 140, 64], 7168, 2048), True)
     _check(*_call(which, [3, 0, 290, 17, 140, 64], 7168, 2048, ints=False), False)
+
+
+@pytest.mark.parametrize("which", ["w2", "w13"])
+@pytest.mark.parametrize("H,I", [(512, 256), (2048, 1152), (1152, 1024)])
+def test_scales_above_one_factors_range(which, H, I):
+    """Scale bytes on both sides of 128, where a bf16 factor ends: |dy| <= 2, weights up to
+    6 * 2^5 in steps of 2^-3, sums of 2304 terms below 2^20 = 2^23 steps."""
+    _check(*_call(which, [40, 200, 0, 3, 129], H, I, scales=(125, 133)), True)
 
 
 @pytest.mark.parametrize("which", ["w2", "w13"])
@@ -150,6 +158,42 @@ def test_non_finite_rows_stay_in_their_rows():
 def test_outputs_are_the_same_in_every_run(which):
     a, b = (_call(which, [100, 3, 600, 40], 1152, 640, ints=False)[4] for _ in range(2))
     assert torch.equal(a, b)
+
+
+def test_two_streams_and_two_graphs_with_one_workspace():
+    """Calls that overlap share a workspace (its status word is all they write there)."""
+    H, I, rows = 512, 384, 300
+    g = torch.Generator(device=DEV).manual_seed(11)
+    off = torch.tensor([0, 100, rows], dtype=I32, device=DEV)
+    w = torch.randint(0, 256, (2, H, I // 2), generator=g, device=DEV).to(U8)
+    w_s = torch.full((2, H, I // 32), 127, dtype=U8, device=DEV)
+    d = moe.dims(rows, H, I, 2, 1, 0)
+    ws = moe.alloc_workspace(moe.gemm_backward_workspace_size(d))
+    dy = [torch.randint(-2, 3, (rows, H), generator=g, device=DEV).to(BF) for _ in range(2)]
+    want = [ref.expert_grad(v, off, w, w_s, rows, I)[0].to(BF) for v in dy]
+    dx = [torch.empty(rows, I, dtype=BF, device=DEV) for _ in range(2)]
+    call = lambda i: moe.moe_grouped_gemm_w2_backward(d, dy[i], off, w, w_s, dx[i], ws)  # noqa: E731
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(i)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(dx, want))
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            call(i)
+    for v in dx:
+        v.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(dx, want))
+    assert moe.moe_check_status(ws) == 0
 
 
 def test_past_2_31_values():

@@ -174,6 +174,29 @@ def test_refusals_of_the_layer():
 
 
 @pytest.mark.gpu
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """(One GPU: the current device is made to look like another.)"""
+    layer, x, logits, dout = _layer(4, False)
+    s = layer.forward_train(x, logits)[1]
+    d, bf = layer.dims(4), lambda *n: torch.empty(*n, dtype=BF, device=DEV)
+    u8 = lambda *n: torch.empty(*n, dtype=torch.uint8, device=DEV)  # noqa: E731
+    R, H, I = 4 * layer.k, layer.H, layer.I
+    ws = layer.train_workspaces(4)[1]
+    monkeypatch.setattr(moe, "_current_device", lambda: 1)
+    calls = [lambda: moe.moe_dispatch(d, x, s["inv"], bf(R, H)),
+             lambda: moe.moe_dispatch_backward(d, bf(R, H), s["inv"], bf(4, H)),
+             lambda: moe.moe_combine_backward(d, dout, None, s["inv"], s["w"], dy2=bf(R, H)),
+             lambda: moe.moe_swiglu_quant_save(bf(R, 2 * I), u8(R, I), u8(R, I // 128),
+                                               u8(R, 2 * I), u8(R, I // 64)),
+             lambda: moe.moe_swiglu_backward(bf(R, I), bf(R, 2 * I), y13=bf(R, 2 * I)),
+             lambda: moe.moe_grouped_gemm_w2_backward(d, bf(R, H), s["offsets"], layer.w2,
+                                                      layer.w2_s, bf(R, I), ws)]
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("form", ["fp8", "bf16"])
 def test_captured_and_replayed_on_new_inputs(form):
     T = 130

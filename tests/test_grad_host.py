@@ -84,7 +84,7 @@ def test_swiglu_quant_save_refusals(lib):
     f = lib.moe_swiglu_quant_save
     good = [4, 256, A, A, A, A, A, None]  # rows I y13 hq hs yq ys stream
     assert f(*_with(good, 0, 0)) == OK
-    for i, v in ((0, -1), (1, 0), (1, 200), (1, -128)):
+    for i, v in ((0, -1), (1, 0), (1, 200), (1, -128), (0, (1 << 30) + 1), (1, (1 << 29) + 128)):
         assert f(*_with(good, i, v)) == SHAPE
     for i in (2, 3, 4, 5, 6):
         assert f(*_with(good, i, None)) == ARG
@@ -99,7 +99,8 @@ def test_swiglu_backward_refusals(lib):
     good = [desc(), A, None, A, A, A, A, A, A, A, A, None]
     assert f(*_with(good, 0, desc(rows=0, R=0))) == OK
     assert f(*_with(good, 0, None)) == SHAPE
-    for bad in (dict(rows=-1), dict(R=5), dict(R=-1), dict(I=200), dict(I=0)):
+    for bad in (dict(rows=-1), dict(R=5), dict(R=-1), dict(I=200), dict(I=0),
+                dict(rows=(1 << 30) + 1), dict(I=(1 << 29) + 128)):
         assert f(*_with(good, 0, desc(**bad))) == SHAPE
     for i in (1, 3, 4, 5, 6, 7, 9):
         assert f(*_with(good, i, None)) == ARG
