@@ -441,11 +441,12 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = tmem + C::kTmemA + st.s * C::kACols;
-          const uint64_t db = db0 + st.s * (C::kBBytes / 16);
+          const uint32_t db = static_cast<uint32_t>(db0) + st.s * (C::kBBytes / 16);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t dk = db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2;
+              const uint64_t dk = (db0 >> 32) << 32 |
+                                  (db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2);
               if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
               else mma_bf16_ts(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
             }
@@ -526,14 +527,15 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           const int at = st.s * C::kRawScales + h * 1024;
           const uint32_t x = *reinterpret_cast<const uint32_t*>(lo + at);
           const uint32_t y = *reinterpret_cast<const uint32_t*>(hi + at);
+          // a byte above 128 has its highest bit and another
+          over |= (((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & x) | (((y & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & y);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t v = __byte_perm(x, y, q | (4 + q) << 8) & 0x00FF00FFu;
-            over |= v + 0x007F007Fu;
             to[st.s * (C::kFactors / 4) + h * 128 + q * 16] = v * 128 + 0x3F003F00u;
           }
         }
-        const bool any = __any_sync(0xFFFFFFFFu, (over & 0x01000100u) != 0);
+        const bool any = __any_sync(0xFFFFFFFFu, (over & 0x80808080u) != 0);
         if (lane == 0) {
           *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + kBK * 8) = any;
         }
