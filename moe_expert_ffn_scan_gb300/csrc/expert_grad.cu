@@ -13,24 +13,28 @@
 // side, one per TMEM lane.  The weights lie with the features contiguous, so a transpose is
 // needed, and ldmatrix makes it on the codes: read as 16-bit values (four features of one c),
 // transposed, a thread's 32-bit register holds four features of two consecutive c, and the codes
-// of one feature are 16 bits apart: a shift and two masks put them into the two halves of one
+// of one feature are 16 bits apart: two masks and a product put them into the two halves of one
 // TMEM column, one multiplication by the two c's scales finishes them.  (Through shared memory
-// the converted weights cost 328 of a stage's 773 cycles of its bandwidth, and bound it.)
+// the converted weights cost 328 of the 773 cycles of its bandwidth that 64 c took, and bound
+// the kernel.)
 //
 // Two forms of one kernel, P CTAs a tile:
-//   * P = 2, SM pairs (cta_group::2 MMAs of M = 256): 256 features x up to 192 rows of one group.
+//   * P = 2, SM pairs (cta_group::2 MMAs of M = 256): 256 features x up to 256 rows of one group.
 //     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
-//     of the shared-memory traffic for dy that a tile of its own would.
+//     of the shared-memory traffic for dy that a tile of its own would.  Bound by the tensor
+//     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 511 us, 1.88 PFLOP/s; in long runs by the
+//     power cap, 1.6 to 1.7.
 //   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
-//     weights' way from HBM and their conversion are the work.
-// A stage is 64 values of c, in each CTA:
-//   * warp 2 brings the codes of 64 weight rows x 128 features (4 KB, TMA) and their scales
-//     (cp.async: 4 bytes a row) into a ring, so that many stages of the weights are on their way;
+//     weights' way from HBM and their conversion are the work.  Bound by the conversion's
+//     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s.
+// In each CTA, a stage at a time:
+//   * warp 2 brings the codes of 128 weight rows x 128 features (8 KB, TMA) and their scales
+//     (cp.async) into a ring, so that many stages of the weights are on their way;
 //   * warp 3 makes the scales what the converters multiply by;
-//   * groups of four converter warps, a stage each in turn; a warp has 32 features, so one
-//     scale a row;
+//   * three groups of four converter warps, a stage each in turn; a warp has 32 features, so
+//     one scale a row (its wait on warp 3's word covers the codes too: warp 3 waited for both);
 //   * warp 0 brings dy's rows (K-major, TMA), warp 1 (of the pair's first CTA) issues the MMAs;
-//   * four warps store the fp32 sums of the last tile from TMEM under the next one's MMAs.
+//   * four or eight warps store the sums of the last tile under the next one's MMAs.
 // Persistent; every CTA finds its tiles from the group offsets by itself (no plan kernel).
 // Every wait is bounded; one that expires sets the workspace's status word.
 #include "grad.cuh"
@@ -140,7 +144,7 @@ __device__ __forceinline__ void mbar_arrive_other(uint32_t cluster_addr) {
 // One lane of a converged warp, always the same.  The warps that issue TMA loads and MMAs run
 // their loops as a whole and branch to one lane for the issue alone: their addresses and
 // descriptors then live in uniform registers, as those instructions take them.  (A loop that one
-// lane runs alone spent 660 cycles a stage on four MMAs and their commit.)
+// lane runs alone spent 660 cycles on four MMAs and their commit.)
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -395,10 +399,9 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const CUtensorMap* map = small ? &tmBs : &tmB;
       const uint32_t bytes = P * boxes * box * kBK * 2;
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
-        if (st.round && !mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag)) {
-          ok = false;
-          break;
-        }
+        if (st.round) ok = mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);  // (the lanes part only together)
+        if (!ok) break;
         uint8_t* b = smem + st.s * C::kBBytes;
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(&full[st.s], bytes);
@@ -433,11 +436,13 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         const uint32_t idesc =
             idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit);
         const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
-        if (use && !mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag)) break;
+        if (use) ok = mbar_wait(&acc_empty[b], (use - 1) & 1u, p.status, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + b * C::kRowsMax;
         for (int kb = 0; kb < nk; ++kb, st.next()) {
-          ok = mbar_wait(&full[st.s], st.phase, p.status, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st.s], st.phase, p.status, abort_flag));
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = tmem + C::kTmemA + st.s * C::kACols;
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         __syncwarp();
       }
       // after an abort: the MMAs already issued
-      if (*abort_flag) {
+      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) {
         if (elect_one()) {
           if (P == 2) tc_commit_pair_mc(drain, 1);
           else tc_commit(drain);
@@ -480,11 +485,9 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
       ScaleLoad<P> sc(p, t, f0, lane);
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
-        if (st.round && !mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag)) ok = false;
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+        if (st.round) ok = mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&raw_full[st.s], C::kRawCodes);
           tma_load_2d(smem + C::kOffRaw + st.s * C::kRawCodes, &tmW, &raw_full[st.s], f0 / 2,
@@ -515,11 +518,8 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       const uint8_t* lo = smem + C::kOffScale + scale_at(2 * lane, f0, p.F);
       const uint8_t* hi = smem + C::kOffScale + scale_at(2 * lane + 1, f0, p.F);
       for (int kb = 0; kb < nk; ++kb, st.next()) {
-        ok = mbar_wait(&raw_full[st.s], st.phase, p.status, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&raw_full[st.s], st.phase, p.status, abort_flag));
+        if (!ok) break;
         uint32_t over = 0;
 #pragma unroll
         for (int h = 0; h < kBK / 64; ++h) {

