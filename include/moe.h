@@ -574,8 +574,8 @@ int moe_swiglu_backward(const moe_swiglu_backward_desc* d, const uint16_t* dh, c
  * forward: rows outside every group are not read and not written; offsets that decrease or
  * leave [0, Rs] set the status word and nothing is written.
  *   ws: moe_gemm_backward_workspace_size bytes, 256-byte aligned.  Its first 4 bytes are a
- *   status word that these two calls only set bits of: zero it once, before the first use and
- *   in an order with it, and keep the workspace to them; moe_check_status reads it. */
+ *   status word that these calls only set bits of: zero it once, before the first use and in
+ *   an order with it, and keep the workspace to them; moe_check_status reads it. */
 size_t moe_gemm_backward_workspace_size(const moe_dims* d);
 int moe_grouped_gemm_w2_backward(const moe_dims* d, const uint16_t* dy2,
                                  const int32_t* group_offsets, const uint8_t* w2,
@@ -585,6 +585,18 @@ int moe_grouped_gemm_w13_backward(const moe_dims* d, const uint16_t* dy13,
                                   const int32_t* group_offsets, const uint8_t* w13,
                                   const uint8_t* w13_s, uint16_t* dxp, void* ws, size_t ws_bytes,
                                   void* stream);
+
+/* The same with NVFP4 weights (codes, E4M3 scales per 16 features, tensor scales as for the
+ * forward: w2_gs [G], w13_gs [G][2] for the gate and up rows; NULL = 1), which multiply the fp32
+ * sums (W13: of its two halves) in front of the one rounding.  H % 256 == 0 and I % 256 == 0. */
+int moe_grouped_gemm_w2_backward_nvfp4(const moe_dims* d, const uint16_t* dy2,
+                                       const int32_t* group_offsets, const uint8_t* w2,
+                                       const uint8_t* w2_s, const float* w2_gs, uint16_t* dh,
+                                       void* ws, size_t ws_bytes, void* stream);
+int moe_grouped_gemm_w13_backward_nvfp4(const moe_dims* d, const uint16_t* dy13,
+                                        const int32_t* group_offsets, const uint8_t* w13,
+                                        const uint8_t* w13_s, const float* w13_gs, uint16_t* dxp,
+                                        void* ws, size_t ws_bytes, void* stream);
 
 /* Debug helper (synchronises `stream`): reads the device status word at the start of
  * a workspace used by the calls above.  Returns MOE_OK if no bit is set, else

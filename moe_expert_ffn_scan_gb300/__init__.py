@@ -166,6 +166,8 @@ def lib():
         L.moe_gemm_backward_workspace_size.restype = _SZ
         for fn in ("moe_grouped_gemm_w2_backward", "moe_grouped_gemm_w13_backward"):
             getattr(L, fn).argtypes = [_DP] + [_P] * 6 + [_SZ, _P]
+            getattr(L, fn + "_nvfp4").argtypes = [_DP] + [_P] * 7 + [_SZ, _P]
+            getattr(L, fn + "_nvfp4").restype = ctypes.c_int
         for fn in ("moe_dispatch", "moe_dispatch_backward", "moe_combine_backward",
                    "moe_swiglu_quant_save", "moe_swiglu_backward",
                    "moe_grouped_gemm_w2_backward", "moe_grouped_gemm_w13_backward"):
@@ -740,14 +742,15 @@ def gemm_backward_workspace_size(d) -> int:
     return lib().moe_gemm_backward_workspace_size(_d(d))
 
 
-def _gemm_backward(name, d, dy, cols_in, group_offsets, w, w_s, dx, cols_out, ws, stream):
+def _gemm_backward(name, d, dy, cols_in, group_offsets, w, w_s, dx, cols_out, ws, stream,
+                   block=32, scales=()):
     _here(dy, "dy")
     rows, G = _packed_rows(d), d.E + d.has_shared
     rc = getattr(lib(), name)(
         _d(d), _t(dy, _BF16, (rows, cols_in), "dy"),
         _t(group_offsets, _I32, (G + 1,), "group_offsets"),
         _t(w, _U8, (G, cols_in, cols_out // 2), "w"),
-        _t(w_s, _U8, (G, cols_in, cols_out // 32), "w_s"),
+        _t(w_s, _U8, (G, cols_in, cols_out // block), "w_s"), *scales,
         _t(dx, _BF16, (rows, cols_out), "dx"), _p(ws), ws.numel(), _raw_stream(stream))
     if rc:
         raise MoeError(name, rc)
@@ -764,6 +767,23 @@ def moe_grouped_gemm_w13_backward(d, dy13, group_offsets, w13, w13_s, dxp, ws, s
     """dxp [Rs, H] = dy13 [Rs, 2I] . deq(w13[g]) [2I, H], as moe_grouped_gemm_w2_backward."""
     _gemm_backward("moe_grouped_gemm_w13_backward", d, dy13, 2 * d.I, group_offsets, w13, w13_s,
                    dxp, d.H, ws, stream)
+
+
+def moe_grouped_gemm_w2_backward_nvfp4(d, dy2, group_offsets, w2, w2_s, w2_gs, dh, ws,
+                                       stream=None):
+    """moe_grouped_gemm_w2_backward with NVFP4 weights: w2_s [G, H, I/16] E4M3 scales, w2_gs [G]
+    fp32 (None: 1)."""
+    _gemm_backward("moe_grouped_gemm_w2_backward_nvfp4", d, dy2, d.H, group_offsets, w2, w2_s, dh,
+                   d.I, ws, stream, 16, (_t(w2_gs, _F32, (d.E + d.has_shared,), "w2_gs"),))
+
+
+def moe_grouped_gemm_w13_backward_nvfp4(d, dy13, group_offsets, w13, w13_s, w13_gs, dxp, ws,
+                                        stream=None):
+    """moe_grouped_gemm_w13_backward with NVFP4 weights: w13_s [G, 2I, H/16] E4M3 scales, w13_gs
+    [G, 2] fp32 of the gate and up rows (None: 1)."""
+    _gemm_backward("moe_grouped_gemm_w13_backward_nvfp4", d, dy13, 2 * d.I, group_offsets, w13,
+                   w13_s, dxp, d.H, ws, stream, 16,
+                   (_t(w13_gs, _F32, (d.E + d.has_shared, 2), "w13_gs"),))
 
 
 def moe_check_status(ws, stream=None) -> int:
@@ -958,7 +978,8 @@ class MoELayer:
         reads the checks of the last forward_train, and of every backward since they were made)."""
         if getattr(self, "_tws", None) is None or self._tT < T:
             d = self.dims(T)
-            sizes = (max(route_workspace_size(d), gemm_workspace_size(d)),
+            gemm = gemm_workspace_size if self.fmt == "mxfp4" else gemm_workspace_size_nvfp4
+            sizes = (max(route_workspace_size(d), gemm(d)) if gemm(d) else 0,
                      gemm_backward_workspace_size(d))
             if 0 in sizes:
                 raise ValueError("unsupported dims")
@@ -972,8 +993,7 @@ class MoELayer:
         one of two forms:
           checkpoint="fp8"   the experts' inner activations in 8 bits (3 I bytes a row),
           checkpoint="bf16"  in bf16, with the experts' outputs (4 I + 2 H bytes a row).
-        MXFP4 weights.  Steps of one layer share its workspaces: one at a time, as forward."""
-        self._mxfp4_only("training")
+        Steps of one layer share its workspaces: one at a time, as forward."""
         if checkpoint not in ("fp8", "bf16"):
             raise ValueError(f"unknown checkpoint form {checkpoint!r}")
         T, H, I, k, sh, E = x.shape[0], self.H, self.I, self.k, self.has_shared, self.E
@@ -992,8 +1012,13 @@ class MoELayer:
             xq, xs = new(T, H, dt=_U8), new(T, H // 128, dt=_U8)
             moe_quant_act(x, xq, xs)
             y13, y2 = new(Rs, 2 * I), new(Rs, H)
-            moe_grouped_gemm_w13(d, xq, xs, s["perm_src"], s["offsets"], self.w13, self.w13_s, y13,
-                                 ws)
+            nv = self.fmt != "mxfp4"
+            if nv:
+                moe_grouped_gemm_w13_nvfp4(d, xq, xs, s["perm_src"], s["offsets"], self.w13,
+                                           self.w13_s, self.w13_gs, y13, ws)
+            else:
+                moe_grouped_gemm_w13(d, xq, xs, s["perm_src"], s["offsets"], self.w13, self.w13_s,
+                                     y13, ws)
             hq, hs = new(Rs, I, dt=_U8), new(Rs, I // 128, dt=_U8)
             if checkpoint == "fp8":
                 s |= dict(hq=hq, hs=hs, yq=new(Rs, 2 * I, dt=_U8),
@@ -1002,7 +1027,11 @@ class MoELayer:
             else:
                 s |= dict(y13=y13, y2=y2)
                 moe_swiglu_quant(y13, hq, hs)
-            moe_grouped_gemm_w2(d, hq, hs, s["offsets"], self.w2, self.w2_s, y2, ws)
+            if nv:
+                moe_grouped_gemm_w2_nvfp4(d, hq, hs, s["offsets"], self.w2, self.w2_s, self.w2_gs,
+                                          y2, ws)
+            else:
+                moe_grouped_gemm_w2(d, hq, hs, s["offsets"], self.w2, self.w2_s, y2, ws)
             moe_combine(d, y2, s["inv"], s["w"], out)
         return out, s
 
@@ -1012,7 +1041,6 @@ class MoELayer:
         gradient that reaches x by other ways, or None) + the experts' part, and dw [T, k] fp32,
         the combine weights' gradient, which moe_balance_loss_backward takes to the logits.
         The experts' weights have none."""
-        self._mxfp4_only("training")
         T, H, I = saved["T"], self.H, self.I
         d = self.dims(T)
         Rs = T * (self.k + self.has_shared)
@@ -1030,9 +1058,18 @@ class MoELayer:
                 moe_combine_backward(d, dout, saved["y2"], saved["inv"], saved["w"], dy2=rows,
                                      dw=dw)
                 act = dict(y13=saved["y13"])
-            moe_grouped_gemm_w2_backward(d, rows, saved["offsets"], self.w2, self.w2_s, dh, ws)
+            off, nv = saved["offsets"], self.fmt != "mxfp4"
+            if nv:
+                moe_grouped_gemm_w2_backward_nvfp4(d, rows, off, self.w2, self.w2_s, self.w2_gs, dh,
+                                                   ws)
+            else:
+                moe_grouped_gemm_w2_backward(d, rows, off, self.w2, self.w2_s, dh, ws)
             moe_swiglu_backward(dh, dy13, **act)
-            moe_grouped_gemm_w13_backward(d, dy13, saved["offsets"], self.w13, self.w13_s, rows, ws)
+            if nv:
+                moe_grouped_gemm_w13_backward_nvfp4(d, dy13, off, self.w13, self.w13_s, self.w13_gs,
+                                                    rows, ws)
+            else:
+                moe_grouped_gemm_w13_backward(d, dy13, off, self.w13, self.w13_s, rows, ws)
             moe_dispatch_backward(d, rows, saved["inv"], dx, dx_in=dx_in)
         return dx, dw
 

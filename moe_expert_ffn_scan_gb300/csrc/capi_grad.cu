@@ -23,19 +23,28 @@ bool swiglu_ok(int rows, int I) {
 int rows_R(const moe_dims* d) { return d->T * d->k; }
 int rows_Rs(const moe_dims* d) { return rows_R(d) + (d->has_shared ? d->T : 0); }
 
-// dx of the rows of dy through the weights w [G][C][F/2], w_s [G][C][F/32].
+// Weights of C rows of F features: codes w [G][C][F/2], scales w_s [G][C][F/32] or (segments > 0:
+// NVFP4) [G][C][F/16] and gs [G][segments].
+struct GradWeights {
+  const uint8_t *w, *w_s;
+  const float* gs;
+  int segments;
+};
+
+// dx of the rows of dy through those weights.
 int expert_grad(const moe_dims* d, int C, int F, const uint16_t* dy, const int32_t* offsets,
-                const uint8_t* w, const uint8_t* w_s, uint16_t* dx, void* ws, size_t ws_bytes,
-                void* stream) {
+                const GradWeights& W, uint16_t* dx, void* ws, size_t ws_bytes, void* stream) {
   if (!dims_ok(d) || static_cast<long long>(d->E + 1) * C >= (1LL << 31))
     return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (!dy || !offsets || !w || !w_s || !dx || !ws) return MOE_ERR_INVALID_ARG;
-  if (!aligned(dy, 16) || !aligned(offsets, 4) || !aligned(w, 32) || !aligned(w_s, 16) ||
-      !aligned(dx, 16) || !aligned(ws, kAlign))
+  if (W.segments && (d->H % 256 || d->I % 256)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!dy || !offsets || !W.w || !W.w_s || !dx || !ws) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(offsets, 4) || !aligned(W.w, 32) || !aligned(W.w_s, 16) ||
+      !null_or(W.gs, 4) || !aligned(dx, 16) || !aligned(ws, kAlign))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_gemm_backward_workspace_size(d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   ExpertGradCall a = {};
-  a.dy = dy, a.offsets = offsets, a.w = w, a.w_s = w_s, a.dx = dx;
+  a.dy = dy, a.offsets = offsets, a.w = W.w, a.w_s = W.w_s, a.dx = dx;
+  a.nv = W.segments > 0, a.gs_segments = W.segments, a.gs = W.gs;
   a.E = d->E, a.G = d->E + d->has_shared, a.routed = rows_R(d), a.rows = rows_Rs(d);
   a.C = C, a.F = F;
   a.status = static_cast<uint32_t*>(ws);
@@ -118,7 +127,8 @@ int moe_grouped_gemm_w2_backward(const moe_dims* d, const uint16_t* dy2,
                                  const uint8_t* w2_s, uint16_t* dh, void* ws, size_t ws_bytes,
                                  void* stream) {
   if (!d) return MOE_ERR_UNSUPPORTED_SHAPE;
-  return expert_grad(d, d->H, d->I, dy2, group_offsets, w2, w2_s, dh, ws, ws_bytes, stream);
+  return expert_grad(d, d->H, d->I, dy2, group_offsets, {w2, w2_s, nullptr, 0}, dh, ws, ws_bytes,
+                     stream);
 }
 
 int moe_grouped_gemm_w13_backward(const moe_dims* d, const uint16_t* dy13,
@@ -126,8 +136,26 @@ int moe_grouped_gemm_w13_backward(const moe_dims* d, const uint16_t* dy13,
                                   const uint8_t* w13_s, uint16_t* dxp, void* ws, size_t ws_bytes,
                                   void* stream) {
   if (!d || d->I > (1 << 29)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  return expert_grad(d, 2 * d->I, d->H, dy13, group_offsets, w13, w13_s, dxp, ws, ws_bytes,
+  return expert_grad(d, 2 * d->I, d->H, dy13, group_offsets, {w13, w13_s, nullptr, 0}, dxp, ws,
+                     ws_bytes, stream);
+}
+
+int moe_grouped_gemm_w2_backward_nvfp4(const moe_dims* d, const uint16_t* dy2,
+                                       const int32_t* group_offsets, const uint8_t* w2,
+                                       const uint8_t* w2_s, const float* w2_gs, uint16_t* dh,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  if (!d) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return expert_grad(d, d->H, d->I, dy2, group_offsets, {w2, w2_s, w2_gs, 1}, dh, ws, ws_bytes,
                      stream);
+}
+
+int moe_grouped_gemm_w13_backward_nvfp4(const moe_dims* d, const uint16_t* dy13,
+                                        const int32_t* group_offsets, const uint8_t* w13,
+                                        const uint8_t* w13_s, const float* w13_gs, uint16_t* dxp,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  if (!d || d->I > (1 << 29)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return expert_grad(d, 2 * d->I, d->H, dy13, group_offsets, {w13, w13_s, w13_gs, 2}, dxp, ws,
+                     ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -52,26 +52,33 @@ constexpr int kBK = 128;
 constexpr int kFeat = 128;       // features per CTA
 constexpr int kMaxGroups = 1025;
 
-template <int P>
+// Weight formats: MXFP4, and NVFP4 with one tensor scale for all of a weight's rows or one for
+// each half of them (W13's gate and up projection), whose sums are kept apart until the end.
+enum Format { kMx = 0, kNv = 1, kNvHalves = 2 };
+
+template <int P, int F>
 struct Cfg {
   static constexpr int kOcc = P == 2 ? 1 : 2;         // CTAs per SM
+  static constexpr int kBlock = F == kMx ? 32 : 16;   // features per scale byte
   static constexpr int kACols = kBK / 2;              // TMEM columns of a stage of A
   static constexpr int kRawCodes = kFeat / 2 * kBK;
-  static constexpr int kRawScales = 16 * kBK;         // 16 bytes a weight row, 4 of them the CTA's
-  // The scales of a stage as the converters multiply by them: [32 c][quarter of the features]
+  static constexpr int kRawScales = 16 * kBK;         // 16 bytes a weight row, 4 or 8 the CTA's
+  // The scales of a stage as the converters multiply by them: [32 c][block of the features]
   // [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a byte is above 128.
-  static constexpr int kFactors = kBK * 8 + 16;
+  static constexpr int kFactors = kBK * 2 * (kFeat / kBlock) + 16;
   static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
   static constexpr int kGroups = 3;                   // converter groups of four warps
   static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
-  static constexpr int kRowsMax = P == 2 ? 256 : 32;  // rows per tile
+  static constexpr int kSums = F == kNvHalves ? 2 : 1;          // of a tile
+  static constexpr int kRowsMax = P == 2 ? 256 / kSums : 32;    // rows per tile
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
-  static constexpr int kBox = P == 2 ? 128 : 32, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
-  static constexpr int kAcc = P == 2 ? 1 : 2;         // accumulators
+  static constexpr int kBox = kRowsMax / P, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
+  static constexpr int kAcc = P == 2 ? 1 : 2 / kSums; // accumulators (each of kSums sums)
+  static constexpr int kAccCols = kSums * kRowsMax;
   static constexpr int kSt = P == 2 ? 4 : 3;          // stages of both operands
-  static constexpr int kRaw = 7;                      // of codes and scales
+  static constexpr int kRaw = P == 1 && F != kMx ? 6 : 7;       // of codes and scales
   static constexpr int kTmemCols = P == 2 ? 512 : 256;
-  static constexpr int kTmemA = kAcc * kRowsMax;      // A's stages behind the accumulators
+  static constexpr int kTmemA = kAcc * kAccCols;      // A's stages behind the accumulators
   static constexpr int kBBytes = kRowsMax / P * kBK * 2;
   static constexpr int kOffRaw = kSt * kBBytes;
   static constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
@@ -88,6 +95,7 @@ struct Cfg {
 struct GradParams {
   const int32_t* offsets;
   const uint8_t* scales;
+  const float* gs;  // NVFP4: [G][kSums] tensor scales, or null (1)
   uint16_t* dx;
   int G, rows, C, F;
   uint32_t* status;
@@ -172,11 +180,11 @@ struct Ring {
 // Tile L: chunks of a group's rows (at most kRowsMax, near-equal multiples of kUnit) inside a
 // block of features, so that a weight tile is read for all of its group's chunks at about the
 // same time.
-template <int P>
+template <int P, int F>
 __device__ __forceinline__ int chunks_of(int m) {
-  return (m + Cfg<P>::kRowsMax - 1) / Cfg<P>::kRowsMax;
+  return (m + Cfg<P, F>::kRowsMax - 1) / Cfg<P, F>::kRowsMax;
 }
-template <int P>
+template <int P, int F>
 __device__ __forceinline__ GradTile tile_at(long long L, int f_tiles, int G, const int* off,
                                             const int* first) {
   const int item = static_cast<int>(L / f_tiles);
@@ -188,7 +196,7 @@ __device__ __forceinline__ GradTile tile_at(long long L, int f_tiles, int G, con
   }
   const int m = off[lo + 1] - off[lo], nch = first[lo + 1] - first[lo];
   const int in = static_cast<int>(L - static_cast<long long>(first[lo]) * f_tiles);
-  constexpr int U = Cfg<P>::kUnit;
+  constexpr int U = Cfg<P, F>::kUnit;
   const int per = ((m + nch - 1) / nch + U - 1) / U * U;
   const int chunk = in % nch;
   GradTile t;
@@ -252,17 +260,17 @@ __device__ __forceinline__ void cp_async_wait_all() {
 }
 
 // A tile's scales, kBK weight rows a stage: lane l has rows l, l + 32, ...  Of each row the CTA's
-// four bytes are loaded with the aligned 16 around them (which end inside the tensor: its size
-// is a multiple of 512 bytes), because copies of 16 bytes pass L1 by: with 4 bytes a row 32 groups
+// four or eight bytes are loaded with the aligned 16 around them (which end inside the tensor: its
+// size is a multiple of 512 bytes), because copies of 16 bytes pass L1 by: with 4 bytes a row 32 groups
 // of one row took 158 us in place of 132.  Their arrival counts on the stage's barrier.
-template <int P>
+template <int P, int F>
 struct ScaleLoad {
   const uint8_t* at;
   size_t row;
   bool there;  // (a pair's second half may lie past the last feature)
   __device__ __forceinline__ ScaleLoad(const GradParams& p, const GradTile& t, int f0, int lane)
-      : row(p.F / 32), there(f0 < p.F) {
-    at = p.scales + (static_cast<size_t>(t.g) * p.C + lane) * row + f0 / 32;
+      : row(p.F / Cfg<P, F>::kBlock), there(f0 < p.F) {
+    at = p.scales + (static_cast<size_t>(t.g) * p.C + lane) * row + f0 / Cfg<P, F>::kBlock;
   }
   __device__ __forceinline__ void stage(uint8_t* to, uint64_t* bar, int lane) {
     if (there) {
@@ -277,17 +285,26 @@ struct ScaleLoad {
                  : "memory");
   }
 };
-// Where row c of a stage has the four bytes: a stage's first row, and so a group's, starts at a
-// multiple of 16 bytes.
-__device__ __forceinline__ int scale_at(int c, int f0, int F) {
-  return c * 16 + ((c * (F / 128) + f0 / 128) & 3) * 4;
+// Where row c of a stage has them (`own` bytes): a stage's first row, and so a group's, starts at
+// a multiple of 16 bytes.
+__device__ __forceinline__ int scale_at(int c, int f0, int features, int own) {
+  return c * 16 + ((c * (features / kFeat) + f0 / kFeat) & (16 / own - 1)) * own;
 }
+// Two E4M3 scales as bf16 factors, times 2^119 (448 * 2^119 is below bf16's largest value); the
+// codes come times 2^-126, so products are short of 2^7, which the epilogue makes up for.
+__device__ __forceinline__ uint32_t factor_e4m3(uint32_t lo_hi) {
+  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+      static_cast<__nv_fp8x2_storage_t>(lo_hi & 0xFFFFu), __NV_E4M3);
+  const float2 v = __half22float2(__half2(hr));
+  return bf16x2_of(v.x * 0x1p119f, v.y * 0x1p119f);
+}
+constexpr float kNvShort = 128.f;
 
-template <int P>
-__global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
+template <int P, int F>
+__global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     k_expert_grad(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmBs, const GradParams p) {
-  using C = Cfg<P>;
+  using C = Cfg<P, F>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t rank = P == 2 ? cluster_ctarank() : 0;
   const bool leader = rank == 0;
@@ -349,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       if (g < G) {
         const int a = off[g], b = off[g + 1];
         if (a < 0 || b < a || b > p.rows) bad = true;
-        else total += chunks_of<P>(b - a);
+        else total += chunks_of<P, F>(b - a);
       }
     }
     int scan = total;
@@ -391,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     uint32_t issued = 0;
     const uint32_t bar0 = P == 2 ? leader_addr(&full[0]) : 0;
     for (long long L = cl; L < total && ok; L += ncl) {
-      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const int mine = (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit / P;  // rows in this CTA
       const int row0 = t.row0 + static_cast<int>(rank) * mine;
       const bool small = mine <= 2 * C::kBoxSmall;
@@ -432,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       // (of a descriptor only the address, the low 14 bits, moves)
       const uint64_t db0 = smem_desc(smem_u32(smem), 0, 1024, kLayoutSw128);
       for (long long L = cl; L < total && ok; L += ncl, ++tc) {
-        const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+        const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
         const uint32_t idesc =
             idesc_bf16(kFeat * P, (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit);
         const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
@@ -440,11 +457,14 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + b * C::kRowsMax;
+        const uint32_t d0 = tmem + b * C::kAccCols;
         for (int kb = 0; kb < nk; ++kb, st.next()) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st.s], st.phase, p.status, abort_flag));
           if (!ok) break;
           tc_fence_after();
+          const bool second = C::kSums == 2 && kb >= nk / 2;
+          const uint32_t d = d0 + (second ? C::kRowsMax : 0);
+          const int k0 = second ? nk / 2 : 0;  // the sum's first stage
           const uint32_t at = tmem + C::kTmemA + st.s * C::kACols;
           const uint32_t db = static_cast<uint32_t>(db0) + st.s * (C::kBBytes / 16);
           if (elect_one()) {
@@ -452,8 +472,8 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
             for (int kk = 0; kk < kBK / 16; ++kk) {
               const uint64_t dk = (db0 >> 32) << 32 |
                                   (db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2);
-              if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
-              else mma_bf16_ts(d, at + kk * 8, dk, idesc, kb > 0 || kk > 0);
+              if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, kb > k0 || kk > 0);
+              else mma_bf16_ts(d, at + kk * 8, dk, idesc, kb > k0 || kk > 0);
             }
             if (P == 2) tc_commit_pair_mc(&empty[st.s], 3);
             else tc_commit(&empty[st.s]);
@@ -481,9 +501,9 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     bool ok = true;
     uint32_t issued = 0;
     for (long long L = cl; L < total && ok; L += ncl) {
-      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
-      ScaleLoad<P> sc(p, t, f0, lane);
+      ScaleLoad<P, F> sc(p, t, f0, lane);
       for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
         if (st.round) ok = mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -506,17 +526,18 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- factors
-    // lane l has c = 2 l, 2 l + 1 of every 64: factors 2^(s - 127 + 126), a bf16 each, for every
-    // quarter
+    // lane l has c = 2 l, 2 l + 1 of every 64: a bf16 factor each for every block of features,
+    // of an E8M0 byte s 2^(s - 127 + 126)
+    constexpr int kBlocks = kFeat / C::kBlock, kOwn = kBlocks;  // bytes a row
     Ring<C::kRaw> st;
     bool ok = true;
-    uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::kOffFactor) + (lane >> 4) * 64 +
+    uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::kOffFactor) + (lane >> 4) * (kBlocks * 16) +
                    (lane & 3) * 4 + ((lane >> 2) & 3);
     for (long long L = cl; L < total && ok; L += ncl) {
-      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
-      const uint8_t* lo = smem + C::kOffScale + scale_at(2 * lane, f0, p.F);
-      const uint8_t* hi = smem + C::kOffScale + scale_at(2 * lane + 1, f0, p.F);
+      const uint8_t* lo = smem + C::kOffScale + scale_at(2 * lane, f0, p.F, kOwn);
+      const uint8_t* hi = smem + C::kOffScale + scale_at(2 * lane + 1, f0, p.F, kOwn);
       for (int kb = 0; kb < nk; ++kb, st.next()) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&raw_full[st.s], st.phase, p.status, abort_flag));
         if (!ok) break;
@@ -525,19 +546,28 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
         for (int h = 0; h < kBK / 64; ++h) {
           // (64 rows further the bytes' place in their 16 is the same)
           const int at = st.s * C::kRawScales + h * 1024;
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(lo + at);
-          const uint32_t y = *reinterpret_cast<const uint32_t*>(hi + at);
-          // a byte above 128 has its highest bit and another
-          over |= (((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & x) | (((y & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & y);
+          uint32_t* out = to + st.s * (C::kFactors / 4) + h * (kBlocks * 32);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t v = __byte_perm(x, y, q | (4 + q) << 8) & 0x00FF00FFu;
-            to[st.s * (C::kFactors / 4) + h * 128 + q * 16] = v * 128 + 0x3F003F00u;
+          for (int v = 0; v < kOwn / 4; ++v) {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(lo + at + 4 * v);
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(hi + at + 4 * v);
+            if (F == kMx)  // a byte above 128 has its highest bit and another
+              over |= (((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & x) |
+                      (((y & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (F == kMx)
+                out[q * 16] =
+                    (__byte_perm(x, y, q | (4 + q) << 8) & 0x00FF00FFu) * 128 + 0x3F003F00u;
+              else
+                out[(4 * v + q) * 16] = factor_e4m3(__byte_perm(x, y, q | (4 + q) << 4));
+            }
           }
         }
         const bool any = __any_sync(0xFFFFFFFFu, (over & 0x80808080u) != 0);
         if (lane == 0) {
-          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + kBK * 8) = any;
+          *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + C::kFactors - 16) =
+              any;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&fac_full[st.s]);
@@ -549,7 +579,10 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     // (64-byte swizzle: eight rows' 16-byte chunks fall on all the banks)
     const uint32_t src =
         smem_u32(smem + C::kOffRaw) + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
-    const uint8_t* factors = smem + C::kOffFactor + q * 64 + (lane & 3) * 16;
+    // (a lane's four features: in the warp's one block of 32, or the first or second of 16)
+    constexpr int kStep = 64 * (kFeat / C::kBlock);  // bytes of factors per 32 c
+    const uint8_t* factors =
+        smem + C::kOffFactor + (F == kMx ? q : 2 * q + (lane >> 4)) * 64 + (lane & 3) * 16;
     const uint32_t dst = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::kTmemA;
     const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
     const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
@@ -563,15 +596,15 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
       if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
       tc_fence_after();
       const uint32_t over = *reinterpret_cast<const uint32_t*>(
-          smem + C::kOffFactor + rr.s * C::kFactors + kBK * 8);
+          smem + C::kOffFactor + rr.s * C::kFactors + C::kFactors - 16);
       constexpr int kH = kBK / 32;  // 32 c each
       const uint32_t to = dst + ra.s * C::kACols;
-      if (!over) {
+      if (F != kMx || !over) {
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
           uint32_t w[4], lo[8], hi[8];  // features 0, 1 and 2, 3 of the thread's four
           ldmatrix_x4_trans(src + rr.s * C::kRawCodes + h * 2048, w);
-          const uint4 f = *reinterpret_cast<const uint4*>(factors + rr.s * C::kFactors + h * 256);
+          const uint4 f = *reinterpret_cast<const uint4*>(factors + rr.s * C::kFactors + h * kStep);
           if (h == kH - 1) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&raw_empty[rr.s]);
@@ -595,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           for (int m = 0; m < 4; ++m) {
             // the two bytes again, of what the factor's arithmetic made of them
             const uint32_t f = *reinterpret_cast<const uint32_t*>(
-                factors + rr.s * C::kFactors + h * 256 + m * 4);
+                factors + rr.s * C::kFactors + h * kStep + m * 4);
             const uint32_t sc = ((f - 0x3F003F00u) >> 7) & 0x01FF01FFu;
             uint32_t o[4], rest = factor_rest(sc);
             codes_to_bf16(w[m], factor_most(sc), o);
@@ -629,14 +662,14 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
     constexpr int kCols = P == 2 ? C::kRowsMax / (C::kEpi / 4) : 16;
     uint32_t tc = 0;
     for (long long L = cl; L < total; L += ncl, ++tc) {
-      const GradTile t = tile_at<P>(L, f_tiles, G, off, first);
+      const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
       int w_ok = 1;
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
       tc_fence_after();
       const int c0 = P == 2 ? ((warp - 4) >> 2) * kCols : 0;
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kRowsMax + c0;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAccCols + c0;
       const int f = t.f0 + static_cast<int>(rank) * kFeat + q * 32;
       const int rows = f < p.F ? t.rows - c0 : 0;
       uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0 + (lane >> 3)) * p.F + f + 4 * (lane & 7);
@@ -648,6 +681,11 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           else mbar_arrive(&acc_empty[b]);
         }
       };
+      float gs0 = 1.f, gs1 = 1.f;
+      if (F != kMx) {
+        gs0 = kNvShort * (p.gs ? __ldg(p.gs + t.g * C::kSums) : 1.f);
+        if (C::kSums == 2) gs1 = kNvShort * (p.gs ? __ldg(p.gs + t.g * 2 + 1) : 1.f);
+      }
       uint32_t v[kCols / 2];  // two rows a register
       for (int r0 = 0; r0 < (P == 2 ? 1 : rows); r0 += kCols) {
 #pragma unroll
@@ -655,7 +693,21 @@ __global__ void __launch_bounds__(Cfg<P>::kThreads, Cfg<P>::kOcc)
           if (r0 + c < rows) {
             uint32_t x[8];
             tmem_ld_32x32b_x8(acc + r0 + c, x);
-            tmem_ld_wait();
+            if (C::kSums == 2) {
+              uint32_t y[8];
+              tmem_ld_32x32b_x8(acc + C::kRowsMax + r0 + c, y);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                x[i] = __float_as_uint(
+                    fmaf(gs0, __uint_as_float(x[i]), gs1 * __uint_as_float(y[i])));
+            } else {
+              tmem_ld_wait();
+              if (F != kMx) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(gs0 * __uint_as_float(x[i]));
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               v[c / 2 + i] = bf16x2_of(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
@@ -709,9 +761,9 @@ bool encode_dy(CUtensorMap* m, const ExpertGradCall& a, int box_rows) {
          CUDA_SUCCESS;
 }
 
-template <int P>
+template <int P, int F>
 cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
-  using C = Cfg<P>;
+  using C = Cfg<P, F>;
   static OncePerContext once;  // how many of its clusters fit the GPU at once
   int dev = 0, clusters = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -730,7 +782,7 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
   if (once.ready(dev, current_context_id())) {
     clusters = once.value(dev);
   } else {
-    e = cudaFuncSetAttribute(k_expert_grad<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_expert_grad<P, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem);
     if (e != cudaSuccess) return e;
     int sms = 0;
@@ -740,7 +792,7 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
       cfg.gridDim = dim3(sms / P * P);
       cfg.attrs = attr + 1;
       cfg.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&clusters, k_expert_grad<P>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&clusters, k_expert_grad<P, F>, &cfg);
       if (e != cudaSuccess) return e;
       if (clusters < 1) return cudaErrorInvalidConfiguration;
     } else {
@@ -751,11 +803,11 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
   CUtensorMap tmW, tmB, tmBs;
   if (!encode_w(&tmW, a, kBK) || !encode_dy(&tmB, a, C::kBox) || !encode_dy(&tmBs, a, C::kBoxSmall))
     return cudaErrorInvalidValue;
-  const GradParams p = {a.offsets, a.w_s, a.dx, a.G, a.rows, a.C, a.F, a.status};
+  const GradParams p = {a.offsets, a.w_s, a.gs, a.dx, a.G, a.rows, a.C, a.F, a.status};
   cfg.gridDim = dim3(clusters * P);
   cfg.attrs = attr;
   cfg.numAttrs = P == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_expert_grad<P>, tmW, tmB, tmBs, p);
+  return cudaLaunchKernelEx(&cfg, k_expert_grad<P, F>, tmW, tmB, tmBs, p);
 }
 
 // The form that should take less time, from what the host knows: the dims, not the routing.  Of
@@ -767,14 +819,14 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
 // of 2048 x 1024, 16 groups of 50: 25, 15 and 22, 14, of 150: 46, 28 and 26, 17; w2 of 1024 x 1024,
 // 64 groups of 20, 80: 16, 33 and 24, 30; w2 of 1152 x 640, 13 groups of 60, 179: 8.5, 15.8 and
 // 10.8, 13.7.
-template <int P>
+template <int P, int F>
 double cost_us(const ExpertGradCall& a) {
-  const double M = Cfg<P>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
+  const double M = Cfg<P, F>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
   auto chunks = [&](double rows) { return rows <= 0.75 * M ? 1.0 : rows / M + 0.4; };
   double items = groups * chunks(a.routed / groups);
   if (a.G > a.E) items += chunks(a.rows - a.routed);
   const double tiles = items * ((a.F + kFeat * P - 1) / (kFeat * P));
-  const double waves = ceil(tiles * P / (kSms * Cfg<P>::kOcc));
+  const double waves = ceil(tiles * P / (kSms * Cfg<P, F>::kOcc));
   const double stages = a.C / kBK;
   // (a CTA that has its SM for itself is faster; a pair's MMAs take longer for more rows)
   if (P == 1) return 3.5 + waves * (stages * (tiles <= kSms ? 0.45 : 0.56) + 1.2);
@@ -782,10 +834,16 @@ double cost_us(const ExpertGradCall& a) {
   return 7.0 + waves * (stages * (0.36 + 0.28 * (rows < M ? rows / M : 1.0)) + 0.7);
 }
 
+template <int F>
+cudaError_t launch_form(const ExpertGradCall& a, cudaStream_t st) {
+  return cost_us<1, F>(a) <= cost_us<2, F>(a) ? launch_grad<1, F>(a, st) : launch_grad<2, F>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_grad(const ExpertGradCall& a, cudaStream_t st) {
-  return cost_us<1>(a) <= cost_us<2>(a) ? launch_grad<1>(a, st) : launch_grad<2>(a, st);
+  if (!a.nv) return launch_form<kMx>(a, st);
+  return a.gs_segments == 2 ? launch_form<kNvHalves>(a, st) : launch_form<kNv>(a, st);
 }
 
 }  // namespace moe

@@ -53,12 +53,16 @@ struct SwigluBwdCall {
 };
 cudaError_t launch_swiglu_bwd(const SwigluBwdCall& a, cudaStream_t st);
 
-// Gradient products of the MXFP4 experts (expert_grad.cu): for every row r of group g,
-// dx[r][f] = sum_c dy[r][c] * deq(w[g])[c][f], with w [G][C][F/2], scales [G][C][F/32].
+// Gradient products of the experts (expert_grad.cu): for every row r of group g,
+// dx[r][f] = sum_c dy[r][c] * deq(w[g])[c][f], with codes w [G][C][F/2] and scales [G][C][F/32]
+// (MXFP4) or [G][C][F/16] and gs [G][gs_segments] (NVFP4: a tensor scale per equal part of the C
+// rows).
 struct ExpertGradCall {
   const uint16_t* dy;       // [rows][C]
   const int32_t* offsets;   // [G + 1]
   const uint8_t *w, *w_s;
+  const float* gs;          // or null: 1
+  int nv, gs_segments;      // NVFP4; 1 or 2
   uint16_t* dx;             // [rows][F]
   int E, G, routed, rows, C, F;  // G = E, or E + 1 with a shared expert; routed: rows of the E
   uint32_t* status;

@@ -54,14 +54,27 @@ def mxfp4(codes, scales):
     return v * torch.exp2(scales.to(F64) - 127).repeat_interleave(32, -1)
 
 
-def expert_grad(dy, off, w, w_s, rows, F):
+def nvfp4(codes, scales, gs=None):
+    """[.., C, F/2] codes, [.., C, F/16] E4M3 scales and the tensor scales of the equal parts of
+    the C rows -> [.., C, F] values."""
+    lut = torch.tensor(E2M1 + [-v for v in E2M1], dtype=F64, device=codes.device)
+    v = torch.stack([lut[(codes & 15).long()], lut[(codes >> 4).long()]], -1).flatten(-2)
+    v = v * scales.view(torch.float8_e4m3fn).to(F64).repeat_interleave(16, -1)
+    if gs is not None:
+        gs = gs.to(F64).reshape(-1)
+        v = v * gs.repeat_interleave(v.shape[-2] // gs.numel())[:, None]
+    return v
+
+
+def expert_grad(dy, off, w, w_s, rows, F, gs=None, nv=False):
     """dx (rows of no group: NaN) and the sum of its terms' magnitudes."""
     dx = torch.full((rows, F), float("nan"), dtype=F64, device=dy.device)
     size = torch.zeros_like(dx)
     off = off.tolist()
     for g in range(len(off) - 1):
         if off[g] < off[g + 1]:
-            d, v = dy[off[g]:off[g + 1]].to(F64), mxfp4(w[g], w_s[g])
+            d = dy[off[g]:off[g + 1]].to(F64)
+            v = nvfp4(w[g], w_s[g], None if gs is None else gs[g]) if nv else mxfp4(w[g], w_s[g])
             dx[off[g]:off[g + 1]] = d @ v
             size[off[g]:off[g + 1]] = d.abs() @ v.abs()
     return dx, size

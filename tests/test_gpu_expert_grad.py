@@ -154,6 +154,84 @@ def test_non_finite_rows_stay_in_their_rows():
     assert torch.all(torch.isnan(out[3])) and not torch.any(torch.isfinite(out[33]))
 
 
+def _call_nv(which, lens, H, I, seed=0, ints=True, gs=True):
+    """_call with NVFP4 weights.  ints: scales 1, 2, 3 and tensor scales 1, 2 and 1/2: terms are
+    multiples of 1/4 up to 2 * 6 * 3 * 2."""
+    g = torch.Generator(device=DEV).manual_seed(seed + H + 3 * I + len(lens))
+    rows, (C, F), G = sum(lens), (H, I) if which == "w2" else (2 * I, H), len(lens)
+    off = torch.tensor([sum(lens[:i]) for i in range(G + 1)], dtype=I32, device=DEV)
+    ri = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=DEV)  # noqa: E731
+    w = ri(0, 256, G, C, F // 2).to(U8)
+    shape = (G,) if which == "w2" else (G, 2)
+    if ints:
+        dy = ri(-2, 3, rows, C).to(BF)
+        w_s = ri(1, 4, G, C, F // 16).float().to(torch.float8_e4m3fn).view(U8)
+        t = torch.tensor([0.5, 1.0, 2.0], device=DEV)[ri(0, 3, *shape)]
+    else:
+        dy = torch.randn(rows, C, generator=g, device=DEV).to(BF)
+        w_s = ri(1, 120, G, C, F // 16).to(U8)  # every positive E4M3 value up to 256
+        t = torch.rand(*shape, generator=g, device=DEV) + 0.5
+    t = t if gs else None
+    d = moe.dims(rows, H, I, G, 1, 0)
+    dx = torch.full((rows, F), 7.0, dtype=BF, device=DEV)
+    ws = moe.alloc_workspace(moe.gemm_backward_workspace_size(d))
+    f = moe.moe_grouped_gemm_w2_backward_nvfp4 if which == "w2" \
+        else moe.moe_grouped_gemm_w13_backward_nvfp4
+    f(d, dy, off, w, w_s, t, dx, ws)
+    assert moe.moe_check_status(ws) == 0
+    want, size = ref.expert_grad(dy, off, w, w_s, rows, F, t, True)
+    if ints:
+        assert torch.equal(dx, want.to(BF))
+    else:
+        # the scale's product and the halves' sum besides
+        tol = ref.U16 * want.abs() + (C / 16 + 3) * 2.0 ** -22 * size
+        assert torch.all((dx.double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("which", ["w2", "w13"])
+@pytest.mark.parametrize("H,I", [(256, 256), (512, 768), (1280, 256), (4096, 1280), (1280, 2048)])
+@pytest.mark.parametrize("ints", [True, False])
+def test_nvfp4_group_lengths(which, H, I, ints):
+    _call_nv(which, EDGES, H, I, ints=ints)
+
+
+@pytest.mark.parametrize("which", ["w2", "w13"])
+@pytest.mark.parametrize("lens", [[1], [0, 3], [16] * 40, [1] * 300, [2000], [260, 3, 700, 1]])
+@pytest.mark.parametrize("gs", [True, False])
+def test_nvfp4_few_and_many_groups(which, lens, gs):
+    _call_nv(which, lens, 512, 256, gs=gs)
+
+
+@pytest.mark.parametrize("which", ["w2", "w13"])
+def test_nvfp4_layer_sizes(which):
+    _call_nv(which, [3, 0, 290, 17, 140, 64], 7168, 2048)
+    _call_nv(which, [3, 0, 290, 17, 140, 64], 7168, 2048, ints=False)
+
+
+def test_nvfp4_every_scale_byte():
+    """One-hot rows read single weight rows back: group b has scale byte b in row b (bytes 127 and
+    255 are NaN, those from 128 on negative)."""
+    H, I, G = 256, 256, 256
+    g = torch.Generator(device=DEV).manual_seed(6)
+    w = torch.randint(0, 256, (G, H, I // 2), generator=g, device=DEV).to(U8)
+    w_s = torch.full((G, H, I // 16), 56, dtype=U8, device=DEV)  # 1.0
+    b = torch.arange(G, device=DEV)
+    w_s[b, b] = b.to(U8)[:, None]
+    dy = torch.zeros(G, H, dtype=BF, device=DEV)
+    dy[b, b] = 1.0
+    d = moe.dims(G, H, I, G, 1, 0)
+    dx = torch.empty(G, I, dtype=BF, device=DEV)
+    ws = moe.alloc_workspace(moe.gemm_backward_workspace_size(d))
+    moe.moe_grouped_gemm_w2_backward_nvfp4(d, dy, torch.arange(G + 1, dtype=I32, device=DEV), w, w_s,
+                                           None, dx, ws)
+    nan = torch.tensor([127, 255], device=DEV)
+    assert torch.all(torch.isnan(dx[nan]))
+    rest = torch.ones(G, dtype=torch.bool, device=DEV)
+    rest[nan] = False
+    want = ref.nvfp4(w[b, b][:, None], w_s[b, b][:, None])[:, 0].to(BF)
+    assert torch.equal(dx[rest].float(), want[rest].float())
+
+
 @pytest.mark.parametrize("which", ["w2", "w13"])
 def test_outputs_are_the_same_in_every_run(which):
     a, b = (_call(which, [100, 3, 600, 40], 1152, 640, ints=False)[4] for _ in range(2))

@@ -54,7 +54,7 @@ def test_formulas_against_difference_quotients():
         assert abs((f(x, w + s) - f(x, w - s)) / (2 * eps) - dw[j]) < 1e-7 * (1 + abs(dw[j]))
 
 
-def _layer(T, shared, seed=0):
+def _layer(T, shared, seed=0, fmt="mxfp4"):
     d, t = gi.make_layer("tiny", seed=seed)
     g = torch.Generator().manual_seed(seed + 5)
     t = with_gate_logits(t)
@@ -62,11 +62,26 @@ def _layer(T, shared, seed=0):
     w = {n: t[n].to(DEV) for n in ("w13", "w13_s", "w2", "w2_s")}
     if shared and not sh:  # one more group from the first
         w = {n: torch.cat([v, v[:1].flip(1)]) for n, v in w.items()}
-    layer = moe.MoELayer(d.H, d.I, d.E, d.k, int(shared), *w.values())
+    more = {}
+    if fmt == "nvfp4":  # E4M3 scales of 2^-4 .. 15 per 16, tensor scales around one
+        for n in ("w13_s", "w2_s"):
+            v = torch.randint(24, 80, (*w[n].shape[:2], w[n].shape[2] * 2), generator=g)
+            w[n] = v.to(torch.uint8).to(DEV)
+        G = d.E + int(shared)
+        more = dict(fmt=fmt, w13_gs=(torch.rand(G, 2, generator=g) + 0.5).to(DEV),
+                    w2_gs=(torch.rand(G, generator=g) + 0.5).to(DEV))
+    layer = moe.MoELayer(d.H, d.I, d.E, d.k, int(shared), *w.values(), **more)
     x = torch.randn(T, d.H, generator=g).to(BF).to(DEV)
     logits = torch.randn(T, d.E, generator=g).to(DEV)
     dout = torch.randn(T, d.H, generator=g).to(BF).to(DEV)
     return layer, x, logits, dout
+
+
+def _through(layer, name, dy, off, F):
+    w, w_s = getattr(layer, name), getattr(layer, name + "_s")
+    nv = layer.fmt == "nvfp4"
+    return ref.expert_grad(dy, off, w, w_s, dy.shape[0], F,
+                           getattr(layer, name + "_gs") if nv else None, nv)
 
 
 def _whole(layer, s, dout, dx_in=None, dx_bf16=True):
@@ -84,7 +99,7 @@ def _whole(layer, s, dout, dx_in=None, dx_bf16=True):
         rows[R:] = dout.double()
     wr = torch.ones(Rs, 1, dtype=torch.float64, device=DEV)
     wr[:R, 0] = s["w"].double().view(-1)[perm]
-    dh, size = ref.expert_grad(rows, off, layer.w2, layer.w2_s, Rs, I)
+    dh, size = _through(layer, 'w2', rows, off, I)
     # (with bf16 the weight comes in front of the product and its rounding, in that of dy2)
     e_dh = ref.U16 * dh.abs() + (H / 16 + 1) * 2.0 ** -22 * size
     if "yq" not in s:
@@ -97,9 +112,9 @@ def _whole(layer, s, dout, dx_in=None, dx_bf16=True):
     e_g = (u * sg * (1 + g * (1 - sg))).abs() * wr * e_dh + ref.U16 * dg.abs() + c * scale
     e_u = (g * sg).abs() * wr * e_dh + (ref.U16 + c) * du.abs()
     dy, e_dy = torch.cat([dg, du], 1), torch.cat([e_g, e_u], 1)
-    rows, size = ref.expert_grad(dy, off, layer.w13, layer.w13_s, Rs, H)
+    rows, size = _through(layer, 'w13', dy, off, H)
     e_rows = ref.U16 * rows.abs() + (2 * I / 16 + 1) * 2.0 ** -22 * size
-    e_rows += ref.expert_grad(e_dy, off, layer.w13, layer.w13_s, Rs, H)[1]
+    e_rows += _through(layer, 'w13', e_dy, off, H)[1]
     dx, size = ref.dispatch_bwd(rows, s["inv"], T, k, R, sh, dx_in)
     e_dx = (k + 2) * ref.U32 * size + ref.dispatch_bwd(e_rows, s["inv"], T, k, R, sh)[0]
     if dx_bf16:
@@ -132,8 +147,9 @@ _np = lambda t: t.detach().double().cpu().numpy()  # noqa: E731
 @pytest.mark.parametrize("T", [1, 7, 64, 300, 1500])
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("form", ["fp8", "bf16"])
-def test_layer(T, shared, form):
-    layer, x, logits, dout = _layer(T, shared)
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_layer(T, shared, form, fmt):
+    layer, x, logits, dout = _layer(T, shared, fmt=fmt)
     out, s = layer.forward_train(x, logits, checkpoint=form)
     assert torch.equal(out, layer.forward(x, logits))
     dx, dw = layer.backward(dout, s)
@@ -166,11 +182,8 @@ def test_refusals_of_the_layer():
     layer, x, logits, dout = _layer(4, False)
     with pytest.raises(ValueError, match="checkpoint"):
         layer.forward_train(x, logits, checkpoint="int8")
-    layer.fmt = "nvfp4"
-    with pytest.raises(NotImplementedError):
-        layer.forward_train(x, logits)
-    with pytest.raises(NotImplementedError):
-        layer.backward(dout, {})
+    with pytest.raises(ValueError, match="dx: expected bfloat16 or float32"):
+        layer.backward(dout, layer.forward_train(x, logits)[1], dx=torch.empty_like(dout).half())
 
 
 @pytest.mark.gpu

@@ -45,6 +45,9 @@ def test_dims_are_refused_by_every_call(lib, bad):
     for f in (lib.moe_grouped_gemm_w2_backward, lib.moe_grouped_gemm_w13_backward):
         assert f(d, A, A, A, A, A, A, 1 << 30, None) == SHAPE
         assert f(None, A, A, A, A, A, A, 1 << 30, None) == SHAPE
+    for f in (lib.moe_grouped_gemm_w2_backward_nvfp4, lib.moe_grouped_gemm_w13_backward_nvfp4):
+        assert f(d, A, A, A, A, A, A, A, 1 << 30, None) == SHAPE
+        assert f(None, A, A, A, A, A, A, A, 1 << 30, None) == SHAPE
 
 
 def test_weights_past_the_tiles_row_coordinates_are_refused(lib):
@@ -127,6 +130,23 @@ def test_gradient_product_refusals(lib, name):
     assert f(*_with(good, 3, P(0x10010))) == ARG                 # codes: 32 bytes
     assert f(*_with(good, 6, P(0x10080))) == ARG                 # the workspace: 256
     assert f(*_with(good, 7, size - 1)) == SMALL
+
+
+@pytest.mark.parametrize("name", ["moe_grouped_gemm_w2_backward_nvfp4",
+                                  "moe_grouped_gemm_w13_backward_nvfp4"])
+def test_nvfp4_gradient_product_refusals(lib, name):
+    f, d = getattr(lib, name), _d(I=256)
+    size = lib.moe_gemm_backward_workspace_size(d)
+    good = [d, A, A, A, A, A, A, A, size, None]  # d dy offsets w w_s gs dx ws bytes stream
+    for bad in (dict(), dict(H=384, I=256), dict(H=256, I=384)):  # whole 256s
+        assert f(*_with(good, 0, _d(**bad))) == SHAPE
+    for i in (1, 2, 3, 4, 6, 7):
+        assert f(*_with(good, i, None)) == ARG
+    for i in (1, 3, 4, 6, 7):
+        assert f(*_with(good, i, BAD)) == ARG
+    for i in (2, 5):
+        assert f(*_with(good, i, ODD)) == ARG
+    assert f(*_with(good, 8, size - 1)) == SMALL
 
 
 def test_binding_refuses_host_tensors_types_and_shapes():
