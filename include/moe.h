@@ -507,9 +507,9 @@ int moe_linear_backward(const moe_linear_desc* d, const uint16_t* x, const uint1
  * the experts' 4-bit weights as they are: they have no gradient of their own.  The same
  * conventions.  The FP8 quantisations pass their gradient straight through.  In order:
  *     moe_dispatch           dout's tokens to their packed rows         [Rs][H]
- *     _w2_backward           dh = dout W2, unweighted                   [Rs][I]
+ *     _w2_backward(_nvfp4)   dh = dout W2, unweighted                   [Rs][I]
  *     moe_swiglu_backward    dy13 (with the combine weights), and dw    [Rs][2I]
- *     _w13_backward          dxp = dy13 W13                             [Rs][H]
+ *     _w13_backward(_nvfp4)  dxp = dy13 W13                             [Rs][H]
  *     moe_dispatch_backward  dx                                         [T][H]
  * dw then goes to moe_balance_loss_backward.  Where y2 was kept, moe_combine_backward takes
  * the first step's place, with the weights applied and dw. */

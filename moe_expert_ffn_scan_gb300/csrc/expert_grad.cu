@@ -1,13 +1,14 @@
-// Gradient products of the MXFP4 experts: for every packed row r of group g
+// Gradient products of the experts: for every packed row r of group g
 //     dx[r][f] = sum_c dy[r][c] * deq(w[g])[c][f]
-// with w [G][C][F/2] (E2M1 codes) and scales [G][C][F/32] as the forward has them: W2 is
-// [H][I] (C = H, F = I), W13 [2I][H] (C = 2I, F = H).
+// with codes w [G][C][F/2] (E2M1) and scales [G][C][F/32] (MXFP4) or [G][C][F/16] (NVFP4) as the
+// forward has them: W2 is [H][I] (C = H, F = I), W13 [2I][H] (C = 2I, F = H).
 //
-// The contraction runs over the weight's ROWS, so its scales (one per 32 elements of a row)
-// lie along the output axis: the block-scaled MMA kinds, whose scales go along the
+// The contraction runs over the weight's ROWS, so its scales (one per 32 or 16 elements of a
+// row) lie along the output axis: the block-scaled MMA kinds, whose scales go along the
 // contraction, cannot apply them, and a transposed copy would be a second set of weights.  The
-// kernel multiplies in bf16 instead: E2M1 times a power of two is exact there (2 significant
-// bits), dy is bf16 as it comes, the products are exact in fp32 and are summed in fp32.
+// kernel multiplies in bf16 instead: E2M1 times a power of two or an E4M3 scale is exact there (2
+// or 6 significant bits), dy is bf16 as it comes, the products are exact in fp32 and are summed in
+// fp32; NVFP4's tensor scales multiply the sums.
 //
 // The codes become bf16 straight in tensor memory, the MMA's A operand: the features are its M
 // side, one per TMEM lane.  The weights lie with the features contiguous, so a transpose is
@@ -23,10 +24,10 @@
 //     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
 //     of the shared-memory traffic for dy that a tile of its own would.  Bound by the tensor
 //     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 511 us, 1.88 PFLOP/s; in long runs by the
-//     power cap, 1.6 to 1.7.
+//     power cap, 1.6 to 1.7.  (NVFP4's W13 keeps two sums, so 128 rows: 755 us, 1.27.)
 //   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
 //     weights' way from HBM and their conversion are the work.  Bound by the conversion's
-//     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s.
+//     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s (NVFP4 134, 4.0).
 // In each CTA, a stage at a time:
 //   * warp 2 brings the codes of 128 weight rows x 128 features (8 KB, TMA) and their scales
 //     (cp.async) into a ring, so that many stages of the weights are on their way;
