@@ -166,6 +166,40 @@ def test_layer(T, shared, form, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [7, 400])
+def test_full_size_layer_on_sampled_tokens(T):
+    """384 experts of 7168 x 2048, top-8 and shared, uneven popularity; whole tokens in float64.
+    Four roundings to bf16 on dx's way (dh, dy13, the rows, dx), each of at most 2^-8 of its
+    values in norm, one on dw's."""
+    H, I, E, k = 7168, 2048, 384, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ri = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=DEV, dtype=torch.uint8)  # noqa: E731
+    layer = moe.MoELayer(H, I, E, k, 1, ri(0, 256, E + 1, 2 * I, H // 2),
+                         ri(114, 119, E + 1, 2 * I, H // 32), ri(0, 256, E + 1, H, I // 2),
+                         ri(114, 119, E + 1, H, I // 32))
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    x, dout, logits = rn(T, H).to(BF), rn(T, H).to(BF), rn(T, E) + 2 * rn(E)
+    s = layer.forward_train(x, logits)[1]
+    dx, dw = layer.backward(dout, s)
+    assert [moe.moe_check_status(w) for w in layer.train_workspaces(T)] == [0, 0]
+    assert torch.all(torch.isfinite(dx.float())) and torch.all(torch.isfinite(dw))
+    for t in (0, T // 2, T - 1):
+        rows, experts = s["inv"][t * k:(t + 1) * k].tolist() + [T * k + t], s["idx"][t].tolist() + [E]
+        weights, want, wdw = s["w"][t].tolist() + [1.0], 0, []
+        for r, e, w in zip(rows, experts, weights):
+            dh = dout[t].double() @ ref.mxfp4(layer.w2[e], layer.w2_s[e])
+            y = ref.fp8_values(s["yq"][r:r + 1], s["ys"][r:r + 1])[0]
+            h = ref.fp8_values(s["hq"][r:r + 1], s["hs"][r:r + 1])[0]
+            wdw.append((dh * h).sum())
+            dg, du, _ = ref.swiglu_bwd(y[:I], y[I:], w * dh)
+            want = want + torch.cat([dg, du]) @ ref.mxfp4(layer.w13[e], layer.w13_s[e])
+        assert (dx[t].double() - want).norm() <= 4 * ref.U16 * want.norm()
+        wdw = torch.stack(wdw[:k])
+        # (dw's terms of random signs: the sum's error against the largest of the token's)
+        assert torch.all((dw[t].double() - wdw).abs() <= 4 * ref.U16 * wdw.abs().max())
+
+
+@pytest.mark.gpu
 def test_the_two_checkpoints_agree():
     """The 8-bit checkpoint's rounding (half a step: 2^-4) is in dx of one and not the other, its
     sign random from value to value."""
