@@ -24,7 +24,7 @@
 //     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
 //     of the shared-memory traffic for dy that a tile of its own would.  Bound by the tensor
 //     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 511 us, 1.88 PFLOP/s; in long runs by the
-//     power cap, 1.6 to 1.7.  (NVFP4's W13 keeps two sums, so 128 rows: 755 us, 1.27.)
+//     power cap, 1.6 to 1.7.  (NVFP4's W13, whose halves have a scale each: 542 us, 1.77.)
 //   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
 //     weights' way from HBM and their conversion are the work.  Bound by the conversion's
 //     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s (NVFP4 134, 4.0).
@@ -54,7 +54,11 @@ constexpr int kFeat = 128;       // features per CTA
 constexpr int kMaxGroups = 1025;
 
 // Weight formats: MXFP4, and NVFP4 with one tensor scale for all of a weight's rows or one for
-// each half of them (W13's gate and up projection), whose sums are kept apart until the end.
+// each half of them (W13's gate and up projection).  The halves' sums are kept apart until the
+// end where tensor memory has room for two: up to 32 rows, or 128 of a pair.  In a pair's tile of
+// more rows the half of the smaller scale is summed first, that sum is then multiplied in place by
+// the scales' quotient, and the other half added to it (w13 of 7168 x 2048, 32 groups of 256 rows:
+// 287 us, by two tiles of 128 rows 388; 16 groups of 1024: 542, 758).
 enum Format { kMx = 0, kNv = 1, kNvHalves = 2 };
 
 template <int P, int F>
@@ -70,8 +74,12 @@ struct Cfg {
   static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
   static constexpr int kGroups = 3;                   // converter groups of four warps
   static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
-  static constexpr int kSums = F == kNvHalves ? 2 : 1;          // of a tile
-  static constexpr int kRowsMax = P == 2 ? 256 / kSums : 32;    // rows per tile
+  static constexpr int kSums = F == kNvHalves && P == 1 ? 2 : 1;  // of a tile
+  static constexpr bool kHalves = F == kNvHalves && P == 2;
+  // parts of the contraction, in loops of their own: of the loads, of the sums
+  static constexpr int kLoads = kHalves ? 2 : 1, kParts = F == kNvHalves ? 2 : 1;
+  static constexpr int kTwoMax = F != kNvHalves ? 0 : P == 2 ? 128 : 32;  // rows that have two
+  static constexpr int kRowsMax = P == 2 ? 256 : 32;  // rows per tile
   static constexpr int kUnit = 16 * P;                // its N is a multiple of this
   static constexpr int kBox = kRowsMax / P, kBoxSmall = P == 2 ? 32 : 16;  // rows a TMA load
   static constexpr int kAcc = P == 2 ? 1 : 2 / kSums; // accumulators (each of kSums sums)
@@ -85,8 +93,9 @@ struct Cfg {
   static constexpr int kOffScale = kOffRaw + kRaw * kRawCodes;
   static constexpr int kOffFactor = kOffScale + kRaw * kRawScales;
   static constexpr int kOffBar = kOffFactor + kRaw * kFactors;
-  // full, empty [St], raw_full, raw_empty, fac_full [R], acc_full, acc_empty [2], drain
-  static constexpr int kOffMisc = kOffBar + (2 * kSt + 3 * kRaw + 5) * 8;
+  // full, empty [St], raw_full, raw_empty, fac_full [R], acc_full, acc_empty [2], drain, half,
+  // scaled
+  static constexpr int kOffMisc = kOffBar + (2 * kSt + 3 * kRaw + 7) * 8;
   static constexpr int kOffGroups = kOffMisc + 16;  // tmem slot, abort flag; then off[], first[]
   static constexpr int kSmem = kOffGroups + 2 * (kMaxGroups + 1) * 4 + kThreads / 32 * 4;
   static_assert(kTmemA + kSt * kACols <= kTmemCols, "tensor memory");
@@ -96,7 +105,7 @@ struct Cfg {
 struct GradParams {
   const int32_t* offsets;
   const uint8_t* scales;
-  const float* gs;  // NVFP4: [G][kSums] tensor scales, or null (1)
+  const float* gs;  // NVFP4: [G] or, for two halves, [G][2] tensor scales; null: 1
   uint16_t* dx;
   int G, rows, C, F;
   uint32_t* status;
@@ -260,7 +269,7 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A tile's scales, kBK weight rows a stage: lane l has rows l, l + 32, ...  Of each row the CTA's
+// A tile's scales, from weight row c (of all groups) on, kBK a stage: lane l has rows l, l + 32, ...  Of each row the CTA's
 // four or eight bytes are loaded with the aligned 16 around them (which end inside the tensor: its
 // size is a multiple of 512 bytes), because copies of 16 bytes pass L1 by: with 4 bytes a row 32 groups
 // of one row took 158 us in place of 132.  Their arrival counts on the stage's barrier.
@@ -269,9 +278,9 @@ struct ScaleLoad {
   const uint8_t* at;
   size_t row;
   bool there;  // (a pair's second half may lie past the last feature)
-  __device__ __forceinline__ ScaleLoad(const GradParams& p, const GradTile& t, int f0, int lane)
+  __device__ __forceinline__ ScaleLoad(const GradParams& p, int c, int f0, int lane)
       : row(p.F / Cfg<P, F>::kBlock), there(f0 < p.F) {
-    at = p.scales + (static_cast<size_t>(t.g) * p.C + lane) * row + f0 / Cfg<P, F>::kBlock;
+    at = p.scales + (static_cast<size_t>(c) + lane) * row + f0 / Cfg<P, F>::kBlock;
   }
   __device__ __forceinline__ void stage(uint8_t* to, uint64_t* bar, int lane) {
     if (there) {
@@ -301,6 +310,26 @@ __device__ __forceinline__ uint32_t factor_e4m3(uint32_t lo_hi) {
 }
 constexpr float kNvShort = 128.f;
 
+// The halves of a group's contraction in the order of their tensor scales' magnitudes, so that the
+// quotient overflows nowhere: last * (quotient * first sum + second sum).
+struct Halves {
+  bool swap;  // the second half first
+  float quotient, last;
+  __device__ __forceinline__ Halves(const float* gs, int g) {
+    const float a = gs ? __ldg(gs + 2 * g) : 1.f, b = gs ? __ldg(gs + 2 * g + 1) : 1.f;
+    swap = fabsf(a) > fabsf(b);
+    last = swap ? a : b;
+    quotient = last == 0.f ? 0.f : (swap ? b : a) / last;
+  }
+};
+template <int P, int F>
+__device__ __forceinline__ bool rescaled(const GradTile& t) {
+  return Cfg<P, F>::kHalves && t.rows > Cfg<P, F>::kTwoMax;
+}
+template <int P, int F>
+__device__ __forceinline__ bool swapped(const GradParams& p, const GradTile& t) {
+  return Cfg<P, F>::kHalves && Halves(p.gs, t.g).swap;
+}
 template <int P, int F>
 __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     k_expert_grad(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
@@ -317,6 +346,8 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
   uint64_t* acc_full = fac_full + C::kRaw;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
+  uint64_t* half = drain + 1;   // of a rescaled tile the first half is summed,
+  uint64_t* scaled = half + 1;  // and multiplied
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   int* off = reinterpret_cast<int*>(smem + C::kOffGroups);
@@ -339,6 +370,8 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
       mbar_init(&acc_empty[b], C::kEpi * P);
     }
     mbar_init(drain, 1);
+    mbar_init(half, 1);
+    mbar_init(scaled, C::kEpi * P);
     const bool bad = (smem_u32(smem) & 1023u) != 0;
     *abort_flag = bad ? 1 : 0;
     if (bad) set_status(p.status, STATUS_BAD_PLAN);
@@ -397,7 +430,8 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P), nk = p.C / kBK;
+  const int f_tiles = (p.F + kFeat * P - 1) / (kFeat * P);
+  const int nk = p.C / kBK;  // stages
   const long long total = *abort_flag ? 0 : static_cast<long long>(first[G]) * f_tiles;
   const int cl = blockIdx.x / P, ncl = gridDim.x / P;
   auto leader_addr = [&](const uint64_t* b) -> uint32_t { return mapa_shared(smem_u32(b), 0); };
@@ -416,23 +450,28 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
       const int box = small ? C::kBoxSmall : C::kBox, boxes = (mine + box - 1) / box;
       const CUtensorMap* map = small ? &tmBs : &tmB;
       const uint32_t bytes = P * boxes * box * kBK * 2;
-      for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
-        if (st.round) ok = mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);  // (the lanes part only together)
-        if (!ok) break;
-        uint8_t* b = smem + st.s * C::kBBytes;
-        if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(&full[st.s], bytes);
+      const bool swap = swapped<P, F>(p, t);
+      for (int part = 0; part < C::kLoads; ++part) {
+        int c = (part != 0) != swap ? p.C / 2 : 0;
+        for (int kb = 0; kb < nk / C::kLoads; ++kb, c += kBK, ++issued, st.next()) {
+          if (st.round) ok = mbar_wait(&empty[st.s], st.phase ^ 1u, p.status, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);  // (the lanes part only together)
+          if (!ok) break;
+          uint8_t* b = smem + st.s * C::kBBytes;
+          if (elect_one()) {
+            if (leader) mbar_arrive_expect_tx(&full[st.s], bytes);
 #pragma unroll
-          for (int h = 0; h < kBK / 64; ++h)  // 64 c, one 128-byte swizzle row, each
-            for (int i = 0; i < boxes; ++i) {
-              uint8_t* to = b + (h * (C::kRowsMax / P) + i * box) * 128;
-              if (P == 2)
-                tma_load_2d_pair(to, map, bar0 + st.s * 8, kb * kBK + h * 64, row0 + i * box);
-              else
-                tma_load_2d(to, map, &full[st.s], kb * kBK + h * 64, row0 + i * box);
-            }
+            for (int h = 0; h < kBK / 64; ++h)  // 64 c, one 128-byte swizzle row, each
+              for (int i = 0; i < boxes; ++i) {
+                uint8_t* to = b + (h * (C::kRowsMax / P) + i * box) * 128;
+                if (P == 2)
+                  tma_load_2d_pair(to, map, bar0 + st.s * 8, c + h * 64, row0 + i * box);
+                else
+                  tma_load_2d(to, map, &full[st.s], c + h * 64, row0 + i * box);
+              }
+          }
         }
+        if (!ok) break;
       }
     }
     // after an abort: the loads still in flight (all counted on the first CTA's barriers)
@@ -445,7 +484,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     // ---------------------------------------------------------------- MMA
     if (leader) {
       Ring<C::kSt> st;
-      uint32_t tc = 0;
+      uint32_t tc = 0, rescales = 0;
       bool ok = true;
       // (of a descriptor only the address, the low 14 bits, moves)
       const uint64_t db0 = smem_desc(smem_u32(smem), 0, 1024, kLayoutSw128);
@@ -459,27 +498,38 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d0 = tmem + b * C::kAccCols;
-        for (int kb = 0; kb < nk; ++kb, st.next()) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st.s], st.phase, p.status, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-          const bool second = C::kSums == 2 && kb >= nk / 2;
-          const uint32_t d = d0 + (second ? C::kRowsMax : 0);
-          const int k0 = second ? nk / 2 : 0;  // the sum's first stage
-          const uint32_t at = tmem + C::kTmemA + st.s * C::kACols;
-          const uint32_t db = static_cast<uint32_t>(db0) + st.s * (C::kBBytes / 16);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t dk = (db0 >> 32) << 32 |
-                                  (db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2);
-              if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, kb > k0 || kk > 0);
-              else mma_bf16_ts(d, at + kk * 8, dk, idesc, kb > k0 || kk > 0);
-            }
-            if (P == 2) tc_commit_pair_mc(&empty[st.s], 3);
-            else tc_commit(&empty[st.s]);
+        const bool twice = rescaled<P, F>(t), two = C::kTwoMax && !twice;
+        for (int part = 0; part < C::kParts; ++part) {
+          if (part && twice) {
+            if (elect_one()) tc_commit_pair_mc(half, 3);
+            __syncwarp();
+            ok = mbar_wait(scaled, rescales++ & 1u, p.status, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
           }
-          __syncwarp();
+          const uint32_t d = d0 + (part && two ? C::kTwoMax : 0);
+          const bool add = part && twice;
+          for (int kb = 0; kb < nk / C::kParts; ++kb, st.next()) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st.s], st.phase, p.status, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t at = tmem + C::kTmemA + st.s * C::kACols;
+            const uint32_t db = static_cast<uint32_t>(db0) + st.s * (C::kBBytes / 16);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                const uint64_t dk = (db0 >> 32) << 32 |
+                                    (db + kk / 4 * (C::kRowsMax / P * 128 / 16) + kk % 4 * 2);
+                if (P == 2) mma_bf16_ts_pair(d, at + kk * 8, dk, idesc, add || kb > 0 || kk > 0);
+                else mma_bf16_ts(d, at + kk * 8, dk, idesc, add || kb > 0 || kk > 0);
+              }
+              if (P == 2) tc_commit_pair_mc(&empty[st.s], 3);
+              else tc_commit(&empty[st.s]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
         }
         if (ok && elect_one()) {
           if (P == 2) tc_commit_pair_mc(&acc_full[b], 3);
@@ -504,18 +554,22 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     for (long long L = cl; L < total && ok; L += ncl) {
       const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const int f0 = t.f0 + static_cast<int>(rank) * kFeat;
-      ScaleLoad<P, F> sc(p, t, f0, lane);
-      for (int kb = 0; kb < nk; ++kb, ++issued, st.next()) {
-        if (st.round) ok = mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&raw_full[st.s], C::kRawCodes);
-          tma_load_2d(smem + C::kOffRaw + st.s * C::kRawCodes, &tmW, &raw_full[st.s], f0 / 2,
-                      t.g * p.C + kb * kBK);
+      const bool swap = swapped<P, F>(p, t);
+      for (int part = 0; part < C::kLoads; ++part) {
+        int c = t.g * p.C + ((part != 0) != swap ? p.C / 2 : 0);  // of all the groups' weight rows
+        ScaleLoad<P, F> sc(p, c, f0, lane);
+        for (int kb = 0; kb < nk / C::kLoads; ++kb, c += kBK, ++issued, st.next()) {
+          if (st.round) ok = mbar_wait(&raw_empty[st.s], st.phase ^ 1u, p.status, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&raw_full[st.s], C::kRawCodes);
+            tma_load_2d(smem + C::kOffRaw + st.s * C::kRawCodes, &tmW, &raw_full[st.s], f0 / 2, c);
+          }
+          __syncwarp();
+          sc.stage(smem + C::kOffScale + st.s * C::kRawScales, &raw_full[st.s], lane);
         }
-        __syncwarp();
-        sc.stage(smem + C::kOffScale + st.s * C::kRawScales, &raw_full[st.s], lane);
+        if (!ok) break;
       }
     }
     cp_async_wait_all();
@@ -658,21 +712,61 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     // P = 2: one accumulator, so the sums are first all taken to registers (eight warps, two
-    // for the same lanes with half of the rows each) and stored under the next tile's MMAs.
+    // for the same lanes with a part of the tile's rows each) and stored under the next tile's MMAs.
     const int q = warp & 3;
     constexpr int kCols = P == 2 ? C::kRowsMax / (C::kEpi / 4) : 16;
-    uint32_t tc = 0;
+    uint32_t tc = 0, rescales = 0;
     for (long long L = cl; L < total; L += ncl, ++tc) {
       const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
+      // the warp's rows of the tile (columns of the sums)
+      const int part = P == 2 ? (t.rows + 31) / 32 * 16 : t.rows;
+      const int c0 = P == 2 ? ((warp - 4) >> 2) * part : 0;
+      const int own = t.rows - c0 < part ? t.rows - c0 : part;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAccCols + c0;
       int w_ok = 1;
+      float gs0 = 1.f, gs1 = 1.f;
+      const bool twice = rescaled<P, F>(t);
+      if (C::kHalves) {  // the first sum times the quotient, plus the second if that is apart
+        const Halves h(p.gs, t.g);
+        gs0 = kNvShort * h.last;
+        if (lane == 0) {
+          if (twice) w_ok = mbar_wait(half, rescales & 1u, p.status, abort_flag);
+          else w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
+        }
+        rescales += twice;
+        if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < own; c += 8) {
+          uint32_t x[8], y[8] = {};
+          tmem_ld_32x32b_x8(acc + c, x);
+          if (!twice) tmem_ld_32x32b_x8(acc + C::kTwoMax + c, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i] = __float_as_uint(
+                fmaf(h.quotient, __uint_as_float(x[i]), __uint_as_float(y[i])));
+          tmem_st_32x32b_x8(acc + c, x);
+        }
+        tmem_st_wait();
+        if (twice) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (!leader) mbar_arrive_other(leader_addr(scaled));
+            else mbar_arrive(scaled);
+          }
+        }
+      } else if (F != kMx) {
+        gs0 = kNvShort * (p.gs ? __ldg(p.gs + t.g * C::kSums) : 1.f);
+        if (C::kSums == 2) gs1 = kNvShort * (p.gs ? __ldg(p.gs + t.g * 2 + 1) : 1.f);
+      }
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
       tc_fence_after();
-      const int c0 = P == 2 ? ((warp - 4) >> 2) * kCols : 0;
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAccCols + c0;
       const int f = t.f0 + static_cast<int>(rank) * kFeat + q * 32;
-      const int rows = f < p.F ? t.rows - c0 : 0;
+      const int rows = f < p.F ? own : 0;
       uint16_t* out = p.dx + static_cast<size_t>(t.row0 + c0 + (lane >> 3)) * p.F + f + 4 * (lane & 7);
       auto release = [&] {
         tc_fence_before();
@@ -682,11 +776,6 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
           else mbar_arrive(&acc_empty[b]);
         }
       };
-      float gs0 = 1.f, gs1 = 1.f;
-      if (F != kMx) {
-        gs0 = kNvShort * (p.gs ? __ldg(p.gs + t.g * C::kSums) : 1.f);
-        if (C::kSums == 2) gs1 = kNvShort * (p.gs ? __ldg(p.gs + t.g * 2 + 1) : 1.f);
-      }
       uint32_t v[kCols / 2];  // two rows a register
       for (int r0 = 0; r0 < (P == 2 ? 1 : rows); r0 += kCols) {
 #pragma unroll
@@ -696,7 +785,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
             tmem_ld_32x32b_x8(acc + r0 + c, x);
             if (C::kSums == 2) {
               uint32_t y[8];
-              tmem_ld_32x32b_x8(acc + C::kRowsMax + r0 + c, y);
+              tmem_ld_32x32b_x8(acc + C::kTwoMax + r0 + c, y);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
