@@ -23,19 +23,19 @@
 //   * P = 2, SM pairs (cta_group::2 MMAs of M = 256): 256 features x up to 256 rows of one group.
 //     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
 //     of the shared-memory traffic for dy that a tile of its own would.  Bound by the tensor
-//     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 511 us, 1.88 PFLOP/s; in long runs by the
-//     power cap, 1.6 to 1.7.  (NVFP4's W13, whose halves have a scale each: 542 us, 1.77.)
+//     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 496 us, 1.94 PFLOP/s; in long runs by the
+//     power cap, 1.6 to 1.7.  (NVFP4's W13, whose halves have a scale each: 534 us, 1.80.)
 //   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
 //     weights' way from HBM and their conversion are the work.  Bound by the conversion's
-//     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s (NVFP4 134, 4.0).
+//     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s (NVFP4 126, 4.3).
 // In each CTA, a stage at a time:
 //   * warp 2 brings the codes of 128 weight rows x 128 features (8 KB, TMA) and their scales
 //     (cp.async) into a ring, so that many stages of the weights are on their way;
-//   * warp 3 makes the scales what the converters multiply by;
+//   * warp 3, of NVFP4 with the last warp, makes the scales what the converters multiply by;
 //   * three groups of four converter warps, a stage each in turn; a warp has 32 features, so
-//     one scale a row (its wait on warp 3's word covers the codes too: warp 3 waited for both);
+//     one scale a row (its wait on the factors covers the codes too: warp 3 waited for both);
 //   * warp 0 brings dy's rows (K-major, TMA), warp 1 (of the pair's first CTA) issues the MMAs;
-//   * four or eight warps store the sums of the last tile under the next one's MMAs.
+//   * four or twelve warps store the sums of the last tile under the next one's MMAs.
 // Persistent; every CTA finds its tiles from the group offsets by itself (no plan kernel).
 // Every wait is bounded; one that expires sets the workspace's status word.
 #include "grad.cuh"
@@ -58,7 +58,7 @@ constexpr int kMaxGroups = 1025;
 // end where tensor memory has room for two: up to 32 rows, or 128 of a pair.  In a pair's tile of
 // more rows the half of the smaller scale is summed first, that sum is then multiplied in place by
 // the scales' quotient, and the other half added to it (w13 of 7168 x 2048, 32 groups of 256 rows:
-// 287 us, by two tiles of 128 rows 388; 16 groups of 1024: 542, 758).
+// 279 us, by two tiles of 128 rows 388; 16 groups of 1024: 534, 758).
 enum Format { kMx = 0, kNv = 1, kNvHalves = 2 };
 
 template <int P, int F>
@@ -71,9 +71,16 @@ struct Cfg {
   // The scales of a stage as the converters multiply by them: [32 c][block of the features]
   // [lane % 4][register of ldmatrix], two bf16 each; behind them, whether a byte is above 128.
   static constexpr int kFactors = kBK * 2 * (kFeat / kBlock) + 16;
-  static constexpr int kEpi = P == 2 ? 8 : 4;         // epilogue warps
+  // Epilogue warps.  A pair's hold a tile's sums in registers: of eight warps with 128 rows each these
+  // were too many, and spilled ones go to L2, as shared memory leaves hardly any L1 (w13 of
+  // 7168 x 2048, 32 groups of 64, 128, 192 rows: 174, 195, 217 us in place of 167, 187, 209).
+  static constexpr int kEpi = P == 2 ? 12 : 4;
   static constexpr int kGroups = 3;                   // converter groups of four warps
-  static constexpr int kThreads = 32 * (4 + kEpi + 4 * kGroups);
+  // Warps that make factors: NVFP4's are twice as many and take a conversion each (32 groups of
+  // 64 rows, w13 by one warp 206 us, without their work 178, by two 184; w2 117, 103).
+  static constexpr int kScalers = F == kMx ? 1 : 2;
+  static constexpr int kConv0 = 4 + kEpi, kScaler1 = kConv0 + 4 * kGroups;  // warps
+  static constexpr int kThreads = 32 * (kScaler1 + kScalers - 1);
   static constexpr int kSums = F == kNvHalves && P == 1 ? 2 : 1;  // of a tile
   static constexpr bool kHalves = F == kNvHalves && P == 2;
   // parts of the contraction, in loops of their own: of the loads, of the sums
@@ -311,7 +318,8 @@ __device__ __forceinline__ uint32_t factor_e4m3(uint32_t lo_hi) {
 constexpr float kNvShort = 128.f;
 
 // The halves of a group's contraction in the order of their tensor scales' magnitudes, so that the
-// quotient overflows nowhere: last * (quotient * first sum + second sum).
+// quotient overflows nowhere: last * (quotient * first sum + second sum).  (Of scales more than
+// 2^126 apart the smaller one's half is lost.)
 struct Halves {
   bool swap;  // the second half first
   float quotient, last;
@@ -363,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(&raw_full[s], 1 + 32);
       mbar_init(&raw_empty[s], 4);
-      mbar_init(&fac_full[s], 1);
+      mbar_init(&fac_full[s], C::kScalers);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -579,10 +587,11 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
       for (uint32_t i = from; i < issued; ++i)
         mbar_wait_drain(&raw_full[i % C::kRaw], (i / C::kRaw) & 1u);
     }
-  } else if (warp == 3) {
+  } else if (warp == 3 || warp >= C::kScaler1) {
     // ---------------------------------------------------------------- factors
     // lane l has c = 2 l, 2 l + 1 of every 64: a bf16 factor each for every block of features,
-    // of an E8M0 byte s 2^(s - 127 + 126)
+    // of an E8M0 byte s 2^(s - 127 + 126); of two warps each has every other 64
+    const int h0 = C::kScalers > 1 && warp != 3;
     constexpr int kBlocks = kFeat / C::kBlock, kOwn = kBlocks;  // bytes a row
     Ring<C::kRaw> st;
     bool ok = true;
@@ -598,7 +607,8 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
         if (!ok) break;
         uint32_t over = 0;
 #pragma unroll
-        for (int h = 0; h < kBK / 64; ++h) {
+        for (int i = 0; i < kBK / 64 / C::kScalers; ++i) {
+          const int h = h0 + i * C::kScalers;
           // (64 rows further the bytes' place in their 16 is the same)
           const int at = st.s * C::kRawScales + h * 1024;
           uint32_t* out = to + st.s * (C::kFactors / 4) + h * (kBlocks * 32);
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
           }
         }
         const bool any = __any_sync(0xFFFFFFFFu, (over & 0x80808080u) != 0);
-        if (lane == 0) {
+        if (F == kMx && lane == 0) {
           *reinterpret_cast<uint32_t*>(smem + C::kOffFactor + st.s * C::kFactors + C::kFactors - 16) =
               any;
         }
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
         if (lane == 0) mbar_arrive(&fac_full[st.s]);
       }
     }
-  } else if (warp >= 4 + C::kEpi) {
+  } else if (warp >= C::kConv0) {
     // ---------------------------------------------------------------- converters
     const int q = warp & 3;  // its features' quarter, and TMEM lanes
     // (64-byte swizzle: eight rows' 16-byte chunks fall on all the banks)
@@ -641,7 +651,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     const uint32_t dst = tmem + (static_cast<uint32_t>(q * 32) << 16) + C::kTmemA;
     const uint32_t tiles = cl < total ? static_cast<uint32_t>((total - cl + ncl - 1) / ncl) : 0;
     const unsigned long long end = static_cast<unsigned long long>(tiles) * nk;
-    const uint32_t group = (warp - 4 - C::kEpi) >> 2;
+    const uint32_t group = (warp - C::kConv0) >> 2;
     const uint32_t full0 = P == 2 ? leader_addr(&full[0]) : 0;
     Ring<C::kSt, C::kGroups> ra(group);
     Ring<C::kRaw, C::kGroups> rr(group);
@@ -711,16 +721,17 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
     }
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
-    // P = 2: one accumulator, so the sums are first all taken to registers (eight warps, two
+    // P = 2: one accumulator, so the sums are first all taken to registers (twelve warps, three
     // for the same lanes with a part of the tile's rows each) and stored under the next tile's MMAs.
     const int q = warp & 3;
-    constexpr int kCols = P == 2 ? C::kRowsMax / (C::kEpi / 4) : 16;
+    constexpr int kShares = P == 2 ? C::kEpi / 4 : 1;
+    constexpr int kCols = P == 2 ? (C::kRowsMax + kShares * 8 - 1) / (kShares * 8) * 8 : 16;
     uint32_t tc = 0, rescales = 0;
     for (long long L = cl; L < total; L += ncl, ++tc) {
       const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const uint32_t b = tc % C::kAcc, use = tc / C::kAcc;
       // the warp's rows of the tile (columns of the sums)
-      const int part = P == 2 ? (t.rows + 31) / 32 * 16 : t.rows;
+      const int part = P == 2 ? (t.rows + kShares * 8 - 1) / (kShares * 8) * 8 : t.rows;
       const int c0 = P == 2 ? ((warp - 4) >> 2) * part : 0;
       const int own = t.rows - c0 < part ? t.rows - c0 : part;
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAccCols + c0;
@@ -776,7 +787,8 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
           else mbar_arrive(&acc_empty[b]);
         }
       };
-      uint32_t v[kCols / 2];  // two rows a register
+      // two rows a register (without the zeros they count as live from tile to tile)
+      uint32_t v[kCols / 2] = {};
       for (int r0 = 0; r0 < (P == 2 ? 1 : rows); r0 += kCols) {
 #pragma unroll
         for (int c = 0; c < kCols; c += 8) {
