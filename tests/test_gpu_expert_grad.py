@@ -232,6 +232,32 @@ def test_nvfp4_every_scale_byte():
     assert torch.equal(dx[rest].float(), want[rest].float())
 
 
+PAIRS = [(1.0, 0.375), (0.375, 1.0), (-3.0, 0.5), (0.5, -3.0), (0.0, 2.5), (2.5, 0.0), (0.0, 0.0),
+         (2.0 ** -60, 1.5), (1.5, 2.0 ** -60), (3e30, 1e30), (1e-30, 3e-30)]
+
+
+@pytest.mark.parametrize("H,I", [(256, 256), (1280, 2048)])
+@pytest.mark.parametrize("rows", [1, 31, 128, 129, 200, 257])
+def test_nvfp4_w13_halves_of_any_scales(H, I, rows):
+    """Tensor scales of either order, sign and size, and none: one or two sums a tile.  Besides the
+    sums' steps: the quotient, its product and that with the last scale round once each."""
+    g = torch.Generator(device=DEV).manual_seed(rows + H)
+    G, C, F = len(PAIRS), 2 * I, H
+    off = torch.arange(G + 1, dtype=I32, device=DEV) * rows
+    dy = torch.randn(G * rows, C, generator=g, device=DEV).to(BF)
+    w = torch.randint(0, 256, (G, C, F // 2), generator=g, device=DEV).to(U8)
+    w_s = torch.randint(1, 120, (G, C, F // 16), generator=g, device=DEV).to(U8)
+    t = torch.tensor(PAIRS, device=DEV)
+    dx = torch.full((G * rows, F), 7.0, dtype=BF, device=DEV)
+    d = moe.dims(G * rows, H, I, G, 1, 0)
+    ws = moe.alloc_workspace(moe.gemm_backward_workspace_size(d))
+    moe.moe_grouped_gemm_w13_backward_nvfp4(d, dy, off, w, w_s, t, dx, ws)
+    assert moe.moe_check_status(ws) == 0
+    want, size = ref.expert_grad(dy, off, w, w_s, G * rows, F, t, True)
+    tol = ref.U16 * want.abs() + (C / 16 + 3) * 2.0 ** -22 * size
+    assert torch.all((dx.double() - want).abs() <= tol)
+
+
 @pytest.mark.parametrize("which", ["w2", "w13"])
 def test_outputs_are_the_same_in_every_run(which):
     a, b = (_call(which, [100, 3, 600, 40], 1152, 640, ints=False)[4] for _ in range(2))
