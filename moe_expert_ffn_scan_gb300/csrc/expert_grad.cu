@@ -916,11 +916,11 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
 // a form's tiles as many run at once as CTAs or pairs fit, each a stage's time per stage and a
 // tile's own besides.  A group of R / E rows is taken to have one chunk up to three quarters of a
 // tile's rows, above that what its rows fill and 0.4 (the groups' sizes vary).  Costs as measured
-// on GB300, weights from HBM (us; P = 1 and 2): w13 of 7168 x 2048, 32 groups of 16, 40, 64 rows:
-// 114, 224, 220 and 164, 167, 169; 2 groups of 32, 100, 250: 17, 41, 59 and 19, 22, 28; w13 and w2
-// of 2048 x 1024, 16 groups of 50: 25, 15 and 22, 14, of 150: 46, 28 and 26, 17; w2 of 1024 x 1024,
-// 64 groups of 20, 80: 16, 33 and 24, 30; w2 of 1152 x 640, 13 groups of 60, 179: 8.5, 15.8 and
-// 10.8, 13.7.
+// on GB300, weights from HBM (us; P = 1 and 2): w13 of 7168 x 2048, 32 groups of 24, 33, 40 rows:
+// 118, 223, 224 and 167, 168, 168; 8 groups of 30, 64: 41, 62 and 48, 48; 2 groups of 32, 100: 17, 41
+// and 19, 21; w13 and w2 of 2048 x 1024, 16 groups of 50: 25, 15.2 and 21, 13.7; w2 of 1024 x 1024,
+// 64 groups of 20, 40: 17, 27 and 23, 23; w2 of 1280 x 768, 13 groups of 60, 179: 11.1, 18.0 and
+// 10.8, 12.8 (NVFP4 up to a tenth more of each).
 template <int P, int F>
 double cost_us(const ExpertGradCall& a) {
   const double M = Cfg<P, F>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
@@ -930,10 +930,12 @@ double cost_us(const ExpertGradCall& a) {
   const double tiles = items * ((a.F + kFeat * P - 1) / (kFeat * P));
   const double waves = ceil(tiles * P / (kSms * Cfg<P, F>::kOcc));
   const double stages = a.C / kBK;
-  // (a CTA that has its SM for itself is faster; a pair's MMAs take longer for more rows)
-  if (P == 1) return 3.5 + waves * (stages * (tiles <= kSms ? 0.45 : 0.56) + 1.2);
+  // (a CTA that has its SM for itself is faster: w2 of 2048 x 1024, 16 groups of 24 rows 11.4 us; a
+  // pair's MMAs take longer for more rows)
+  const bool alone = tiles <= kSms;
+  if (P == 1) return (alone ? 3.8 : 4.5) + waves * (stages * (alone ? 0.38 : 0.56) + 1.2);
   const double rows = a.rows / items;
-  return 7.0 + waves * (stages * (0.36 + 0.28 * (rows < M ? rows / M : 1.0)) + 0.7);
+  return 6.2 + waves * (stages * (0.36 + 0.28 * (rows < M ? rows / M : 1.0)) + 0.7);
 }
 
 template <int F>
