@@ -589,7 +589,8 @@ int moe_grouped_gemm_w13_backward(const moe_dims* d, const uint16_t* dy13,
 /* The same with NVFP4 weights (codes, E4M3 scales per 16 features, tensor scales as for the
  * forward: w2_gs [G], w13_gs [G][2] for the gate and up rows; NULL = 1), which multiply the fp32
  * sums (W13: of its two halves; of an expert's two scales more than 2^126 apart the smaller one
- * may count as 0) in front of the one rounding.  H % 256 == 0 and I % 256 == 0. */
+ * may count as 0, of two infinite ones the values may be NaN) in front of the one rounding.
+ * H % 256 == 0 and I % 256 == 0. */
 int moe_grouped_gemm_w2_backward_nvfp4(const moe_dims* d, const uint16_t* dy2,
                                        const int32_t* group_offsets, const uint8_t* w2,
                                        const uint8_t* w2_s, const float* w2_gs, uint16_t* dh,

@@ -319,7 +319,8 @@ constexpr float kNvShort = 128.f;
 
 // The halves of a group's contraction in the order of their tensor scales' magnitudes, so that the
 // quotient overflows nowhere: last * (quotient * first sum + second sum).  (Of scales more than
-// 2^126 apart the smaller one's half is lost.)
+// 2^126 apart the smaller one's half is lost.)  A NaN is the first scale or makes the quotient one,
+// also where the other scale is 0; of two infinite scales the quotient is NaN.
 struct Halves {
   bool swap;  // the second half first
   float quotient, last;
@@ -327,7 +328,8 @@ struct Halves {
     const float a = gs ? __ldg(gs + 2 * g) : 1.f, b = gs ? __ldg(gs + 2 * g + 1) : 1.f;
     swap = fabsf(a) > fabsf(b);
     last = swap ? a : b;
-    quotient = last == 0.f ? 0.f : (swap ? b : a) / last;
+    const float other = swap ? b : a;
+    quotient = last == 0.f ? other : other / last;  // (0, or the other one's NaN)
   }
 };
 template <int P, int F>

@@ -1,0 +1,73 @@
+"""The layer's gradient where fp32's range ends: NVFP4 tensor scales that are infinite or NaN."""
+
+import pytest
+import torch
+
+import moe_expert_ffn_scan_gb300 as moe
+from tests import _grad_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
+NAN, INF = float("nan"), float("inf")
+
+
+def _nvfp4(which, H, I, rows, t):
+    """dx of groups of `rows` rows whose tensor scales are t.  dy is -2 .. 2 steps of 2^-14 and the
+    block scales 1, 2 or 3: the sums are exact in fp32 (multiples of 2^-15, of 2 I <= 4096 terms up
+    to 2^-14 * 36 below 9)."""
+    g = torch.Generator(device=DEV).manual_seed(rows + H)
+    ri = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=DEV)  # noqa: E731
+    G, (C, F) = len(t), (H, I) if which == "w2" else (2 * I, H)
+    off = torch.arange(G + 1, dtype=I32, device=DEV) * rows
+    dy = (ri(-2, 3, G * rows, C) * 2.0 ** -14).to(BF)
+    w = ri(0, 256, G, C, F // 2).to(U8)
+    w_s = ri(1, 4, G, C, F // 16).float().to(torch.float8_e4m3fn).view(U8)
+    dx = torch.full((G * rows, F), 7.0, dtype=BF, device=DEV)
+    d = moe.dims(G * rows, H, I, G, 1, 0)
+    ws = moe.alloc_workspace(moe.gemm_backward_workspace_size(d))
+    f = moe.moe_grouped_gemm_w2_backward_nvfp4 if which == "w2" \
+        else moe.moe_grouped_gemm_w13_backward_nvfp4
+    f(d, dy, off, w, w_s, t, dx, ws)
+    assert moe.moe_check_status(ws) == 0
+    return dy, off, w, w_s, dx
+
+
+def _agrees(dy, off, w, w_s, t, dx):
+    """The formula's value, rounded to bf16, where it is finite: half a step, 2^-22 of the halves'
+    magnitudes for each step of 16 of a half that is summed onto the multiplied other one (each
+    half by itself is exact), and 2^-22 for the scales' quotient, its product and that with the
+    last scale.  Else the same infinity, or NaN."""
+    want, size = 0.0, 0.0
+    parts = 1 if t.ndim == 1 else 2  # (the scales multiply the sums: 0 times an infinite one is NaN)
+    rows, C = dx.shape[0] // len(t), dy.shape[1] // parts
+    for p in range(parts):
+        c = slice(p * C, (p + 1) * C)
+        total, m = ref.expert_grad(dy[:, c], off, w[:, c], w_s[:, c], *dx.shape, nv=True)
+        scale = t.view(len(t), parts)[:, p].double().repeat_interleave(rows)[:, None]
+        want, size = want + scale * total, size + scale.abs() * m
+    got, fine = dx.double(), torch.isfinite(want)
+    tol = ref.U16 * want.abs() + (dy.shape[1] / 16 + 3) * 2.0 ** -22 * size
+    assert torch.all((got - want).abs()[fine] <= tol[fine])
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf])
+
+
+# (few features run on single CTAs, many on SM pairs: with two sums a tile, and with one)
+SHAPES = [(256, 256, 100), (256, 256, 200), (1280, 2048, 100), (1280, 2048, 200)]
+
+
+@pytest.mark.parametrize("H,I,rows", SHAPES)
+def test_w13_tensor_scales_that_are_nan(H, I, rows):
+    t = torch.tensor([(NAN, 0.0), (0.0, NAN), (NAN, 1.0), (1.0, NAN), (NAN, NAN), (NAN, INF),
+                      (-INF, NAN), (1.0, 0.5)], device=DEV)
+    dx = _nvfp4("w13", H, I, rows, t)[-1].view(len(t), -1)
+    assert torch.all(torch.isnan(dx[:-1])) and torch.all(torch.isfinite(dx[-1]))
+
+
+@pytest.mark.parametrize("H,I,rows", SHAPES)
+def test_w13_tensor_scales_that_are_infinite(H, I, rows):
+    t = torch.tensor([(INF, 0.5), (0.5, -INF), (-INF, 1.5), (0.375, INF), (1.0, 0.5)], device=DEV)
+    dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, t)
+    _agrees(dy, off, w, w_s, t, dx)
