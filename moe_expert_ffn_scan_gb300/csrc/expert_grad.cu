@@ -308,14 +308,23 @@ __device__ __forceinline__ int scale_at(int c, int f0, int features, int own) {
   return c * 16 + ((c * (features / kFeat) + f0 / kFeat) & (16 / own - 1)) * own;
 }
 // Two E4M3 scales as bf16 factors, times 2^119 (448 * 2^119 is below bf16's largest value); the
-// codes come times 2^-126, so products are short of 2^7, which the epilogue makes up for.
+// codes come times 2^-126, so products are short of 2^7, which the epilogue makes up for (Scaled).
 __device__ __forceinline__ uint32_t factor_e4m3(uint32_t lo_hi) {
   const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
       static_cast<__nv_fp8x2_storage_t>(lo_hi & 0xFFFFu), __NV_E4M3);
   const float2 v = __half22float2(__half2(hr));
   return bf16x2_of(v.x * 0x1p119f, v.y * 0x1p119f);
 }
-constexpr float kNvShort = 128.f;
+
+// A sum short of 2^7 times its tensor scale.  The 2^7 goes to the scale where that is below 1, else
+// to the sum: 128 * scale would overflow from 2^121 on, and a sum that overflows in 128 * sum does so
+// with a scale of 1 or more anyway.
+struct Scaled {
+  float up, scale;
+  __device__ __forceinline__ explicit Scaled(float gs)
+      : up(fabsf(gs) >= 1.f ? 128.f : 1.f), scale(fabsf(gs) >= 1.f ? gs : 128.f * gs) {}
+  __device__ __forceinline__ float of(float sum) const { return scale * (up * sum); }
+};
 
 // The halves of a group's contraction in the order of their tensor scales' magnitudes, so that the
 // quotient overflows nowhere: last * (quotient * first sum + second sum).  (Of scales more than
@@ -738,11 +747,11 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
       const int own = t.rows - c0 < part ? t.rows - c0 : part;
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAccCols + c0;
       int w_ok = 1;
-      float gs0 = 1.f, gs1 = 1.f;
+      Scaled gs0(1.f), gs1(1.f);
       const bool twice = rescaled<P, F>(t);
       if (C::kHalves) {  // the first sum times the quotient, plus the second if that is apart
         const Halves h(p.gs, t.g);
-        gs0 = kNvShort * h.last;
+        gs0 = Scaled(h.last);
         if (lane == 0) {
           if (twice) w_ok = mbar_wait(half, rescales & 1u, p.status, abort_flag);
           else w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
@@ -772,8 +781,8 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
           }
         }
       } else if (F != kMx) {
-        gs0 = kNvShort * (p.gs ? __ldg(p.gs + t.g * C::kSums) : 1.f);
-        if (C::kSums == 2) gs1 = kNvShort * (p.gs ? __ldg(p.gs + t.g * 2 + 1) : 1.f);
+        gs0 = Scaled(p.gs ? __ldg(p.gs + t.g * C::kSums) : 1.f);
+        if (C::kSums == 2) gs1 = Scaled(p.gs ? __ldg(p.gs + t.g * 2 + 1) : 1.f);
       }
       if (lane == 0) w_ok = mbar_wait(&acc_full[b], use & 1u, p.status, abort_flag);
       if (!__shfl_sync(0xFFFFFFFFu, w_ok, 0)) break;
@@ -803,13 +812,13 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                x[i] = __float_as_uint(
-                    fmaf(gs0, __uint_as_float(x[i]), gs1 * __uint_as_float(y[i])));
+                x[i] = __float_as_uint(fmaf(gs0.scale, gs0.up * __uint_as_float(x[i]),
+                                            gs1.of(__uint_as_float(y[i]))));
             } else {
               tmem_ld_wait();
               if (F != kMx) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(gs0 * __uint_as_float(x[i]));
+                for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(gs0.of(__uint_as_float(x[i])));
               }
             }
 #pragma unroll

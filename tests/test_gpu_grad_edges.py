@@ -1,4 +1,5 @@
-"""The layer's gradient where fp32's range ends: NVFP4 tensor scales that are infinite or NaN."""
+"""The layer's gradient where fp32's range ends: NVFP4 tensor scales that are large, infinite or
+NaN."""
 
 import pytest
 import torch
@@ -54,6 +55,7 @@ def _agrees(dy, off, w, w_s, t, dx):
     assert torch.equal(got[inf], want[inf])
 
 
+BIG = 2.0 ** 122
 # (few features run on single CTAs, many on SM pairs: with two sums a tile, and with one)
 SHAPES = [(256, 256, 100), (256, 256, 200), (1280, 2048, 100), (1280, 2048, 200)]
 
@@ -70,4 +72,20 @@ def test_w13_tensor_scales_that_are_nan(H, I, rows):
 def test_w13_tensor_scales_that_are_infinite(H, I, rows):
     t = torch.tensor([(INF, 0.5), (0.5, -INF), (-INF, 1.5), (0.375, INF), (1.0, 0.5)], device=DEV)
     dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, t)
+    _agrees(dy, off, w, w_s, t, dx)
+
+
+@pytest.mark.parametrize("H,I,rows", SHAPES)
+def test_w13_tensor_scales_that_are_large(H, I, rows):
+    t = torch.tensor([(BIG, 1.0), (1.0, -BIG), (BIG, BIG), (-BIG, 2.0 ** 100), (2.0 ** 60, BIG),
+                      (2.0 ** 120, 2.0 ** 121), (1.0, 1.0)], device=DEV)
+    dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, t)
+    assert torch.all(torch.isfinite(dx))
+    _agrees(dy, off, w, w_s, t, dx)
+
+
+@pytest.mark.parametrize("H,I,rows", SHAPES)
+def test_w2_tensor_scales_of_every_kind(H, I, rows):
+    t = torch.tensor([BIG, -BIG, 2.0 ** 121, NAN, INF, -INF, 1.0, 0.0, 2.0 ** -100], device=DEV)
+    dy, off, w, w_s, dx = _nvfp4("w2", H, I, rows, t)
     _agrees(dy, off, w, w_s, t, dx)
