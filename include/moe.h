@@ -557,7 +557,9 @@ int moe_swiglu_quant_save(int32_t rows, int32_t I, const uint16_t* y13, uint8_t*
  *   with h the values of hq, hs (what W2 took) where given, else silu(g) u.  A row whose
  *   perm_src is outside [0, R) has weight 1 and no dw; entries of dw that no row names are
  *   left as they were.
- *   Finite for finite inputs whose formulas are.  rows == 0 is a no-op. */
+ *   dy13 is finite where its value is and g, u (a code's value too) and d are in fp32; a sigmoid
+ *   below 2^-126 may count as 0.  dw is finite where in fp32 its terms, also those with hq's codes in
+ *   h's place, and their sums are.  rows == 0 is a no-op. */
 typedef struct moe_swiglu_backward_desc {
   int32_t rows, R, I; /* 0 <= R <= rows <= 2^30; I % 128 == 0, I <= 2^29 */
 } moe_swiglu_backward_desc;

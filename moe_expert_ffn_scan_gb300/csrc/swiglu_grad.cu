@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) k_swiglu_save(const uint16_t* __restrict_
 // A CTA per row, or with kPack `pack` warps per row and as many rows as the CTA's warps do for; 8
 // columns a thread at a time; all of a thread's loads are in flight before the first is used,
 // and what they bring stays packed until its four columns' turn, so that registers leave room
-// for full occupancy (73728 rows of 2048: 222 us, 0.92 of HBM; with 40 registers a thread 272,
+// for full occupancy (73728 rows of 2048: 227 us, 0.90 of HBM; with 40 registers a thread 272,
 // with 16 columns and 64 registers 254).  kCodes: g and u from the checkpoint; kH: h from hq.
 template <bool kCodes, bool kH, bool kPack>
 __global__ void __launch_bounds__(kPack ? 256 : kBwdThreads, kPack ? 6 : kBwdCtas)
@@ -161,10 +161,21 @@ __global__ void __launch_bounds__(kPack ? 256 : kBwdThreads, kPack ? 6 : kBwdCta
       sh = scale_of(a.hs[(row * I + c) / 128]);
     }
     float sum = 0.f;
+    if (kH) {  // (first, so that h's codes hold no registers beside the products below)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float d[4], h[4];
+        bf16x4(dv[2 * i], dv[2 * i + 1], d);
+        codes4(hv[i], h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum = fmaf(d[j], h[j], sum);
+      }
+      dot = fmaf(sum, sh, dot);  // (h's scale is a power of two)
+    }
     uint32_t og[4], ou[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // four columns
-      float d[4], g[4], u[4], h[4], dg[4], du[4];
+      float d[4], g[4], u[4], dg[4], du[4];
       bf16x4(dv[2 * i], dv[2 * i + 1], d);
       if (kCodes) {
         codes4(gv[i], g);
@@ -173,19 +184,22 @@ __global__ void __launch_bounds__(kPack ? 256 : kBwdThreads, kPack ? 6 : kBwdCta
         bf16x4(gv[2 * i], gv[2 * i + 1], g);
         bf16x4(uv[2 * i], uv[2 * i + 1], u);
       }
-      if (kH) codes4(hv[i], h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float gj = kCodes ? g[j] * sg : g[j], uj = kCodes ? u[j] * su : u[j];
-        const float s = sigmoid_of(gj), silu = gj * s, dd = w * d[j];
-        sum = fmaf(d[j], kH ? h[j] : silu * uj, sum);
-        dg[j] = dd * uj * fmaf(silu, 1.f - s, s);
+        const float s = sigmoid_of(gj), silu = gj * s, dd = w * d[j], f = fmaf(silu, 1.f - s, s);
+        if (!kH) sum = fmaf(d[j], silu * uj, sum);
+        // (where d u is past fp32 both are above 1, and |f| is at most 1.1: d f overflows only if dg
+        // does.  In the other order a small d f would lose its bits)
+        const float p = dd * uj;
+        const bool far = fabsf(p) == INFINITY;
+        dg[j] = (far ? dd * f : p) * (far ? uj : f);
         du[j] = dd * silu;
       }
       og[2 * i] = bf16x2_of(dg[0], dg[1]), og[2 * i + 1] = bf16x2_of(dg[2], dg[3]);
       ou[2 * i] = bf16x2_of(du[0], du[1]), ou[2 * i + 1] = bf16x2_of(du[2], du[3]);
     }
-    dot = fmaf(sum, sh, dot);  // (h's scale is a power of two)
+    if (!kH) dot += sum;
     st_bf16x8(a.dy13 + row * 2 * I + c, og);
     st_bf16x8(a.dy13 + row * 2 * I + I + c, ou);
   }

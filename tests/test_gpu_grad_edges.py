@@ -1,5 +1,5 @@
 """The layer's gradient where fp32's range ends: NVFP4 tensor scales that are large, infinite or
-NaN."""
+NaN, and SwiGLU's gradient where the product of its factors leaves fp32's range on the way."""
 
 import pytest
 import torch
@@ -89,3 +89,40 @@ def test_w2_tensor_scales_of_every_kind(H, I, rows):
     t = torch.tensor([BIG, -BIG, 2.0 ** 121, NAN, INF, -INF, 1.0, 0.0, 2.0 ** -100], device=DEV)
     dy, off, w, w_s, dx = _nvfp4("w2", H, I, rows, t)
     _agrees(dy, off, w, w_s, t, dx)
+
+
+GATES = [0.0, 1.5, -1.2785, 20, -20, -60, 60, -80, 87, -87, 88, -88, -100, 1000, -1000, 2e38, -2e38]
+ROWS = [(u, dh) for u in (3e38, -1e30, 1e20, 1.0, 1e-30) for dh in (3e38, 1e20, -1e30, 0.5, 1e-38)]
+
+
+@pytest.mark.parametrize("form", ["bf16", "codes"])
+def test_swiglu_factors_whose_product_is_past_fp32(form):
+    """|d u| up to 1e77.  Where the formula's value fits bf16 the gradient is finite and within the
+    bound of the kernel's other tests: a sigmoid below 2^-126 may count as 0, and (|g| + 16) * 2^-22
+    covers the sigmoid's error and the products behind it."""
+    I = 128
+    gates = GATES if form == "bf16" else GATES[:-2]  # (one scale for a row's gates)
+    y13 = torch.empty(len(ROWS), 2 * I, dtype=BF, device=DEV)
+    y13[:, :I] = torch.tensor(gates, device=DEV).repeat(I)[:I]
+    y13[:, I:] = torch.tensor([u for u, _ in ROWS], device=DEV)[:, None]
+    dh = torch.tensor([d for _, d in ROWS], device=DEV).to(BF)[:, None].repeat(1, I).contiguous()
+    dy = torch.empty_like(y13)
+    if form == "bf16":
+        moe.moe_swiglu_backward(dh, dy, y13=y13)
+        y = y13.double()
+    else:
+        yq, ys = (torch.empty(len(ROWS), n, dtype=U8, device=DEV) for n in (2 * I, 2 * I // 128))
+        moe.moe_quant_act(y13, yq, ys)
+        moe.moe_swiglu_backward(dh, dy, yq=yq, ys=ys)
+        y = ref.fp8_values(yq, ys)
+    g, u, d = y[:, :I], y[:, I:], dh.double()
+    dg, du, scale = ref.swiglu_bwd(g, u, d)
+    c, tiny = (g.abs() + 16) * 2.0 ** -22, d.abs() * (1 + g.abs()) * 2.0 ** -126
+    most = torch.finfo(BF).max
+    for got, want, tol in ((dy[:, :I], dg, ref.U16 * dg.abs() + c * scale + u.abs() * tiny),
+                           (dy[:, I:], du, (ref.U16 + c) * du.abs() + tiny)):
+        tol = tol + 2.0 ** -126
+        fits, past = want.abs() + tol <= most, want.abs() - tol > most * (1 + ref.U16)
+        assert torch.all(torch.isfinite(got[fits].float()))
+        assert torch.all((got.double() - want).abs()[fits] <= tol[fits])
+        assert torch.equal(got[past].double(), torch.sign(want[past]) * INF)
