@@ -893,11 +893,40 @@ class HostPipeline:
             pass
 
 
+class _LayerWorkspace:
+    """A layer's workspace for the longest step so far (size: T -> bytes), made anew for a longer
+    one.  A graph goes on using the one it was captured with, which therefore stays as long as
+    the layer; any other is given back once the streams that used it are through."""
+
+    def __init__(self, size):
+        self.size, self.ws, self.T, self.stream = size, None, -1, None
+        self.in_graph, self.of_graphs = False, []
+
+    def get(self, T, weight, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.get(T, weight)
+        if T > self.T:
+            n = self.size(T)
+            if self.ws is None or n > self.ws.numel():
+                if self.in_graph:
+                    self.of_graphs.append(self.ws)
+                self.ws, self.stream = alloc_workspace(n, weight.device), _raw_stream(None)
+                self.in_graph = False
+            self.T = T
+        if torch.cuda.is_current_stream_capturing():
+            self.in_graph = True
+        elif _raw_stream(None) != self.stream:
+            self.ws.record_stream(torch.cuda.current_stream())
+        return self.ws
+
+
 class MoELayer:
     """The user-facing layer: resident MXFP4 weights plus a reusable workspace.
 
     `forward(x, logits)` runs moe_forward on the current stream and returns the
-    bf16 output [T, H]."""
+    bf16 output [T, H].  Graphs captured with a layer keep its workspaces of that time: they may
+    be replayed after longer steps."""
 
     def __init__(self, H, I, E, k, has_shared, w13, w13_s, w2, w2_s, fmt="mxfp4", w13_gs=None,
                  w2_gs=None, fuse_combine=False, fuse_swiglu=False, pair_tiles=False,
@@ -913,20 +942,25 @@ class MoELayer:
         self.H, self.I, self.E, self.k, self.has_shared = H, I, E, k, has_shared
         self.w13, self.w13_s, self.w2, self.w2_s = w13, w13_s, w2, w2_s
         self.fmt, self.w13_gs, self.w2_gs = fmt, w13_gs, w2_gs
-        self._ws = None
-        self._T = -1
+        self._ws = _LayerWorkspace(self._forward_size)
+        self._hws = _LayerWorkspace(lambda T: host_workspace_size(self.dims(T)))
+        self._tws = _LayerWorkspace(self._forward_train_size)
+        self._bws = None
+        if w13 is not None and w13.is_cuda and not torch.cuda.is_current_stream_capturing():
+            self._backward_workspace()
+            torch.cuda.current_stream(w13.device).synchronize()
 
     def dims(self, T):
         return dims(T, self.H, self.I, self.E, self.k, self.has_shared)
 
+    def _forward_size(self, T):
+        size = (workspace_size if self.fmt == "mxfp4" else workspace_size_nvfp4)(self.dims(T))
+        if size == 0:
+            raise ValueError(f"unsupported dims for {self.fmt} weights")
+        return size
+
     def workspace(self, T, stream=None):
-        if self._ws is None or self._T < T:
-            size = (workspace_size if self.fmt == "mxfp4" else workspace_size_nvfp4)(self.dims(T))
-            if size == 0:
-                raise ValueError(f"unsupported dims for {self.fmt} weights")
-            self._ws = alloc_workspace(size, self.w13.device, stream)
-            self._T = T
-        return self._ws
+        return self._ws.get(T, self.w13, stream)
 
     def _mxfp4_only(self, what):
         if self.fmt != "mxfp4":
@@ -934,11 +968,7 @@ class MoELayer:
 
     def host_workspace(self, T, stream=None):
         self._mxfp4_only("the host-buffer forward")
-        if getattr(self, "_hws", None) is None or self._hT < T:
-            self._hws = alloc_workspace(host_workspace_size(self.dims(T)), self.w13.device,
-                                        stream)
-            self._hT = T
-        return self._hws
+        return self._hws.get(T, self.w13, stream)
 
     def host_pipeline(self, T, depth=2):
         """A HostPipeline for T-token steps (its own workspace and streams)."""
@@ -973,19 +1003,26 @@ class MoELayer:
                               debug=debug, stream=stream)
         return out
 
+    def _forward_train_size(self, T):
+        d = self.dims(T)
+        gemm = (gemm_workspace_size if self.fmt == "mxfp4" else gemm_workspace_size_nvfp4)(d)
+        if gemm == 0:
+            raise ValueError("unsupported dims")
+        return max(route_workspace_size(d), gemm)
+
+    def _backward_workspace(self):
+        """The gradient products' status word collects the bits of every step: one for all of
+        them, made with the layer, so that it is zeroed before any stream or graph has it."""
+        if self._bws is None:
+            size = gemm_backward_workspace_size(self.dims(1))
+            self._bws = alloc_workspace(size, self.w13.device) if size else None
+        return self._bws
+
     def train_workspaces(self, T, stream=None):
         """The workspaces of forward_train and backward steps of up to T tokens (moe_check_status
-        reads the checks of the last forward_train, and of every backward since they were made)."""
-        if getattr(self, "_tws", None) is None or self._tT < T:
-            d = self.dims(T)
-            gemm = gemm_workspace_size if self.fmt == "mxfp4" else gemm_workspace_size_nvfp4
-            sizes = (max(route_workspace_size(d), gemm(d)) if gemm(d) else 0,
-                     gemm_backward_workspace_size(d))
-            if 0 in sizes:
-                raise ValueError("unsupported dims")
-            self._tws = tuple(alloc_workspace(n, self.w13.device, stream) for n in sizes)
-            self._tT = T
-        return self._tws
+        reads the checks of the last forward_train, and of every backward since the layer was
+        made)."""
+        return self._tws.get(T, self.w13, stream), self._backward_workspace()
 
     def forward_train(self, x, logits, out=None, checkpoint="fp8", stream=None):
         """forward by its stages, keeping what backward needs.  Returns the output [T, H] and the
