@@ -42,8 +42,9 @@ class MoEBlock:
         dev = w_o.device
         d = layer.dims(T)
         N, K = w_o.shape
-        self.ws = moe.alloc_workspace(max(moe.route_workspace_size(d), moe.gemm_workspace_size(d)),
-                                      dev)
+        # the layer's three stages: a status word each in one buffer
+        self.ws = moe.stage_workspaces(moe.alloc_workspace(
+            max(moe.route_workspace_size(d), 512 + moe.gemm_workspace_size(d)), dev), 3)
         self.ws_linear = moe.alloc_workspace(moe.linear_workspace_size(T, N, K), dev)
         self.ws_balance = moe.alloc_workspace(
             moe.balance_loss_workspace_size(T, self.E, self.k, n_seq), dev)
@@ -70,19 +71,21 @@ class MoEBlock:
         moe.moe_router_logits(f["y"], self.wg, f["logits"])
         offsets = new(E + sh + 1, dt=torch.int32)
         perm, inv = new(R, dt=torch.int32), new(R, dt=torch.int32)
-        moe.moe_route(d, f["logits"], f["idx"], f["w"], f["counts"], offsets, perm, inv, self.ws)
+        moe.moe_route(d, f["logits"], f["idx"], f["w"], f["counts"], offsets, perm, inv,
+                      self.ws[0])
         y13, hq = new(Rs, 2 * I), new(Rs, I, dt=torch.uint8)
         hs, y2, out = new(Rs, I // 128, dt=torch.uint8), new(Rs, H), new(T, H)
         L = self.layer
-        moe.moe_grouped_gemm_w13(d, q, s, perm, offsets, L.w13, L.w13_s, y13, self.ws)
+        moe.moe_grouped_gemm_w13(d, q, s, perm, offsets, L.w13, L.w13_s, y13, self.ws[1])
         if save:
             f.update(perm=perm, inv=inv, offsets=offsets, hq=hq, hs=hs,
                      yq=new(Rs, 2 * I, dt=torch.uint8), ys=new(Rs, 2 * I // 128, dt=torch.uint8))
             moe.moe_swiglu_quant_save(y13, hq, hs, f["yq"], f["ys"])
         else:
             moe.moe_swiglu_quant(y13, hq, hs)
-        moe.moe_grouped_gemm_w2(d, hq, hs, offsets, L.w2, L.w2_s, y2, self.ws)
+        moe.moe_grouped_gemm_w2(d, hq, hs, offsets, L.w2, L.w2_s, y2, self.ws[2])
         moe.moe_combine(d, y2, inv, f["w"], out)
+        moe.moe_join_status(self.ws[0], self.ws[1:])
         f["out"] = out
         return f
 
@@ -138,9 +141,11 @@ class MoEBlock:
         return o, g
 
     def check(self):
-        """The device-side checks of the calls since the workspaces were made."""
-        bits = [moe.moe_check_status(w) for w in (self.ws, self.ws_linear, self.ws_balance,
-                                                 self.ws_grad)]
+        """The device-side checks of the last step: of the projection, the layer's stages, the
+        balance loss and the gradients (those of the projections and of the gradient products: of
+        every step since the workspaces were made)."""
+        bits = [moe.moe_check_status(w) for w in (self.ws[0], self.ws_linear,
+                                                 self.ws_balance, self.ws_grad)]
         bits[3] |= moe.moe_check_status(self.ws_experts)
         return bits
 

@@ -608,6 +608,13 @@ int moe_grouped_gemm_w13_backward_nvfp4(const moe_dims* d, const uint16_t* dy13,
  * cleared by moe_forward / moe_route / the GEMMs at their start. */
 int moe_check_status(const void* ws, void* stream, uint32_t* bits_out);
 
+/* One status word for a step of several calls, each of which clears its own at its start: ORs
+ * the words of n workspaces (from: a host array; 1 <= n <= 8; all 256-byte aligned) into that of
+ * ws, on `stream`.  Behind its first 256 bytes, the status word's, a workspace is scratch of the
+ * call that has it: calls one behind another on a stream may have workspaces that start 256
+ * bytes apart in one buffer, the last of them with its full size. */
+int moe_join_status(void* ws, const void* const* from, int32_t n, void* stream);
+
 /* Failure-path self-test; the pages have no counterpart.  Launches one CTA whose
  * mbarrier wait can never complete (nothing arrives), so the library's bounded wait
  * (kWaitLimitNs = 2 s of the GPU's global timer) gives up, sets STATUS_WAIT_TIMEOUT

@@ -127,6 +127,8 @@ def lib():
         L.moe_route_static.argtypes = [_DP, _P, _P, _P, _P, _P, _P, _P, _P]
         L.moe_route_static_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
         L.moe_check_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_uint32)]
+        L.moe_join_status.argtypes = [_P, ctypes.POINTER(_P), _I, _P]
+        L.moe_join_status.restype = ctypes.c_int
         L.moe_selftest_wait_timeout.argtypes = [_P, _P]
         L.moe_host_pipeline_workspace_size.argtypes = [_DP, _I]
         L.moe_host_pipeline_workspace_size.restype = _SZ
@@ -795,6 +797,19 @@ def moe_check_status(ws, stream=None) -> int:
     return bits.value
 
 
+def stage_workspaces(ws, n):
+    """n workspaces in one buffer, for calls one behind another on a stream: a status word each,
+    256 bytes apart, the scratch behind them shared (the buffer: 256 (n - 1) bytes and the largest
+    call's).  moe_join_status makes their words one."""
+    return [ws[256 * i:] for i in range(n)]
+
+
+def moe_join_status(ws, others, stream=None):
+    """ORs the status words of the workspaces `others` (up to 8) into that of ws, on the stream."""
+    _check("moe_join_status", lib().moe_join_status(
+        _p(ws), (_P * len(others))(*[_p(w) for w in others]), len(others), _stream(stream)))
+
+
 def moe_selftest_wait_timeout(ws, stream=None):
     """Runs the failure-path self-test (a wait that must time out) on ws's status word."""
     _check("moe_selftest_wait_timeout", lib().moe_selftest_wait_timeout(_p(ws), _stream(stream)))
@@ -1008,7 +1023,7 @@ class MoELayer:
         gemm = (gemm_workspace_size if self.fmt == "mxfp4" else gemm_workspace_size_nvfp4)(d)
         if gemm == 0:
             raise ValueError("unsupported dims")
-        return max(route_workspace_size(d), gemm)
+        return max(route_workspace_size(d), 512 + gemm)  # (the stages': see forward_train)
 
     def _backward_workspace(self):
         """The gradient products' status word collects the bits of every step: one for all of
@@ -1040,22 +1055,23 @@ class MoELayer:
             new = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=x.device)  # noqa: E731
             if out is None:
                 out = new(T, H)
-            ws = self.train_workspaces(T)[0]
+            # each stage clears its status word at its start: one each, joined at the end
+            stages = stage_workspaces(self.train_workspaces(T)[0], 3)
             s = dict(T=T, idx=new(T, k, dt=_I32), w=new(T, k, dt=_F32), counts=new(E, dt=_I32),
                      offsets=new(E + sh + 1, dt=_I32), perm_src=new(R, dt=_I32),
                      inv=new(R, dt=_I32))
             moe_route(d, logits, s["idx"], s["w"], s["counts"], s["offsets"], s["perm_src"],
-                      s["inv"], ws)
+                      s["inv"], stages[0])
             xq, xs = new(T, H, dt=_U8), new(T, H // 128, dt=_U8)
             moe_quant_act(x, xq, xs)
             y13, y2 = new(Rs, 2 * I), new(Rs, H)
             nv = self.fmt != "mxfp4"
             if nv:
                 moe_grouped_gemm_w13_nvfp4(d, xq, xs, s["perm_src"], s["offsets"], self.w13,
-                                           self.w13_s, self.w13_gs, y13, ws)
+                                           self.w13_s, self.w13_gs, y13, stages[1])
             else:
                 moe_grouped_gemm_w13(d, xq, xs, s["perm_src"], s["offsets"], self.w13, self.w13_s,
-                                     y13, ws)
+                                     y13, stages[1])
             hq, hs = new(Rs, I, dt=_U8), new(Rs, I // 128, dt=_U8)
             if checkpoint == "fp8":
                 s |= dict(hq=hq, hs=hs, yq=new(Rs, 2 * I, dt=_U8),
@@ -1066,10 +1082,11 @@ class MoELayer:
                 moe_swiglu_quant(y13, hq, hs)
             if nv:
                 moe_grouped_gemm_w2_nvfp4(d, hq, hs, s["offsets"], self.w2, self.w2_s, self.w2_gs,
-                                          y2, ws)
+                                          y2, stages[2])
             else:
-                moe_grouped_gemm_w2(d, hq, hs, s["offsets"], self.w2, self.w2_s, y2, ws)
+                moe_grouped_gemm_w2(d, hq, hs, s["offsets"], self.w2, self.w2_s, y2, stages[2])
             moe_combine(d, y2, s["inv"], s["w"], out)
+            moe_join_status(stages[0], stages[1:])
         return out, s
 
     def backward(self, dout, saved, dx=None, dx_in=None, stream=None):

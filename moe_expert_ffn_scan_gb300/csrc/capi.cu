@@ -301,6 +301,17 @@ __global__ void k_selftest_wait(uint32_t* status) {
   }
 }
 
+struct StatusWords {
+  const uint32_t* from[8];
+};
+__global__ void k_join_status(uint32_t* status, const StatusWords w, int n) {
+  pdl_wait();
+  pdl_trigger();
+  uint32_t bits = 0;
+  for (int i = 0; i < n; ++i) bits |= *w.from[i];
+  set_status(status, bits);
+}
+
 bool weights_ok(const uint8_t* c, const uint8_t* s) {
   return c && s && aligned(c, 32) && aligned(s, 16);
 }
@@ -884,6 +895,17 @@ int moe_check_status(const void* ws, void* stream, uint32_t* bits_out) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
   if (bits_out) *bits_out = bits;
   return bits ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+}
+
+int moe_join_status(void* ws, const void* const* from, int32_t n, void* stream) {
+  StatusWords w = {};
+  if (!ws || !from || !aligned(ws, kAlign) || n < 1 || n > 8) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    if (!from[i] || !aligned(from[i], kAlign)) return MOE_ERR_INVALID_ARG;
+    w.from[i] = static_cast<const uint32_t*>(from[i]);
+  }
+  return cuda_rc(launch_k(k_join_status, 1, 1, 0, static_cast<cudaStream_t>(stream),
+                          static_cast<uint32_t*>(ws), w, n));
 }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 gradient products' status word is never replaced.  The bookkeeping on the CPU, with torch's
 capture state and streams played by the test; on the GPU a graph replayed after longer steps."""
 
+import ctypes
 import gc
 import weakref
 
@@ -175,3 +176,29 @@ def test_a_host_graph_replayed_after_longer_steps():
     torch.cuda.synchronize()
     assert torch.equal(got, layer.forward(x, logits).cpu())
     assert all(bool(torch.all(t == 0x5A)) for t in filled)
+
+
+def test_joined_status_words_refusals():
+    P = ctypes.c_void_p
+    f, A, odd = moe.lib().moe_join_status, P(0x10000), P(0x10080)
+    two = (P * 2)(A, A)
+    assert f(None, two, 2, None) == 1 and f(odd, two, 2, None) == 1 and f(A, None, 2, None) == 1
+    assert f(A, two, 0, None) == 1 and f(A, (P * 9)(*[A] * 9), 9, None) == 1
+    assert f(A, (P * 2)(A, None), 2, None) == 1 and f(A, (P * 2)(odd, A), 2, None) == 1
+
+
+@pytest.mark.gpu
+def test_joined_status_words():
+    words = [0, 4, 1, 0, 2, 0, 0, 1]
+    ws = [moe.alloc_workspace(256) for _ in words]
+    for n in range(1, 9):
+        for w, v in zip(ws, words):
+            w[0] = v
+        into = moe.alloc_workspace(256)
+        into[0] = 8
+        moe.moe_join_status(into, ws[:n])
+        want = 8
+        for v in words[:n]:
+            want |= v
+        assert moe.moe_check_status(into) == want
+        assert [moe.moe_check_status(w) for w in ws] == words
