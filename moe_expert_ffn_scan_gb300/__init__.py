@@ -225,17 +225,6 @@ def _t(t, dtype, shape, name):
     return _p(t)  # raises
 
 
-def _flat(t, dtype, n, name):
-    """_p of n contiguous values of any shape (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.numel() == n and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype or t.numel() != n:
-        raise ValueError(f"{name}: expected {n} values of {dtype}, got {t.numel()} of {t.dtype}")
-    return _p(t)  # raises
-
-
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float32: 1}  # MOE_DTYPE_*
 
 
@@ -658,20 +647,46 @@ def _packed_rows(d):
     return d.T * (d.k + d.has_shared)
 
 
-def _here(t, name):
-    """The call runs on the current device: so must its tensors (checked on its main one)."""
-    if t.is_cuda and t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+# (each call's first tensor says on which device it is, here `dev`: the others have to be there,
+# and it has to be the current one, on whose streams the call runs)
+
+def _on(dev, t, dtype, shape, name):
+    """_t of a tensor on that device."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    _t(t, dtype, shape, name)  # raises, but for another device
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _flat(dev, t, dtype, n, name):
+    """_on of n contiguous values of any shape."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.numel() == n and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} values of {dtype}, got {t.numel()} of {t.dtype}")
+    return _on(dev, t, dtype, t.shape, name)  # raises
+
+
+def _stream_on(dev, stream):
+    """_raw_stream of a call on that device."""
+    now = _current_device()
+    if now != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{now}")
+    return stream.cuda_stream if stream is not None else _current_raw_stream(now)
 
 
 def moe_dispatch(d, x, inv, xp, stream=None):
     """x [T, H] bf16 to the packed rows of its experts, xp [Rs, H]: row inv[t*k+j] (moe_route's
     inv, [T*k] int32; an entry outside [0, T*k): no row) and, with a shared expert, row
     T*k + t."""
-    _here(x, "x")
+    dev = x.get_device()
     rc = lib().moe_dispatch(
-        _d(d), _t(x, _BF16, (d.T, d.H), "x"), _flat(inv, _I32, d.T * d.k, "inv"),
-        _t(xp, _BF16, (_packed_rows(d), d.H), "xp"), _raw_stream(stream))
+        _d(d), _on(dev, x, _BF16, (d.T, d.H), "x"), _flat(dev, inv, _I32, d.T * d.k, "inv"),
+        _on(dev, xp, _BF16, (_packed_rows(d), d.H), "xp"), _stream_on(dev, stream))
     if rc:
         raise MoeError("moe_dispatch", rc)
 
@@ -679,12 +694,12 @@ def moe_dispatch(d, x, inv, xp, stream=None):
 def moe_dispatch_backward(d, dxp, inv, dx, dx_in=None, stream=None):
     """Gradient of moe_dispatch: dx [T, H] (bf16 or fp32) = dx_in (dx's type, or None) + the sum
     of each token's rows of dxp [Rs, H] bf16."""
-    _here(dx, "dx")
+    dev = dx.get_device()
     shape, dt, code = (d.T, d.H), dx.dtype, _dtype_code(dx, "dx")
     rc = lib().moe_dispatch_backward(
-        _d(d), _t(dxp, _BF16, (_packed_rows(d), d.H), "dxp"),
-        _flat(inv, _I32, d.T * d.k, "inv"), _t(dx_in, dt, shape, "dx_in"),
-        code, _t(dx, dt, shape, "dx"), _raw_stream(stream))
+        _d(d), _on(dev, dxp, _BF16, (_packed_rows(d), d.H), "dxp"),
+        _flat(dev, inv, _I32, d.T * d.k, "inv"), _on(dev, dx_in, dt, shape, "dx_in"),
+        code, _on(dev, dx, dt, shape, "dx"), _stream_on(dev, stream))
     if rc:
         raise MoeError("moe_dispatch_backward", rc)
 
@@ -693,12 +708,13 @@ def moe_combine_backward(d, dout, y2, inv, w, dy2=None, dw=None, stream=None):
     """Gradient of moe_combine from dout [T, H] bf16: writes what is given of dy2 [Rs, H] bf16
     (w [T, k] fp32 times the token's dout) and dw [T, k] fp32 (from y2 [Rs, H] bf16, else
     None)."""
-    _here(dout, "dout")
+    dev = dout.get_device()
     rows = (_packed_rows(d), d.H)
     rc = lib().moe_combine_backward(
-        _d(d), _t(dout, _BF16, (d.T, d.H), "dout"), _t(y2, _BF16, rows, "y2"),
-        _flat(inv, _I32, d.T * d.k, "inv"), _t(w, _F32, (d.T, d.k), "w"),
-        _t(dy2, _BF16, rows, "dy2"), _t(dw, _F32, (d.T, d.k), "dw"), _raw_stream(stream))
+        _d(d), _on(dev, dout, _BF16, (d.T, d.H), "dout"), _on(dev, y2, _BF16, rows, "y2"),
+        _flat(dev, inv, _I32, d.T * d.k, "inv"), _on(dev, w, _F32, (d.T, d.k), "w"),
+        _on(dev, dy2, _BF16, rows, "dy2"), _on(dev, dw, _F32, (d.T, d.k), "dw"),
+        _stream_on(dev, stream))
     if rc:
         raise MoeError("moe_combine_backward", rc)
 
@@ -706,13 +722,13 @@ def moe_combine_backward(d, dout, y2, inv, w, dy2=None, dw=None, stream=None):
 def moe_swiglu_quant_save(y13, hq, hs, yq, ys, stream=None):
     """moe_swiglu_quant of y13 [rows, 2I] bf16 (hq [rows, I], hs [rows, I/128]) that also saves
     y13 in 8 bits, yq [rows, 2I] and ys [rows, 2I/128], for moe_swiglu_backward (all uint8)."""
-    _here(y13, "y13")
+    dev = y13.get_device()
     rows, two_i = y13.shape
     I = two_i // 2
     rc = lib().moe_swiglu_quant_save(
-        rows, I, _t(y13, _BF16, (rows, 2 * I), "y13"), _t(hq, _U8, (rows, I), "hq"),
-        _t(hs, _U8, (rows, I // 128), "hs"), _t(yq, _U8, (rows, 2 * I), "yq"),
-        _t(ys, _U8, (rows, 2 * I // 128), "ys"), _raw_stream(stream))
+        rows, I, _on(dev, y13, _BF16, (rows, 2 * I), "y13"), _on(dev, hq, _U8, (rows, I), "hq"),
+        _on(dev, hs, _U8, (rows, I // 128), "hs"), _on(dev, yq, _U8, (rows, 2 * I), "yq"),
+        _on(dev, ys, _U8, (rows, 2 * I // 128), "ys"), _stream_on(dev, stream))
     if rc:
         raise MoeError("moe_swiglu_quant_save", rc)
 
@@ -724,18 +740,18 @@ def moe_swiglu_backward(dh, dy13, y13=None, yq=None, ys=None, hq=None, hs=None, 
     routed row's (the first perm_src.numel() of them) times its weight of w [T, k] fp32 (None:
     1), and, if given, dw [T, k] fp32: the weights' gradient, from the values of hq, hs if given,
     else from silu(g) u."""
-    _here(dh, "dh")
+    dev = dh.get_device()
     rows, I = dh.shape
     R = perm_src.numel() if perm_src is not None else 0
-    wp, dwp = _flat(w, _F32, R, "w"), _flat(dw, _F32, R, "dw")
+    wp, dwp = _flat(dev, w, _F32, R, "w"), _flat(dev, dw, _F32, R, "dw")
     desc = moe_swiglu_backward_desc(rows, R, I)
     two, blocks = (rows, 2 * I), I // 128
     rc = lib().moe_swiglu_backward(
-        ctypes.byref(desc), _t(dh, _BF16, (rows, I), "dh"), _t(y13, _BF16, two, "y13"),
-        _t(yq, _U8, two, "yq"), _t(ys, _U8, (rows, 2 * blocks), "ys"),
-        _t(hq, _U8, (rows, I), "hq"), _t(hs, _U8, (rows, blocks), "hs"),
-        _flat(perm_src, _I32, R, "perm_src"), wp, _t(dy13, _BF16, two, "dy13"), dwp,
-        _raw_stream(stream))
+        ctypes.byref(desc), _on(dev, dh, _BF16, (rows, I), "dh"), _on(dev, y13, _BF16, two, "y13"),
+        _on(dev, yq, _U8, two, "yq"), _on(dev, ys, _U8, (rows, 2 * blocks), "ys"),
+        _on(dev, hq, _U8, (rows, I), "hq"), _on(dev, hs, _U8, (rows, blocks), "hs"),
+        _flat(dev, perm_src, _I32, R, "perm_src"), wp, _on(dev, dy13, _BF16, two, "dy13"), dwp,
+        _stream_on(dev, stream))
     if rc:
         raise MoeError("moe_swiglu_backward", rc)
 
@@ -746,14 +762,16 @@ def gemm_backward_workspace_size(d) -> int:
 
 def _gemm_backward(name, d, dy, cols_in, group_offsets, w, w_s, dx, cols_out, ws, stream,
                    block=32, scales=()):
-    _here(dy, "dy")
+    dev = dy.get_device()
     rows, G = _packed_rows(d), d.E + d.has_shared
     rc = getattr(lib(), name)(
-        _d(d), _t(dy, _BF16, (rows, cols_in), "dy"),
-        _t(group_offsets, _I32, (G + 1,), "group_offsets"),
-        _t(w, _U8, (G, cols_in, cols_out // 2), "w"),
-        _t(w_s, _U8, (G, cols_in, cols_out // block), "w_s"), *scales,
-        _t(dx, _BF16, (rows, cols_out), "dx"), _p(ws), ws.numel(), _raw_stream(stream))
+        _d(d), _on(dev, dy, _BF16, (rows, cols_in), "dy"),
+        _on(dev, group_offsets, _I32, (G + 1,), "group_offsets"),
+        _on(dev, w, _U8, (G, cols_in, cols_out // 2), "w"),
+        _on(dev, w_s, _U8, (G, cols_in, cols_out // block), "w_s"),
+        *[_on(dev, t, _F32, shape, n) for t, shape, n in scales],
+        _on(dev, dx, _BF16, (rows, cols_out), "dx"), _on(dev, ws, ws.dtype, ws.shape, "ws"),
+        ws.numel(), _stream_on(dev, stream))
     if rc:
         raise MoeError(name, rc)
 
@@ -776,7 +794,7 @@ def moe_grouped_gemm_w2_backward_nvfp4(d, dy2, group_offsets, w2, w2_s, w2_gs, d
     """moe_grouped_gemm_w2_backward with NVFP4 weights: w2_s [G, H, I/16] E4M3 scales, w2_gs [G]
     fp32 (None: 1)."""
     _gemm_backward("moe_grouped_gemm_w2_backward_nvfp4", d, dy2, d.H, group_offsets, w2, w2_s, dh,
-                   d.I, ws, stream, 16, (_t(w2_gs, _F32, (d.E + d.has_shared,), "w2_gs"),))
+                   d.I, ws, stream, 16, [(w2_gs, (d.E + d.has_shared,), "w2_gs")])
 
 
 def moe_grouped_gemm_w13_backward_nvfp4(d, dy13, group_offsets, w13, w13_s, w13_gs, dxp, ws,
@@ -785,7 +803,7 @@ def moe_grouped_gemm_w13_backward_nvfp4(d, dy13, group_offsets, w13, w13_s, w13_
     [G, 2] fp32 of the gate and up rows (None: 1)."""
     _gemm_backward("moe_grouped_gemm_w13_backward_nvfp4", d, dy13, 2 * d.I, group_offsets, w13,
                    w13_s, dxp, d.H, ws, stream, 16,
-                   (_t(w13_gs, _F32, (d.E + d.has_shared, 2), "w13_gs"),))
+                   [(w13_gs, (d.E + d.has_shared, 2), "w13_gs")])
 
 
 def moe_check_status(ws, stream=None) -> int:
