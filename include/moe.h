@@ -602,6 +602,17 @@ int moe_grouped_gemm_w13_backward_nvfp4(const moe_dims* d, const uint16_t* dy13,
                                         const uint8_t* w13_s, const float* w13_gs, uint16_t* dxp,
                                         void* ws, size_t ws_bytes, void* stream);
 
+/* Debug helpers of the gradient products.  Their kernel has two forms, tiles of one CTA (1) and of
+ * SM pairs (2): moe_gemm_backward_ctas says which one a call of these dims takes (product: 2 or
+ * 13, either weight format; 0: unsupported), moe_gemm_backward_form is the call with the form
+ * named (the arguments of the four above, nvfp4 1 with gs or 0; the results are the same up
+ * to the roundings of the fp32 sums). */
+int moe_gemm_backward_ctas(const moe_dims* d, int32_t product);
+int moe_gemm_backward_form(const moe_dims* d, int32_t product, int32_t nvfp4, int32_t ctas,
+                           const uint16_t* dy, const int32_t* group_offsets, const uint8_t* w,
+                           const uint8_t* w_s, const float* gs, uint16_t* dx, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* Debug helper (synchronises `stream`): reads the device status word at the start of
  * a workspace used by the calls above.  Returns MOE_OK if no bit is set, else
  * MOE_ERR_DEVICE_CHECK and the bits in *bits_out (if not NULL).  The word is

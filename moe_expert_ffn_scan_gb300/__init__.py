@@ -170,6 +170,10 @@ def lib():
             getattr(L, fn).argtypes = [_DP] + [_P] * 6 + [_SZ, _P]
             getattr(L, fn + "_nvfp4").argtypes = [_DP] + [_P] * 7 + [_SZ, _P]
             getattr(L, fn + "_nvfp4").restype = ctypes.c_int
+        L.moe_gemm_backward_ctas.argtypes = [_DP, _I]
+        L.moe_gemm_backward_ctas.restype = ctypes.c_int
+        L.moe_gemm_backward_form.argtypes = [_DP, _I, _I, _I] + [_P] * 7 + [_SZ, _P]
+        L.moe_gemm_backward_form.restype = ctypes.c_int
         for fn in ("moe_dispatch", "moe_dispatch_backward", "moe_combine_backward",
                    "moe_swiglu_quant_save", "moe_swiglu_backward",
                    "moe_grouped_gemm_w2_backward", "moe_grouped_gemm_w13_backward"):
@@ -761,11 +765,11 @@ def gemm_backward_workspace_size(d) -> int:
 
 
 def _gemm_backward(name, d, dy, cols_in, group_offsets, w, w_s, dx, cols_out, ws, stream,
-                   block=32, scales=()):
+                   block=32, scales=(), form=()):
     dev = dy.get_device()
     rows, G = _packed_rows(d), d.E + d.has_shared
     rc = getattr(lib(), name)(
-        _d(d), _on(dev, dy, _BF16, (rows, cols_in), "dy"),
+        _d(d), *form, _on(dev, dy, _BF16, (rows, cols_in), "dy"),
         _on(dev, group_offsets, _I32, (G + 1,), "group_offsets"),
         _on(dev, w, _U8, (G, cols_in, cols_out // 2), "w"),
         _on(dev, w_s, _U8, (G, cols_in, cols_out // block), "w_s"),
@@ -804,6 +808,21 @@ def moe_grouped_gemm_w13_backward_nvfp4(d, dy13, group_offsets, w13, w13_s, w13_
     _gemm_backward("moe_grouped_gemm_w13_backward_nvfp4", d, dy13, 2 * d.I, group_offsets, w13,
                    w13_s, dxp, d.H, ws, stream, 16,
                    [(w13_gs, (d.E + d.has_shared, 2), "w13_gs")])
+
+
+def gemm_backward_ctas(d, product) -> int:
+    """CTAs a tile that the gradient product (2 or 13) of these dims runs with: 1, or 2 (SM pairs)."""
+    return lib().moe_gemm_backward_ctas(_d(d), product)
+
+
+def moe_gemm_backward_form(d, product, ctas, dy, group_offsets, w, w_s, dx, ws, gs=None,
+                           nvfp4=False, stream=None):
+    """The gradient product 2 or 13 with `ctas` CTAs a tile, whatever the dims' cost (for tests)."""
+    cols = (d.H, d.I) if product == 2 else (2 * d.I, d.H)
+    G = d.E + d.has_shared
+    _gemm_backward("moe_gemm_backward_form", d, dy, cols[0], group_offsets, w, w_s, dx, cols[1], ws,
+                   stream, 16 if nvfp4 else 32, [(gs, (G,) if product == 2 else (G, 2), "gs")],
+                   (product, int(nvfp4), ctas))
 
 
 def moe_check_status(ws, stream=None) -> int:

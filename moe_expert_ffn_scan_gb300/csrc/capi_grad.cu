@@ -31,9 +31,17 @@ struct GradWeights {
   int segments;
 };
 
-// dx of the rows of dy through those weights.
+ExpertGradCall sizes_of(const moe_dims* d, int C, int F) {
+  ExpertGradCall a = {};
+  a.E = d->E, a.G = d->E + d->has_shared, a.routed = rows_R(d), a.rows = rows_Rs(d);
+  a.C = C, a.F = F;
+  return a;
+}
+
+// dx of the rows of dy through those weights, with 1 or 2 CTAs a tile or (0) as the sizes have it.
 int expert_grad(const moe_dims* d, int C, int F, const uint16_t* dy, const int32_t* offsets,
-                const GradWeights& W, uint16_t* dx, void* ws, size_t ws_bytes, void* stream) {
+                const GradWeights& W, uint16_t* dx, void* ws, size_t ws_bytes, void* stream,
+                int ctas = 0) {
   if (!dims_ok(d) || static_cast<long long>(d->E + 1) * C >= (1LL << 31))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (W.segments && (d->H % 256 || d->I % 256)) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -42,13 +50,12 @@ int expert_grad(const moe_dims* d, int C, int F, const uint16_t* dy, const int32
       !null_or(W.gs, 4) || !aligned(dx, 16) || !aligned(ws, kAlign))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_gemm_backward_workspace_size(d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  ExpertGradCall a = {};
+  ExpertGradCall a = sizes_of(d, C, F);
   a.dy = dy, a.offsets = offsets, a.w = W.w, a.w_s = W.w_s, a.dx = dx;
   a.nv = W.segments > 0, a.gs_segments = W.segments, a.gs = W.gs;
-  a.E = d->E, a.G = d->E + d->has_shared, a.routed = rows_R(d), a.rows = rows_Rs(d);
-  a.C = C, a.F = F;
   a.status = static_cast<uint32_t*>(ws);
-  return cuda_rc(launch_expert_grad(a, static_cast<cudaStream_t>(stream)));
+  return cuda_rc(launch_expert_grad(a, ctas ? ctas : expert_grad_ctas(a),
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -156,6 +163,25 @@ int moe_grouped_gemm_w13_backward_nvfp4(const moe_dims* d, const uint16_t* dy13,
   if (!d || d->I > (1 << 29)) return MOE_ERR_UNSUPPORTED_SHAPE;
   return expert_grad(d, 2 * d->I, d->H, dy13, group_offsets, {w13, w13_s, w13_gs, 2}, dxp, ws,
                      ws_bytes, stream);
+}
+
+int moe_gemm_backward_ctas(const moe_dims* d, int32_t product) {
+  if (!dims_ok(d) || d->I > (1 << 29) || (product != 2 && product != 13)) return 0;
+  return expert_grad_ctas(product == 2 ? sizes_of(d, d->H, d->I) : sizes_of(d, 2 * d->I, d->H));
+}
+
+int moe_gemm_backward_form(const moe_dims* d, int32_t product, int32_t nvfp4, int32_t ctas,
+                           const uint16_t* dy, const int32_t* group_offsets, const uint8_t* w,
+                           const uint8_t* w_s, const float* gs, uint16_t* dx, void* ws,
+                           size_t ws_bytes, void* stream) {
+  if (!d || d->I > (1 << 29)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((product != 2 && product != 13) || (nvfp4 != 0 && nvfp4 != 1) || (ctas != 1 && ctas != 2) ||
+      (gs && !nvfp4))
+    return MOE_ERR_INVALID_ARG;
+  const bool two = product == 2;
+  const GradWeights W = {w, w_s, gs, !nvfp4 ? 0 : two ? 1 : 2};
+  return expert_grad(d, two ? d->H : 2 * d->I, two ? d->I : d->H, dy, group_offsets, W, dx, ws,
+                     ws_bytes, stream, ctas);
 }
 
 }  // extern "C"

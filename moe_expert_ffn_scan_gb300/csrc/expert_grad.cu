@@ -932,14 +932,16 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
 // and 19, 21; w13 and w2 of 2048 x 1024, 16 groups of 50: 25, 15.2 and 21, 13.7; w2 of 1024 x 1024,
 // 64 groups of 20, 40: 17, 27 and 23, 23; w2 of 1280 x 768, 13 groups of 60, 179: 11.1, 18.0 and
 // 10.8, 12.8 (NVFP4 up to a tenth more of each).
-template <int P, int F>
+// (The formats' tiles have the same rows, features and stages.)
+template <int P>
 double cost_us(const ExpertGradCall& a) {
-  const double M = Cfg<P, F>::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
+  using C = Cfg<P, kMx>;
+  const double M = C::kRowsMax, groups = a.routed < a.E ? a.routed : a.E;
   auto chunks = [&](double rows) { return rows <= 0.75 * M ? 1.0 : rows / M + 0.4; };
   double items = groups * chunks(a.routed / groups);
   if (a.G > a.E) items += chunks(a.rows - a.routed);
   const double tiles = items * ((a.F + kFeat * P - 1) / (kFeat * P));
-  const double waves = ceil(tiles * P / (kSms * Cfg<P, F>::kOcc));
+  const double waves = ceil(tiles * P / (kSms * C::kOcc));
   const double stages = a.C / kBK;
   // (a CTA that has its SM for itself is faster: w2 of 2048 x 1024, 16 groups of 24 rows 11.4 us; a
   // pair's MMAs take longer for more rows)
@@ -950,15 +952,19 @@ double cost_us(const ExpertGradCall& a) {
 }
 
 template <int F>
-cudaError_t launch_form(const ExpertGradCall& a, cudaStream_t st) {
-  return cost_us<1, F>(a) <= cost_us<2, F>(a) ? launch_grad<1, F>(a, st) : launch_grad<2, F>(a, st);
+cudaError_t launch_form(const ExpertGradCall& a, int ctas, cudaStream_t st) {
+  return ctas == 1 ? launch_grad<1, F>(a, st) : launch_grad<2, F>(a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_expert_grad(const ExpertGradCall& a, cudaStream_t st) {
-  if (!a.nv) return launch_form<kMx>(a, st);
-  return a.gs_segments == 2 ? launch_form<kNvHalves>(a, st) : launch_form<kNv>(a, st);
+int expert_grad_ctas(const ExpertGradCall& a) {
+  return cost_us<1>(a) <= cost_us<2>(a) ? 1 : 2;
+}
+
+cudaError_t launch_expert_grad(const ExpertGradCall& a, int ctas, cudaStream_t st) {
+  if (!a.nv) return launch_form<kMx>(a, ctas, st);
+  return a.gs_segments == 2 ? launch_form<kNvHalves>(a, ctas, st) : launch_form<kNv>(a, ctas, st);
 }
 
 }  // namespace moe

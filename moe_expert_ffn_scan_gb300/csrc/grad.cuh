@@ -67,6 +67,8 @@ struct ExpertGradCall {
   int E, G, routed, rows, C, F;  // G = E, or E + 1 with a shared expert; routed: rows of the E
   uint32_t* status;
 };
-cudaError_t launch_expert_grad(const ExpertGradCall& a, cudaStream_t st);
+// CTAs a tile: single ones (1) or SM pairs (2), as the sizes' cost has it.
+int expert_grad_ctas(const ExpertGradCall& a);
+cudaError_t launch_expert_grad(const ExpertGradCall& a, int ctas, cudaStream_t st);
 
 }  // namespace moe

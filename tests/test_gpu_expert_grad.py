@@ -57,8 +57,8 @@ def _check(dy, off, w, w_s, dx, ints):
         assert torch.all((dx.double() - want).abs()[~out] <= tol[~out])
 
 
-# (the first five shapes run on single CTAs, the others on SM pairs: longer contractions, and
-# features that end in a pair's first half)
+# (on single CTAs or SM pairs by the sizes' cost; some features end in a pair's first half.  Each
+# form by name: test_gpu_grad_forms.py)
 @pytest.mark.parametrize("which", ["w2", "w13"])
 @pytest.mark.parametrize("H,I", [(128, 128), (256, 384), (640, 128), (1152, 256), (384, 640),
                                  (4096, 1152), (1152, 2048), (2048, 2048)])

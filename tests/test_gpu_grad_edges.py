@@ -13,10 +13,10 @@ BF, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
 NAN, INF = float("nan"), float("inf")
 
 
-def _nvfp4(which, H, I, rows, t):
-    """dx of groups of `rows` rows whose tensor scales are t.  dy is -2 .. 2 steps of 2^-14 and the
-    block scales 1, 2 or 3: the sums are exact in fp32 (multiples of 2^-15, of 2 I <= 4096 terms up
-    to 2^-14 * 36 below 9)."""
+def _nvfp4(which, H, I, rows, ctas, t):
+    """dx of groups of `rows` rows whose tensor scales are t, by `ctas` CTAs a tile.  dy is -2 .. 2
+    steps of 2^-14 and the block scales 1, 2 or 3: the sums are exact in fp32 (multiples of 2^-15, of
+    2 I <= 4096 terms up to 2^-14 * 36 below 9)."""
     g = torch.Generator(device=DEV).manual_seed(rows + H)
     ri = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=DEV)  # noqa: E731
     G, (C, F) = len(t), (H, I) if which == "w2" else (2 * I, H)
@@ -27,9 +27,7 @@ def _nvfp4(which, H, I, rows, t):
     dx = torch.full((G * rows, F), 7.0, dtype=BF, device=DEV)
     d = moe.dims(G * rows, H, I, G, 1, 0)
     ws = moe.alloc_workspace(moe.gemm_backward_workspace_size(d))
-    f = moe.moe_grouped_gemm_w2_backward_nvfp4 if which == "w2" \
-        else moe.moe_grouped_gemm_w13_backward_nvfp4
-    f(d, dy, off, w, w_s, t, dx, ws)
+    moe.moe_gemm_backward_form(d, 2 if which == "w2" else 13, ctas, dy, off, w, w_s, dx, ws, t, True)
     assert moe.moe_check_status(ws) == 0
     return dy, off, w, w_s, dx
 
@@ -56,38 +54,39 @@ def _agrees(dy, off, w, w_s, t, dx):
 
 
 BIG = 2.0 ** 122
-# (few features run on single CTAs, many on SM pairs: with two sums a tile, and with one)
-SHAPES = [(256, 256, 100), (256, 256, 200), (1280, 2048, 100), (1280, 2048, 200)]
+# (pairs have two sums of W13's halves a tile up to 128 rows, above that one)
+SHAPES = [(256, 256, 100, 1), (256, 256, 100, 2), (256, 256, 200, 2), (1280, 2048, 200, 1),
+          (1280, 2048, 200, 2)]
 
 
-@pytest.mark.parametrize("H,I,rows", SHAPES)
-def test_w13_tensor_scales_that_are_nan(H, I, rows):
+@pytest.mark.parametrize("H,I,rows,ctas", SHAPES)
+def test_w13_tensor_scales_that_are_nan(H, I, rows, ctas):
     t = torch.tensor([(NAN, 0.0), (0.0, NAN), (NAN, 1.0), (1.0, NAN), (NAN, NAN), (NAN, INF),
                       (-INF, NAN), (1.0, 0.5)], device=DEV)
-    dx = _nvfp4("w13", H, I, rows, t)[-1].view(len(t), -1)
+    dx = _nvfp4("w13", H, I, rows, ctas, t)[-1].view(len(t), -1)
     assert torch.all(torch.isnan(dx[:-1])) and torch.all(torch.isfinite(dx[-1]))
 
 
-@pytest.mark.parametrize("H,I,rows", SHAPES)
-def test_w13_tensor_scales_that_are_infinite(H, I, rows):
+@pytest.mark.parametrize("H,I,rows,ctas", SHAPES)
+def test_w13_tensor_scales_that_are_infinite(H, I, rows, ctas):
     t = torch.tensor([(INF, 0.5), (0.5, -INF), (-INF, 1.5), (0.375, INF), (1.0, 0.5)], device=DEV)
-    dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, t)
+    dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, ctas, t)
     _agrees(dy, off, w, w_s, t, dx)
 
 
-@pytest.mark.parametrize("H,I,rows", SHAPES)
-def test_w13_tensor_scales_that_are_large(H, I, rows):
+@pytest.mark.parametrize("H,I,rows,ctas", SHAPES)
+def test_w13_tensor_scales_that_are_large(H, I, rows, ctas):
     t = torch.tensor([(BIG, 1.0), (1.0, -BIG), (BIG, BIG), (-BIG, 2.0 ** 100), (2.0 ** 60, BIG),
                       (2.0 ** 120, 2.0 ** 121), (1.0, 1.0)], device=DEV)
-    dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, t)
+    dy, off, w, w_s, dx = _nvfp4("w13", H, I, rows, ctas, t)
     assert torch.all(torch.isfinite(dx))
     _agrees(dy, off, w, w_s, t, dx)
 
 
-@pytest.mark.parametrize("H,I,rows", SHAPES)
-def test_w2_tensor_scales_of_every_kind(H, I, rows):
+@pytest.mark.parametrize("H,I,rows,ctas", SHAPES)
+def test_w2_tensor_scales_of_every_kind(H, I, rows, ctas):
     t = torch.tensor([BIG, -BIG, 2.0 ** 121, NAN, INF, -INF, 1.0, 0.0, 2.0 ** -100], device=DEV)
-    dy, off, w, w_s, dx = _nvfp4("w2", H, I, rows, t)
+    dy, off, w, w_s, dx = _nvfp4("w2", H, I, rows, ctas, t)
     _agrees(dy, off, w, w_s, t, dx)
 
 
