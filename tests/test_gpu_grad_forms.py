@@ -86,6 +86,15 @@ def test_rows_outside_every_group(ctas, product, nv, lens, gap):
 
 @both
 @formats
+def test_rows_outside_every_group_have_no_part(ctas, product, nv):
+    c = _Case(product, nv, [3, 40, 0, 270], gap=(5, 9))
+    want = c.want()
+    c.dy[:5], c.dy[-9:] = float("nan"), float("inf")
+    assert torch.equal(c.run(ctas).dx, want)
+
+
+@both
+@formats
 @pytest.mark.parametrize("lens", [[5, -2, 6, 3], [5, 200], [-1, 5, 8]])
 def test_offsets_that_are_no_plan(ctas, product, nv, lens):
     c = _Case(product, nv, [3, 3, 3, 3])
