@@ -574,8 +574,8 @@ int moe_swiglu_backward(const moe_swiglu_backward_desc* d, const uint16_t* dh, c
  *     dxp[r][h] = sum_n dy13[r][n] * deq(w13[g])[n][h],   dy13 [Rs][2I], dxp [Rs][H],
  * bf16 rows, exact products, fp32 sums, one rounding to bf16.  group_offsets [G+1] as for the
  * forward: rows outside every group are not written, and have no part in the others (they may be
- * read: nothing else may write any row of dy2 or dy13 meanwhile); offsets that decrease or leave [0, Rs]
- * set the status word and nothing is written.
+ * read: nothing else may write any row of dy2 or dy13 meanwhile); offsets that decrease or leave
+ * [0, Rs] set the status word and nothing is written.
  *   ws: moe_gemm_backward_workspace_size bytes, 256-byte aligned.  Its first 4 bytes are a
  *   status word that these calls only set bits of: zero it once, before the first use and in
  *   an order with it, and keep the workspace to them; moe_check_status reads it. */

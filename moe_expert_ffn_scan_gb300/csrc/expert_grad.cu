@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(Cfg<P, F>::kThreads, Cfg<P, F>::kOcc)
       const GradTile t = tile_at<P, F>(L, f_tiles, G, off, first);
       const int mine = (t.rows + C::kUnit - 1) / C::kUnit * C::kUnit / P;  // rows in this CTA
       const int row0 = t.row0 + static_cast<int>(rank) * mine;
-      const bool small = mine <= 2 * C::kBoxSmall;
+      const bool small = mine <= P * C::kBoxSmall;  // (at most P loads)
       const int box = small ? C::kBoxSmall : C::kBox, boxes = (mine + box - 1) / box;
       const CUtensorMap* map = small ? &tmBs : &tmB;
       const uint32_t bytes = P * boxes * box * kBK * 2;
@@ -928,7 +928,7 @@ cudaError_t launch_grad(const ExpertGradCall& a, cudaStream_t st) {
 // tile's own besides.  A group of R / E rows is taken to have one chunk up to three quarters of a
 // tile's rows, above that what its rows fill and 0.4 (the groups' sizes vary).  Costs as measured
 // on GB300, weights from HBM (us; P = 1 and 2): w13 of 7168 x 2048, 32 groups of 24, 33, 40 rows:
-// 118, 223, 224 and 167, 168, 168; 8 groups of 30, 64: 41, 62 and 48, 48; 2 groups of 32, 100: 17, 41
+// 113, 223, 224 and 167, 168, 168; 8 groups of 30, 64: 41, 62 and 48, 48; 2 groups of 32, 100: 17, 41
 // and 19, 21; w13 and w2 of 2048 x 1024, 16 groups of 50: 25, 15.2 and 21, 13.7; w2 of 1024 x 1024,
 // 64 groups of 20, 40: 17, 27 and 23, 23; w2 of 1280 x 768, 13 groups of 60, 179: 11.1, 18.0 and
 // 10.8, 12.8 (NVFP4 up to a tenth more of each).
