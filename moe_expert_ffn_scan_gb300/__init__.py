@@ -843,8 +843,10 @@ def stage_workspaces(ws, n):
 
 def moe_join_status(ws, others, stream=None):
     """ORs the status words of the workspaces `others` (up to 8) into that of ws, on the stream."""
-    _check("moe_join_status", lib().moe_join_status(
-        _p(ws), (_P * len(others))(*[_p(w) for w in others]), len(others), _stream(stream)))
+    n = len(others)
+    rc = lib().moe_join_status(_p(ws), (_P * n)(*[_p(w) for w in others]), n, _raw_stream(stream))
+    if rc:
+        raise MoeError("moe_join_status", rc)
 
 
 def moe_selftest_wait_timeout(ws, stream=None):
@@ -996,7 +998,7 @@ class MoELayer:
         self.fmt, self.w13_gs, self.w2_gs = fmt, w13_gs, w2_gs
         self._ws = _LayerWorkspace(self._forward_size)
         self._hws = _LayerWorkspace(lambda T: host_workspace_size(self.dims(T)))
-        self._tws = _LayerWorkspace(self._forward_train_size)
+        self._tws, self._stages = _LayerWorkspace(self._forward_train_size), None
         self._bws = None
         if w13 is not None and w13.is_cuda and not torch.cuda.is_current_stream_capturing():
             self._backward_workspace()
@@ -1093,7 +1095,10 @@ class MoELayer:
             if out is None:
                 out = new(T, H)
             # each stage clears its status word at its start: one each, joined at the end
-            stages = stage_workspaces(self.train_workspaces(T)[0], 3)
+            ws = self.train_workspaces(T)[0]
+            if self._stages is None or self._stages[0].data_ptr() != ws.data_ptr():
+                self._stages = stage_workspaces(ws, 3)
+            stages = self._stages
             s = dict(T=T, idx=new(T, k, dt=_I32), w=new(T, k, dt=_F32), counts=new(E, dt=_I32),
                      offsets=new(E + sh + 1, dt=_I32), perm_src=new(R, dt=_I32),
                      inv=new(R, dt=_I32))
