@@ -24,7 +24,7 @@
 //     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
 //     of the shared-memory traffic for dy that a tile of its own would.  Bound by the tensor
 //     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 496 us, 1.94 PFLOP/s; in long runs by the
-//     power cap, 1.6 to 1.7.  (NVFP4's W13, whose halves have a scale each: 534 us, 1.80.)
+//     power cap, w13 1.62 to 1.67, w2 1.52 to 1.57.  (NVFP4's W13, whose halves have a scale each: 534 us, 1.80.)
 //   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
 //     weights' way from HBM and their conversion are the work.  Bound by the conversion's
 //     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s (NVFP4 126, 4.3).
@@ -73,7 +73,8 @@ struct Cfg {
   static constexpr int kFactors = kBK * 2 * (kFeat / kBlock) + 16;
   // Epilogue warps.  A pair's hold a tile's sums in registers: of eight warps with 128 rows each these
   // were too many, and spilled ones go to L2, as shared memory leaves hardly any L1 (w13 of
-  // 7168 x 2048, 32 groups of 64, 128, 192 rows: 174, 195, 217 us in place of 167, 187, 209).
+  // 7168 x 2048, 32 groups of 64, 128, 192 rows: 174, 195, 217 us in place of 167, 187, 209; twelve
+  // warps spill none with MXFP4 and up to 28 bytes a thread with NVFP4).
   static constexpr int kEpi = P == 2 ? 12 : 4;
   static constexpr int kGroups = 3;                   // converter groups of four warps
   // Warps that make factors: NVFP4's are twice as many and take a conversion each (32 groups of

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) k_swiglu_save(const uint16_t* __restrict_
 // A CTA per row, or with kPack `pack` warps per row and as many rows as the CTA's warps do for; 8
 // columns a thread at a time; all of a thread's loads are in flight before the first is used,
 // and what they bring stays packed until its four columns' turn, so that registers leave room
-// for full occupancy (73728 rows of 2048: 227 us, 0.90 of HBM; with 40 registers a thread 272,
+// for full occupancy (73728 rows of 2048: 224 to 227 us, 0.91 of HBM; with 40 registers a thread 272,
 // with 16 columns and 64 registers 254).  kCodes: g and u from the checkpoint; kH: h from hq.
 template <bool kCodes, bool kH, bool kPack>
 __global__ void __launch_bounds__(kPack ? 256 : kBwdThreads, kPack ? 6 : kBwdCtas)
