@@ -1000,9 +1000,6 @@ class MoELayer:
         self._hws = _LayerWorkspace(lambda T: host_workspace_size(self.dims(T)))
         self._tws, self._stages = _LayerWorkspace(self._forward_train_size), None
         self._bws = None
-        if w13 is not None and w13.is_cuda and not torch.cuda.is_current_stream_capturing():
-            self._backward_workspace()
-            torch.cuda.current_stream(w13.device).synchronize()
 
     def dims(self, T):
         return dims(T, self.H, self.I, self.E, self.k, self.has_shared)
@@ -1065,18 +1062,20 @@ class MoELayer:
         return max(route_workspace_size(d), 512 + gemm)  # (the stages': see forward_train)
 
     def _backward_workspace(self):
-        """The gradient products' status word collects the bits of every step: one for all of
-        them, made with the layer, so that it is zeroed before any stream or graph has it."""
+        """The gradient products' status word collects the bits of every step: made once, and
+        zeroed before any other stream can have it (in a capture: by that graph's replays)."""
         if self._bws is None:
-            size = gemm_backward_workspace_size(self.dims(1))
-            self._bws = alloc_workspace(size, self.w13.device) if size else None
+            self._bws = alloc_workspace(gemm_backward_workspace_size(self.dims(1)), self.w13.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self.w13.device).synchronize()
         return self._bws
 
     def train_workspaces(self, T, stream=None):
         """The workspaces of forward_train and backward steps of up to T tokens (moe_check_status
-        reads the checks of the last forward_train, and of every backward since the layer was
-        made)."""
-        return self._tws.get(T, self.w13, stream), self._backward_workspace()
+        reads the checks of the last forward_train, and of every backward so far; where a capture
+        was the first to ask for them, of every one since that graph's last replay began)."""
+        with torch.cuda.stream(stream):
+            return self._tws.get(T, self.w13), self._backward_workspace()
 
     def forward_train(self, x, logits, out=None, checkpoint="fp8", stream=None):
         """forward by its stages, keeping what backward needs.  Returns the output [T, H] and the
@@ -1095,7 +1094,7 @@ class MoELayer:
             if out is None:
                 out = new(T, H)
             # each stage clears its status word at its start: one each, joined at the end
-            ws = self.train_workspaces(T)[0]
+            ws = self._tws.get(T, self.w13)
             if self._stages is None or self._stages[0].data_ptr() != ws.data_ptr():
                 self._stages = stage_workspaces(ws, 3)
             stages = self._stages
@@ -1142,7 +1141,7 @@ class MoELayer:
         Rs = T * (self.k + self.has_shared)
         with torch.cuda.stream(stream):
             new = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=dout.device)  # noqa: E731
-            ws = self.train_workspaces(T)[1]
+            ws = self._backward_workspace()
             if dx is None:
                 dx = new(T, H)
             rows, dh, dy13, dw = new(Rs, H), new(Rs, I), new(Rs, 2 * I), new(T, self.k, dt=_F32)

@@ -25,6 +25,11 @@ class _Recorded:
         self.streams.append(s)
 
 
+class _Stream(int):
+    def synchronize(self):
+        pass
+
+
 @pytest.fixture
 def played(monkeypatch):
     """The capture state, the current stream, and the workspaces that are alive."""
@@ -37,7 +42,7 @@ def played(monkeypatch):
     monkeypatch.setattr(moe, "alloc_workspace", alloc)
     monkeypatch.setattr(moe, "_raw_stream", lambda s: now["stream"])
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: now["stream"])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: _Stream(now["stream"]))
     return now
 
 
