@@ -1087,9 +1087,12 @@ class MoELayer:
         if checkpoint not in ("fp8", "bf16"):
             raise ValueError(f"unknown checkpoint form {checkpoint!r}")
         T, H, I, k, sh, E = x.shape[0], self.H, self.I, self.k, self.has_shared, self.E
-        d = self.dims(T)
+        d, dev = self.dims(T), x.get_device()
         R, Rs = T * k, T * (k + sh)
         with torch.cuda.stream(stream):
+            # (the stages take what they are given)
+            _on(dev, x, _BF16, (T, H), "x"), _on(dev, logits, _F32, (T, E), "logits")
+            _on(dev, out, _BF16, (T, H), "out"), _stream_on(dev, None)
             new = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device=x.device)  # noqa: E731
             if out is None:
                 out = new(T, H)

@@ -1,5 +1,5 @@
 """The device checks of the layer's gradient: a call runs on the current device, and each of its
-tensors has to be there.  Stand-ins for tensors of two GPUs and for the library; no GPU."""
+tensors has to be there; the layer's training step checks what it is given.  Stand-ins for tensors of two GPUs and for the library; no GPU."""
 
 import pytest
 import torch
@@ -95,3 +95,22 @@ def test_every_tensor_of_a_call(monkeypatch, name, args):
         with pytest.raises(ValueError, match="cuda:1"):
             call(away=n)
     assert library.calls == 1
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x=f32(T, H)), dict(x=bf(T, H + 128)), dict(logits=bf(T, E)), dict(logits=f32(T - 1, E)),
+    dict(logits=f32(T, E + 1)), dict(out=f32(T, H)), dict(out=bf(T + 1, H)),
+    dict(x=dict(shape=(T, H), dt=BF, device=1)), dict(logits=dict(shape=(T, E), dt=F32, device=1)),
+    dict(out=dict(shape=(T, H), dt=BF, device=1))], ids=str)
+def test_forward_train_checks_its_tensors(monkeypatch, bad):
+    """(Its stages take what they are given.)"""
+    library = _Library()
+    monkeypatch.setattr(moe, "lib", lambda: library)
+    monkeypatch.setattr(moe, "_current_device", lambda: 0)
+    layer = moe.MoELayer(H, I, E, k, 1, None, None, None, None)
+    args = dict(x=bf(T, H), logits=f32(T, E), out=bf(T, H)) | bad
+    name = next(iter(bad))
+    tensors = {n: _T(*v["shape"], dt=v["dt"], device=v.get("device", 0)) for n, v in args.items()}
+    with pytest.raises(ValueError, match=name + ("" if "device" not in bad[name] else ".*cuda:1|cuda:1")):
+        layer.forward_train(**tensors)
+    assert library.calls == 0
