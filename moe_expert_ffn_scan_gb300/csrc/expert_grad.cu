@@ -24,7 +24,7 @@
 //     Each CTA converts its 128 features and loads half of the rows, so a stage costs an SM half
 //     of the shared-memory traffic for dy that a tile of its own would.  Bound by the tensor
 //     cores: w13 of 7168 x 2048, 16 groups of 1024 rows 496 us, 1.94 PFLOP/s; in long runs by the
-//     power cap, w13 1.62 to 1.67, w2 1.52 to 1.57.  (NVFP4's W13, whose halves have a scale each: 534 us, 1.80.)
+//     power cap, w13 1.62 to 1.67, w2 1.52 to 1.57.  (NVFP4's W13, whose halves have a scale each: 541 us, 1.78.)
 //   * P = 1, two CTAs an SM: 128 features x up to 32 rows, for groups of few rows, where the
 //     weights' way from HBM and their conversion are the work.  Bound by the conversion's
 //     instructions: 32 groups of 16 rows 114 us, the weights at 4.5 TB/s (NVFP4 126, 4.3).
@@ -58,7 +58,7 @@ constexpr int kMaxGroups = 1025;
 // end where tensor memory has room for two: up to 32 rows, or 128 of a pair.  In a pair's tile of
 // more rows the half of the smaller scale is summed first, that sum is then multiplied in place by
 // the scales' quotient, and the other half added to it (w13 of 7168 x 2048, 32 groups of 256 rows:
-// 279 us, by two tiles of 128 rows 388; 16 groups of 1024: 534, 758).
+// 281 us, by two tiles of 128 rows 388; 16 groups of 1024: 541, 758).
 enum Format { kMx = 0, kNv = 1, kNvHalves = 2 };
 
 template <int P, int F>
